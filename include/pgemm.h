@@ -278,6 +278,80 @@ int preduce_sum_f32(const float* x, float* o, int64_t R, int64_t n, pgemm_stream
 int pgemm_test_fill_f32(float* o, float v, int64_t n, pgemm_stream_t stream);
 int pgemm_test_iota_f32(float* o, int64_t n, pgemm_stream_t stream);
 
+/* ===========================================================================
+ * Layers of a language model's step: the linear layer, the gated feed-forward
+ * block, the softmax cross entropy over a vocabulary, and gradient clipping.
+ *
+ * Common to them, beyond the contract above:
+ *  - dtype is the 16-bit element type of every matrix of a call (PGEMM_F16 or
+ *    PGEMM_BF16).  Sums, activations and softmax statistics are fp32 (the
+ *    squares of gradients fp64); each output is rounded once, to nearest even.
+ *  - Matrices are row-major with a row pitch ld (in elements, at least the
+ *    row's length; not looked at when there is a single row).  Any sizes,
+ *    pitches and 2-byte aligned addresses are accepted; M, N and K may be 0
+ *    (an empty sum is 0).  Rows of whole 16-byte pieces (16-byte aligned
+ *    address, pitch and length multiples of 8) are copied from where they
+ *    lie; other operands of a matrix product are first copied to padded rows
+ *    in the workspace.
+ *  - An output must not overlap an input or another output in memory
+ *    (PGEMM_EINVAL), except where said; matrices that are disjoint column
+ *    ranges of one buffer do not overlap.
+ *  - Workspace: the caller's, 16-byte aligned, at least the bytes that the
+ *    call's _workspace_bytes function gives for the same arguments (0: may be
+ *    NULL), disjoint from every other buffer, free to reuse once the stream
+ *    has passed the call.  Those functions look at pointers' alignment only,
+ *    and return a negative status for arguments that the call would refuse.
+ *  - Results are the same bits call after call for the same arguments.
+ *  - PGEMM_EUNSUPPORTED: unknown dtype or activation, an odd address, a row
+ *    length or pitch of 2^22 or more, 2^31 - 256 rows or more, or an output of
+ *    more than 2^37 elements.
+ * ======================================================================== */
+enum pgemm_dtype { PGEMM_F16 = 0, PGEMM_BF16 = 1, PGEMM_F32 = 2 };
+
+/* Activations: z; max(z, 0); z Phi(z) with the normal distribution function
+ * Phi; its tanh form 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))); and
+ * z / (1 + exp(-z)).  The derivative of max(z, 0) at 0 is 0. */
+enum pgemm_activation {
+    PGEMM_ACT_NONE = 0,
+    PGEMM_ACT_RELU = 1,
+    PGEMM_ACT_GELU = 2,
+    PGEMM_ACT_GELU_TANH = 3,
+    PGEMM_ACT_SILU = 4
+};
+
+/*
+ * Linear layer: z = x W + bias, y = act(z) + residual.
+ *   x [M,K], W [K,N], bias [N], residual [M,N], y [M,N]; bias and residual may
+ *   be NULL.  preact [M,N] (may be NULL) receives z rounded to dtype, which
+ *   the backward pass needs for every activation but PGEMM_ACT_NONE.  y may be
+ *   exactly residual (same address and pitch).
+ */
+int plinear(int dtype, const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
+            const void* residual, int64_t ldr, void* y, int64_t ldy, void* preact, int64_t ldp,
+            int64_t M, int64_t N, int64_t K, int act, void* workspace, int64_t workspace_bytes,
+            pgemm_stream_t stream);
+int64_t plinear_workspace_bytes(int dtype, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                int64_t M, int64_t N, int64_t K);
+
+/*
+ * Backward pass of the linear layer: with dz = dy * act'(z),
+ *   dx = dz W^T + add,  dW = x^T dz,  dbias[n] = sum over m of dz[m][n].
+ * (The gradient of residual is dy itself.)  dy [M,N]; preact as the forward
+ * pass wrote it (unused and may be NULL for PGEMM_ACT_NONE); add [M,K] (may be
+ * NULL) is added to dx before rounding, for instance dy where x was also the
+ * residual; dx may be exactly add.  dx, dW and dbias may each be NULL: that gradient is
+ * not computed, and W (without dx) and x (without dW) may be NULL too.
+ */
+int plinear_bwd(int dtype, const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w,
+                int64_t ldw, const void* preact, int64_t ldp, const void* add, int64_t ldadd,
+                void* dx, int64_t lddx, void* dw, int64_t lddw, void* dbias, int64_t M, int64_t N,
+                int64_t K, int act, void* workspace, int64_t workspace_bytes,
+                pgemm_stream_t stream);
+/* need_dx, need_dw, need_dbias: whether the call will have that output. */
+int64_t plinear_bwd_workspace_bytes(int dtype, const void* dy, int64_t lddy, const void* x,
+                                    int64_t ldx, const void* w, int64_t ldw, int64_t M, int64_t N,
+                                    int64_t K, int act, int need_dx, int need_dw, int need_dbias);
+
 /* Static English text for a status code (never NULL). */
 const char* pgemm_status_string(int status);
 

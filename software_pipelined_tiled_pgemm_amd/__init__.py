@@ -19,6 +19,7 @@ __all__ = [
     "pgemm_f16_splitk_default_splits",
     "pstream_add", "pstream_add_blocked", "pstream_add_scalar", "preduce_sum_f32",
     "pgemm_test_fill_f32", "pgemm_test_iota_f32",
+    "plinear", "plinear_bwd",
     "lib", "status_string", "PgemmError",
     "PGEMM_OK", "PGEMM_EINVAL", "PGEMM_EUNSUPPORTED", "PGEMM_EHIP", "PGEMM_ESCRATCH",
     "STATIC_SCRATCH_BYTES",
@@ -317,3 +318,6 @@ def pgemm_test_iota_f32(n, device="cuda", out=None, stream=None):
     rc = _invoke(o, stream, lambda h: f(o.data_ptr(), o.numel(), h))
     _call(rc, "pgemm_test_iota_f32")
     return o
+
+
+from .layers import plinear, plinear_bwd  # noqa: E402  (uses the helpers above)

@@ -48,6 +48,13 @@ def _declare(lib):
         "preduce_sum_f32": (i32, [p, p, i64, i64, p]),
         "pgemm_test_fill_f32": (i32, [p, ctypes.c_float, i64, p]),
         "pgemm_test_iota_f32": (i32, [p, i64, p]),
+        "plinear": (i32, [i32, p, i64, p, i64, p, p, i64, p, i64, p, i64, i64, i64, i64, i32, p,
+                          i64, p]),
+        "plinear_workspace_bytes": (i64, [i32, p, i64, p, i64, i64, i64, i64]),
+        "plinear_bwd": (i32, [i32, p, i64, p, i64, p, i64, p, i64, p, i64, p, i64, p, i64, p, i64,
+                              i64, i64, i32, p, i64, p]),
+        "plinear_bwd_workspace_bytes": (i64, [i32, p, i64, p, i64, p, i64, i64, i64, i64, i32, i32,
+                                              i32, i32]),
         "pgemm_status_string": (ctypes.c_char_p, [i32]),
         "pgemm_last_hip_error": (i32, []),
         "pgemm_version": (i32, []),

@@ -47,6 +47,12 @@ PER_FILE = {
     # the compiler moves accumulator blocks between register files inside
     # the K loop; see the file's header comment).
     "gemm_f16_m16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    # The layer operators' products are the same kernels with other
+    # operand layouts and epilogues.
+    "linear.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "layer_split.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "ffn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "xent.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
 }
 
 
@@ -79,7 +85,7 @@ def build(verbose: bool = False, extra_flags=None) -> str:
         cmd = ([HIPCC] + FLAGS + PER_FILE.get(name, []) + list(extra_flags or [])
                + ["-c", src, "-o", obj])
         jobs.append((cmd, obj))
-    with ThreadPoolExecutor(max_workers=min(4, len(jobs))) as ex:
+    with ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
         list(ex.map(lambda j: _run(j[0], verbose), jobs))
     tmp = LIB + ".tmp%d" % os.getpid()
     objs = [o for _, o in jobs]

@@ -7,6 +7,10 @@
 
 namespace pgemm {
 
+// The status of a HIP result; a failure is kept for pgemm_last_hip_error on
+// the calling thread.
+int record_hip_status(hipError_t e);
+
 // GEMM tile configurations (ids match pgemm_f16_variant).
 enum GemmVariant : int {
     kGemmAuto = 0,

@@ -1,0 +1,219 @@
+// C entry points of the layer operators: argument checks, workspace, status.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/pgemm.h"
+#include "linear.h"
+
+namespace {
+
+using namespace pgemm::layer;
+
+constexpr int64_t kMaxCols = (int64_t)1 << 22;  // row lengths and pitches
+constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 256;
+constexpr int64_t kMaxElems = (int64_t)1 << 37;
+
+// A matrix argument: what overlap and size checks need of it.
+struct Mat {
+    const void* p;
+    int64_t rows, cols, ld;  // ld in elements
+    int bytes;               // per element
+    bool empty() const { return !p || rows == 0 || cols == 0; }
+    int64_t extent() const { return ((rows - 1) * ld + cols) * bytes; }
+};
+
+Mat mat(const void* p, int64_t rows, int64_t cols, int64_t ld) {
+    return {p, rows, cols, rows > 1 ? ld : cols, 2};
+}
+Mat flat(const void* p, int64_t n, int bytes) { return {p, 1, n, n, bytes}; }
+
+// Status of a matrix's own description; `needed`: it must not be NULL unless
+// it is empty.
+int check(const Mat& m, bool needed) {
+    if (m.rows < 0 || m.cols < 0) return PGEMM_EINVAL;
+    if (m.rows == 0 || m.cols == 0) return PGEMM_OK;
+    if (!m.p) return needed ? PGEMM_EINVAL : PGEMM_OK;
+    if (m.ld < m.cols) return PGEMM_EINVAL;
+    if (m.bytes == 2 && (m.ld >= kMaxCols || m.cols >= kMaxCols)) return PGEMM_EUNSUPPORTED;
+    if (m.rows >= kMaxRows || m.rows > kMaxElems / m.cols) return PGEMM_EUNSUPPORTED;
+    if (reinterpret_cast<uintptr_t>(m.p) % (uintptr_t)m.bytes) return PGEMM_EUNSUPPORTED;
+    return PGEMM_OK;
+}
+
+// The two matrices share an element.  Column ranges of one buffer (the same
+// pitch) are told apart by their column offsets.
+bool shares(const Mat& a, const Mat& b) {
+    if (a.empty() || b.empty()) return false;
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+    if (a0 >= b0 + (uintptr_t)b.extent() || b0 >= a0 + (uintptr_t)a.extent()) return false;
+    if (a.rows > 1 && b.rows > 1 && a.ld == b.ld && a.bytes == b.bytes) {
+        const int64_t pitch = a.ld * a.bytes;
+        int64_t d = (int64_t)(b0 - a0) % pitch;
+        if (d < 0) d += pitch;
+        if (d >= a.cols * a.bytes && d + b.cols * b.bytes <= pitch) return false;
+    }
+    return true;
+}
+
+// Outputs against everything: `same` names an input that an output may equal
+// exactly.
+struct Outputs {
+    int rc = PGEMM_OK;
+    void fail(int status) {
+        if (rc == PGEMM_OK) rc = status;
+    }
+    void apart(const Mat& out, const Mat& other, bool may_equal = false) {
+        if (may_equal && out.p == other.p && out.ld == other.ld && out.cols == other.cols) return;
+        if (shares(out, other)) fail(PGEMM_EINVAL);
+    }
+    void add(int status) { if (status != PGEMM_OK) fail(status); }
+};
+
+int hip_status(hipError_t e) { return pgemm::record_hip_status(e); }
+
+bool known(int dtype, int act) {
+    return (dtype == PGEMM_F16 || dtype == PGEMM_BF16) && act >= PGEMM_ACT_NONE &&
+           act <= PGEMM_ACT_SILU;
+}
+
+// Runs `f` once dry, to size the workspace, and then on it.  `others`: the
+// call's buffers, which the workspace must not share memory with.
+template <class F>
+int with_workspace(F&& f, void* workspace, int64_t workspace_bytes, const Mat* others, int n) {
+    Arena dry = {nullptr, 0};
+    hipError_t e = f(dry);
+    if (e != hipSuccess) return hip_status(e);
+    Arena ar = {static_cast<char*>(workspace), 0};
+    if (dry.used > 0) {
+        if (!workspace || workspace_bytes < dry.used) return PGEMM_EINVAL;
+        if (!aligned16(workspace)) return PGEMM_EUNSUPPORTED;
+        const Mat ws = flat(workspace, dry.used, 1);
+        for (int i = 0; i < n; ++i)
+            if (shares(ws, others[i])) return PGEMM_EINVAL;
+    } else {
+        // nothing will be taken, but a null base would mean a dry run
+        static char none;
+        ar.base = &none;
+    }
+    return hip_status(f(ar));
+}
+
+int check_linear(int dtype, int act, int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || N < 0 || K < 0) return PGEMM_EINVAL;
+    if (!known(dtype, act)) return PGEMM_EUNSUPPORTED;
+    if (M >= kMaxRows || N >= kMaxCols || K >= kMaxCols) return PGEMM_EUNSUPPORTED;
+    return PGEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int plinear(int dtype, const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
+            const void* residual, int64_t ldr, void* y, int64_t ldy, void* preact, int64_t ldp,
+            int64_t M, int64_t N, int64_t K, int act, void* workspace, int64_t workspace_bytes,
+            pgemm_stream_t stream) {
+    int rc = check_linear(dtype, act, M, N, K);
+    if (rc != PGEMM_OK) return rc;
+    if (M == 0 || N == 0) return PGEMM_OK;
+    const Mat mx = mat(x, M, K, ldx), mw = mat(w, K, N, ldw), mb = flat(bias, N, 2),
+              mr = mat(residual, M, N, ldr), my = mat(y, M, N, ldy), mp = mat(preact, M, N, ldp);
+    Outputs o;
+    o.add(check(mx, true));
+    o.add(check(mw, true));
+    o.add(check(mb, false));
+    o.add(check(mr, false));
+    o.add(check(my, true));
+    o.add(check(mp, false));
+    if (o.rc != PGEMM_OK) return o.rc;
+    for (const Mat* in : {&mx, &mw, &mb}) {
+        o.apart(my, *in);
+        o.apart(mp, *in);
+    }
+    o.apart(my, mr, true);
+    o.apart(mp, mr);
+    o.apart(mp, my);
+    if (o.rc != PGEMM_OK) return o.rc;
+    const LinearCall c = {dtype, x, mx.ld, w, mw.ld, bias, residual, mr.ld, y, my.ld, preact, mp.ld,
+                          M, N, K, act};
+    const Mat all[] = {mx, mw, mb, mr, my, mp};
+    return with_workspace(
+        [&](Arena& ar) { return linear_forward(c, ar, static_cast<hipStream_t>(stream)); },
+        workspace, workspace_bytes, all, 6);
+}
+
+int64_t plinear_workspace_bytes(int dtype, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                int64_t M, int64_t N, int64_t K) {
+    int rc = check_linear(dtype, PGEMM_ACT_NONE, M, N, K);
+    if (rc != PGEMM_OK) return rc;
+    if (M == 0 || N == 0) return 0;
+    const Mat mx = mat(x, M, K, ldx), mw = mat(w, K, N, ldw);
+    if ((rc = check(mx, true)) != PGEMM_OK || (rc = check(mw, true)) != PGEMM_OK) return rc;
+    LinearCall c = {};
+    c.dtype = dtype;
+    c.x = x, c.ldx = mx.ld, c.w = w, c.ldw = mw.ld;
+    c.M = M, c.N = N, c.K = K;
+    Arena dry = {nullptr, 0};
+    const hipError_t e = linear_forward(c, dry, nullptr);
+    return e == hipSuccess ? dry.used : hip_status(e);
+}
+
+int plinear_bwd(int dtype, const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w,
+                int64_t ldw, const void* preact, int64_t ldp, const void* add, int64_t ldadd,
+                void* dx, int64_t lddx, void* dw, int64_t lddw, void* dbias, int64_t M, int64_t N,
+                int64_t K, int act, void* workspace, int64_t workspace_bytes,
+                pgemm_stream_t stream) {
+    int rc = check_linear(dtype, act, M, N, K);
+    if (rc != PGEMM_OK) return rc;
+    const Mat mdy = mat(dy, M, N, lddy), mx = mat(x, M, K, ldx), mw = mat(w, K, N, ldw),
+              mp = mat(preact, M, N, ldp), ma = mat(add, M, K, ldadd), mdx = mat(dx, M, K, lddx),
+              mdw = mat(dw, K, N, lddw), mdb = flat(dbias, N, 2);
+    Outputs o;
+    o.add(check(mdy, dx || dw || dbias));
+    o.add(check(mx, dw != nullptr));
+    o.add(check(mw, dx != nullptr));
+    o.add(check(mp, act != PGEMM_ACT_NONE && (dx || dw || dbias)));
+    o.add(check(ma, false));
+    o.add(check(mdx, false));
+    o.add(check(mdw, false));
+    o.add(check(mdb, false));
+    if (o.rc != PGEMM_OK) return o.rc;
+    for (const Mat* out : {&mdx, &mdw, &mdb}) {
+        for (const Mat* in : {&mdy, &mx, &mw, &mp}) o.apart(*out, *in);
+        o.apart(*out, ma, out == &mdx);
+    }
+    o.apart(mdx, mdw);
+    o.apart(mdx, mdb);
+    o.apart(mdw, mdb);
+    if (o.rc != PGEMM_OK) return o.rc;
+    const LinearGradCall c = {dtype, dy, mdy.ld, x, mx.ld, w, mw.ld, preact, mp.ld, add, ma.ld,
+                              dx, mdx.ld, dw, mdw.ld, dbias, M, N, K, act};
+    const Mat all[] = {mdy, mx, mw, mp, ma, mdx, mdw, mdb};
+    return with_workspace(
+        [&](Arena& ar) { return linear_backward(c, ar, static_cast<hipStream_t>(stream)); },
+        workspace, workspace_bytes, all, 8);
+}
+
+int64_t plinear_bwd_workspace_bytes(int dtype, const void* dy, int64_t lddy, const void* x,
+                                    int64_t ldx, const void* w, int64_t ldw, int64_t M, int64_t N,
+                                    int64_t K, int act, int need_dx, int need_dw, int need_dbias) {
+    int rc = check_linear(dtype, act, M, N, K);
+    if (rc != PGEMM_OK) return rc;
+    const Mat mdy = mat(dy, M, N, lddy), mx = mat(x, M, K, ldx), mw = mat(w, K, N, ldw);
+    if ((rc = check(mdy, need_dx || need_dw || need_dbias)) != PGEMM_OK ||
+        (rc = check(mx, need_dw != 0)) != PGEMM_OK || (rc = check(mw, need_dx != 0)) != PGEMM_OK)
+        return rc;
+    LinearGradCall c = {};
+    void* const some = reinterpret_cast<void*>(16);  // stands for an output; never touched
+    c.dtype = dtype;
+    c.dy = dy, c.lddy = mdy.ld, c.x = x, c.ldx = mx.ld, c.w = w, c.ldw = mw.ld;
+    c.dx = need_dx ? some : nullptr;
+    c.dw = need_dw ? some : nullptr;
+    c.dbias = need_dbias ? some : nullptr;
+    c.M = M, c.N = N, c.K = K, c.act = act;
+    Arena dry = {nullptr, 0};
+    const hipError_t e = linear_backward(c, dry, nullptr);
+    return e == hipSuccess ? dry.used : hip_status(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,192 @@
+// The linear layer with its epilogue, and its backward pass.
+//
+//   forward    z = x W + b,  y = act(z) + r           x [M,K], W [K,N]
+//   backward   dz = dy * act'(z)
+//              dx = dz W^T (+ a),  dW = x^T dz,  db = sum over rows of dz
+//
+// z is summed in fp32 and y rounded once; the backward pass takes z as the
+// forward pass stored it (rounded to the type, which moves act' by no more
+// than a rounding of dy would), computes dz in fp32 and rounds it once, as
+// the operand of two products.  db adds the unrounded dz in fp32, in a fixed
+// order.
+#include "layer_pipe.h"
+#include "linear.h"
+
+namespace pgemm {
+namespace layer {
+namespace {
+
+// y = act(v + bias) + residual; z = v + bias is stored too where asked for.
+template <class E>
+struct LinearEpi {
+    static constexpr lp::EpiKind kind = lp::kPlain;
+    Rows y, res, pre;
+    const uint16_t* bias;
+    int bias_vec;
+    int act;
+    __device__ __forceinline__ void operator()(int row, int col, int nv, float (&v)[8]) const {
+        float t[8];
+        if (bias) {
+            load8_vec<E>(bias, bias_vec, col, nv, t);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] += t[q];
+        }
+        if (pre) store8<E>(pre, row, col, nv, v);
+        if (act != PGEMM_ACT_NONE) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = act_value(act, v[q]);
+        }
+        if (res) {
+            load8<E>(res, row, col, nv, t);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] += t[q];
+        }
+        store8<E>(y, row, col, nv, v);
+    }
+};
+
+// dz = dy * act'(z), and the column sums of each block of `per` rows.  A
+// workgroup covers 512 columns (64 lanes of 8) in 4 row lanes.  Memory
+// bound: reads dy and z, writes dz, once each.
+constexpr int64_t kDzRows = 64;
+constexpr int64_t kDzBlocks = 32768;  // most row blocks of a launch (grid y)
+
+template <class E>
+__global__ __launch_bounds__(256) void dz_kernel(const Rows dy, const Rows pre, const Rows dz,
+                                                 float* __restrict__ part, int64_t M, int N,
+                                                 int dz_cols, int64_t per, int act) {
+    __shared__ float sums[4][512];
+    const int cl = threadIdx.x & 63, rl = threadIdx.x >> 6;
+    const int col = (blockIdx.x * 64 + cl) * 8;
+    const int nv = min(8, N - col);
+    const int64_t r0 = (int64_t)blockIdx.y * per;
+    const int64_t r1 = r0 + per < M ? r0 + per : M;
+    float s[8] = {};
+    if (col < dz_cols) {
+        for (int64_t r = r0 + rl; r < r1; r += 4) {
+            float d[8], z[8], unused;
+            load8<E>(dy, r, col, nv, d);
+            if (pre) {
+                load8<E>(pre, r, col, nv, z);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) d[q] *= act_grad(act, z[q], unused);
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                if (q >= nv) d[q] = 0.0f;
+                s[q] += d[q];
+            }
+            // dz rows are padded with zeros to whole chunks
+            if (dz) store8<E>(dz, r, col, 8, d);
+        }
+    }
+    if (part) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sums[rl][cl * 8 + q] = s[q];
+        __syncthreads();
+        for (int c = threadIdx.x; c < 512; c += 256) {
+            const int64_t gc = (int64_t)blockIdx.x * 512 + c;
+            if (gc < N)
+                part[blockIdx.y * (int64_t)N + gc] =
+                    ((sums[0][c] + sums[1][c]) + sums[2][c]) + sums[3][c];
+        }
+    }
+}
+
+Rows rows(const void* p, int64_t ld) {
+    return {static_cast<uint16_t*>(const_cast<void*>(p)), ld, p ? vector_rows(p, ld) : 0};
+}
+
+template <class E>
+struct Linear {
+    static hipError_t forward(const LinearCall& c, Arena& ar, hipStream_t stream) {
+        View x, w;
+        hipError_t rc;
+        if ((rc = operand(c.x, c.ldx, c.M, c.K, ar, stream, x)) != hipSuccess) return rc;
+        if ((rc = operand(c.w, c.ldw, c.K, c.N, ar, stream, w)) != hipSuccess) return rc;
+        const Cut cut = choose_cut(c.M, c.N, c.K, compute_units(), 16);
+        Args g = args(x, w, c.M, c.N, c.K, cut, ar);
+        if (ar.dry()) return hipSuccess;
+        const LinearEpi<E> epi = {rows(c.y, c.ldy),
+                                  rows(c.residual, c.ldr),
+                                  rows(c.preact, c.ldp),
+                                  static_cast<const uint16_t*>(c.bias),
+                                  aligned16(c.bias),
+                                  c.act};
+        return lp::launch_product<E, true, false>(g, cut, epi, stream);
+    }
+
+    static hipError_t backward(const LinearGradCall& c, Arena& ar, hipStream_t stream) {
+        hipError_t rc;
+        const bool act = c.act != PGEMM_ACT_NONE;
+        // dz: dy itself where there is no activation and it can be copied
+        // from where it lies, else a padded copy in the workspace.
+        View dz = {static_cast<const uint16_t*>(c.dy), (int)c.lddy};
+        const bool need_dz = (c.dx || c.dw) && (act || !direct(c.dy, c.lddy, c.N));
+        const int64_t n8 = round_up(c.N, 8);
+        uint16_t* dzw = nullptr;
+        if (need_dz) {
+            dzw = static_cast<uint16_t*>(ar.take(c.M * n8 * 2));
+            dz = {dzw, (int)n8};
+        }
+        const int64_t per = kDzRows * std::max<int64_t>(1, (c.M + kDzRows * kDzBlocks - 1) /
+                                                              (kDzRows * kDzBlocks));
+        const int64_t blocks = (c.M + per - 1) / per;
+        float* part = nullptr;
+        if (c.dbias) part = static_cast<float*>(ar.take(std::max<int64_t>(blocks, 1) * c.N * 4));
+        if (!ar.dry() && c.M > 0 && c.N > 0 && (need_dz || c.dbias)) {
+            const dim3 grid((unsigned)((n8 + 511) / 512), (unsigned)blocks);
+            hipLaunchKernelGGL(dz_kernel<E>, grid, dim3(256), 0, stream, rows(c.dy, c.lddy),
+                               act ? rows(c.preact, c.ldp) : Rows{nullptr, 0, 0},
+                               need_dz ? Rows{dzw, n8, 1} : Rows{nullptr, 0, 0}, part, c.M,
+                               (int)c.N, need_dz ? (int)n8 : (int)c.N, per, c.act);
+            if ((rc = hipGetLastError()) != hipSuccess) return rc;
+        }
+        if (!ar.dry() && c.dbias && c.N > 0) {
+            rc = launch_column_sum(dtype(), part, c.M > 0 ? blocks : 0, c.N, c.dbias, stream);
+            if (rc != hipSuccess) return rc;
+        }
+        if (c.dx && c.M > 0 && c.K > 0) {
+            View w;
+            if ((rc = operand(c.w, c.ldw, c.K, c.N, ar, stream, w)) != hipSuccess) return rc;
+            const Cut cut = choose_cut(c.M, c.K, c.N, compute_units(), 16);
+            Args g = args(dz, w, c.M, c.K, c.N, cut, ar);
+            if (!ar.dry()) {
+                const LinearEpi<E> epi = {rows(c.dx, c.lddx), rows(c.add, c.ldadd),
+                                          Rows{nullptr, 0, 0}, nullptr, 0, PGEMM_ACT_NONE};
+                rc = lp::launch_product<E, true, true>(g, cut, epi, stream);
+                if (rc != hipSuccess) return rc;
+            }
+        }
+        if (c.dw && c.K > 0 && c.N > 0) {
+            View x;
+            if ((rc = operand(c.x, c.ldx, c.M, c.K, ar, stream, x)) != hipSuccess) return rc;
+            const Cut cut = choose_cut(c.K, c.N, c.M, compute_units(), 16);
+            Args g = args(x, dz, c.K, c.N, c.M, cut, ar);
+            if (!ar.dry()) {
+                const LinearEpi<E> epi = {rows(c.dw, c.lddw), Rows{nullptr, 0, 0},
+                                          Rows{nullptr, 0, 0}, nullptr, 0, PGEMM_ACT_NONE};
+                rc = lp::launch_product<E, false, false>(g, cut, epi, stream);
+                if (rc != hipSuccess) return rc;
+            }
+        }
+        return hipSuccess;
+    }
+
+    static constexpr int dtype() { return std::is_same<E, BF16>::value ? kBF16 : kF16; }
+};
+
+}  // namespace
+
+hipError_t linear_forward(const LinearCall& c, Arena& ar, hipStream_t stream) {
+    return c.dtype == kBF16 ? Linear<BF16>::forward(c, ar, stream)
+                            : Linear<F16>::forward(c, ar, stream);
+}
+
+hipError_t linear_backward(const LinearGradCall& c, Arena& ar, hipStream_t stream) {
+    return c.dtype == kBF16 ? Linear<BF16>::backward(c, ar, stream)
+                            : Linear<F16>::backward(c, ar, stream);
+}
+
+}  // namespace layer
+}  // namespace pgemm

@@ -12,11 +12,7 @@ namespace {
 
 thread_local int g_last_hip_error = 0;
 
-int hip_status(hipError_t e) {
-    if (e == hipSuccess) return PGEMM_OK;
-    g_last_hip_error = (int)e;
-    return PGEMM_EHIP;
-}
+int hip_status(hipError_t e) { return pgemm::record_hip_status(e); }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -69,6 +65,12 @@ int64_t splitk_parts(int64_t K, int splits) {
 }
 
 }  // namespace
+
+int pgemm::record_hip_status(hipError_t e) {
+    if (e == hipSuccess) return PGEMM_OK;
+    g_last_hip_error = (int)e;
+    return PGEMM_EHIP;
+}
 
 extern "C" {
 

@@ -1,0 +1,187 @@
+"""The layer operators of libpgemm (include/pgemm.h, second part) on torch
+tensors: the linear layer, the gated feed-forward block, the softmax cross
+entropy over a vocabulary and gradient clipping, each with its backward pass.
+
+As in the rest of the package the functions check arguments, allocate the
+outputs and workspaces that were not given (from the pool of the stream the
+call runs on) and pass pointers.  Matrices are 2-D tensors whose last
+dimension is contiguous; their rows may be strided.
+"""
+from __future__ import annotations
+
+from . import _lib
+from ._lib import PgemmError, lib
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+def _base():
+    from . import _torch
+    return _torch()
+
+
+def _new(shape, dtype, device, stream):
+    from . import _new as new
+    return new(shape, dtype, device, stream)
+
+
+def _invoke(t, stream, fn):
+    from . import _invoke as invoke
+    return invoke(t, stream, fn)
+
+
+def _act(act):
+    try:
+        return ACTIVATIONS[act]
+    except (KeyError, TypeError):
+        raise ValueError("act must be one of %s, got %r" % (", ".join(ACTIVATIONS), act)) from None
+
+
+def _dtype(t, name):
+    torch = _base()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype is torch.float16:
+        return 0
+    if t.dtype is torch.bfloat16:
+        return 1
+    raise TypeError("%s must be float16 or bfloat16, got %s" % (name, t.dtype))
+
+
+def _mat(t, name, like, rows=None, cols=None):
+    """Checks a matrix against the call's first tensor `like` (type, device)
+    and a shape; returns its row pitch in elements."""
+    torch = _base()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a device (HIP) tensor, got %s" % (name, t.device))
+    if t.dtype is not like.dtype:
+        raise TypeError("%s must be %s, got %s" % (name, like.dtype, t.dtype))
+    if t.get_device() != like.get_device():
+        raise ValueError("%s is on another device than the other tensors" % name)
+    if t.dim() != 2:
+        raise ValueError("%s must have 2 dimensions" % name)
+    r, c = t.shape
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError("%s must have shape (%s, %s), got %s"
+                         % (name, "any" if rows is None else rows, "any" if cols is None else cols,
+                            tuple(t.shape)))
+    if r == 0 or c == 0:  # no element: torch's strides mean nothing
+        return max(c, 1)
+    s0, s1 = t.stride()
+    if c > 1 and s1 != 1:
+        raise ValueError("%s must be contiguous along its rows" % name)
+    if r > 1 and s0 < c:
+        raise ValueError("%s must not have overlapping rows" % name)
+    return s0 if r > 1 else max(c, 1)
+
+
+def _vec(t, name, like, n):
+    torch = _base()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda or t.get_device() != like.get_device():
+        raise ValueError("%s must be on the other tensors' device" % name)
+    if t.dtype is not like.dtype:
+        raise TypeError("%s must be %s, got %s" % (name, like.dtype, t.dtype))
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous vector of %d elements" % (name, n))
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _out(t, name, like, shape, stream):
+    if t is None:
+        t = _new(shape, like.dtype, like.device, stream)
+    return t, _mat(t, name, like, *shape)
+
+
+def _workspace(need, given, like, stream, what):
+    """(pointer, bytes, tensor to keep alive) of a call's workspace."""
+    if need < 0:
+        raise PgemmError(int(need), what)
+    if given is not None:
+        if given.device != like.device or not given.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on %s" % like.device)
+        return given.data_ptr(), given.numel() * given.element_size(), given
+    if need == 0:
+        return None, 0, None
+    w = _new(int(need), _base().uint8, like.device, stream)
+    return w.data_ptr(), int(need), w
+
+
+def _call(rc, what):
+    if rc != _lib.PGEMM_OK:
+        raise PgemmError(rc, what)
+
+
+def plinear(x, w, bias=None, residual=None, act="none", preact=None, out=None, workspace=None,
+            stream=None):
+    """act(x @ w + bias) + residual for x [M,K], w [K,N] (float16 or bfloat16).
+
+    act: "none", "relu", "gelu", "gelu_tanh" or "silu".  preact: an [M,N] tensor
+    that receives x @ w + bias, which plinear_bwd needs unless act is "none".
+    out may be residual."""
+    dt = _dtype(x, "x")
+    a = _act(act)
+    ldx = _mat(x, "x", x)
+    M, K = x.shape
+    ldw = _mat(w, "w", x, rows=K)
+    N = w.shape[1]
+    if bias is not None:
+        _vec(bias, "bias", x, N)
+    ldr = _mat(residual, "residual", x, M, N) if residual is not None else 0
+    ldp = _mat(preact, "preact", x, M, N) if preact is not None else 0
+    out, ldy = _out(out, "out", x, (M, N), stream)
+    L = lib()
+
+    def run(h):
+        need = L.plinear_workspace_bytes(dt, x.data_ptr(), ldx, w.data_ptr(), ldw, M, N, K)
+        ws, nws, keep = _workspace(need, workspace, x, stream, "plinear")
+        return L.plinear(dt, x.data_ptr(), ldx, w.data_ptr(), ldw, _ptr(bias), _ptr(residual), ldr,
+                         out.data_ptr(), ldy, _ptr(preact), ldp, M, N, K, a, ws, nws, h)
+    _call(_invoke(x, stream, run), "plinear")
+    return out
+
+
+def plinear_bwd(dy, x, w, preact=None, act="none", dx_residual=None, needs=(True, True, True),
+                dx=None, dw=None, dbias=None, workspace=None, stream=None):
+    """(dx, dw, dbias) of plinear for the gradient dy [M,N] of its output
+    (which is also the gradient of its residual).  `needs` says which are
+    computed; the others are None.  dx_residual [M,K] is added to dx (dy, where
+    x was also the residual)."""
+    dt = _dtype(dy, "dy")
+    a = _act(act)
+    lddy = _mat(dy, "dy", dy)
+    M, N = dy.shape
+    ldx = _mat(x, "x", dy, rows=M)
+    K = x.shape[1]
+    ldw = _mat(w, "w", dy, K, N)
+    if a and preact is None and any(needs):
+        raise ValueError("preact is needed for act=%r" % act)
+    ldp = _mat(preact, "preact", dy, M, N) if preact is not None else 0
+    lda = _mat(dx_residual, "dx_residual", dy, M, K) if dx_residual is not None else 0
+    lddx = lddw = 0
+    if needs[0]:
+        dx, lddx = _out(dx, "dx", dy, (M, K), stream)
+    if needs[1]:
+        dw, lddw = _out(dw, "dw", dy, (K, N), stream)
+    if needs[2]:
+        if dbias is None:
+            dbias = _new((N,), dy.dtype, dy.device, stream)
+        _vec(dbias, "dbias", dy, N)
+    dx, dw, dbias = (t if n else None for t, n in zip((dx, dw, dbias), needs))
+    L = lib()
+
+    def run(h):
+        need = L.plinear_bwd_workspace_bytes(dt, dy.data_ptr(), lddy, x.data_ptr(), ldx,
+                                             w.data_ptr(), ldw, M, N, K, a, *map(int, map(bool, needs)))
+        ws, nws, keep = _workspace(need, workspace, dy, stream, "plinear_bwd")
+        return L.plinear_bwd(dt, dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(), ldw,
+                             _ptr(preact), ldp, _ptr(dx_residual), lda, _ptr(dx), lddx, _ptr(dw),
+                             lddw, _ptr(dbias), M, N, K, a, ws, nws, h)
+    _call(_invoke(dy, stream, run), "plinear_bwd")
+    return dx, dw, dbias

@@ -1,0 +1,175 @@
+"""The layer operators on the GPU against plain formulas in binary64 on the
+CPU (numpy), written apart from the kernels.
+
+Tolerances, derived before the first run.  u is the output type's rounding
+(2^-11 for float16, 2^-8 for bfloat16: half an ulp relative to the value), and
+a stored intermediate adds another rounding of the same relative size to each
+term that it enters.  For an output that is a sum of terms t_i, each carrying
+relative errors of at most c roundings, |got - exact| <= u |exact| + c u sum|t_i|
++ (n + 16) 2^-23 sum|t_i| + tiny, where the third part is fp32 accumulation
+over n terms in any order with the activations' few fp32 roundings, and tiny
+covers the type's subnormals.  Each test states its c (0 where no intermediate
+is rounded)."""
+import sys
+
+import numpy as np
+import pytest
+
+import software_pipelined_tiled_pgemm_amd as pg
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+UNIT = {torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+TINY = {torch.float16: 2.0 ** -24, torch.bfloat16: 2.0 ** -126}
+DTYPES = [torch.float16, torch.bfloat16]
+ACTS = ["none", "relu", "gelu", "gelu_tanh", "silu"]
+
+
+def say(*a):
+    print(*a, flush=True)
+    sys.stdout.flush()
+
+
+def rand(shape, dtype, seed, std=1.0, pitch=None, offset=0):
+    """Normal values of the type on the device, rows `pitch` apart (default:
+    dense), the first one `offset` elements into its buffer; the gaps hold
+    NaN."""
+    rng = np.random.default_rng(seed)
+    v = torch.from_numpy(rng.normal(0.0, std, size=shape)).to(dtype)
+    if pitch is None and offset == 0:
+        return v.cuda()
+    r, c = shape
+    pitch = pitch or c
+    buf = torch.full((offset + r * pitch + 16,), float("nan"), dtype=dtype)
+    view = buf.cuda()[offset:offset + r * pitch].view(r, pitch)[:, :c]
+    view.copy_(v)
+    return view
+
+
+def f64(t):
+    torch.cuda.synchronize()
+    return t.detach().cpu().double().numpy()
+
+
+def erf(x):
+    return torch.special.erf(torch.from_numpy(np.ascontiguousarray(x))).numpy()
+
+
+def act_exact(z, act):
+    if act == "relu":
+        return np.maximum(z, 0.0)
+    if act == "gelu":
+        return z * 0.5 * (1 + erf(z / np.sqrt(2)))
+    if act == "gelu_tanh":
+        return 0.5 * z * (1 + np.tanh(np.sqrt(2 / np.pi) * (z + 0.044715 * z ** 3)))
+    if act == "silu":
+        return z / (1 + np.exp(-z))
+    return z
+
+
+def grad_exact(z, act):
+    if act == "relu":
+        return (z > 0).astype(np.float64)
+    if act == "gelu":
+        return 0.5 * (1 + erf(z / np.sqrt(2))) + z * np.exp(-z * z / 2) / np.sqrt(2 * np.pi)
+    if act == "gelu_tanh":
+        t = np.tanh(np.sqrt(2 / np.pi) * (z + 0.044715 * z ** 3))
+        return 0.5 * (1 + t) + 0.5 * z * (1 - t * t) * np.sqrt(2 / np.pi) * (1 + 3 * 0.044715 * z * z)
+    if act == "silu":
+        p = 1 / (1 + np.exp(-z))
+        return p * (1 + z * (1 - p))
+    return np.ones_like(z)
+
+
+def assert_near(got, exact, scale, dtype, n, c, what):
+    """scale: sum of the terms' magnitudes."""
+    g = f64(got)
+    u = UNIT[dtype]
+    bound = u * np.abs(exact) + (c * u + (n + 16) * 2.0 ** -23) * scale + TINY[dtype]
+    err = np.abs(g - exact)
+    bad = ~(err <= bound)
+    if bad.any():
+        i = tuple(np.argwhere(bad)[0])
+        pytest.fail("%s: %d of %d outside; first %s: got %r, exact %r, bound %r"
+                    % (what, bad.sum(), bad.size, i, g[i], exact[i], bound[i]))
+
+
+# M, N, K: one row and column, tile corners, whole 16-byte rows and not, an
+# empty sum, K around the ring's 5 steps of 32, a split K, large
+SHAPES = [(1, 1, 1), (1, 8, 8), (3, 5, 7), (17, 24, 40), (64, 256, 512), (127, 129, 131),
+          (128, 128, 160), (256, 256, 288), (257, 264, 320), (130, 72, 0), (300, 520, 999),
+          (16, 4096, 1024), (5, 1000, 2056), (511, 768, 1024), (33, 40, 8192), (1100, 1032, 96)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", SHAPES)
+def test_linear_forward(shape, dtype):
+    M, N, K = shape
+    act = ACTS[(M + N + K) % len(ACTS)]
+    say("linear", shape, dtype, act)
+    x = rand((M, K), dtype, 1)
+    w = rand((K, N), dtype, 2, std=max(K, 1) ** -0.5)
+    b = rand((N,), dtype, 3, std=0.3)
+    r = rand((M, N), dtype, 4)
+    z = torch.full((M, N), float("nan"), dtype=dtype, device="cuda")
+    y = pg.plinear(x, w, bias=b, residual=r, act=act, preact=z)
+    X, W, B, R = f64(x), f64(w), f64(b), f64(r)
+    Z = X @ W + B
+    S = np.abs(X) @ np.abs(W) + np.abs(B)
+    assert_near(z, Z, S, dtype, K, 0, "preact")
+    # an activation moves by at most 1.2 of its argument's error
+    assert_near(y, act_exact(Z, act) + R, 1.2 * S + np.abs(R), dtype, K, 0, "y")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", SHAPES)
+def test_linear_backward(shape, dtype):
+    M, N, K = shape
+    act = ACTS[(M + N + K + 1) % len(ACTS)]
+    say("linear backward", shape, dtype, act)
+    x = rand((M, K), dtype, 11)
+    w = rand((K, N), dtype, 12, std=max(K, 1) ** -0.5)
+    z = rand((M, N), dtype, 13)
+    dy = rand((M, N), dtype, 14)
+    a = rand((M, K), dtype, 15)
+    dx, dw, db = pg.plinear_bwd(dy, x, w, preact=z, act=act, dx_residual=a)
+    X, W, Z, DY, A = f64(x), f64(w), f64(z), f64(dy), f64(a)
+    DZ = DY * grad_exact(Z, act)
+    mag = np.abs(DY) * 1.2  # |act'| is below 1.13 everywhere
+    c = 1 if act != "none" else 0  # dz is rounded once
+    assert_near(dx, DZ @ W.T + A, mag @ np.abs(W).T + np.abs(A), dtype, N, c, "dx")
+    assert_near(dw, X.T @ DZ, np.abs(X).T @ mag, dtype, M, c, "dw")
+    assert_near(db, DZ.sum(0), mag.sum(0), dtype, M, 0, "dbias")
+
+
+# (pitch beyond the row, offset of the first element): whole 16-byte rows,
+# rows off by some elements, an address off by one element
+STRIDES = [(8, 0), (64, 8), (3, 0), (0, 1), (5, 3), (16, 4)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("pad,offset", STRIDES)
+@pytest.mark.parametrize("shape", [(130, 136, 72), (4, 264, 520), (37, 51, 43)])
+def test_linear_strides(shape, pad, offset, dtype):
+    M, N, K = shape
+    say("linear strides", shape, pad, offset, dtype)
+    x = rand((M, K), dtype, 21, pitch=K + pad, offset=offset)
+    w = rand((K, N), dtype, 22, std=K ** -0.5, pitch=N + pad, offset=offset)
+    r = rand((M, N), dtype, 23, pitch=N + pad, offset=offset)
+    out = rand((M, N), dtype, 24, pitch=N + pad, offset=offset)
+    z = rand((M, N), dtype, 25, pitch=N + pad, offset=offset)
+    got = pg.plinear(x, w, residual=r, act="silu", preact=z, out=out)
+    assert got is out
+    dense = pg.plinear(x.contiguous(), w.contiguous(), residual=r.contiguous(), act="silu")
+    assert torch.equal(out, dense)
+    # the gaps between rows keep their NaN
+    if pad:
+        whole = torch.as_strided(out, (M, N + pad), (N + pad, 1), out.storage_offset())
+        assert bool(torch.isnan(whole[:, N:]).all())
+    dy = rand((M, N), dtype, 26, pitch=N + pad, offset=offset)
+    g = pg.plinear_bwd(dy, x, w, preact=z, act="silu")
+    h = pg.plinear_bwd(dy.contiguous(), x.contiguous(), w.contiguous(), preact=z.contiguous(),
+                       act="silu")
+    for u, v in zip(g, h):
+        assert torch.equal(u, v)
