@@ -352,6 +352,46 @@ int64_t plinear_bwd_workspace_bytes(int dtype, const void* dy, int64_t lddy, con
                                     int64_t ldx, const void* w, int64_t ldw, int64_t M, int64_t N,
                                     int64_t K, int act, int need_dx, int need_dw, int need_dbias);
 
+/*
+ * Gated feed-forward block: [g | u] = x W_in, h = act(g) * u,
+ * y = h W_out + residual.
+ *   x [M,D], W_in [D,2F] (the F gate columns, then the F up columns),
+ *   W_out [F,N], residual [M,N] (may be NULL), y [M,N].
+ *   gate_up [M,2F] (may be NULL) receives [g | u] rounded to dtype, which the
+ *   backward pass needs.  h is rounded once, as the operand of W_out.
+ *   y may be exactly residual or x.
+ * Both projections, the activation and the product are one kernel.  The
+ * workspace holds h (and what operands that need padding, and products cut
+ * along their contraction, take).
+ */
+int pffn(int dtype, const void* x, int64_t ldx, const void* w_in, int64_t ldwi, const void* w_out,
+         int64_t ldwo, const void* residual, int64_t ldr, void* y, int64_t ldy, void* gate_up,
+         int64_t ldgu, int64_t M, int64_t D, int64_t F, int64_t N, int act, void* workspace,
+         int64_t workspace_bytes, pgemm_stream_t stream);
+int64_t pffn_workspace_bytes(int dtype, const void* x, int64_t ldx, const void* w_in, int64_t ldwi,
+                             const void* w_out, int64_t ldwo, int64_t M, int64_t D, int64_t F,
+                             int64_t N);
+
+/*
+ * Backward pass of the block: with dh = dy W_out^T,
+ *   [dg | du] = [dh * u * act'(g) | dh * act(g)],
+ *   dx = [dg | du] W_in^T + add,  dW_in = x^T [dg | du],  dW_out = h^T dy.
+ * (The gradient of residual is dy itself.)  dy [M,N]; gate_up as the forward
+ * pass wrote it; add [M,D] (may be NULL) is added to dx before rounding, for
+ * instance dy where x was also the residual; dx may be exactly add.  dx,
+ * dW_in and dW_out may each be NULL: that gradient is not computed, and x
+ * (without dW_in) and W_in (without dx) may be NULL too.
+ */
+int pffn_bwd(int dtype, const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w_in,
+             int64_t ldwi, const void* w_out, int64_t ldwo, const void* gate_up, int64_t ldgu,
+             const void* add, int64_t ldadd, void* dx, int64_t lddx, void* dw_in, int64_t lddwi,
+             void* dw_out, int64_t lddwo, int64_t M, int64_t D, int64_t F, int64_t N, int act,
+             void* workspace, int64_t workspace_bytes, pgemm_stream_t stream);
+int64_t pffn_bwd_workspace_bytes(int dtype, const void* dy, int64_t lddy, const void* x,
+                                 int64_t ldx, const void* w_in, int64_t ldwi, const void* w_out,
+                                 int64_t ldwo, int64_t M, int64_t D, int64_t F, int64_t N,
+                                 int need_dx, int need_dw_in, int need_dw_out);
+
 /* Static English text for a status code (never NULL). */
 const char* pgemm_status_string(int status);
 

@@ -19,7 +19,7 @@ __all__ = [
     "pgemm_f16_splitk_default_splits",
     "pstream_add", "pstream_add_blocked", "pstream_add_scalar", "preduce_sum_f32",
     "pgemm_test_fill_f32", "pgemm_test_iota_f32",
-    "plinear", "plinear_bwd",
+    "plinear", "plinear_bwd", "pffn", "pffn_bwd",
     "lib", "status_string", "PgemmError",
     "PGEMM_OK", "PGEMM_EINVAL", "PGEMM_EUNSUPPORTED", "PGEMM_EHIP", "PGEMM_ESCRATCH",
     "STATIC_SCRATCH_BYTES",
@@ -320,4 +320,4 @@ def pgemm_test_iota_f32(n, device="cuda", out=None, stream=None):
     return o
 
 
-from .layers import plinear, plinear_bwd  # noqa: E402  (uses the helpers above)
+from .layers import pffn, pffn_bwd, plinear, plinear_bwd  # noqa: E402  (uses the helpers above)

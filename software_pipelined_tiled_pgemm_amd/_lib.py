@@ -55,6 +55,12 @@ def _declare(lib):
                               i64, i64, i32, p, i64, p]),
         "plinear_bwd_workspace_bytes": (i64, [i32, p, i64, p, i64, p, i64, i64, i64, i64, i32, i32,
                                               i32, i32]),
+        "pffn": (i32, [i32, p, i64, p, i64, p, i64, p, i64, p, i64, p, i64, i64, i64, i64, i64, i32,
+                       p, i64, p]),
+        "pffn_workspace_bytes": (i64, [i32, p, i64, p, i64, p, i64, i64, i64, i64, i64]),
+        "pffn_bwd": (i32, [i32] + [p, i64] * 9 + [i64, i64, i64, i64, i32, p, i64, p]),
+        "pffn_bwd_workspace_bytes": (i64, [i32] + [p, i64] * 4 + [i64, i64, i64, i64, i32, i32,
+                                                                 i32]),
         "pgemm_status_string": (ctypes.c_char_p, [i32]),
         "pgemm_last_hip_error": (i32, []),
         "pgemm_version": (i32, []),

@@ -1,0 +1,195 @@
+// The gated feed-forward block and its backward pass.
+//
+//   forward    [g | u] = x W_in,  h = act(g) * u,  y = h W_out + r
+//              x [M,D], W_in [D,2F] (gate columns, then up columns), W_out [F,N]
+//   backward   dh = dy W_out^T
+//              dg = dh * u * act'(g),  du = dh * act(g)
+//              dx = [dg | du] W_in^T (+ a),  dW_in = x^T [dg | du],  dW_out = h^T dy
+//
+// Both projections, the activation and the product are one kernel: a tile's
+// columns are 32 gate columns and the same 32 up columns per wave, so g and u
+// of a value meet in the epilogue, and only h is written (and g, u for a
+// backward pass).  The backward pass computes dg, du and h (again, from g
+// and u) in the epilogue of dh, which is never written.  Since [dg | du] and
+// W_in lie side by side, dx and dW_in are one product each.
+//
+// Roundings beyond one per output: h and [dg | du], once each, as operands of
+// the next product; g and u as kept for the backward pass.
+#include "ffn.h"
+
+#include "layer_pipe.h"
+#include "linear.h"
+
+namespace pgemm {
+namespace layer {
+namespace {
+
+template <class E>
+struct GluEpi {
+    static constexpr lp::EpiKind kind = lp::kPaired;
+    Rows h;  // padded rows: whole chunks
+    Rows gate, up;
+    int act;
+    __device__ __forceinline__ void operator()(int row, int col, int nv, float (&g)[8],
+                                               float (&u)[8]) const {
+        if (gate) {
+            store8<E>(gate, row, col, nv, g);
+            store8<E>(up, row, col, nv, u);
+        }
+        // past F both are 0, and so is h
+#pragma unroll
+        for (int q = 0; q < 8; ++q) u[q] *= act_value(act, g[q]);
+        store8<E>(h, row, col, 8, u);
+    }
+};
+
+template <class E>
+struct GluGradEpi {
+    static constexpr lp::EpiKind kind = lp::kPlain;
+    Rows gate, up;       // as the forward pass kept them
+    Rows h, dgate, dup;  // padded rows: whole chunks, zeros past F
+    int act;
+    __device__ __forceinline__ void operator()(int row, int col, int nv, float (&d)[8]) const {
+        float g[8], u[8];
+        load8<E>(gate, row, col, nv, g);
+        load8<E>(up, row, col, nv, u);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            float a;
+            const float s = act_grad(act, g[q], a);
+            g[q] = d[q] * u[q] * s;
+            u[q] *= a;   // h
+            d[q] *= a;   // du
+        }
+        if (h) store8<E>(h, row, col, 8, u);
+        if (dgate) {
+            store8<E>(dgate, row, col, 8, g);
+            store8<E>(dup, row, col, 8, d);
+        }
+    }
+};
+
+// W_in as a product's operand: both halves in rows of whole chunks, the up
+// half `shift` columns after the gate half.
+hipError_t halves(const void* w, int64_t ld, int64_t rows, int64_t F, Arena& ar, hipStream_t stream,
+                  View& out) {
+    const uint16_t* p = static_cast<const uint16_t*>(w);
+    if (direct(w, ld, F)) {
+        out = {p, (int)ld};
+        return hipSuccess;
+    }
+    const int64_t f8 = round_up(F, 8);
+    uint16_t* dst = static_cast<uint16_t*>(ar.take(rows * 2 * f8 * 2));
+    out = {dst, (int)(2 * f8)};
+    if (ar.dry()) return hipSuccess;
+    const hipError_t rc = launch_pack(p, ld, dst, 2 * f8, rows, F, stream);
+    if (rc != hipSuccess) return rc;
+    return launch_pack(p + F, ld, dst + f8, 2 * f8, rows, F, stream);
+}
+
+template <class E>
+struct Ffn {
+    static constexpr int dtype = std::is_same<E, BF16>::value ? kBF16 : kF16;
+
+    static hipError_t forward(const FfnCall& c, Arena& ar, hipStream_t stream) {
+        const int cus = compute_units();
+        const int64_t f8 = round_up(c.F, 8);
+        hipError_t rc;
+        uint16_t* h = static_cast<uint16_t*>(ar.take(c.M * f8 * 2));
+        if (c.F > 0) {
+            View x, w;
+            if ((rc = operand(c.x, c.ldx, c.M, c.D, ar, stream, x)) != hipSuccess) return rc;
+            if ((rc = halves(c.w_in, c.ldwi, c.D, c.F, ar, stream, w)) != hipSuccess) return rc;
+            const Cut cut = choose_cut(c.M, 2 * f8, c.D, cus, 16);
+            Args g = args(x, w, c.M, 2 * f8, c.D, cut, ar);
+            g.N = (int)c.F;
+            g.pair_shift = (int)f8;
+            if (!ar.dry()) {
+                uint16_t* gu = static_cast<uint16_t*>(c.gate_up);
+                const GluEpi<E> epi = {{h, f8, 1},
+                                       make_rows(gu, c.ldgu),
+                                       make_rows(gu ? gu + c.F : nullptr, c.ldgu),
+                                       c.act};
+                rc = lp::launch_product<E, true, false>(g, cut, epi, stream);
+                if (rc != hipSuccess) return rc;
+            }
+        }
+        View wo;
+        if ((rc = operand(c.w_out, c.ldwo, c.F, c.N, ar, stream, wo)) != hipSuccess) return rc;
+        const Cut cut = choose_cut(c.M, c.N, c.F, cus, 16);
+        const Args g = args({h, (int)f8}, wo, c.M, c.N, c.F, cut, ar);
+        if (ar.dry()) return hipSuccess;
+        const Sink s = {c.y, c.ldy, c.residual, c.ldr, nullptr, 0, nullptr, 0, 0};
+        return launch_linear(dtype, kNN, g, cut, s, stream);
+    }
+
+    static hipError_t backward(const FfnGradCall& c, Arena& ar, hipStream_t stream) {
+        const int cus = compute_units();
+        const int64_t f8 = round_up(c.F, 8);
+        const bool need_d = c.dx || c.dw_in;
+        hipError_t rc;
+        View dy = {}, wo = {};
+        if ((rc = operand(c.dy, c.lddy, c.M, c.N, ar, stream, dy)) != hipSuccess) return rc;
+        uint16_t* h = nullptr;
+        if (c.dw_out) h = static_cast<uint16_t*>(ar.take(c.M * f8 * 2));
+        uint16_t* d = nullptr;
+        if (need_d) d = static_cast<uint16_t*>(ar.take(c.M * 2 * f8 * 2));
+        if (c.M > 0 && c.F > 0) {
+            if ((rc = operand(c.w_out, c.ldwo, c.F, c.N, ar, stream, wo)) != hipSuccess) return rc;
+            const Cut cut = choose_cut(c.M, c.F, c.N, cus, 16);
+            const Args g = args(dy, wo, c.M, c.F, c.N, cut, ar);
+            if (!ar.dry()) {
+                const uint16_t* gu = static_cast<const uint16_t*>(c.gate_up);
+                const GluGradEpi<E> epi = {make_rows(gu, c.ldgu), make_rows(gu + c.F, c.ldgu),
+                                           {h, f8, 1},            {d, 2 * f8, 1},
+                                           {d ? d + f8 : d, 2 * f8, 1}, c.act};
+                rc = lp::launch_product<E, true, true>(g, cut, epi, stream);
+                if (rc != hipSuccess) return rc;
+            }
+        }
+        const View dv = {d, (int)(2 * f8)};
+        if (c.dw_out && c.F > 0 && c.N > 0) {
+            const Cut cut = choose_cut(c.F, c.N, c.M, cus, 16);
+            const Args g = args({h, (int)f8}, dy, c.F, c.N, c.M, cut, ar);
+            if (!ar.dry()) {
+                const Sink s = {c.dw_out, c.lddwo, nullptr, 0, nullptr, 0, nullptr, 0, 0};
+                if ((rc = launch_linear(dtype, kTN, g, cut, s, stream)) != hipSuccess) return rc;
+            }
+        }
+        if (c.dx && c.M > 0 && c.D > 0) {
+            View wi;
+            if ((rc = halves(c.w_in, c.ldwi, c.D, c.F, ar, stream, wi)) != hipSuccess) return rc;
+            const Cut cut = choose_cut(c.M, c.D, 2 * f8, cus, 16);
+            const Args g = args(dv, wi, c.M, c.D, 2 * f8, cut, ar);
+            if (!ar.dry()) {
+                const Sink s = {c.dx, c.lddx, c.add, c.ldadd, nullptr, 0, nullptr, 0, 0};
+                if ((rc = launch_linear(dtype, kNT, g, cut, s, stream)) != hipSuccess) return rc;
+            }
+        }
+        if (c.dw_in && c.D > 0 && c.F > 0) {
+            View x;
+            if ((rc = operand(c.x, c.ldx, c.M, c.D, ar, stream, x)) != hipSuccess) return rc;
+            const Cut cut = choose_cut(c.D, 2 * f8, c.M, cus, 16);
+            const Args g = args(x, dv, c.D, 2 * f8, c.M, cut, ar);
+            if (!ar.dry()) {
+                const Sink s = {c.dw_in, c.lddwi, nullptr, 0, nullptr, 0, nullptr, 0, (int)c.F};
+                if ((rc = launch_linear(dtype, kTN, g, cut, s, stream)) != hipSuccess) return rc;
+            }
+        }
+        return hipSuccess;
+    }
+};
+
+}  // namespace
+
+hipError_t ffn_forward(const FfnCall& c, Arena& ar, hipStream_t stream) {
+    return c.dtype == kBF16 ? Ffn<BF16>::forward(c, ar, stream) : Ffn<F16>::forward(c, ar, stream);
+}
+
+hipError_t ffn_backward(const FfnGradCall& c, Arena& ar, hipStream_t stream) {
+    return c.dtype == kBF16 ? Ffn<BF16>::backward(c, ar, stream)
+                            : Ffn<F16>::backward(c, ar, stream);
+}
+
+}  // namespace layer
+}  // namespace pgemm

@@ -54,13 +54,11 @@ struct Arena {
 inline bool direct(const void* p, int64_t ld, int64_t cols) {
     return aligned16(p) && ld % 8 == 0 && cols % 8 == 0;
 }
-// Whole chunks of 8 values of every row can be accessed as 16 bytes.
-inline int vector_rows(const void* p, int64_t ld) { return aligned16(p) && ld % 8 == 0; }
 
-// dst[r][c] = src[r][c], c < cols, zeros up to round_up(cols, 8), the pitch
-// of dst (layer_common.hip).
-hipError_t launch_pack(const uint16_t* src, int64_t ld, uint16_t* dst, int64_t rows, int64_t cols,
-                       hipStream_t stream);
+// dst[r][c] = src[r][c], c < cols, zeros up to round_up(cols, 8); dst is
+// 16-byte aligned, its pitch a multiple of 8 (layer_common.hip).
+hipError_t launch_pack(const uint16_t* src, int64_t ld, uint16_t* dst, int64_t dst_ld, int64_t rows,
+                       int64_t cols, hipStream_t stream);
 
 // How a product is cut: 256x256 tiles (8 waves, one workgroup per CU) or
 // 128x128 ones (4 waves, two per CU), and the number of K splits.

@@ -3,6 +3,7 @@
 #include <stdint.h>
 
 #include "../../include/pgemm.h"
+#include "ffn.h"
 #include "linear.h"
 
 namespace {
@@ -103,6 +104,13 @@ int check_linear(int dtype, int act, int64_t M, int64_t N, int64_t K) {
     if (!known(dtype, act)) return PGEMM_EUNSUPPORTED;
     if (M >= kMaxRows || N >= kMaxCols || K >= kMaxCols) return PGEMM_EUNSUPPORTED;
     return PGEMM_OK;
+}
+
+int check_ffn(int dtype, int act, int64_t M, int64_t D, int64_t F, int64_t N) {
+    if (F < 0 || N < 0) return PGEMM_EINVAL;
+    const int rc = check_linear(dtype, act, M, D, N);
+    if (rc != PGEMM_OK) return rc;
+    return F >= kMaxCols / 2 ? PGEMM_EUNSUPPORTED : PGEMM_OK;
 }
 
 }  // namespace
@@ -213,6 +221,129 @@ int64_t plinear_bwd_workspace_bytes(int dtype, const void* dy, int64_t lddy, con
     c.M = M, c.N = N, c.K = K, c.act = act;
     Arena dry = {nullptr, 0};
     const hipError_t e = linear_backward(c, dry, nullptr);
+    return e == hipSuccess ? dry.used : hip_status(e);
+}
+
+int pffn(int dtype, const void* x, int64_t ldx, const void* w_in, int64_t ldwi, const void* w_out,
+         int64_t ldwo, const void* residual, int64_t ldr, void* y, int64_t ldy, void* gate_up,
+         int64_t ldgu, int64_t M, int64_t D, int64_t F, int64_t N, int act, void* workspace,
+         int64_t workspace_bytes, pgemm_stream_t stream) {
+    const int rc = check_ffn(dtype, act, M, D, F, N);
+    if (rc != PGEMM_OK) return rc;
+    if (M == 0 || (N == 0 && !gate_up)) return PGEMM_OK;
+    const Mat mx = mat(x, M, D, ldx), mwi = mat(w_in, D, 2 * F, ldwi), mwo = mat(w_out, F, N, ldwo),
+              mr = mat(residual, M, N, ldr), my = mat(y, M, N, ldy),
+              mgu = mat(gate_up, M, 2 * F, ldgu);
+    Outputs o;
+    o.add(check(mx, F > 0));
+    o.add(check(mwi, true));
+    o.add(check(mwo, true));
+    o.add(check(mr, false));
+    o.add(check(my, true));
+    o.add(check(mgu, false));
+    if (o.rc != PGEMM_OK) return o.rc;
+    for (const Mat* in : {&mx, &mwi, &mwo}) {
+        // y is written by the last launch, which no longer reads x: y may
+        // take the place of x where x is the residual
+        o.apart(my, *in, in == &mx);
+        o.apart(mgu, *in);
+    }
+    o.apart(my, mr, true);
+    o.apart(mgu, mr);
+    o.apart(mgu, my);
+    if (o.rc != PGEMM_OK) return o.rc;
+    const FfnCall c = {dtype, x, mx.ld, w_in, mwi.ld, w_out, mwo.ld, residual, mr.ld, y, my.ld,
+                       gate_up, mgu.ld, M, D, F, N, act};
+    const Mat all[] = {mx, mwi, mwo, mr, my, mgu};
+    return with_workspace(
+        [&](Arena& ar) { return ffn_forward(c, ar, static_cast<hipStream_t>(stream)); }, workspace,
+        workspace_bytes, all, 6);
+}
+
+int64_t pffn_workspace_bytes(int dtype, const void* x, int64_t ldx, const void* w_in, int64_t ldwi,
+                             const void* w_out, int64_t ldwo, int64_t M, int64_t D, int64_t F,
+                             int64_t N) {
+    const int rc = check_ffn(dtype, PGEMM_ACT_NONE, M, D, F, N);
+    if (rc != PGEMM_OK) return rc;
+    if (M == 0) return 0;
+    const Mat mx = mat(x, M, D, ldx), mwi = mat(w_in, D, 2 * F, ldwi), mwo = mat(w_out, F, N, ldwo);
+    Outputs o;
+    o.add(check(mx, F > 0));
+    o.add(check(mwi, true));
+    o.add(check(mwo, true));
+    if (o.rc != PGEMM_OK) return o.rc;
+    FfnCall c = {};
+    c.dtype = dtype;
+    c.x = x, c.ldx = mx.ld, c.w_in = w_in, c.ldwi = mwi.ld, c.w_out = w_out, c.ldwo = mwo.ld;
+    c.M = M, c.D = D, c.F = F, c.N = N;
+    Arena dry = {nullptr, 0};
+    const hipError_t e = ffn_forward(c, dry, nullptr);
+    return e == hipSuccess ? dry.used : hip_status(e);
+}
+
+int pffn_bwd(int dtype, const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w_in,
+             int64_t ldwi, const void* w_out, int64_t ldwo, const void* gate_up, int64_t ldgu,
+             const void* add, int64_t ldadd, void* dx, int64_t lddx, void* dw_in, int64_t lddwi,
+             void* dw_out, int64_t lddwo, int64_t M, int64_t D, int64_t F, int64_t N, int act,
+             void* workspace, int64_t workspace_bytes, pgemm_stream_t stream) {
+    const int rc = check_ffn(dtype, act, M, D, F, N);
+    if (rc != PGEMM_OK) return rc;
+    if (!dx && !dw_in && !dw_out) return PGEMM_OK;
+    const Mat mdy = mat(dy, M, N, lddy), mx = mat(x, M, D, ldx), mwi = mat(w_in, D, 2 * F, ldwi),
+              mwo = mat(w_out, F, N, ldwo), mgu = mat(gate_up, M, 2 * F, ldgu),
+              ma = mat(add, M, D, ldadd), mdx = mat(dx, M, D, lddx),
+              mdwi = mat(dw_in, D, 2 * F, lddwi), mdwo = mat(dw_out, F, N, lddwo);
+    Outputs o;
+    o.add(check(mdy, true));
+    o.add(check(mx, dw_in != nullptr));
+    o.add(check(mwi, dx != nullptr));
+    o.add(check(mwo, true));
+    o.add(check(mgu, true));
+    for (const Mat* m : {&ma, &mdx, &mdwi, &mdwo}) o.add(check(*m, false));
+    if (o.rc != PGEMM_OK) return o.rc;
+    for (const Mat* out : {&mdx, &mdwi, &mdwo}) {
+        for (const Mat* in : {&mdy, &mx, &mwi, &mwo, &mgu}) o.apart(*out, *in);
+        o.apart(*out, ma, out == &mdx);
+    }
+    o.apart(mdx, mdwi);
+    o.apart(mdx, mdwo);
+    o.apart(mdwi, mdwo);
+    if (o.rc != PGEMM_OK) return o.rc;
+    const FfnGradCall c = {dtype, dy, mdy.ld, x, mx.ld, w_in, mwi.ld, w_out, mwo.ld, gate_up,
+                           mgu.ld, add, ma.ld, dx, mdx.ld, dw_in, mdwi.ld, dw_out, mdwo.ld,
+                           M, D, F, N, act};
+    const Mat all[] = {mdy, mx, mwi, mwo, mgu, ma, mdx, mdwi, mdwo};
+    return with_workspace(
+        [&](Arena& ar) { return ffn_backward(c, ar, static_cast<hipStream_t>(stream)); }, workspace,
+        workspace_bytes, all, 9);
+}
+
+int64_t pffn_bwd_workspace_bytes(int dtype, const void* dy, int64_t lddy, const void* x,
+                                 int64_t ldx, const void* w_in, int64_t ldwi, const void* w_out,
+                                 int64_t ldwo, int64_t M, int64_t D, int64_t F, int64_t N,
+                                 int need_dx, int need_dw_in, int need_dw_out) {
+    const int rc = check_ffn(dtype, PGEMM_ACT_NONE, M, D, F, N);
+    if (rc != PGEMM_OK) return rc;
+    if (!need_dx && !need_dw_in && !need_dw_out) return 0;
+    const Mat mdy = mat(dy, M, N, lddy), mx = mat(x, M, D, ldx), mwi = mat(w_in, D, 2 * F, ldwi),
+              mwo = mat(w_out, F, N, ldwo);
+    Outputs o;
+    o.add(check(mdy, true));
+    o.add(check(mx, need_dw_in != 0));
+    o.add(check(mwi, need_dx != 0));
+    o.add(check(mwo, true));
+    if (o.rc != PGEMM_OK) return o.rc;
+    FfnGradCall c = {};
+    void* const some = reinterpret_cast<void*>(16);  // stands for an output; never touched
+    c.dtype = dtype;
+    c.dy = dy, c.lddy = mdy.ld, c.x = x, c.ldx = mx.ld;
+    c.w_in = w_in, c.ldwi = mwi.ld, c.w_out = w_out, c.ldwo = mwo.ld;
+    c.dx = need_dx ? some : nullptr;
+    c.dw_in = need_dw_in ? some : nullptr;
+    c.dw_out = need_dw_out ? some : nullptr;
+    c.M = M, c.D = D, c.F = F, c.N = N;
+    Arena dry = {nullptr, 0};
+    const hipError_t e = ffn_backward(c, dry, nullptr);
     return e == hipSuccess ? dry.used : hip_status(e);
 }
 

@@ -14,8 +14,8 @@ namespace {
 // boundary (the compiler's unaligned global load), element by element at
 // the row's end.  Bound by memory: each value is read and written once.
 __global__ __launch_bounds__(256) void pack_kernel(const uint16_t* __restrict__ src, int64_t ld,
-                                                   uint16_t* __restrict__ dst, int64_t rows,
-                                                   int cols) {
+                                                   uint16_t* __restrict__ dst, int64_t dst_ld,
+                                                   int64_t rows, int cols) {
     const int cpr = (cols + 7) / 8;
     const int64_t total = rows * cpr;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
@@ -33,7 +33,7 @@ __global__ __launch_bounds__(256) void pack_kernel(const uint16_t* __restrict__ 
 #pragma unroll
             for (int q = 0; q < 4; ++q) w[q] = e[2 * q] | ((uint32_t)e[2 * q + 1] << 16);
         }
-        reinterpret_cast<u4_t*>(dst)[i] = w;
+        *reinterpret_cast<u4_t*>(dst + r * dst_ld + c) = w;
     }
 }
 
@@ -60,13 +60,13 @@ __global__ __launch_bounds__(256) void column_sum_kernel(const float* __restrict
 
 }  // namespace
 
-hipError_t launch_pack(const uint16_t* src, int64_t ld, uint16_t* dst, int64_t rows, int64_t cols,
-                       hipStream_t stream) {
+hipError_t launch_pack(const uint16_t* src, int64_t ld, uint16_t* dst, int64_t dst_ld, int64_t rows,
+                       int64_t cols, hipStream_t stream) {
     const int64_t chunks = rows * ((cols + 7) / 8);
     if (chunks == 0) return hipSuccess;
     const int64_t blocks = std::min<int64_t>((chunks + 255) / 256, 1 << 16);
-    hipLaunchKernelGGL(pack_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, src, ld, dst, rows,
-                       (int)cols);
+    hipLaunchKernelGGL(pack_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, src, ld, dst, dst_ld,
+                       rows, (int)cols);
     return hipGetLastError();
 }
 

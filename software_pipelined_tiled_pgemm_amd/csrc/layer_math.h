@@ -144,6 +144,11 @@ struct Rows {
     __host__ __device__ explicit operator bool() const { return ptr != nullptr; }
 };
 
+inline Rows make_rows(const void* p, int64_t ld) {
+    const bool vec = p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0;
+    return {static_cast<uint16_t*>(const_cast<void*>(p)), ld, vec};
+}
+
 typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
 
 template <class E>

@@ -44,6 +44,24 @@ struct LinearGradCall {
     int act;
 };
 
+// Where a product's values go: y = act(v + bias) + residual, v + bias to
+// preact; null members are left out.  half > 0: the product's columns are two
+// halves, each padded from `half` to round_up(half, 8) columns, which y holds
+// without the padding (no bias, residual or preact then).
+struct Sink {
+    void* y;
+    int64_t ldy;
+    const void* residual;
+    int64_t ldr;
+    void* preact;
+    int64_t ldp;
+    const void* bias;
+    int act;
+    int half;
+};
+hipError_t launch_linear(int dtype, int layout, const Args& g, const Cut& cut, const Sink& sink,
+                         hipStream_t stream);
+
 // With a dry arena nothing is launched and only the workspace is counted.
 hipError_t linear_forward(const LinearCall& c, Arena& ar, hipStream_t stream);
 hipError_t linear_backward(const LinearGradCall& c, Arena& ar, hipStream_t stream);
@@ -60,7 +78,7 @@ inline hipError_t operand(const void* p, int64_t ld, int64_t rows, int64_t cols,
     uint16_t* dst = static_cast<uint16_t*>(ar.take(rows * c8 * 2));
     out = {dst, (int)c8};
     if (ar.dry()) return hipSuccess;
-    return launch_pack(static_cast<const uint16_t*>(p), ld, dst, rows, cols, stream);
+    return launch_pack(static_cast<const uint16_t*>(p), ld, dst, c8, rows, cols, stream);
 }
 
 // The arguments of C[M, N] = a . b over K, with room for the cut's partials.

@@ -24,6 +24,7 @@ struct LinearEpi {
     const uint16_t* bias;
     int bias_vec;
     int act;
+    int half;  // > 0: two padded halves of columns (Sink)
     __device__ __forceinline__ void operator()(int row, int col, int nv, float (&v)[8]) const {
         float t[8];
         if (bias) {
@@ -40,6 +41,13 @@ struct LinearEpi {
             load8<E>(res, row, col, nv, t);
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] += t[q];
+        }
+        if (half > 0) {
+            const int h8 = (half + 7) & ~7;
+            const int second = col >= h8;
+            const int c = col - (second ? h8 : 0);
+            nv = min(8, half - c);
+            col = c + (second ? half : 0);
         }
         store8<E>(y, row, col, nv, v);
     }
@@ -93,8 +101,23 @@ __global__ __launch_bounds__(256) void dz_kernel(const Rows dy, const Rows pre, 
     }
 }
 
-Rows rows(const void* p, int64_t ld) {
-    return {static_cast<uint16_t*>(const_cast<void*>(p)), ld, p ? vector_rows(p, ld) : 0};
+template <class E>
+hipError_t launch_linear_as(int layout, const Args& g, const Cut& cut, const Sink& s,
+                            hipStream_t stream) {
+    Rows y = make_rows(s.y, s.ldy);
+    if (s.half % 8 != 0) y.vec = 0;  // the second half's chunks are not 16-byte aligned
+    const LinearEpi<E> epi = {y,
+                              make_rows(s.residual, s.ldr),
+                              make_rows(s.preact, s.ldp),
+                              static_cast<const uint16_t*>(s.bias),
+                              aligned16(s.bias),
+                              s.act,
+                              s.half};
+    switch (layout) {
+        case kNN: return lp::launch_product<E, true, false>(g, cut, epi, stream);
+        case kNT: return lp::launch_product<E, true, true>(g, cut, epi, stream);
+        default: return lp::launch_product<E, false, false>(g, cut, epi, stream);
+    }
 }
 
 template <class E>
@@ -105,15 +128,10 @@ struct Linear {
         if ((rc = operand(c.x, c.ldx, c.M, c.K, ar, stream, x)) != hipSuccess) return rc;
         if ((rc = operand(c.w, c.ldw, c.K, c.N, ar, stream, w)) != hipSuccess) return rc;
         const Cut cut = choose_cut(c.M, c.N, c.K, compute_units(), 16);
-        Args g = args(x, w, c.M, c.N, c.K, cut, ar);
+        const Args g = args(x, w, c.M, c.N, c.K, cut, ar);
         if (ar.dry()) return hipSuccess;
-        const LinearEpi<E> epi = {rows(c.y, c.ldy),
-                                  rows(c.residual, c.ldr),
-                                  rows(c.preact, c.ldp),
-                                  static_cast<const uint16_t*>(c.bias),
-                                  aligned16(c.bias),
-                                  c.act};
-        return lp::launch_product<E, true, false>(g, cut, epi, stream);
+        const Sink s = {c.y, c.ldy, c.residual, c.ldr, c.preact, c.ldp, c.bias, c.act, 0};
+        return launch_linear_as<E>(kNN, g, cut, s, stream);
     }
 
     static hipError_t backward(const LinearGradCall& c, Arena& ar, hipStream_t stream) {
@@ -136,8 +154,8 @@ struct Linear {
         if (c.dbias) part = static_cast<float*>(ar.take(std::max<int64_t>(blocks, 1) * c.N * 4));
         if (!ar.dry() && c.M > 0 && c.N > 0 && (need_dz || c.dbias)) {
             const dim3 grid((unsigned)((n8 + 511) / 512), (unsigned)blocks);
-            hipLaunchKernelGGL(dz_kernel<E>, grid, dim3(256), 0, stream, rows(c.dy, c.lddy),
-                               act ? rows(c.preact, c.ldp) : Rows{nullptr, 0, 0},
+            hipLaunchKernelGGL(dz_kernel<E>, grid, dim3(256), 0, stream, make_rows(c.dy, c.lddy),
+                               act ? make_rows(c.preact, c.ldp) : Rows{nullptr, 0, 0},
                                need_dz ? Rows{dzw, n8, 1} : Rows{nullptr, 0, 0}, part, c.M,
                                (int)c.N, need_dz ? (int)n8 : (int)c.N, per, c.act);
             if ((rc = hipGetLastError()) != hipSuccess) return rc;
@@ -150,11 +168,10 @@ struct Linear {
             View w;
             if ((rc = operand(c.w, c.ldw, c.K, c.N, ar, stream, w)) != hipSuccess) return rc;
             const Cut cut = choose_cut(c.M, c.K, c.N, compute_units(), 16);
-            Args g = args(dz, w, c.M, c.K, c.N, cut, ar);
+            const Args g = args(dz, w, c.M, c.K, c.N, cut, ar);
             if (!ar.dry()) {
-                const LinearEpi<E> epi = {rows(c.dx, c.lddx), rows(c.add, c.ldadd),
-                                          Rows{nullptr, 0, 0}, nullptr, 0, PGEMM_ACT_NONE};
-                rc = lp::launch_product<E, true, true>(g, cut, epi, stream);
+                const Sink s = {c.dx, c.lddx, c.add, c.ldadd, nullptr, 0, nullptr, 0, 0};
+                rc = launch_linear_as<E>(kNT, g, cut, s, stream);
                 if (rc != hipSuccess) return rc;
             }
         }
@@ -162,11 +179,10 @@ struct Linear {
             View x;
             if ((rc = operand(c.x, c.ldx, c.M, c.K, ar, stream, x)) != hipSuccess) return rc;
             const Cut cut = choose_cut(c.K, c.N, c.M, compute_units(), 16);
-            Args g = args(x, dz, c.K, c.N, c.M, cut, ar);
+            const Args g = args(x, dz, c.K, c.N, c.M, cut, ar);
             if (!ar.dry()) {
-                const LinearEpi<E> epi = {rows(c.dw, c.lddw), Rows{nullptr, 0, 0},
-                                          Rows{nullptr, 0, 0}, nullptr, 0, PGEMM_ACT_NONE};
-                rc = lp::launch_product<E, false, false>(g, cut, epi, stream);
+                const Sink s = {c.dw, c.lddw, nullptr, 0, nullptr, 0, nullptr, 0, 0};
+                rc = launch_linear_as<E>(kTN, g, cut, s, stream);
                 if (rc != hipSuccess) return rc;
             }
         }
@@ -177,6 +193,12 @@ struct Linear {
 };
 
 }  // namespace
+
+hipError_t launch_linear(int dtype, int layout, const Args& g, const Cut& cut, const Sink& sink,
+                         hipStream_t stream) {
+    return dtype == kBF16 ? launch_linear_as<BF16>(layout, g, cut, sink, stream)
+                          : launch_linear_as<F16>(layout, g, cut, sink, stream);
+}
 
 hipError_t linear_forward(const LinearCall& c, Arena& ar, hipStream_t stream) {
     return c.dtype == kBF16 ? Linear<BF16>::forward(c, ar, stream)

@@ -185,3 +185,78 @@ def plinear_bwd(dy, x, w, preact=None, act="none", dx_residual=None, needs=(True
                              lddw, _ptr(dbias), M, N, K, a, ws, nws, h)
     _call(_invoke(dy, stream, run), "plinear_bwd")
     return dx, dw, dbias
+
+
+def pffn(x, w_in, w_out, residual=None, act="silu", gate_up=None, out=None, workspace=None,
+         stream=None):
+    """(act(g) * u) @ w_out + residual with [g | u] = x @ w_in: the gated
+    feed-forward block for x [M,D], w_in [D,2F], w_out [F,N].
+
+    gate_up: an [M,2F] tensor that receives [g | u], which pffn_bwd needs.
+    out may be residual or x."""
+    dt = _dtype(x, "x")
+    a = _act(act)
+    ldx = _mat(x, "x", x)
+    M, D = x.shape
+    ldwi = _mat(w_in, "w_in", x, rows=D)
+    if w_in.shape[1] % 2:
+        raise ValueError("w_in must have an even number of columns (gate, then up)")
+    F = w_in.shape[1] // 2
+    ldwo = _mat(w_out, "w_out", x, rows=F)
+    N = w_out.shape[1]
+    ldr = _mat(residual, "residual", x, M, N) if residual is not None else 0
+    ldgu = _mat(gate_up, "gate_up", x, M, 2 * F) if gate_up is not None else 0
+    out, ldy = _out(out, "out", x, (M, N), stream)
+    L = lib()
+
+    def run(h):
+        need = L.pffn_workspace_bytes(dt, x.data_ptr(), ldx, w_in.data_ptr(), ldwi,
+                                      w_out.data_ptr(), ldwo, M, D, F, N)
+        ws, nws, keep = _workspace(need, workspace, x, stream, "pffn")
+        return L.pffn(dt, x.data_ptr(), ldx, w_in.data_ptr(), ldwi, w_out.data_ptr(), ldwo,
+                      _ptr(residual), ldr, out.data_ptr(), ldy, _ptr(gate_up), ldgu, M, D, F, N, a,
+                      ws, nws, h)
+    _call(_invoke(x, stream, run), "pffn")
+    return out
+
+
+def pffn_bwd(dy, x, w_in, w_out, gate_up, act="silu", dx_residual=None, needs=(True, True, True),
+             dx=None, dw_in=None, dw_out=None, workspace=None, stream=None):
+    """(dx, dw_in, dw_out) of pffn for the gradient dy [M,N] of its output
+    (which is also the gradient of its residual).  `needs` says which are
+    computed; the others are None.  dx_residual [M,D] is added to dx (dy, where
+    x was also the residual)."""
+    dt = _dtype(dy, "dy")
+    a = _act(act)
+    lddy = _mat(dy, "dy", dy)
+    M, N = dy.shape
+    ldx = _mat(x, "x", dy, rows=M)
+    D = x.shape[1]
+    ldwi = _mat(w_in, "w_in", dy, rows=D)
+    if w_in.shape[1] % 2:
+        raise ValueError("w_in must have an even number of columns (gate, then up)")
+    F = w_in.shape[1] // 2
+    ldwo = _mat(w_out, "w_out", dy, F, N)
+    ldgu = _mat(gate_up, "gate_up", dy, M, 2 * F)
+    lda = _mat(dx_residual, "dx_residual", dy, M, D) if dx_residual is not None else 0
+    lddx = lddwi = lddwo = 0
+    if needs[0]:
+        dx, lddx = _out(dx, "dx", dy, (M, D), stream)
+    if needs[1]:
+        dw_in, lddwi = _out(dw_in, "dw_in", dy, (D, 2 * F), stream)
+    if needs[2]:
+        dw_out, lddwo = _out(dw_out, "dw_out", dy, (F, N), stream)
+    dx, dw_in, dw_out = (t if n else None for t, n in zip((dx, dw_in, dw_out), needs))
+    L = lib()
+
+    def run(h):
+        need = L.pffn_bwd_workspace_bytes(dt, dy.data_ptr(), lddy, x.data_ptr(), ldx,
+                                          w_in.data_ptr(), ldwi, w_out.data_ptr(), ldwo, M, D, F,
+                                          N, *map(int, map(bool, needs)))
+        ws, nws, keep = _workspace(need, workspace, dy, stream, "pffn_bwd")
+        return L.pffn_bwd(dt, dy.data_ptr(), lddy, x.data_ptr(), ldx, w_in.data_ptr(), ldwi,
+                          w_out.data_ptr(), ldwo, gate_up.data_ptr(), ldgu, _ptr(dx_residual), lda,
+                          _ptr(dx), lddx, _ptr(dw_in), lddwi, _ptr(dw_out), lddwo, M, D, F, N, a,
+                          ws, nws, h)
+    _call(_invoke(dy, stream, run), "pffn_bwd")
+    return dx, dw_in, dw_out

@@ -173,3 +173,80 @@ def test_linear_strides(shape, pad, offset, dtype):
                        act="silu")
     for u, v in zip(g, h):
         assert torch.equal(u, v)
+
+
+# (M, D, F, N): single values, whole and broken 16-byte rows, tile edges, a
+# split contraction, more outputs than inputs, an empty block
+FFN = [(1, 1, 1, 1), (1, 64, 96, 64), (5, 37, 51, 29), (130, 72, 129, 72), (64, 512, 256, 512),
+       (257, 264, 520, 136), (3, 1024, 2048, 1024), (300, 100, 36, 260), (40, 8, 0, 16),
+       (129, 4096, 136, 24)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", FFN)
+def test_ffn(shape, dtype):
+    M, D, F, N = shape
+    act = ACTS[(M + D + F) % len(ACTS)]
+    say("ffn", shape, dtype, act)
+    x = rand((M, D), dtype, 31)
+    wi = rand((D, 2 * F), dtype, 32, std=D ** -0.5)
+    wo = rand((F, N), dtype, 33, std=max(F, 1) ** -0.5)
+    r = rand((M, N), dtype, 34)
+    gu = torch.full((M, 2 * F), float("nan"), dtype=dtype, device="cuda")
+    y = pg.pffn(x, wi, wo, residual=r, act=act, gate_up=gu)
+    X, WI, WO, R = f64(x), f64(wi), f64(wo), f64(r)
+    G, U = (X @ WI)[:, :F], (X @ WI)[:, F:]
+    S = np.abs(X) @ np.abs(WI)
+    assert_near(gu, X @ WI, S, dtype, D, 0, "gate_up")
+    H = act_exact(G, act) * U
+    # an error of g or u (fp32 accumulation) reaches h through the product
+    e32 = (D + 16) * 2.0 ** -23
+    HE = e32 * 1.2 * (S[:, :F] * np.abs(U) + np.abs(act_exact(G, act)) * S[:, F:])
+    Y = H @ WO + R
+    bound = HE @ np.abs(WO)
+    exact_scale = np.abs(H) @ np.abs(WO) + np.abs(R)
+    u = UNIT[dtype]
+    tol = (u * np.abs(Y) + (u + (F + 16) * 2.0 ** -23) * exact_scale + bound * 1.01 + TINY[dtype]
+           + TINY[dtype] * np.abs(WO).sum(0))
+    assert (np.abs(f64(y) - Y) <= tol).all()
+
+    # the backward pass takes gate_up as kept
+    dy = rand((M, N), dtype, 35)
+    a = rand((M, D), dtype, 36)
+    dx, dwi, dwo = pg.pffn_bwd(dy, x, wi, wo, gu, act=act, dx_residual=a)
+    GU, DY, A = f64(gu), f64(dy), f64(a)
+    G, U = GU[:, :F], GU[:, F:]
+    DH = DY @ WO.T
+    DHS = np.abs(DY) @ np.abs(WO).T
+    AG, DG = act_exact(G, act), grad_exact(G, act)
+    DIN = np.concatenate([DH * U * DG, DH * AG], axis=1)
+    # magnitudes: the rounding of an entry, and fp32 accumulation over N in dh
+    # (17 + N of 2^-23 of DHS) is far below half a rounding of it only where dh does
+    # not cancel, so it is added
+    mag = np.abs(DIN) + 2 * (N + 17) * 2.0 ** -23 / u * np.concatenate(
+        [DHS * np.abs(U) * 1.2, DHS * (np.abs(AG) + 1e-6 * np.abs(G))], axis=1)
+    assert_near(dx, DIN @ WI.T + A, mag @ np.abs(WI).T + np.abs(A), dtype, 2 * F, 1, "dx")
+    assert_near(dwi, X.T @ DIN, np.abs(X).T @ mag, dtype, M, 1, "dw_in")
+    assert_near(dwo, (AG * U).T @ DY, (np.abs(AG) * np.abs(U) * 1.0001 + 1e-6 * np.abs(G * U)).T
+                @ np.abs(DY), dtype, M, 1, "dw_out")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("pad,offset", STRIDES)
+@pytest.mark.parametrize("shape", [(130, 72, 136, 40), (4, 264, 520, 264), (37, 51, 43, 27)])
+def test_ffn_strides(shape, pad, offset, dtype):
+    M, D, F, N = shape
+    say("ffn strides", shape, pad, offset, dtype)
+    x = rand((M, D), dtype, 41, pitch=D + pad, offset=offset)
+    wi = rand((D, 2 * F), dtype, 42, std=D ** -0.5, pitch=2 * F + pad, offset=offset)
+    wo = rand((F, N), dtype, 43, std=F ** -0.5, pitch=N + pad, offset=offset)
+    gu = rand((M, 2 * F), dtype, 44, pitch=2 * F + pad, offset=offset)
+    gu2 = torch.empty((M, 2 * F), dtype=dtype, device="cuda")
+    y = pg.pffn(x, wi, wo, gate_up=gu)
+    z = pg.pffn(x.contiguous(), wi.contiguous(), wo.contiguous(), gate_up=gu2)
+    assert torch.equal(y, z) and torch.equal(gu, gu2)
+    dy = rand((M, N), dtype, 45, pitch=N + pad, offset=offset)
+    g = pg.pffn_bwd(dy, x, wi, wo, gu)
+    h = pg.pffn_bwd(dy.contiguous(), x.contiguous(), wi.contiguous(), wo.contiguous(), gu2)
+    for u, v in zip(g, h):
+        assert torch.equal(u, v)
