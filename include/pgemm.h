@@ -392,6 +392,46 @@ int64_t pffn_bwd_workspace_bytes(int dtype, const void* dy, int64_t lddy, const 
                                  int64_t ldwo, int64_t M, int64_t D, int64_t F, int64_t N,
                                  int need_dx, int need_dw_in, int need_dw_out);
 
+/* How the losses of the rows are put together: each row's loss; their mean
+ * over the rows that are not ignored (0 if all are); their sum. */
+enum pgemm_reduction { PGEMM_REDUCE_NONE = 0, PGEMM_REDUCE_MEAN = 1, PGEMM_REDUCE_SUM = 2 };
+
+/*
+ * Softmax cross entropy over a vocabulary: with l = x W^T,
+ *   lse[m] = log sum over v of exp(l[m][v]),  loss[m] = lse[m] - l[m][target[m]].
+ *   x [M,D], W [V,D] (one row per vocabulary entry), target [M] int64.
+ *   A row whose target is ignore_index has the loss 0; a target outside
+ *   [0, V) that is not ignore_index gives the loss NaN (and NaN gradients).
+ *   loss: one float (mean, sum) or M floats (none); lse: M floats, every row,
+ *   which the backward pass needs.
+ * The logits are not kept: each 256 of a row leave 8 bytes in the workspace.
+ * V >= 1 (PGEMM_EINVAL).  V may be 2^22 and more; M * V <= 2^37.
+ */
+int pxent(int dtype, const void* x, int64_t ldx, const void* w, int64_t ldw, const int64_t* target,
+          int64_t ignore_index, int reduction, float* loss, float* lse, int64_t M, int64_t V,
+          int64_t D, void* workspace, int64_t workspace_bytes, pgemm_stream_t stream);
+int64_t pxent_workspace_bytes(int dtype, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                              int reduction, int64_t M, int64_t V, int64_t D);
+
+/*
+ * Backward pass: with dl[m][v] = g[m] (exp(l[m][v] - lse[m]) - [v = target[m]]),
+ *   dx = dl W,  dW = dl^T x.
+ *   g[m] is dloss[m] (none), dloss[0] / (number of rows not ignored) (mean) or
+ *   dloss[0] (sum), and 0 for an ignored row; dloss is device memory, NULL
+ *   stands for 1.  lse as the forward pass wrote it.  dx and dW may each be
+ *   NULL: that gradient is not computed.
+ * The vocabulary is taken in pieces whose dl (rounded once to dtype, scaled
+ * so that the largest |g| is 2^15 in fp16 and 1 in bf16) takes at most
+ * 512 MiB of workspace, or 1024 entries; dx is summed over the pieces in fp32.
+ */
+int pxent_bwd(int dtype, const void* x, int64_t ldx, const void* w, int64_t ldw,
+              const int64_t* target, int64_t ignore_index, int reduction, const float* lse,
+              const float* dloss, void* dx, int64_t lddx, void* dw, int64_t lddw, int64_t M,
+              int64_t V, int64_t D, void* workspace, int64_t workspace_bytes,
+              pgemm_stream_t stream);
+int64_t pxent_bwd_workspace_bytes(int dtype, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                  int64_t M, int64_t V, int64_t D, int need_dx, int need_dw);
+
 /* Static English text for a status code (never NULL). */
 const char* pgemm_status_string(int status);
 

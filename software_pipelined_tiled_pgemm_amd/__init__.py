@@ -20,6 +20,7 @@ __all__ = [
     "pstream_add", "pstream_add_blocked", "pstream_add_scalar", "preduce_sum_f32",
     "pgemm_test_fill_f32", "pgemm_test_iota_f32",
     "plinear", "plinear_bwd", "pffn", "pffn_bwd",
+    "pxent", "pxent_bwd",
     "lib", "status_string", "PgemmError",
     "PGEMM_OK", "PGEMM_EINVAL", "PGEMM_EUNSUPPORTED", "PGEMM_EHIP", "PGEMM_ESCRATCH",
     "STATIC_SCRATCH_BYTES",
@@ -320,4 +321,5 @@ def pgemm_test_iota_f32(n, device="cuda", out=None, stream=None):
     return o
 
 
-from .layers import pffn, pffn_bwd, plinear, plinear_bwd  # noqa: E402  (uses the helpers above)
+from .layers import (pffn, pffn_bwd, plinear, plinear_bwd,  # noqa: E402  (uses the helpers above)
+                     pxent, pxent_bwd)

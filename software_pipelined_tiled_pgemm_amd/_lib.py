@@ -61,6 +61,11 @@ def _declare(lib):
         "pffn_bwd": (i32, [i32] + [p, i64] * 9 + [i64, i64, i64, i64, i32, p, i64, p]),
         "pffn_bwd_workspace_bytes": (i64, [i32] + [p, i64] * 4 + [i64, i64, i64, i64, i32, i32,
                                                                  i32]),
+        "pxent": (i32, [i32, p, i64, p, i64, p, i64, i32, p, p, i64, i64, i64, p, i64, p]),
+        "pxent_workspace_bytes": (i64, [i32, p, i64, p, i64, i32, i64, i64, i64]),
+        "pxent_bwd": (i32, [i32, p, i64, p, i64, p, i64, i32, p, p, p, i64, p, i64, i64, i64, i64,
+                            p, i64, p]),
+        "pxent_bwd_workspace_bytes": (i64, [i32, p, i64, p, i64, i64, i64, i64, i32, i32]),
         "pgemm_status_string": (ctypes.c_char_p, [i32]),
         "pgemm_last_hip_error": (i32, []),
         "pgemm_version": (i32, []),

@@ -5,6 +5,7 @@
 #include "../../include/pgemm.h"
 #include "ffn.h"
 #include "linear.h"
+#include "xent.h"
 
 namespace {
 
@@ -111,6 +112,16 @@ int check_ffn(int dtype, int act, int64_t M, int64_t D, int64_t F, int64_t N) {
     const int rc = check_linear(dtype, act, M, D, N);
     if (rc != PGEMM_OK) return rc;
     return F >= kMaxCols / 2 ? PGEMM_EUNSUPPORTED : PGEMM_OK;
+}
+
+int check_xent(int dtype, int reduction, int64_t M, int64_t V, int64_t D) {
+    if (M < 0 || V < 1 || D < 0) return PGEMM_EINVAL;
+    if (!known(dtype, PGEMM_ACT_NONE) || reduction < PGEMM_REDUCE_NONE ||
+        reduction > PGEMM_REDUCE_SUM)
+        return PGEMM_EUNSUPPORTED;
+    if (M >= kMaxRows || V >= kMaxRows || D >= kMaxCols || M > kMaxElems / V)
+        return PGEMM_EUNSUPPORTED;
+    return PGEMM_OK;
 }
 
 }  // namespace
@@ -344,6 +355,111 @@ int64_t pffn_bwd_workspace_bytes(int dtype, const void* dy, int64_t lddy, const 
     c.M = M, c.D = D, c.F = F, c.N = N;
     Arena dry = {nullptr, 0};
     const hipError_t e = ffn_backward(c, dry, nullptr);
+    return e == hipSuccess ? dry.used : hip_status(e);
+}
+
+int pxent(int dtype, const void* x, int64_t ldx, const void* w, int64_t ldw, const int64_t* target,
+          int64_t ignore_index, int reduction, float* loss, float* lse, int64_t M, int64_t V,
+          int64_t D, void* workspace, int64_t workspace_bytes, pgemm_stream_t stream) {
+    const int rc = check_xent(dtype, reduction, M, V, D);
+    if (rc != PGEMM_OK) return rc;
+    const bool each = reduction == PGEMM_REDUCE_NONE;
+    if (M == 0 && each) return PGEMM_OK;
+    const Mat mx = mat(x, M, D, ldx), mw = mat(w, V, D, ldw), mt = flat(target, M, 8),
+              ml = flat(loss, each ? M : 1, 4), ms = flat(lse, M, 4);
+    Outputs o;
+    o.add(check(mx, true));
+    o.add(check(mw, true));
+    o.add(check(mt, true));
+    o.add(check(ml, true));
+    o.add(check(ms, true));
+    if (o.rc != PGEMM_OK) return o.rc;
+    for (const Mat* in : {&mx, &mw, &mt}) {
+        o.apart(ml, *in);
+        o.apart(ms, *in);
+    }
+    o.apart(ml, ms);
+    if (o.rc != PGEMM_OK) return o.rc;
+    const XentCall c = {dtype, x, mx.ld, w, mw.ld, target, ignore_index, reduction, loss, lse,
+                        M, V, D};
+    const Mat all[] = {mx, mw, mt, ml, ms};
+    return with_workspace(
+        [&](Arena& ar) { return xent_forward(c, ar, static_cast<hipStream_t>(stream)); }, workspace,
+        workspace_bytes, all, 5);
+}
+
+int64_t pxent_workspace_bytes(int dtype, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                              int reduction, int64_t M, int64_t V, int64_t D) {
+    const int rc = check_xent(dtype, reduction, M, V, D);
+    if (rc != PGEMM_OK) return rc;
+    const Mat mx = mat(x, M, D, ldx), mw = mat(w, V, D, ldw);
+    Outputs o;
+    o.add(check(mx, true));
+    o.add(check(mw, true));
+    if (o.rc != PGEMM_OK) return o.rc;
+    XentCall c = {};
+    c.dtype = dtype;
+    c.x = x, c.ldx = mx.ld, c.w = w, c.ldw = mw.ld, c.reduction = reduction;
+    c.M = M, c.V = V, c.D = D;
+    Arena dry = {nullptr, 0};
+    const hipError_t e = xent_forward(c, dry, nullptr);
+    return e == hipSuccess ? dry.used : hip_status(e);
+}
+
+int pxent_bwd(int dtype, const void* x, int64_t ldx, const void* w, int64_t ldw,
+              const int64_t* target, int64_t ignore_index, int reduction, const float* lse,
+              const float* dloss, void* dx, int64_t lddx, void* dw, int64_t lddw, int64_t M,
+              int64_t V, int64_t D, void* workspace, int64_t workspace_bytes,
+              pgemm_stream_t stream) {
+    const int rc = check_xent(dtype, reduction, M, V, D);
+    if (rc != PGEMM_OK) return rc;
+    if (!dx && !dw) return PGEMM_OK;
+    const bool each = reduction == PGEMM_REDUCE_NONE;
+    const Mat mx = mat(x, M, D, ldx), mw = mat(w, V, D, ldw), mt = flat(target, M, 8),
+              ms = flat(lse, M, 4), mg = flat(dloss, each ? M : 1, 4), mdx = mat(dx, M, D, lddx),
+              mdw = mat(dw, V, D, lddw);
+    Outputs o;
+    o.add(check(mx, true));
+    o.add(check(mw, true));
+    o.add(check(mt, true));
+    o.add(check(ms, true));
+    o.add(check(mg, false));
+    o.add(check(mdx, false));
+    o.add(check(mdw, false));
+    if (o.rc != PGEMM_OK) return o.rc;
+    for (const Mat* in : {&mx, &mw, &mt, &ms, &mg}) {
+        o.apart(mdx, *in);
+        o.apart(mdw, *in);
+    }
+    o.apart(mdx, mdw);
+    if (o.rc != PGEMM_OK) return o.rc;
+    const XentGradCall c = {dtype, x, mx.ld, w, mw.ld, target, ignore_index, reduction, lse, dloss,
+                            dx, mdx.ld, dw, mdw.ld, M, V, D};
+    const Mat all[] = {mx, mw, mt, ms, mg, mdx, mdw};
+    return with_workspace(
+        [&](Arena& ar) { return xent_backward(c, ar, static_cast<hipStream_t>(stream)); }, workspace,
+        workspace_bytes, all, 7);
+}
+
+int64_t pxent_bwd_workspace_bytes(int dtype, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                  int64_t M, int64_t V, int64_t D, int need_dx, int need_dw) {
+    const int rc = check_xent(dtype, PGEMM_REDUCE_MEAN, M, V, D);
+    if (rc != PGEMM_OK) return rc;
+    if (!need_dx && !need_dw) return 0;
+    const Mat mx = mat(x, M, D, ldx), mw = mat(w, V, D, ldw);
+    Outputs o;
+    o.add(check(mx, true));
+    o.add(check(mw, true));
+    if (o.rc != PGEMM_OK) return o.rc;
+    XentGradCall c = {};
+    void* const some = reinterpret_cast<void*>(16);  // stands for an output; never touched
+    c.dtype = dtype;
+    c.x = x, c.ldx = mx.ld, c.w = w, c.ldw = mw.ld;
+    c.dx = need_dx ? some : nullptr;
+    c.dw = need_dw ? some : nullptr;
+    c.M = M, c.V = V, c.D = D;
+    Arena dry = {nullptr, 0};
+    const hipError_t e = xent_backward(c, dry, nullptr);
     return e == hipSuccess ? dry.used : hip_status(e);
 }
 

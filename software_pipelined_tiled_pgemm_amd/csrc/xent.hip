@@ -1,0 +1,397 @@
+// Softmax cross entropy over a vocabulary, and its backward pass, without the
+// [M, V] logits.
+//
+//   l = x W^T            x [M,D], W [V,D]
+//   lse_m = log sum_v exp(l_mv),  loss_m = lse_m - l_m,target(m)
+//   dl_mv = g_m (exp(l_mv - lse_m) - [v = target(m)])
+//   dx = dl W,  dW = dl^T x
+//
+// Forward: one product whose epilogue reduces each tile row to its maximum
+// and its sum of exp(l - maximum) (8 bytes for 256 logits); a second kernel
+// joins the tiles of a row.  Backward, piece by piece of the vocabulary: the
+// piece's logits again, turned into dl in the epilogue and kept in 16 bits;
+// then the piece's part of dx (summed over the pieces in fp32) and its rows
+// of dW.  8 M V D flops in all, 2 of them for the logits that were not kept.
+//
+// dl in 16 bits: |exp(l - lse) - [.]| <= 1, and a softmax over V entries is
+// mostly values near 1/V, which fp16 holds with few bits or none.  So dl is kept
+// as c_m K (exp(l - lse) - [.]) with K = 2^15 in fp16 (exact scaling; bf16
+// needs none), c_m = g_m / max |g|, and max |g| / K is applied in fp32 to the
+// sums.
+#include "xent.h"
+
+#include "layer_pipe.h"
+#include "linear.h"
+
+namespace pgemm {
+namespace layer {
+namespace {
+
+template <class E>
+constexpr float grad_scale() {
+    return std::is_same<E, F16>::value ? 32768.0f : 1.0f;
+}
+
+// Rows of a tile to (maximum, sum of exponentials), and the target's logit
+// from whichever lane holds it.
+struct StatsEpi {
+    static constexpr lp::EpiKind kind = lp::kRows;
+    float2* part;  // [tile][M]
+    float* target_logit;
+    const int64_t* target;
+    int64_t v0;     // vocabulary index of the product's column 0
+    int64_t M;
+    int tile0;
+    template <int LANES>
+    __device__ __forceinline__ void row(int r, int col, int nv, float (&v)[8], int tile) const {
+        const int64_t t = target[r] - v0 - col;
+        float m = -INFINITY, at = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            if (q >= nv) v[q] = -INFINITY;
+            m = fmaxf(m, v[q]);
+            if (t == q) at = v[q];
+        }
+        if (t >= 0 && t < nv) target_logit[r] = at;
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+        const float base = m == -INFINITY ? 0.0f : m;  // a row of -inf has the sum 0
+        float s = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s += exp_fast(v[q] - base);
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
+        if (threadIdx.x % LANES == 0) part[(int64_t)(tile0 + tile) * M + r] = float2{m, s};
+    }
+};
+
+// Joins a row's tiles: 64 rows per workgroup, 4 waves taking every fourth
+// tile.  A target outside the vocabulary that is not ignore_index gives NaN.
+__global__ __launch_bounds__(256) void join_kernel(const float2* __restrict__ part, int tiles,
+                                                   const float* __restrict__ target_logit,
+                                                   const int64_t* __restrict__ target,
+                                                   int64_t ignore_index, int64_t V, int64_t M,
+                                                   float* __restrict__ lse,
+                                                   float* __restrict__ row_loss) {
+    __shared__ float2 seg[4][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int64_t r = (int64_t)blockIdx.x * 64 + lane;
+    float m = -INFINITY, s = 0.0f;
+    auto join = [&](float2 p) {
+        const float top = fmaxf(m, p.x);
+        const float base = top == -INFINITY ? 0.0f : top;
+        s = s * exp_fast(m - base) + p.y * exp_fast(p.x - base);
+        m = top;
+    };
+    if (r < M)
+        for (int t = w; t < tiles; t += 4) join(part[(int64_t)t * M + r]);
+    seg[w][lane] = float2{m, s};
+    __syncthreads();
+    if (w == 0 && r < M) {
+        for (int k = 1; k < 4; ++k) join(seg[k][lane]);
+        const float l = (m == -INFINITY ? 0.0f : m) + logf(s);
+        lse[r] = l;
+        const int64_t t = target[r];
+        if (row_loss)
+            row_loss[r] = t == ignore_index ? 0.0f
+                          : (t >= 0 && t < V) ? l - target_logit[r]
+                                              : __builtin_nanf("");
+    }
+}
+
+// Sum (or mean over the rows that count) of the row losses, in fp64, by one
+// workgroup in a fixed order.
+__global__ __launch_bounds__(1024) void total_kernel(const float* __restrict__ row_loss,
+                                                     const int64_t* __restrict__ target,
+                                                     int64_t ignore_index, int64_t M, int mean,
+                                                     float* __restrict__ loss) {
+    __shared__ double sums[1024];
+    __shared__ int64_t counts[1024];
+    double s = 0.0;
+    int64_t n = 0;
+    for (int64_t r = threadIdx.x; r < M; r += 1024) {
+        s += (double)row_loss[r];
+        n += target[r] != ignore_index;
+    }
+    sums[threadIdx.x] = s;
+    counts[threadIdx.x] = n;
+    for (int h = 512; h > 0; h >>= 1) {
+        __syncthreads();
+        if (threadIdx.x < h) {
+            sums[threadIdx.x] += sums[threadIdx.x + h];
+            counts[threadIdx.x] += counts[threadIdx.x + h];
+        }
+    }
+    if (threadIdx.x == 0) {
+        const double d = mean ? (double)(counts[0] > 0 ? counts[0] : 1) : 1.0;
+        loss[0] = (float)(sums[0] / d);
+    }
+}
+
+// Row weights of the backward pass: c_m in [-1, 1] and the factor of the
+// sums, by one workgroup.  Ignored rows weigh 0; a weight that is not finite,
+// or belongs to an invalid target (NaN), stands for its row alone.
+__global__ __launch_bounds__(1024) void weights_kernel(const int64_t* __restrict__ target,
+                                                       int64_t ignore_index, int64_t V, int64_t M,
+                                                       int reduction,
+                                                       const float* __restrict__ dloss, float scale,
+                                                       float* __restrict__ weight,
+                                                       float* __restrict__ factor) {
+    __shared__ float tops[1024];
+    __shared__ int64_t counts[1024];
+    const bool each = reduction == PGEMM_REDUCE_NONE;
+    float top = 0.0f;
+    int64_t n = 0;
+    for (int64_t r = threadIdx.x; r < M; r += 1024) {
+        if (target[r] == ignore_index) continue;
+        ++n;
+        if (each && dloss) {
+            const float a = fabsf(dloss[r]);
+            if (a < INFINITY) top = fmaxf(top, a);
+        }
+    }
+    tops[threadIdx.x] = top;
+    counts[threadIdx.x] = n;
+    for (int h = 512; h > 0; h >>= 1) {
+        __syncthreads();
+        if (threadIdx.x < h) {
+            tops[threadIdx.x] = fmaxf(tops[threadIdx.x], tops[threadIdx.x + h]);
+            counts[threadIdx.x] += counts[threadIdx.x + h];
+        }
+    }
+    __syncthreads();
+    top = tops[0];
+    n = counts[0];
+    for (int64_t r = threadIdx.x; r < M; r += 1024) {
+        const int64_t t = target[r];
+        float c = 1.0f;
+        if (each && dloss) {
+            const float g = dloss[r];
+            c = fabsf(g) < INFINITY ? (top > 0.0f ? g / top : 0.0f) : g;
+        }
+        if (t == ignore_index)
+            c = 0.0f;
+        else if (t < 0 || t >= V)
+            c = __builtin_nanf("");
+        weight[r] = c;
+    }
+    if (threadIdx.x == 0) {
+        float f = each ? (dloss ? top : 1.0f) : (dloss ? dloss[0] : 1.0f);
+        if (reduction == PGEMM_REDUCE_MEAN) f /= (float)(n > 0 ? n : 1);
+        factor[0] = f / scale;
+    }
+}
+
+// dl of a piece: whole chunks, zeros past its last column.
+template <class E>
+struct DlogitEpi {
+    static constexpr lp::EpiKind kind = lp::kPlain;
+    Rows dl;
+    const float* lse;
+    const float* weight;
+    const int64_t* target;
+    int64_t v0;
+    __device__ __forceinline__ void operator()(int row, int col, int nv, float (&v)[8]) const {
+        const float c = weight[row] * grad_scale<E>();
+        const float l = lse[row];
+        const int64_t t = target[row] - v0 - col;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const float p = exp_fast(v[q] - l) - (t == q ? 1.0f : 0.0f);
+            // an ignored row is 0 whatever its logits are
+            v[q] = (q < nv && c != 0.0f) ? c * p : 0.0f;
+        }
+        store8<E>(dl, row, col, 8, v);
+    }
+};
+
+// dx over the pieces: fp32 sums in the workspace, the last piece rounds.
+template <class E>
+struct SumEpi {
+    static constexpr lp::EpiKind kind = lp::kPlain;
+    float* sum;  // [M][ld], NULL where there is one piece only
+    int64_t ld;
+    Rows out;
+    const float* factor;
+    int first, last;
+    __device__ __forceinline__ void operator()(int row, int col, int nv, float (&v)[8]) const {
+        if (sum) {
+            float* p = sum + (int64_t)row * ld + col;
+            floatx4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+            if (!first) {
+                lo += *reinterpret_cast<const floatx4*>(p);
+                hi += *reinterpret_cast<const floatx4*>(p + 4);
+            }
+            if (!last) {
+                *reinterpret_cast<floatx4*>(p) = lo;
+                *reinterpret_cast<floatx4*>(p + 4) = hi;
+                return;
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                v[q] = lo[q];
+                v[4 + q] = hi[q];
+            }
+        }
+        const float f = factor[0];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] *= f;
+        store8<E>(out, row, col, nv, v);
+    }
+};
+
+// Vocabulary entries per piece: at most `most` bytes of dl, pieces of equal
+// size and whole tiles.
+constexpr int64_t kPieceBytes = (int64_t)1 << 29;
+constexpr int64_t kPieceLeast = 1024;
+constexpr int64_t kPackRows = 32768;  // rows of W padded at a time
+
+int64_t piece_rows(int64_t V, int64_t most) {
+    most = std::max(most / 256 * 256, kPieceLeast);
+    const int64_t n = (V + most - 1) / most;
+    return n <= 1 ? V : round_up((V + n - 1) / n, 256);
+}
+
+// Rows v0 .. v0+n-1 of W as an operand, from where they lie or padded into `room`.
+hipError_t piece(const void* w, int64_t ldw, int64_t v0, int64_t n, int64_t D, uint16_t* room,
+                 bool dry, hipStream_t stream, View& out) {
+    const uint16_t* p = static_cast<const uint16_t*>(w) + v0 * ldw;
+    if (direct(w, ldw, D)) {
+        out = {p, (int)ldw};
+        return hipSuccess;
+    }
+    const int64_t d8 = round_up(D, 8);
+    out = {room, (int)d8};
+    return dry ? hipSuccess : launch_pack(p, ldw, room, d8, n, D, stream);
+}
+
+template <class E>
+struct Xent {
+    static hipError_t forward(const XentCall& c, Arena& ar, hipStream_t stream) {
+        const int cus = compute_units();
+        const bool straight = direct(c.w, c.ldw, c.D);
+        const int64_t step = straight ? c.V : piece_rows(c.V, kPackRows);
+        hipError_t rc;
+        View x, w;
+        if ((rc = operand(c.x, c.ldx, c.M, c.D, ar, stream, x)) != hipSuccess) return rc;
+        uint16_t* room = nullptr;
+        if (!straight) room = static_cast<uint16_t*>(ar.take(step * round_up(c.D, 8) * 2));
+        const Cut cut = choose_cut(c.M, step, c.D, cus, 1);
+        const int64_t bn = cut.big ? 256 : 128;
+        const int64_t tiles = (c.V + step - 1) / step * ((step + bn - 1) / bn);
+        float2* part = static_cast<float2*>(ar.take(tiles * c.M * 8));
+        float* logit = static_cast<float*>(ar.take(c.M * 4));
+        const bool total = c.reduction != PGEMM_REDUCE_NONE;
+        float* row_loss = c.loss;
+        if (total) row_loss = static_cast<float*>(ar.take(c.M * 4));
+        if (ar.dry()) return hipSuccess;
+        int used = 0;
+        for (int64_t v0 = 0; c.M > 0 && v0 < c.V; v0 += step) {
+            const int64_t n = std::min(step, c.V - v0);
+            if ((rc = piece(c.w, c.ldw, v0, n, c.D, room, false, stream, w)) != hipSuccess)
+                return rc;
+            const Args g = args(x, w, c.M, n, c.D, cut, ar);
+            const StatsEpi epi = {part, logit, c.target, v0, c.M, used};
+            using T = lp::Tiles<E, true, true>;
+            rc = cut.big ? lp::launch_tiles<typename T::Big, StatsEpi, false>(g, 1, epi, stream)
+                         : lp::launch_tiles<typename T::Small, StatsEpi, false>(g, 1, epi, stream);
+            if (rc != hipSuccess) return rc;
+            used += (int)((n + bn - 1) / bn);
+        }
+        if (c.M > 0) {
+            hipLaunchKernelGGL(join_kernel, dim3((unsigned)((c.M + 63) / 64)), dim3(256), 0, stream,
+                               part, used, logit, c.target, c.ignore_index, c.V, c.M, c.lse,
+                               row_loss);
+            if ((rc = hipGetLastError()) != hipSuccess) return rc;
+        }
+        if (total) {
+            hipLaunchKernelGGL(total_kernel, dim3(1), dim3(1024), 0, stream, row_loss, c.target,
+                               c.ignore_index, c.M, (int)(c.reduction == PGEMM_REDUCE_MEAN), c.loss);
+            return hipGetLastError();
+        }
+        return hipSuccess;
+    }
+
+    static hipError_t backward(const XentGradCall& c, Arena& ar, hipStream_t stream) {
+        const int cus = compute_units();
+        hipError_t rc;
+        View x, w;
+        if ((rc = operand(c.x, c.ldx, c.M, c.D, ar, stream, x)) != hipSuccess) return rc;
+        const int64_t step = piece_rows(c.V, kPieceBytes / (2 * std::max<int64_t>(c.M, 1)));
+        const int64_t s8 = round_up(step, 8), d8 = round_up(c.D, 8);
+        const int64_t pieces = (c.V + step - 1) / step;
+        uint16_t* room = nullptr;
+        if (!direct(c.w, c.ldw, c.D)) room = static_cast<uint16_t*>(ar.take(step * d8 * 2));
+        float* weight = static_cast<float*>(ar.take(c.M * 4));
+        float* factor = static_cast<float*>(ar.take(4));
+        uint16_t* dl = static_cast<uint16_t*>(ar.take(c.M * s8 * 2));
+        float* sum = nullptr;
+        if (c.dx && pieces > 1) sum = static_cast<float*>(ar.take(c.M * d8 * 4));
+        // The three products of a piece share one buffer for their partials.
+        const Cut cl = choose_cut(c.M, step, c.D, cus, 16), cx = choose_cut(c.M, c.D, step, cus, 16),
+                  cw = choose_cut(step, c.D, c.M, cus, 16);
+        const int64_t pb = std::max(part_bytes(cl, c.M, step),
+                                    std::max(c.dx ? part_bytes(cx, c.M, c.D) : 0,
+                                             c.dw ? part_bytes(cw, step, c.D) : 0));
+        float* part = pb > 0 ? static_cast<float*>(ar.take(pb)) : nullptr;
+        if (ar.dry()) return hipSuccess;
+        auto product = [&](View a, View b, int64_t M, int64_t N, int64_t K) {
+            Args g = {};
+            g.a = a;
+            g.b = b;
+            g.M = (int)M;
+            g.N = (int)N;
+            g.K = (int)K;
+            g.part = part;
+            g.part_ld = (int)round_up(N, 8);
+            return g;
+        };
+        hipLaunchKernelGGL(weights_kernel, dim3(1), dim3(1024), 0, stream, c.target, c.ignore_index,
+                           c.V, c.M, c.reduction, c.dloss, grad_scale<E>(), weight, factor);
+        if ((rc = hipGetLastError()) != hipSuccess) return rc;
+        for (int64_t v0 = 0; v0 < c.V; v0 += step) {
+            const int64_t n = std::min(step, c.V - v0);
+            const bool first = v0 == 0, last = v0 + n == c.V;
+            if ((rc = piece(c.w, c.ldw, v0, n, c.D, room, false, stream, w)) != hipSuccess)
+                return rc;
+            const View dv = {dl, (int)s8};
+            if (c.M > 0) {
+                const DlogitEpi<E> epi = {{dl, s8, 1}, c.lse, weight, c.target, v0};
+                rc = lp::launch_product<E, true, true>(product(x, w, c.M, n, c.D), cl, epi, stream);
+                if (rc != hipSuccess) return rc;
+            }
+            if (c.dx && c.M > 0 && c.D > 0) {
+                const SumEpi<E> epi = {sum, d8, make_rows(c.dx, c.lddx), factor, first, last};
+                // the last piece may be shorter: its own contraction, the same cut
+                Cut cut = cx;
+                if (cut.splits > 1) cut.splits = (int)((n + cut.chunk - 1) / cut.chunk);
+                rc = lp::launch_product<E, true, false>(product(dv, w, c.M, c.D, n), cut, epi,
+                                                        stream);
+                if (rc != hipSuccess) return rc;
+            }
+            if (c.dw && c.D > 0) {
+                uint16_t* out = static_cast<uint16_t*>(c.dw) + v0 * c.lddw;
+                const SumEpi<E> epi = {nullptr, 0, make_rows(out, c.lddw), factor, 1, 1};
+                rc = lp::launch_product<E, false, false>(product(dv, x, n, c.D, c.M), cw, epi,
+                                                         stream);
+                if (rc != hipSuccess) return rc;
+            }
+        }
+        return hipSuccess;
+    }
+};
+
+}  // namespace
+
+hipError_t xent_forward(const XentCall& c, Arena& ar, hipStream_t stream) {
+    return c.dtype == kBF16 ? Xent<BF16>::forward(c, ar, stream)
+                            : Xent<F16>::forward(c, ar, stream);
+}
+
+hipError_t xent_backward(const XentGradCall& c, Arena& ar, hipStream_t stream) {
+    return c.dtype == kBF16 ? Xent<BF16>::backward(c, ar, stream)
+                            : Xent<F16>::backward(c, ar, stream);
+}
+
+}  // namespace layer
+}  // namespace pgemm

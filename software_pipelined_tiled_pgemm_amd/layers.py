@@ -13,6 +13,7 @@ from . import _lib
 from ._lib import PgemmError, lib
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+REDUCTIONS = {"none": 0, "mean": 1, "sum": 2}
 
 
 def _base():
@@ -260,3 +261,91 @@ def pffn_bwd(dy, x, w_in, w_out, gate_up, act="silu", dx_residual=None, needs=(T
                           ws, nws, h)
     _call(_invoke(dy, stream, run), "pffn_bwd")
     return dx, dw_in, dw_out
+
+
+def _reduction(reduction):
+    try:
+        return REDUCTIONS[reduction]
+    except (KeyError, TypeError):
+        raise ValueError("reduction must be one of %s, got %r"
+                         % (", ".join(REDUCTIONS), reduction)) from None
+
+
+def _flat(t, name, like, dtype, shape):
+    torch = _base()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda or t.get_device() != like.get_device():
+        raise ValueError("%s must be on the other tensors' device" % name)
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous tensor of shape %s" % (name, shape))
+
+
+def _xent_operands(x, w, target):
+    torch = _base()
+    dt = _dtype(x, "x")
+    ldx = _mat(x, "x", x)
+    ldw = _mat(w, "w", x, cols=x.shape[1])
+    _flat(target, "target", x, torch.int64, (x.shape[0],))
+    return dt, ldx, ldw
+
+
+def pxent(x, w, target, ignore_index=-100, reduction="mean", loss=None, lse=None, workspace=None,
+          stream=None):
+    """(loss, lse) of the softmax cross entropy of x [M,D] against the rows of
+    w [V,D] at target [M] (int64): loss is a float32 scalar tensor ("mean" over
+    the rows that are not ignored, "sum") or [M] ("none"), lse [M] the rows'
+    log-sum-exp, which pxent_bwd needs.  The logits are not kept."""
+    torch = _base()
+    dt, ldx, ldw = _xent_operands(x, w, target)
+    red = _reduction(reduction)
+    (M, D), V = x.shape, w.shape[0]
+    shape = (M,) if red == 0 else ()
+    if loss is None:
+        loss = _new(shape, torch.float32, x.device, stream)
+    _flat(loss, "loss", x, torch.float32, shape)
+    if lse is None:
+        lse = _new((M,), torch.float32, x.device, stream)
+    _flat(lse, "lse", x, torch.float32, (M,))
+    L = lib()
+
+    def run(h):
+        need = L.pxent_workspace_bytes(dt, x.data_ptr(), ldx, w.data_ptr(), ldw, red, M, V, D)
+        ws, nws, keep = _workspace(need, workspace, x, stream, "pxent")
+        return L.pxent(dt, x.data_ptr(), ldx, w.data_ptr(), ldw, target.data_ptr(),
+                       int(ignore_index), red, loss.data_ptr(), lse.data_ptr(), M, V, D, ws, nws, h)
+    _call(_invoke(x, stream, run), "pxent")
+    return loss, lse
+
+
+def pxent_bwd(x, w, target, lse, dloss=None, ignore_index=-100, reduction="mean",
+              needs=(True, True), dx=None, dw=None, workspace=None, stream=None):
+    """(dx, dw) of pxent, called with the same x, w, target, ignore_index and
+    reduction, for the gradient dloss of its loss (a float32 tensor of the
+    loss's shape; None: 1).  `needs` says which are computed."""
+    torch = _base()
+    dt, ldx, ldw = _xent_operands(x, w, target)
+    red = _reduction(reduction)
+    (M, D), V = x.shape, w.shape[0]
+    _flat(lse, "lse", x, torch.float32, (M,))
+    if dloss is not None:
+        _flat(dloss, "dloss", x, torch.float32, (M,) if red == 0 else ())
+    lddx = lddw = 0
+    if needs[0]:
+        dx, lddx = _out(dx, "dx", x, (M, D), stream)
+    if needs[1]:
+        dw, lddw = _out(dw, "dw", x, (V, D), stream)
+    dx, dw = (t if n else None for t, n in zip((dx, dw), needs))
+    L = lib()
+
+    def run(h):
+        need = L.pxent_bwd_workspace_bytes(dt, x.data_ptr(), ldx, w.data_ptr(), ldw, M, V, D,
+                                           *map(int, map(bool, needs)))
+        ws, nws, keep = _workspace(need, workspace, x, stream, "pxent_bwd")
+        return L.pxent_bwd(dt, x.data_ptr(), ldx, w.data_ptr(), ldw, target.data_ptr(),
+                           int(ignore_index), red, lse.data_ptr(), _ptr(dloss), _ptr(dx), lddx,
+                           _ptr(dw), lddw, M, V, D, ws, nws, h)
+    _call(_invoke(x, stream, run), "pxent_bwd")
+    return dx, dw

@@ -250,3 +250,137 @@ def test_ffn_strides(shape, pad, offset, dtype):
     h = pg.pffn_bwd(dy.contiguous(), x.contiguous(), wi.contiguous(), wo.contiguous(), gu2)
     for u, v in zip(g, h):
         assert torch.equal(u, v)
+
+
+def xent_exact(X, W, t, V, ignore=-100):
+    L = X @ W.T
+    top = L.max(1, keepdims=True)
+    lse = top[:, 0] + np.log(np.exp(L - top).sum(1))
+    valid = t != ignore
+    at = np.where(valid, t, 0)
+    loss = np.where(valid, lse - L[np.arange(len(t)), at], 0.0)
+    p = np.exp(L - lse[:, None])
+    p[np.arange(len(t)), at] -= 1.0
+    return L, lse, loss, p * valid[:, None], valid
+
+
+# (M, D, V): single values, odd vocabularies, tile edges, several pieces of the
+# backward pass (V > 1024 only with many rows: see below), a long row
+XENT = [(1, 1, 1), (1, 64, 1000), (7, 40, 257), (130, 72, 511), (33, 100, 1025), (300, 264, 640),
+        (5, 1024, 5003), (257, 37, 300)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("reduction", ["mean", "sum", "none"])
+@pytest.mark.parametrize("shape", XENT)
+def test_xent(shape, reduction, dtype):
+    M, D, V = shape
+    say("xent", shape, reduction, dtype)
+    x = rand((M, D), dtype, 51)
+    w = rand((V, D), dtype, 52, std=2 * D ** -0.5)
+    rng = np.random.default_rng(53)
+    t = rng.integers(0, V, size=M)
+    t[rng.random(M) < 0.3] = -100
+    target = torch.from_numpy(t).cuda()
+    loss, lse = pg.pxent(x, w, target, reduction=reduction)
+    X, W = f64(x), f64(w)
+    L, LSE, EACH, P, valid = xent_exact(X, W, t, V)
+    S = np.abs(X) @ np.abs(W).T
+    # a logit's fp32 accumulation, exp and log of fp32 values near |lse|
+    e = (D + 8) * 2.0 ** -23 * S.max(1) + 16 * 2.0 ** -23 * (np.abs(LSE) + 1)
+    assert (np.abs(f64(lse) - LSE) <= e).all()
+    n = max(1, int(valid.sum()))
+    e2 = 2 * e * valid
+    if reduction == "none":
+        assert (np.abs(f64(loss) - EACH) <= e2 + 2.0 ** -23 * np.abs(EACH)).all()
+    else:
+        k = n if reduction == "mean" else 1
+        assert abs(f64(loss) - EACH.sum() / k) <= (e2.sum() + 2.0 ** -22 * np.abs(EACH).sum()) / k
+
+    if reduction == "none":
+        g = rng.normal(0, 1, size=M).astype(np.float32)
+        g[::3] *= 1e-3
+        dloss = torch.from_numpy(g).cuda()
+        G = g.astype(np.float64)
+    else:
+        dloss = torch.tensor(0.37, device="cuda")
+        G = np.full(M, float(np.float32(0.37)) / (n if reduction == "mean" else 1))
+    dx, dw = pg.pxent_bwd(x, w, target, lse, dloss=dloss, reduction=reduction)
+    DL = P * G[:, None]
+    # dl: one rounding, and the absolute error of the logit and lse in the exponent
+    q = np.exp(L - LSE[:, None]) * valid[:, None] * np.abs(G)[:, None]
+    u = UNIT[dtype]
+    top = np.abs(G).max()
+    mag = np.abs(DL) + q * (2 * e[:, None] + 8 * 2.0 ** -23 * (1 + np.abs(L - LSE[:, None]))) / u
+    if dtype is torch.float16:  # subnormals of the scaled dl
+        mag = mag + valid[:, None] * top * 2.0 ** -15 * 2.0 ** -24 / u
+    assert_near(dx, DL @ W, mag @ np.abs(W), dtype, V, 1, "dx")
+    assert_near(dw, DL.T @ X, mag.T @ np.abs(X), dtype, M, 1, "dw")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_xent_pieces_and_strides(dtype):
+    """Rows enough that the backward pass takes the vocabulary in pieces, the
+    last one shorter; strided and misaligned operands give the same bits."""
+    M, D, V = 140000, 24, 4500
+    say("xent pieces", M, D, V, dtype)
+    x = rand((M, D), dtype, 61)
+    w = rand((V, D), dtype, 62, std=2 * D ** -0.5)
+    target = torch.from_numpy(np.random.default_rng(63).integers(0, V, size=M)).cuda()
+    loss, lse = pg.pxent(x, w, target)
+    dx, dw = pg.pxent_bwd(x, w, target, lse, reduction="sum")
+    X, W, T = x.double(), w.double(), target
+    L = X @ W.t()
+    LSE = torch.logsumexp(L, 1)
+    each = LSE - L[torch.arange(M, device="cuda"), T]
+    assert abs(float(loss) - float(each.mean())) <= 1e-5
+    P = torch.exp(L - LSE[:, None])
+    P[torch.arange(M, device="cuda"), T] -= 1.0
+    u = UNIT[dtype]
+    A = P.abs() + 2.0 ** -30
+    DX, DW = P @ W, P.t() @ X
+    ex = 1.5 * u * DX.abs() + (1.5 * u + (V + 64) * 2.0 ** -23) * (A @ W.abs()) + 1e-6
+    ew = 1.5 * u * DW.abs() + (1.5 * u + (M + 64) * 2.0 ** -23) * (A.t() @ X.abs()) + 1e-6
+    assert bool(((dx.double() - DX).abs() <= ex).all())
+    assert bool(((dw.double() - DW).abs() <= ew).all())
+
+    xs = rand((M, D), dtype, 61, pitch=D + 3, offset=1)
+    ws = rand((V, D), dtype, 62, std=2 * D ** -0.5, pitch=D + 5, offset=3)
+    loss2, lse2 = pg.pxent(xs, ws, target)
+    assert torch.equal(loss, loss2) and torch.equal(lse, lse2)
+    dx2, dw2 = pg.pxent_bwd(xs, ws, target, lse, reduction="sum")
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+
+
+def test_xent_masks():
+    """All rows ignored; targets outside the vocabulary; ignored rows with
+    infinite and NaN values in x."""
+    M, D, V = 70, 64, 300
+    x = rand((M, D), torch.bfloat16, 71)
+    w = rand((V, D), torch.bfloat16, 72, std=0.2)
+    t = torch.full((M,), -100, device="cuda")
+    loss, lse = pg.pxent(x, w, t)
+    dx, dw = pg.pxent_bwd(x, w, t, lse)
+    assert float(loss) == 0.0 and not bool(dx.any()) and not bool(dw.any())
+    assert not bool(pg.pxent(x, w, t, reduction="none")[0].any())
+
+    t = torch.arange(M, device="cuda")
+    t[5], t[9] = V, -1
+    loss, lse = pg.pxent(x, w, t, reduction="none")
+    bad = torch.isnan(loss)
+    assert bad[5] and bad[9] and int(bad.sum()) == 2
+    dx, dw = pg.pxent_bwd(x, w, t, lse, reduction="none")
+    rows = torch.isnan(dx).all(1)
+    assert rows[5] and rows[9] and int(torch.isnan(dx).any(1).sum()) == 2
+    assert int(pg.pxent(x, w, t, ignore_index=V, reduction="none")[0].isnan().sum()) == 1
+
+    clean = torch.arange(M, device="cuda")
+    clean[[3, 40]] = -100
+    y = x.clone()
+    y[3], y[40] = float("inf"), float("nan")
+    loss, lse = pg.pxent(y, w, clean)
+    ref, _ = pg.pxent(x, w, clean)
+    assert torch.equal(loss, ref)
+    dx, _ = pg.pxent_bwd(y, w, clean, lse, needs=(True, False))
+    ref, _ = pg.pxent_bwd(x, w, clean, pg.pxent(x, w, clean)[1], needs=(True, False))
+    assert torch.equal(dx, ref) and not bool(dx[3].any()) and not bool(dx[40].any())
