@@ -432,6 +432,28 @@ int pxent_bwd(int dtype, const void* x, int64_t ldx, const void* w, int64_t ldw,
 int64_t pxent_bwd_workspace_bytes(int dtype, const void* x, int64_t ldx, const void* w, int64_t ldw,
                                   int64_t M, int64_t V, int64_t D, int need_dx, int need_dw);
 
+/*
+ * Gradient clipping by the global norm: norm = sqrt of the sum of the squares
+ * of every element of every tensor, and each tensor times
+ * min(1, max_norm / (norm + 1e-6)), to outs[i], or in place where outs is NULL
+ * or outs[i] is grads[i].
+ *   grads, outs, sizes (elements), dtypes (PGEMM_F16, PGEMM_BF16, PGEMM_F32):
+ *   host arrays of `count`, read before the call returns; norm: one device
+ *   float, the norm before clipping.  Tensors are contiguous, of any
+ *   alignment their elements allow, and may be empty.
+ *   workspace: pclip_grad_norm_workspace_bytes(count) bytes.
+ * No value is brought to the host: the factor stays on the device.  The
+ * squares are summed in fp64 (8 fp16 ones at a time in fp32) in a fixed order.
+ * A norm that is NaN makes every output NaN; an infinite one makes the
+ * factor 0.  PGEMM_EINVAL: a negative size, a negative or NaN max_norm, a
+ * written range that overlaps another; PGEMM_EUNSUPPORTED: unknown dtype,
+ * misaligned elements, more than 2^40 elements in a tensor, 2^20 tensors.
+ */
+int pclip_grad_norm(const void* const* grads, void* const* outs, const int64_t* sizes,
+                    const int* dtypes, int64_t count, float max_norm, float* norm, void* workspace,
+                    int64_t workspace_bytes, pgemm_stream_t stream);
+int64_t pclip_grad_norm_workspace_bytes(int64_t count);
+
 /* Static English text for a status code (never NULL). */
 const char* pgemm_status_string(int status);
 

@@ -20,7 +20,7 @@ __all__ = [
     "pstream_add", "pstream_add_blocked", "pstream_add_scalar", "preduce_sum_f32",
     "pgemm_test_fill_f32", "pgemm_test_iota_f32",
     "plinear", "plinear_bwd", "pffn", "pffn_bwd",
-    "pxent", "pxent_bwd",
+    "pxent", "pxent_bwd", "pclip_grad_norm",
     "lib", "status_string", "PgemmError",
     "PGEMM_OK", "PGEMM_EINVAL", "PGEMM_EUNSUPPORTED", "PGEMM_EHIP", "PGEMM_ESCRATCH",
     "STATIC_SCRATCH_BYTES",
@@ -321,5 +321,5 @@ def pgemm_test_iota_f32(n, device="cuda", out=None, stream=None):
     return o
 
 
-from .layers import (pffn, pffn_bwd, plinear, plinear_bwd,  # noqa: E402  (uses the helpers above)
-                     pxent, pxent_bwd)
+from .layers import (pclip_grad_norm, pffn, pffn_bwd, plinear,  # noqa: E402  (uses the helpers above)
+                     plinear_bwd, pxent, pxent_bwd)

@@ -66,6 +66,8 @@ def _declare(lib):
         "pxent_bwd": (i32, [i32, p, i64, p, i64, p, i64, i32, p, p, p, i64, p, i64, i64, i64, i64,
                             p, i64, p]),
         "pxent_bwd_workspace_bytes": (i64, [i32, p, i64, p, i64, i64, i64, i64, i32, i32]),
+        "pclip_grad_norm": (i32, [p, p, p, p, i64, ctypes.c_float, p, p, i64, p]),
+        "pclip_grad_norm_workspace_bytes": (i64, [i64]),
         "pgemm_status_string": (ctypes.c_char_p, [i32]),
         "pgemm_last_hip_error": (i32, []),
         "pgemm_version": (i32, []),

@@ -3,6 +3,11 @@
 #include <stdint.h>
 
 #include "../../include/pgemm.h"
+#include <algorithm>
+#include <memory>
+#include <new>
+
+#include "clip.h"
 #include "ffn.h"
 #include "linear.h"
 #include "xent.h"
@@ -113,6 +118,14 @@ int check_ffn(int dtype, int act, int64_t M, int64_t D, int64_t F, int64_t N) {
     if (rc != PGEMM_OK) return rc;
     return F >= kMaxCols / 2 ? PGEMM_EUNSUPPORTED : PGEMM_OK;
 }
+
+// Gradient clipping.
+constexpr int64_t kMaxTensors = (int64_t)1 << 20;
+constexpr int64_t kMaxTensorElems = (int64_t)1 << 40;
+struct Range {
+    uintptr_t begin, end;
+    bool writes;
+};
 
 int check_xent(int dtype, int reduction, int64_t M, int64_t V, int64_t D) {
     if (M < 0 || V < 1 || D < 0) return PGEMM_EINVAL;
@@ -461,6 +474,57 @@ int64_t pxent_bwd_workspace_bytes(int dtype, const void* x, int64_t ldx, const v
     Arena dry = {nullptr, 0};
     const hipError_t e = xent_backward(c, dry, nullptr);
     return e == hipSuccess ? dry.used : hip_status(e);
+}
+
+int64_t pclip_grad_norm_workspace_bytes(int64_t count) {
+    if (count < 0) return PGEMM_EINVAL;
+    return clip_workspace_bytes(count);
+}
+
+int pclip_grad_norm(const void* const* grads, void* const* outs, const int64_t* sizes,
+                    const int* dtypes, int64_t count, float max_norm, float* norm, void* workspace,
+                    int64_t workspace_bytes, pgemm_stream_t stream) {
+    if (count < 0 || !norm || !(max_norm >= 0.0f)) return PGEMM_EINVAL;
+    if (count > 0 && (!grads || !sizes || !dtypes)) return PGEMM_EINVAL;
+    if (count > kMaxTensors || reinterpret_cast<uintptr_t>(norm) % 4) return PGEMM_EUNSUPPORTED;
+    const int64_t need = clip_workspace_bytes(count);
+    if (!workspace || workspace_bytes < need) return PGEMM_EINVAL;
+    if (!aligned16(workspace)) return PGEMM_EUNSUPPORTED;
+    // Every byte range of the call, to be sorted by address: written ranges
+    // (outputs, norm, workspace) may meet no other, but for an output that is
+    // its own gradient, which counts once.
+    std::unique_ptr<Range[]> ranges(new (std::nothrow) Range[2 * count + 2]);
+    if (!ranges) return hip_status(hipErrorOutOfMemory);
+    int64_t n = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        const int64_t size = sizes[i];
+        if (size < 0) return PGEMM_EINVAL;
+        if (dtypes[i] != PGEMM_F16 && dtypes[i] != PGEMM_BF16 && dtypes[i] != PGEMM_F32)
+            return PGEMM_EUNSUPPORTED;
+        if (size == 0) continue;
+        if (size > kMaxTensorElems) return PGEMM_EUNSUPPORTED;
+        const void* in = grads[i];
+        const void* out = outs ? outs[i] : in;
+        if (!in || !out) return PGEMM_EINVAL;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(in), b = reinterpret_cast<uintptr_t>(out);
+        const int bytes = dtypes[i] == PGEMM_F32 ? 4 : 2;
+        if (a % bytes || b % bytes) return PGEMM_EUNSUPPORTED;
+        if (a != b) ranges[n++] = {a, a + (uintptr_t)(size * bytes), false};
+        ranges[n++] = {b, b + (uintptr_t)(size * bytes), true};
+    }
+    const uintptr_t nb = reinterpret_cast<uintptr_t>(norm), wb = reinterpret_cast<uintptr_t>(workspace);
+    ranges[n++] = {nb, nb + 4, true};
+    ranges[n++] = {wb, wb + (uintptr_t)need, true};
+    std::sort(ranges.get(), ranges.get() + n,
+              [](const Range& u, const Range& v) { return u.begin < v.begin; });
+    uintptr_t any = 0, written = 0;  // furthest ends so far
+    for (int64_t i = 0; i < n; ++i) {
+        if (ranges[i].begin < (ranges[i].writes ? any : written)) return PGEMM_EINVAL;
+        any = std::max(any, ranges[i].end);
+        if (ranges[i].writes) written = std::max(written, ranges[i].end);
+    }
+    const ClipCall c = {grads, outs, sizes, dtypes, count, (double)max_norm, norm};
+    return hip_status(clip(c, workspace, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -349,3 +349,58 @@ def pxent_bwd(x, w, target, lse, dloss=None, ignore_index=-100, reduction="mean"
                            _ptr(dw), lddw, M, V, D, ws, nws, h)
     _call(_invoke(x, stream, run), "pxent_bwd")
     return dx, dw
+
+
+def pclip_grad_norm(tensors, max_norm, out=None, norm=None, workspace=None, stream=None):
+    """Scales the tensors (contiguous; float16, bfloat16 or float32, mixed as
+    they come) by min(1, max_norm / (norm + 1e-6)), norm being that of all
+    their elements together: in place, or into the list `out`.  Returns the
+    norm before clipping as a float32 scalar tensor on the device."""
+    import ctypes
+    torch = _base()
+    tensors = list(tensors)
+    if not tensors:
+        raise ValueError("tensors must not be empty")
+    first = tensors[0]
+    codes = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+    kinds = []
+
+    def check(t, name):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be torch.Tensors" % name)
+        if not t.is_cuda or t.get_device() != index:
+            raise ValueError("%s must be on one HIP device" % name)
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+        code = codes.get(t.dtype)
+        if code is None:
+            raise TypeError("%s must be float16, bfloat16 or float32, got %s" % (name, t.dtype))
+        return code
+    index = first.get_device() if isinstance(first, torch.Tensor) and first.is_cuda else -1
+    for t in tensors:
+        kinds.append(check(t, "tensors"))
+    n = len(tensors)
+    outs = None
+    if out is not None:
+        out = list(out)
+        if len(out) != n:
+            raise ValueError("out must have %d tensors" % n)
+        for t, o, k in zip(tensors, out, kinds):
+            if check(o, "out") != k or o.numel() != t.numel():
+                raise ValueError("out must have the tensors' types and sizes")
+        outs = (ctypes.c_void_p * n)(*[o.data_ptr() for o in out])
+    if norm is None:
+        norm = _new((), torch.float32, first.device, stream)
+    _flat(norm, "norm", first, torch.float32, ())
+    grads = (ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors])
+    sizes = (ctypes.c_int64 * n)(*[t.numel() for t in tensors])
+    dtypes = (ctypes.c_int * n)(*kinds)
+    L = lib()
+
+    def run(h):
+        need = L.pclip_grad_norm_workspace_bytes(n)
+        ws, nws, keep = _workspace(need, workspace, first, stream, "pclip_grad_norm")
+        return L.pclip_grad_norm(grads, outs, sizes, dtypes, n, float(max_norm), norm.data_ptr(),
+                                 ws, nws, h)
+    _call(_invoke(first, stream, run), "pclip_grad_norm")
+    return norm

@@ -384,3 +384,60 @@ def test_xent_masks():
     dx, _ = pg.pxent_bwd(y, w, clean, lse, needs=(True, False))
     ref, _ = pg.pxent_bwd(x, w, clean, pg.pxent(x, w, clean)[1], needs=(True, False))
     assert torch.equal(dx, ref) and not bool(dx[3].any()) and not bool(dx[40].any())
+
+
+CLIP_KINDS = [[torch.float32], [torch.float16], [torch.bfloat16],
+              [torch.float32, torch.float16, torch.bfloat16]]
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("kinds", CLIP_KINDS)
+@pytest.mark.parametrize("sizes", [[1], [7, 0, 4096, 33], [5] * 300, [40000, 1 << 20, 3],
+                                   [17000001, 32768, 32769, 9]])
+def test_clip(sizes, kinds, inplace):
+    say("clip", len(sizes), sum(sizes), kinds, inplace)
+    rng = np.random.default_rng(81)
+    grads = []
+    for i, n in enumerate(sizes):
+        k = kinds[i % len(kinds)]
+        v = torch.from_numpy(rng.normal(0, 1, size=n).astype(np.float32)).to(k)
+        off = i % 5  # elements off a 16-byte boundary
+        buf = torch.empty(n + 8, dtype=k, device="cuda")
+        t = buf[off:off + n]
+        t.copy_(v)
+        grads.append(t)
+    exact = [f64(t) for t in grads]
+    norm = np.sqrt(sum((e * e).sum() for e in exact))
+    for factor in (0.3, 2.0):
+        out = None if inplace else [torch.full_like(t, float("nan")) for t in grads]
+        src = [t.clone() for t in grads] if inplace else grads
+        got = pg.pclip_grad_norm(src, factor * norm, out=out)
+        # fp64 sums (8 fp16 squares in fp32 first), one rounding to fp32
+        assert abs(f64(got) - norm) <= 2.0 ** -22 * norm
+        c = min(1.0, float(np.float32(factor * norm)) / (norm + 1e-6))
+        for e, o in zip(exact, src if inplace else out):
+            u = UNIT.get(o.dtype, 2.0 ** -24)
+            tiny = TINY.get(o.dtype, 2.0 ** -126)
+            # the factor's and the product's fp32 roundings, and the type's
+            assert (np.abs(f64(o) - e * c) <= (u + 2.0 ** -22) * np.abs(e * c) + tiny).all()
+            if factor > 1:
+                assert np.array_equal(f64(o), e)
+
+
+def test_clip_extremes():
+    """Squares beyond fp32's range; NaN and infinite gradients."""
+    big = torch.full((1000,), 1e30, dtype=torch.bfloat16, device="cuda")
+    small = torch.full((1000,), 1e-30, device="cuda")
+    e = f64(big)
+    n = pg.pclip_grad_norm([big.clone()], float("inf"))
+    assert abs(f64(n) - np.sqrt((e * e).sum())) <= 1e-6 * f64(n)
+    n = pg.pclip_grad_norm([small.clone()], 1.0)
+    assert abs(f64(n) - f64(small)[0] * np.sqrt(1000)) <= 1e-6 * f64(n)
+    x = [torch.ones(100, device="cuda"), torch.ones(50, dtype=torch.float16, device="cuda")]
+    x[1][7] = float("nan")
+    n = pg.pclip_grad_norm(x, 1.0)
+    assert bool(torch.isnan(n)) and all(bool(torch.isnan(t).all()) for t in x)
+    y = [torch.ones(100, device="cuda")]
+    y[0][3] = float("inf")
+    n = pg.pclip_grad_norm(y, 1.0)
+    assert bool(torch.isinf(n)) and int((y[0] == 0).sum()) == 99
