@@ -27,45 +27,72 @@ namespace {
 template <class E>
 struct GluEpi {
     static constexpr lp::EpiKind kind = lp::kPaired;
+    static constexpr int kAhead = 1;
     Rows h;  // padded rows: whole chunks
     Rows gate, up;
     int act;
-    __device__ __forceinline__ void operator()(int row, int col, int nv, float (&g)[8],
-                                               float (&u)[8]) const {
-        if (gate) {
-            store8<E>(gate, row, col, nv, g);
-            store8<E>(up, row, col, nv, u);
-        }
-        // past F both are 0, and so is h
+    __device__ __forceinline__ GluEpi from(int64_t r) const {
+        return {h.from(r), gate.from(r), up.from(r), act};
+    }
+    __device__ __forceinline__ lp::Nothing column(int, int) const { return {}; }
+    __device__ __forceinline__ lp::Nothing load(int, int, int) const { return {}; }
+    template <class Run>
+    __device__ __forceinline__ void with(Run&& run) const {
+        with_act(act, [&](auto a) __attribute__((always_inline)) {
+            run([&](int row, int col, int nv, float(&g)[8], float(&u)[8], lp::Nothing, lp::Nothing)
+                    __attribute__((always_inline)) {
+                if (gate) {
+                    store8<E>(gate, row, col, nv, g);
+                    store8<E>(up, row, col, nv, u);
+                }
+                // past F both are 0, and so is h
 #pragma unroll
-        for (int q = 0; q < 8; ++q) u[q] *= act_value(act, g[q]);
-        store8<E>(h, row, col, 8, u);
+                for (int q = 0; q < 8; ++q) u[q] *= decltype(a)::value(g[q]);
+                store8<E>(h, row, col, 8, u);
+            });
+        });
     }
 };
 
 template <class E>
 struct GluGradEpi {
     static constexpr lp::EpiKind kind = lp::kPlain;
+    static constexpr int kAhead = 4;
     Rows gate, up;       // as the forward pass kept them
     Rows h, dgate, dup;  // padded rows: whole chunks, zeros past F
     int act;
-    __device__ __forceinline__ void operator()(int row, int col, int nv, float (&d)[8]) const {
-        float g[8], u[8];
-        load8<E>(gate, row, col, nv, g);
-        load8<E>(up, row, col, nv, u);
+    __device__ __forceinline__ GluGradEpi from(int64_t r) const {
+        return {gate.from(r), up.from(r), h.from(r), dgate.from(r), dup.from(r), act};
+    }
+    struct Kept {
+        u4_t g, u;
+    };
+    __device__ __forceinline__ lp::Nothing column(int, int) const { return {}; }
+    __device__ __forceinline__ Kept load(int row, int col, int nv) const {
+        return {load8_bits(gate, row, col, nv), load8_bits(up, row, col, nv)};
+    }
+    template <class Run>
+    __device__ __forceinline__ void with(Run&& run) const {
+        with_act(act, [&](auto a) __attribute__((always_inline)) {
+            run([&](int row, int col, int nv, float(&d)[8], lp::Nothing, const Kept& k)
+                    __attribute__((always_inline)) {
+                float g[8], u[8], s[8];
+                unpack8<E>(k.g, g);
+                unpack8<E>(k.u, u);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            float a;
-            const float s = act_grad(act, g[q], a);
-            g[q] = d[q] * u[q] * s;
-            u[q] *= a;   // h
-            d[q] *= a;   // du
-        }
-        if (h) store8<E>(h, row, col, 8, u);
-        if (dgate) {
-            store8<E>(dgate, row, col, 8, g);
-            store8<E>(dup, row, col, 8, d);
-        }
+                for (int q = 0; q < 8; ++q) {
+                    float v;
+                    s[q] = decltype(a)::grad(g[q], v) * d[q] * u[q];  // dg
+                    u[q] *= v;                                        // h
+                    d[q] *= v;                                        // du
+                }
+                if (h) store8<E>(h, row, col, 8, u);
+                if (dgate) {
+                    store8<E>(dgate, row, col, 8, s);
+                    store8<E>(dup, row, col, 8, d);
+                }
+            });
+        });
     }
 };
 
@@ -106,7 +133,7 @@ struct Ffn {
             g.pair_shift = (int)f8;
             if (!ar.dry()) {
                 uint16_t* gu = static_cast<uint16_t*>(c.gate_up);
-                const GluEpi<E> epi = {{h, f8, 1},
+                const GluEpi<E> epi = {{h, (int)f8},
                                        make_rows(gu, c.ldgu),
                                        make_rows(gu ? gu + c.F : nullptr, c.ldgu),
                                        c.act};
@@ -141,8 +168,8 @@ struct Ffn {
             if (!ar.dry()) {
                 const uint16_t* gu = static_cast<const uint16_t*>(c.gate_up);
                 const GluGradEpi<E> epi = {make_rows(gu, c.ldgu), make_rows(gu + c.F, c.ldgu),
-                                           {h, f8, 1},            {d, 2 * f8, 1},
-                                           {d ? d + f8 : d, 2 * f8, 1}, c.act};
+                                           {h, (int)f8}, {d, (int)(2 * f8)},
+                                           {d ? d + f8 : d, (int)(2 * f8)}, c.act};
                 rc = lp::launch_product<E, true, true>(g, cut, epi, stream);
                 if (rc != hipSuccess) return rc;
             }

@@ -56,9 +56,9 @@ struct BF16 {
 // exp2 and reciprocal are the hardware's (1 ulp), so an activation costs two
 // quarter-rate instructions and a few ordinary ones per value.
 
-__device__ __forceinline__ float exp_fast(float x) {
-    return __builtin_amdgcn_exp2f(x * 1.4426950408889634f);
-}
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
 __device__ __forceinline__ float sigmoid(float x) {
     return __builtin_amdgcn_rcpf(1.0f + exp_fast(-x));
@@ -83,111 +83,142 @@ __device__ __forceinline__ void normal_cdf_pdf(float z, float& cdf, float& pdf) 
 constexpr float kGeluA = 1.5957691216f;  // 2 sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
 
-__device__ __forceinline__ float act_value(int act, float z) {
-    switch (act) {
-        case PGEMM_ACT_RELU:
-            return z > 0.0f ? z : (z != z ? z : 0.0f);
-        case PGEMM_ACT_GELU: {
-            float c, d;
-            normal_cdf_pdf(z, c, d);
-            return z * c;
-        }
-        case PGEMM_ACT_GELU_TANH:  // 0.5 (1 + tanh u) = sigmoid(2 u)
-            return z * sigmoid(kGeluA * (z + kGeluB * z * z * z));
-        case PGEMM_ACT_SILU:
-            return z * sigmoid(z);
-        default:
-            return z;
-    }
+__device__ __forceinline__ float relu_of(float z) {
+    return z > 0.0f ? z : (z != z ? z : 0.0f);
 }
+__device__ __forceinline__ float gelu_of(float z) {
+    float c, d;
+    normal_cdf_pdf(z, c, d);
+    return z * c;
+}
+// 0.5 (1 + tanh u) = 1 / (1 + exp(-2 u)); the constants carry log2 e.
+__device__ __forceinline__ float gelu_tanh_of(float z) {
+    const float k = fmaf(z * z, -kGeluA * kGeluB * kLog2e, -kGeluA * kLog2e);
+    return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * k));
+}
+__device__ __forceinline__ float silu_of(float z) { return z * sigmoid(z); }
 
 // The derivative, and with it the value (for the gated product, which needs
 // both).  Far out the derivative of the tanh form is 0 or 1 to the last bit;
 // its polynomial is evaluated at z held to +-30, so that it stays finite.
-__device__ __forceinline__ float act_grad(int act, float z, float& value) {
+__device__ __forceinline__ float relu_grad(float z, float& value) {
+    value = relu_of(z);
+    return z > 0.0f ? 1.0f : 0.0f;
+}
+__device__ __forceinline__ float gelu_grad(float z, float& value) {
+    float c, d;
+    normal_cdf_pdf(z, c, d);
+    value = z * c;
+    return d > 0.0f ? fmaf(z, d, c) : c;
+}
+__device__ __forceinline__ float gelu_tanh_grad(float z, float& value) {
+    const float h = fminf(fmaxf(z, -30.0f), 30.0f);
+    const float s = sigmoid(kGeluA * (h + kGeluB * h * h * h));
+    value = z * s;
+    return s + h * s * (1.0f - s) * kGeluA * (1.0f + 3.0f * kGeluB * h * h);
+}
+__device__ __forceinline__ float silu_grad(float z, float& value) {
+    const float s = sigmoid(z);
+    value = z * s;
+    return s * fmaf(z, 1.0f - s, 1.0f);
+}
+
+// An activation as a compile-time choice.
+template <int ACT>
+struct Act {
+    __device__ static __forceinline__ float value(float z) {
+        if constexpr (ACT == PGEMM_ACT_RELU) return relu_of(z);
+        if constexpr (ACT == PGEMM_ACT_GELU) return gelu_of(z);
+        if constexpr (ACT == PGEMM_ACT_GELU_TANH) return gelu_tanh_of(z);
+        if constexpr (ACT == PGEMM_ACT_SILU) return silu_of(z);
+        return z;
+    }
+    __device__ static __forceinline__ float grad(float z, float& value) {
+        if constexpr (ACT == PGEMM_ACT_RELU) return relu_grad(z, value);
+        if constexpr (ACT == PGEMM_ACT_GELU) return gelu_grad(z, value);
+        if constexpr (ACT == PGEMM_ACT_GELU_TANH) return gelu_tanh_grad(z, value);
+        if constexpr (ACT == PGEMM_ACT_SILU) return silu_grad(z, value);
+        value = z;
+        return 1.0f;
+    }
+};
+
+// run(Act<act>{}): one uniform branch.
+template <class Run>
+__device__ __forceinline__ void with_act(int act, Run&& run) {
     switch (act) {
-        case PGEMM_ACT_RELU:
-            value = z > 0.0f ? z : (z != z ? z : 0.0f);
-            return z > 0.0f ? 1.0f : 0.0f;
-        case PGEMM_ACT_GELU: {
-            float c, d;
-            normal_cdf_pdf(z, c, d);
-            value = z * c;
-            return d > 0.0f ? c + z * d : c;
-        }
-        case PGEMM_ACT_GELU_TANH: {
-            const float h = fminf(fmaxf(z, -30.0f), 30.0f);
-            const float s = sigmoid(kGeluA * (h + kGeluB * h * h * h));
-            value = z * s;
-            return s + h * s * (1.0f - s) * kGeluA * (1.0f + 3.0f * kGeluB * h * h);
-        }
-        case PGEMM_ACT_SILU: {
-            const float s = sigmoid(z);
-            value = z * s;
-            return s * (1.0f + z * (1.0f - s));
-        }
-        default:
-            value = z;
-            return 1.0f;
+        case PGEMM_ACT_RELU: run(Act<PGEMM_ACT_RELU>{}); break;
+        case PGEMM_ACT_GELU: run(Act<PGEMM_ACT_GELU>{}); break;
+        case PGEMM_ACT_GELU_TANH: run(Act<PGEMM_ACT_GELU_TANH>{}); break;
+        case PGEMM_ACT_SILU: run(Act<PGEMM_ACT_SILU>{}); break;
+        default: run(Act<PGEMM_ACT_NONE>{}); break;
     }
 }
 
 // ---- rows of 16-bit values ---------------------------------------------------
 // A row-major matrix of 16-bit values: 8 consecutive values of a row at a
-// time.  vec: the pointer is 16-byte aligned and ld a multiple of 8, so whole
-// chunks are single 16-byte accesses; otherwise, and at the right edge
-// (nv < 8), values move one by one.
+// time, as one 16-byte access from any 2-byte boundary (the compiler's
+// unaligned global access; an aligned one where `vec` says that the pointer
+// is 16-byte aligned and ld a multiple of 8), one by one at the right edge
+// (nv < 8).
 struct Rows {
     uint16_t* ptr;
-    int64_t ld;
-    int vec;
+    int ld;  // below 2^22
     __host__ __device__ explicit operator bool() const { return ptr != nullptr; }
+    // The same matrix from row r on.  Kernels address the rows of a tile (at
+    // most 256) from its first one: a uniform 64-bit base and a 32-bit offset.
+    __device__ __forceinline__ Rows from(int64_t r) const {
+        return {ptr ? ptr + r * ld : ptr, ld};
+    }
 };
 
 inline Rows make_rows(const void* p, int64_t ld) {
-    const bool vec = p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0;
-    return {static_cast<uint16_t*>(const_cast<void*>(p)), ld, vec};
+    return {static_cast<uint16_t*>(const_cast<void*>(p)), (int)ld};
 }
 
 typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
 
 template <class E>
-__device__ __forceinline__ void load8(const Rows& m, int64_t row, int64_t col, int nv, float (&v)[8]) {
-    const uint16_t* p = m.ptr + row * m.ld + col;
-    if (m.vec && nv == 8) {
-        const u4_t w = *reinterpret_cast<const u4_t*>(p);
+__device__ __forceinline__ void unpack8(const u4_t& w, float (&v)[8]) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            v[2 * q] = E::get((uint16_t)w[q]);
-            v[2 * q + 1] = E::get((uint16_t)(w[q] >> 16));
-        }
-    } else {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = q < nv ? E::get(p[q]) : 0.0f;
+    for (int q = 0; q < 4; ++q) {
+        v[2 * q] = E::get((uint16_t)w[q]);
+        v[2 * q + 1] = E::get((uint16_t)(w[q] >> 16));
     }
 }
 
+// The bits of 8 values, zeros from nv on; row < 256.
+__device__ __forceinline__ u4_t load8_bits(const Rows& m, int row, int col, int nv) {
+    const uint16_t* p = m.ptr + (uint32_t)(row * m.ld + col);
+    u4_t w = {};
+    if (nv == 8) {
+        __builtin_memcpy(&w, p, 16);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 7; ++q)
+            if (q < nv) w[q >> 1] |= (uint32_t)p[q] << (16 * (q & 1));
+    }
+    return w;
+}
+
 template <class E>
-__device__ __forceinline__ void store8(const Rows& m, int64_t row, int64_t col, int nv,
+__device__ __forceinline__ void load8(const Rows& m, int row, int col, int nv, float (&v)[8]) {
+    unpack8<E>(load8_bits(m, row, col, nv), v);
+}
+
+template <class E>
+__device__ __forceinline__ void store8(const Rows& m, int row, int col, int nv,
                                        const float (&v)[8]) {
-    uint16_t* p = m.ptr + row * m.ld + col;
-    if (m.vec && nv == 8) {
-        const u4_t w = {E::put2(v[0], v[1]), E::put2(v[2], v[3]), E::put2(v[4], v[5]),
-                        E::put2(v[6], v[7])};
-        __builtin_nontemporal_store(w, reinterpret_cast<u4_t*>(p));
+    uint16_t* p = m.ptr + (uint32_t)(row * m.ld + col);
+    const u4_t w = {E::put2(v[0], v[1]), E::put2(v[2], v[3]), E::put2(v[4], v[5]),
+                    E::put2(v[6], v[7])};
+    if (nv == 8) {
+        __builtin_memcpy(p, &w, 16);
     } else {
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-            if (q < nv) p[q] = E::put(v[q]);
+        for (int q = 0; q < 7; ++q)
+            if (q < nv) p[q] = (uint16_t)(w[q >> 1] >> (16 * (q & 1)));
     }
-}
-
-// A vector (bias) over columns: the same chunk of every row.
-template <class E>
-__device__ __forceinline__ void load8_vec(const uint16_t* b, int vec, int64_t col, int nv,
-                                          float (&v)[8]) {
-    const Rows r = {const_cast<uint16_t*>(b), 0, vec};
-    load8<E>(r, 0, col, nv, v);
 }
 
 }  // namespace

@@ -37,6 +37,14 @@ using dm::BK;
 using layer::Args;
 using layer::View;
 
+// A descriptor, which is the same in every lane, as the scalar registers that
+// a copy takes it in, wherever the compiler keeps it.
+__device__ __forceinline__ u32x4 scalar4(u32x4 r) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) r[c] = __builtin_amdgcn_readfirstlane(r[c]);
+    return r;
+}
+
 // The copies of one operand's stage (ROWS x 32 values, 64 * ROWS bytes) by
 // NW waves, CP copies of 1 KiB per wave and step.
 //  KC: stage [ROWS][32], chunk c of row r at c ^ aswz16(r); copies of steps
@@ -91,7 +99,7 @@ struct Operand {
         if constexpr (KC) {
             base = v.ptr + (int64_t)origin * ld;
             rows_valid = min(ROWS, extent - origin);
-            fix = rsrc_words(base, (int64_t)rows_valid * ld * 2);
+            fix = scalar4(rsrc_words(base, (int64_t)rows_valid * ld * 2));
         } else {
             base = v.ptr + origin;
             col0 = origin;
@@ -103,11 +111,11 @@ struct Operand {
         const uint32_t dst = stage + (wave * CP + t) * 1024;
         if constexpr (KC) {
             const u32x4 r = rsrc_words(base + k0, ((int64_t)rows_valid * ld - k0) * 2);
-            dma16(r, kc < K - k0 ? off[t] : kOOB, dst);
+            dma16(scalar4(r), kc < K - k0 ? off[t] : kOOB, dst);
         } else {
             const int kv = min(BK, K - k0);
             const u32x4 r = rsrc_words(base + (int64_t)k0 * ld, ((int64_t)kv * ld - col0) * 2);
-            dma16(r, off[t], dst);
+            dma16(scalar4(r), off[t], dst);
         }
     }
     // Copy t of a step that lies inside K: k_byte = 2 * k0 (KC), row = the
@@ -124,7 +132,7 @@ struct Operand {
             r[1] = (uint32_t)(a >> 32) & 0xFFFFu;
             r[2] = fix_size;
             r[3] = (uint32_t)kRsrcWord3;
-            dma16(r, off[t], dst);
+            dma16(scalar4(r), off[t], dst);
         }
     }
     // This lane's byte offset in a stage for block 0 of the wave's rows
@@ -406,109 +414,166 @@ __device__ __forceinline__ void run_k(Product<TL>& pr, typename TL::OpA& a, type
     wait_vmcnt<0>();  // the copies past the end of K
 }
 
-// Epilogue of a tile: the fp32 accumulators go through LDS in bands of RB
-// rows (half the tile's wave rows at a time, so that every wave writes), and
-// each thread then hands 8 consecutive columns of a row to the functor.
-// 16-byte chunk c of LDS row r sits at (c & 1) * CH/2 + ((c >> 1) ^ (r mod
-// CH/2)): the two chunks of 8 columns are read from the two halves of the
-// row, consecutive lanes from consecutive chunk positions.
-template <class TL>
-struct Bands {
-    static constexpr int CH = TL::BN / 4;
-    static constexpr int ROWB = TL::BN * 4;
-    static constexpr int NB = TL::BM * ROWB <= TL::LDS ? 1 : 2;
-    static constexpr int RB = TL::BM / NB;   // LDS rows per band
-    static constexpr int WR = TL::TM / NB;   // of them per wave row
-    static constexpr int IB = TL::FM / NB;   // 16-row blocks per wave and band
-    static_assert(RB * ROWB <= TL::LDS && TL::FM % NB == 0, "a band fits in the ring");
-    __device__ static __forceinline__ int pos(int c, int row) {
-        return row * ROWB + ((c & 1) * (CH / 2) + ((c >> 1) ^ (row & (CH / 2 - 1)))) * 16;
+// Epilogue of a tile, straight from the accumulators.  Lane (r, g) = (l % 16,
+// l / 16) of block (j, i) holds row 16 i + r, columns 16 j + 4 g .. + 3 of the
+// wave's part.  Exchanging the odd 16-lane rows of block j with the even ones
+// of block j + 1 (one v_permlane16_swap per register) leaves every lane with
+// 8 consecutive columns, 16 (j + g % 2) + 8 (g / 2) .. + 7, of one row: a
+// functor's loads and stores are 16 bytes a lane, 64 bytes a row.  No LDS and
+// no barrier, so the ring is free for the next tile's copies meanwhile.
+//
+// Functors on chunks of 8 fp32 values (columns col .. col + nv - 1 of a row, nv <
+// 8 only at the matrix's edge).  epi.from(m0) is the functor for the tile whose
+// first row is m0; row counts from there:
+//   kPlain:  f(row, col, nv, v, column, aux)
+//   kPaired: f(row, col, nv, first half's v, second half's v, column, aux)
+// with column = epi.column(col, nv), what a column chunk needs (bias), and aux
+// = epi.load(row, col, nv), what the functor reads of memory for the chunk;
+// these loads are issued kAhead chunks before their use, since a wait for
+// memory per chunk would dominate.  epi.with(run) calls run(f) once with the
+// functor proper, so that what is the same for all chunks (the activation) is
+// decided before the first one.
+// Functors on rows (kRows) see the accumulators themselves (see drain_rows).
+enum EpiKind { kPlain, kPaired, kRows };
+struct Nothing {};
+
+__device__ __forceinline__ void swap_rows16(float& a, float& b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a),
+                                                    __builtin_bit_cast(uint32_t, b), false, false);
+    const uint32_t x = r[0], y = r[1];  // (a bit_cast of an element takes element 0)
+    a = __builtin_bit_cast(float, x);
+    b = __builtin_bit_cast(float, y);
+}
+
+// 8 consecutive columns per lane out of two neighbouring blocks.
+__device__ __forceinline__ void chunk8(const floatx4& a, const floatx4& b, float (&v)[8]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        v[q] = a[q];
+        v[4 + q] = b[q];
+        swap_rows16(v[q], v[4 + q]);
     }
-    __device__ static __forceinline__ void write(char* smem, const Product<TL>& pr, int p, int wm,
-                                                 int wn, int lane) {
-        const int r = lane & 15, g = lane >> 4;
+}
+
+// The chunks of one tile; FULL: the tile lies inside the matrix.
+template <class TL, class Epi, bool FULL>
+__device__ __forceinline__ void drain_chunks(const Product<TL>& pr, int M, int N, int row0, int col0,
+                                             const Epi epi) {
+    constexpr bool PAIR = Epi::kind == kPaired;
+    constexpr int JP = TL::FN / (PAIR ? 4 : 2);  // column chunks per lane
+    constexpr int FM = TL::FM;
+    constexpr int AHEAD = Epi::kAhead < FM ? Epi::kAhead : FM;
+    static_assert(!PAIR || TL::TN == 64, "32 columns of each half per wave");
+    epi.with([&](const auto& f) __attribute__((always_inline)) {
+#pragma unroll
+        for (int jp = 0; jp < JP; ++jp) {
+            const int col = col0 + 32 * jp;
+            const int nv = FULL ? 8 : min(8, N - col);
+            const int rows = nv > 0 ? M : 0;  // a lane past the last column has no rows
+            decltype(epi.column(0, 0)) column = {};
+            if (nv > 0) column = epi.column(col, nv);
+            decltype(epi.load(0, 0, 0)) aux[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                if (FULL || row0 + 16 * i < rows) aux[i] = epi.load(row0 + 16 * i, col, nv);
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                const int row = row0 + 16 * i;
+                const auto now = aux[i % AHEAD];
+                if (i + AHEAD < FM && (FULL || row + 16 * AHEAD < rows))
+                    aux[i % AHEAD] = epi.load(row + 16 * AHEAD, col, nv);
+                float v[8];  // every lane takes part in the exchange
+                chunk8(pr.acc[2 * jp][i], pr.acc[2 * jp + 1][i], v);
+                if constexpr (PAIR) {
+                    float u[8];
+                    chunk8(pr.acc[2 * jp + 2][i], pr.acc[2 * jp + 3][i], u);
+                    if (FULL || row < rows) f(row, col, nv, v, u, column, now);
+                } else {
+                    if (FULL || row < rows) f(row, col, nv, v, column, now);
+                }
+                __builtin_amdgcn_sched_barrier(0);  // bounds what is in registers at once
+            }
+        }
+    });
+}
+
+template <class TL, class Epi>
+__device__ __forceinline__ void drain_epi(const Product<TL>& pr, int M, int N, int m0, int n0,
+                                          int tid, int wm, int wn, const Epi& epi) {
+    constexpr bool PAIR = Epi::kind == kPaired;
+    constexpr int COLS = PAIR ? TL::BN / 2 : TL::BN;
+    const int r = tid & 15, g = (tid >> 4) & 3;
+    const int row0 = wm * TL::TM + r;
+    const int col0 = n0 + wn * (PAIR ? 32 : TL::TN) + 16 * (g & 1) + 8 * (g >> 1);
+    if (m0 + TL::BM <= M && n0 + COLS <= N)
+        drain_chunks<TL, Epi, true>(pr, M - m0, N, row0, col0, epi.from(m0));
+    else
+        drain_chunks<TL, Epi, false>(pr, M - m0, N, row0, col0, epi.from(m0));
+}
+
+// Row functors: each row of the tile is reduced over its columns, first in
+// the lanes that hold it (values past column N are passed as -infinity), then
+// over the 4 lanes (r, 0..3), then over the wave columns through LDS.
+//   Acc a = epi.reduce<FN>(row, row < M, column of v[0][0], v), v[j] 16 columns
+//   apart;
+//   epi.join(a, other);  epi.finish(a, row, tile column).
+// Acc is 8 bytes.
+template <class TL, class Epi>
+__device__ __forceinline__ void drain_rows(char* smem, const Product<TL>& pr, int M, int N, int m0,
+                                           int tn, int tid, int wm, int wn, const Epi& epi) {
+    typedef typename Epi::Acc Acc;
+    static_assert(sizeof(Acc) == 8, "exchanged as two words");
+    const int lane = tid & 63;
+    const int r = lane & 15, g = lane >> 4;
+    const int n0 = tn * TL::BN + wn * TL::TN + 4 * g;
+    Acc* const joined = reinterpret_cast<Acc*>(smem);  // [WN][BM]
+    const bool whole = tn * TL::BN + TL::BN <= N;
+#pragma unroll
+    for (int i = 0; i < TL::FM; ++i) {
+        const int row = m0 + wm * TL::TM + 16 * i + r;
+        float v[TL::FN][4];
 #pragma unroll
         for (int j = 0; j < TL::FN; ++j)
 #pragma unroll
-            for (int ii = 0; ii < IB; ++ii)
-                *reinterpret_cast<floatx4*>(
-                    smem + pos((wn * TL::TN + 16 * j) / 4 + g, wm * WR + 16 * ii + r)) =
-                    pr.acc[j][p * IB + ii];
-    }
-    // Row of the tile that LDS row `row` of band p holds.
-    __device__ static __forceinline__ int tile_row(int p, int row) {
-        return (row / WR) * TL::TM + p * WR + row % WR;
-    }
-    __device__ static __forceinline__ void read8(const char* smem, int c, int row, float (&v)[8]) {
-        const floatx4 lo = *reinterpret_cast<const floatx4*>(smem + pos(2 * c, row));
-        const floatx4 hi = *reinterpret_cast<const floatx4*>(smem + pos(2 * c + 1, row));
+            for (int q = 0; q < 4; ++q)
+                v[j][q] = (whole || n0 + 16 * j + q < N) ? pr.acc[j][i][q] : -INFINITY;
+        Acc a = epi.template reduce<TL::FN>(row, row < M, n0, v);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            v[q] = lo[q];
-            v[4 + q] = hi[q];
+        for (int o = 16; o < 64; o <<= 1) {
+            u32x2 w = __builtin_bit_cast(u32x2, a);
+            w[0] = __shfl_xor((int)w[0], o, 64);
+            w[1] = __shfl_xor((int)w[1], o, 64);
+            epi.join(a, __builtin_bit_cast(Acc, w));
         }
+        if (g == 0) joined[wn * TL::BM + wm * TL::TM + 16 * i + r] = a;
     }
-};
-
-// Functors take 8 consecutive fp32 values of row `row`, columns col .. col +
-// nv - 1 (nv < 8 only at the matrix's edge):
-//   PLAIN:  epi(row, col, nv, v)
-//   PAIRED: epi(row, col, nv, first half's v, second half's v)
-//   ROWS:   epi.row(row, col, nv, v, group), called by `group` consecutive
-//           lanes for one row of the tile, all of them, with nv <= 0 past the
-//           edge; they may exchange values.
-enum EpiKind { kPlain, kPaired, kRows };
-
-template <class TL, class Epi>
-__device__ __forceinline__ void drain_epi(char* smem, const Product<TL>& pr, const Args& g, int m0,
-                                          int n0, int tid, int wm, int wn, const Epi& epi) {
-    using Bd = Bands<TL>;
-    constexpr int COLS = Epi::kind == kPaired ? TL::BN / 2 : TL::BN;
-    constexpr int LPR = COLS / 8;          // threads per row
-    constexpr int STEP = TL::T / LPR;      // rows per pass
-    const int cl = tid % LPR, r0 = tid / LPR;
-    const int col = n0 + cl * 8;
-    const int nv = min(8, g.N - col);
+    __syncthreads();
+    for (int k = tid; k < TL::BM; k += TL::T) {
+        if (m0 + k >= M) break;
+        Acc a = joined[k];
 #pragma unroll
-    for (int p = 0; p < Bd::NB; ++p) {
-        Bd::write(smem, pr, p, wm, wn, tid & 63);
-        __syncthreads();
-#pragma unroll 1
-        for (int q = 0; q < Bd::RB / STEP; ++q) {
-            const int lrow = r0 + q * STEP;
-            const int row = m0 + Bd::tile_row(p, lrow);
-            if constexpr (Epi::kind == kPaired) {
-                if (row < g.M && nv > 0) {
-                    const int c = (cl >> 2) * 8 + (cl & 3);  // 8-column chunk of the first half
-                    float u[8], v[8];
-                    Bd::read8(smem, c, lrow, u);
-                    Bd::read8(smem, c + 4, lrow, v);
-                    epi(row, col, nv, u, v);
-                }
-            } else if constexpr (Epi::kind == kRows) {
-                float v[8];
-                Bd::read8(smem, cl, lrow, v);
-                if (row < g.M) epi.template row<LPR>(row, col, nv, v, n0 / TL::BN);
-            } else {
-                if (row < g.M && nv > 0) {
-                    float v[8];
-                    Bd::read8(smem, cl, lrow, v);
-                    epi(row, col, nv, v);
-                }
-            }
-        }
-        if (p + 1 < Bd::NB) __syncthreads();
+        for (int c = 1; c < TL::WN; ++c) epi.join(a, joined[c * TL::BM + k]);
+        epi.finish(a, m0 + k, tn);
     }
 }
 
 // Functor of a split-K launch: the partial product, rows of part_ld floats.
 struct StorePart {
     static constexpr EpiKind kind = kPlain;
+    static constexpr int kAhead = 1;
     float* part;
-    int64_t ld;
-    __device__ __forceinline__ void operator()(int row, int col, int nv, const float (&v)[8]) const {
+    int ld;
+    __device__ __forceinline__ StorePart from(int64_t r) const { return {part + r * ld, ld}; }
+    template <class Run>
+    __device__ __forceinline__ void with(Run&& run) const {
+        run(*this);
+    }
+    __device__ __forceinline__ Nothing column(int, int) const { return {}; }
+    __device__ __forceinline__ Nothing load(int, int, int) const { return {}; }
+    __device__ __forceinline__ void operator()(int row, int col, int nv, const float (&v)[8], Nothing,
+                                               Nothing) const {
         // part_ld is a multiple of 8, so whole chunks always fit the row
-        float* p = part + (int64_t)row * ld + col;
+        float* p = part + (uint32_t)(row * ld + col);
         *reinterpret_cast<floatx4*>(p) = floatx4{v[0], v[1], v[2], v[3]};
         *reinterpret_cast<floatx4*>(p + 4) = floatx4{v[4], v[5], v[6], v[7]};
     }
@@ -555,14 +620,18 @@ void product_kernel(const Args g, const Epi epi) {
                                            });
         });
     }
-    __syncthreads();  // every wave is done with the ring
+    // The epilogue derives its lane addresses afresh, so that none is kept
+    // live across the K loop.
     int tid_d = tid;
     asm volatile("" : "+v"(tid_d));
     if constexpr (SPLIT) {
         const StorePart sp = {g.part + (int64_t)blockIdx.y * g.M * g.part_ld, g.part_ld};
-        drain_epi<TL>(smem, pr, g, m0, n0, tid_d, wm, wn, sp);
+        drain_epi<TL>(pr, g.M, g.N, m0, n0, tid_d, wm, wn, sp);
+    } else if constexpr (Epi::kind == kRows) {
+        __syncthreads();  // every wave is done with the ring
+        drain_rows<TL>(smem, pr, g.M, g.N, m0, tn, tid_d, wm, wn, epi);
     } else {
-        drain_epi<TL>(smem, pr, g, m0, n0, tid_d, wm, wn, epi);
+        drain_epi<TL>(pr, g.M, g.N, m0, n0, tid_d, wm, wn, epi);
     }
 }
 
@@ -607,15 +676,20 @@ __global__ __launch_bounds__(256) void finish_kernel(const float* __restrict__ p
                 v[4 + q] = hi[q];
             }
         };
+        const Epi at = epi.from(row);
+        const auto column = at.column(col, nv);
+        const auto aux = at.load(0, col, nv);
         float v[8];
         sum(p, v);
-        if constexpr (Epi::kind == kPaired) {
-            float u[8];
-            sum(p + pair_shift, u);
-            epi(row, col, nv, v, u);
-        } else {
-            epi(row, col, nv, v);
-        }
+        at.with([&](const auto& f) __attribute__((always_inline)) {
+            if constexpr (Epi::kind == kPaired) {
+                float u[8];
+                sum(p + pair_shift, u);
+                f(0, col, nv, v, u, column, aux);
+            } else {
+                f(0, col, nv, v, column, aux);
+            }
+        });
     }
 }
 

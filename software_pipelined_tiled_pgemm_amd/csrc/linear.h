@@ -45,9 +45,10 @@ struct LinearGradCall {
 };
 
 // Where a product's values go: y = act(v + bias) + residual, v + bias to
-// preact; null members are left out.  half > 0: the product's columns are two
-// halves, each padded from `half` to round_up(half, 8) columns, which y holds
-// without the padding (no bias, residual or preact then).
+// preact; null members are left out.  NT and TN products (gradients) take
+// residual only.  half > 0 (not NN): the product's columns are two halves, each
+// padded from `half` to round_up(half, 8) columns, which y holds without the
+// padding (no residual then).
 struct Sink {
     void* y;
     int64_t ldy;

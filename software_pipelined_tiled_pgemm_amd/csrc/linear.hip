@@ -20,36 +20,80 @@ namespace {
 template <class E>
 struct LinearEpi {
     static constexpr lp::EpiKind kind = lp::kPlain;
+    static constexpr int kAhead = 4;
     Rows y, res, pre;
     const uint16_t* bias;
-    int bias_vec;
     int act;
-    int half;  // > 0: two padded halves of columns (Sink)
-    __device__ __forceinline__ void operator()(int row, int col, int nv, float (&v)[8]) const {
-        float t[8];
-        if (bias) {
-            load8_vec<E>(bias, bias_vec, col, nv, t);
+    __device__ __forceinline__ LinearEpi from(int64_t r) const {
+        return {y.from(r), res.from(r), pre.from(r), bias, act};
+    }
+    struct Column {
+        float bias[8];
+    };
+    __device__ __forceinline__ Column column(int col, int nv) const {
+        Column c = {};
+        if (bias) load8<E>(Rows{const_cast<uint16_t*>(bias), 0}, 0, col, nv, c.bias);
+        return c;
+    }
+    __device__ __forceinline__ u4_t load(int row, int col, int nv) const {
+        return res ? load8_bits(res, row, col, nv) : u4_t{};
+    }
+    template <class Run>
+    __device__ __forceinline__ void with(Run&& run) const {
+        with_act(act, [&](auto a) __attribute__((always_inline)) {
+            run([&](int row, int col, int nv, float(&v)[8], const Column& c, u4_t r)
+                    __attribute__((always_inline)) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] += t[q];
-        }
-        if (pre) store8<E>(pre, row, col, nv, v);
-        if (act != PGEMM_ACT_NONE) {
+                for (int q = 0; q < 8; ++q) v[q] += c.bias[q];
+                if (pre) store8<E>(pre, row, col, nv, v);
+                float t[8];
+                unpack8<E>(r, t);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = act_value(act, v[q]);
-        }
-        if (res) {
-            load8<E>(res, row, col, nv, t);
+                for (int q = 0; q < 8; ++q) v[q] = decltype(a)::value(v[q]);
+                if (res) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] += t[q];
-        }
-        if (half > 0) {
-            const int h8 = (half + 7) & ~7;
-            const int second = col >= h8;
-            const int c = col - (second ? h8 : 0);
-            nv = min(8, half - c);
-            col = c + (second ? half : 0);
-        }
-        store8<E>(y, row, col, nv, v);
+                    for (int q = 0; q < 8; ++q) v[q] += t[q];
+                }
+                store8<E>(y, row, col, nv, v);
+            });
+        });
+    }
+};
+
+// y = v + add, the gradients' epilogue; half > 0: two padded halves of
+// columns (Sink).
+template <class E>
+struct GradEpi {
+    static constexpr lp::EpiKind kind = lp::kPlain;
+    static constexpr int kAhead = 4;
+    Rows y, add;
+    int half;
+    __device__ __forceinline__ GradEpi from(int64_t r) const {
+        return {y.from(r), add.from(r), half};
+    }
+    __device__ __forceinline__ lp::Nothing column(int, int) const { return {}; }
+    __device__ __forceinline__ u4_t load(int row, int col, int nv) const {
+        return add ? load8_bits(add, row, col, nv) : u4_t{};
+    }
+    template <class Run>
+    __device__ __forceinline__ void with(Run&& run) const {
+        run([&](int row, int col, int nv, float(&v)[8], lp::Nothing, u4_t r)
+                __attribute__((always_inline)) {
+            if (add) {
+                float t[8];
+                unpack8<E>(r, t);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[q] += t[q];
+            }
+            if (half > 0) {
+                const int h8 = (half + 7) & ~7;
+                const int second = col >= h8;
+                const int c = col - (second ? h8 : 0);
+                nv = min(8, half - c);
+                col = c + (second ? half : 0);
+            }
+            store8<E>(y, row, col, nv, v);
+        });
     }
 };
 
@@ -60,7 +104,7 @@ constexpr int64_t kDzRows = 64;
 constexpr int64_t kDzBlocks = 32768;  // most row blocks of a launch (grid y)
 
 template <class E>
-__global__ __launch_bounds__(256) void dz_kernel(const Rows dy, const Rows pre, const Rows dz,
+__global__ __launch_bounds__(256) void dz_kernel(const Rows dy0, const Rows pre0, const Rows dz0,
                                                  float* __restrict__ part, int64_t M, int N,
                                                  int dz_cols, int64_t per, int act) {
     __shared__ float sums[4][512];
@@ -68,25 +112,44 @@ __global__ __launch_bounds__(256) void dz_kernel(const Rows dy, const Rows pre, 
     const int col = (blockIdx.x * 64 + cl) * 8;
     const int nv = min(8, N - col);
     const int64_t r0 = (int64_t)blockIdx.y * per;
-    const int64_t r1 = r0 + per < M ? r0 + per : M;
+    const int64_t end = r0 + per < M ? r0 + per : M;
     float s[8] = {};
     if (col < dz_cols) {
-        for (int64_t r = r0 + rl; r < r1; r += 4) {
-            float d[8], z[8], unused;
-            load8<E>(dy, r, col, nv, d);
-            if (pre) {
-                load8<E>(pre, r, col, nv, z);
+        with_act(act, [&](auto a) __attribute__((always_inline)) {
+            auto one = [&](const Rows& dz, int r, const u4_t& db, const u4_t& zb) __attribute__((always_inline)) {
+                float d[8], z[8];
+                unpack8<E>(db, d);
+                unpack8<E>(zb, z);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) d[q] *= act_grad(act, z[q], unused);
-            }
+                for (int q = 0; q < 8; ++q) {
+                    float value;
+                    if (pre0) d[q] *= decltype(a)::grad(z[q], value);
+                    if (q >= nv) d[q] = 0.0f;
+                    s[q] += d[q];
+                }
+                // dz rows are padded with zeros to whole chunks
+                if (dz) store8<E>(dz, r, col, 8, d);
+            };
+            // kDzRows rows at a time, 4 rows' loads in flight per lane
+            for (int64_t rb = r0; rb < end; rb += kDzRows) {
+                const int rows = (int)(end - rb < kDzRows ? end - rb : kDzRows);
+                const Rows dy = dy0.from(rb), pre = pre0.from(rb), dz = dz0.from(rb);
+                int r = rl;
+                for (; r + 12 < rows; r += 16) {
+                    u4_t db[4], zb[4] = {};
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                if (q >= nv) d[q] = 0.0f;
-                s[q] += d[q];
+                    for (int u = 0; u < 4; ++u) {
+                        db[u] = load8_bits(dy, r + 4 * u, col, nv);
+                        if (pre) zb[u] = load8_bits(pre, r + 4 * u, col, nv);
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) one(dz, r + 4 * u, db[u], zb[u]);
+                }
+                for (; r < rows; r += 4)
+                    one(dz, r, load8_bits(dy, r, col, nv),
+                        pre ? load8_bits(pre, r, col, nv) : u4_t{});
             }
-            // dz rows are padded with zeros to whole chunks
-            if (dz) store8<E>(dz, r, col, 8, d);
-        }
+        });
     }
     if (part) {
 #pragma unroll
@@ -104,20 +167,15 @@ __global__ __launch_bounds__(256) void dz_kernel(const Rows dy, const Rows pre, 
 template <class E>
 hipError_t launch_linear_as(int layout, const Args& g, const Cut& cut, const Sink& s,
                             hipStream_t stream) {
-    Rows y = make_rows(s.y, s.ldy);
-    if (s.half % 8 != 0) y.vec = 0;  // the second half's chunks are not 16-byte aligned
-    const LinearEpi<E> epi = {y,
-                              make_rows(s.residual, s.ldr),
-                              make_rows(s.preact, s.ldp),
-                              static_cast<const uint16_t*>(s.bias),
-                              aligned16(s.bias),
-                              s.act,
-                              s.half};
-    switch (layout) {
-        case kNN: return lp::launch_product<E, true, false>(g, cut, epi, stream);
-        case kNT: return lp::launch_product<E, true, true>(g, cut, epi, stream);
-        default: return lp::launch_product<E, false, false>(g, cut, epi, stream);
+    const Rows y = make_rows(s.y, s.ldy), res = make_rows(s.residual, s.ldr);
+    if (layout == kNN) {
+        const LinearEpi<E> epi = {y, res, make_rows(s.preact, s.ldp),
+                                  static_cast<const uint16_t*>(s.bias), s.act};
+        return lp::launch_product<E, true, false>(g, cut, epi, stream);
     }
+    const GradEpi<E> epi = {y, res, s.half};
+    return layout == kNT ? lp::launch_product<E, true, true>(g, cut, epi, stream)
+                         : lp::launch_product<E, false, false>(g, cut, epi, stream);
 }
 
 template <class E>
@@ -155,8 +213,8 @@ struct Linear {
         if (!ar.dry() && c.M > 0 && c.N > 0 && (need_dz || c.dbias)) {
             const dim3 grid((unsigned)((n8 + 511) / 512), (unsigned)blocks);
             hipLaunchKernelGGL(dz_kernel<E>, grid, dim3(256), 0, stream, make_rows(c.dy, c.lddy),
-                               act ? make_rows(c.preact, c.ldp) : Rows{nullptr, 0, 0},
-                               need_dz ? Rows{dzw, n8, 1} : Rows{nullptr, 0, 0}, part, c.M,
+                               act ? make_rows(c.preact, c.ldp) : Rows{nullptr, 0},
+                               need_dz ? Rows{dzw, (int)n8} : Rows{nullptr, 0}, part, c.M,
                                (int)c.N, need_dz ? (int)n8 : (int)c.N, per, c.act);
             if ((rc = hipGetLastError()) != hipSuccess) return rc;
         }

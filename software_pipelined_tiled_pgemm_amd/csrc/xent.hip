@@ -41,27 +41,45 @@ struct StatsEpi {
     const int64_t* target;
     int64_t v0;     // vocabulary index of the product's column 0
     int64_t M;
+    int columns;  // of the product
     int tile0;
-    template <int LANES>
-    __device__ __forceinline__ void row(int r, int col, int nv, float (&v)[8], int tile) const {
-        const int64_t t = target[r] - v0 - col;
-        float m = -INFINITY, at = 0.0f;
+    typedef float2 Acc;  // maximum, sum of exp(value - maximum)
+    template <int FN>
+    __device__ __forceinline__ Acc reduce(int r, bool valid, int col,
+                                          const float (&v)[FN][4]) const {
+        const int64_t t = valid ? target[r] - v0 - col : -1;  // in this lane: 16 j + q
+        float m = -INFINITY;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            if (q >= nv) v[q] = -INFINITY;
-            m = fmaxf(m, v[q]);
-            if (t == q) at = v[q];
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) m = fmaxf(m, v[j][q]);
+        if (t >= 0 && t < 16 * FN && (t & 15) < 4 && t + col < columns) {
+            float at = 0.0f;
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (t == 16 * j + q) at = v[j][q];
+            target_logit[r] = at;
         }
-        if (t >= 0 && t < nv) target_logit[r] = at;
-#pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
         const float base = m == -INFINITY ? 0.0f : m;  // a row of -inf has the sum 0
+        const float scaled = base * kLog2e;
         float s = 0.0f;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) s += exp_fast(v[q] - base);
+        for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
-        if (threadIdx.x % LANES == 0) part[(int64_t)(tile0 + tile) * M + r] = float2{m, s};
+            for (int q = 0; q < 4; ++q)
+                s += __builtin_amdgcn_exp2f(fmaf(v[j][q], kLog2e, -scaled));
+        return float2{m, s};
+    }
+    __device__ __forceinline__ void join(Acc& a, Acc b) const {
+        const float m = fmaxf(a.x, b.x);
+        const float base = m == -INFINITY ? 0.0f : m;
+        a.y = a.y * exp_fast(a.x - base) + b.y * exp_fast(b.x - base);
+        a.x = m;
+    }
+    __device__ __forceinline__ void finish(Acc a, int r, int tile) const {
+        part[(int64_t)(tile0 + tile) * M + r] = a;
     }
 };
 
@@ -186,15 +204,32 @@ __global__ __launch_bounds__(1024) void weights_kernel(const int64_t* __restrict
 template <class E>
 struct DlogitEpi {
     static constexpr lp::EpiKind kind = lp::kPlain;
+    static constexpr int kAhead = 8;
     Rows dl;
     const float* lse;
     const float* weight;
     const int64_t* target;
     int64_t v0;
-    __device__ __forceinline__ void operator()(int row, int col, int nv, float (&v)[8]) const {
-        const float c = weight[row] * grad_scale<E>();
-        const float l = lse[row];
-        const int64_t t = target[row] - v0 - col;
+    __device__ __forceinline__ DlogitEpi from(int64_t r) const {
+        return {dl.from(r), lse + r, weight + r, target + r, v0};
+    }
+    struct Row {
+        float weight, lse;
+        int64_t target;
+    };
+    template <class Run>
+    __device__ __forceinline__ void with(Run&& run) const {
+        run(*this);
+    }
+    __device__ __forceinline__ lp::Nothing column(int, int) const { return {}; }
+    __device__ __forceinline__ Row load(int row, int, int) const {
+        return {weight[row], lse[row], target[row]};
+    }
+    __device__ __forceinline__ void operator()(int row, int col, int nv, float (&v)[8], lp::Nothing,
+                                               const Row& aux) const {
+        const float c = aux.weight * grad_scale<E>();
+        const float l = aux.lse;
+        const int64_t t = aux.target - v0 - col;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             const float p = exp_fast(v[q] - l) - (t == q ? 1.0f : 0.0f);
@@ -209,18 +244,36 @@ struct DlogitEpi {
 template <class E>
 struct SumEpi {
     static constexpr lp::EpiKind kind = lp::kPlain;
+    static constexpr int kAhead = 4;
     float* sum;  // [M][ld], NULL where there is one piece only
-    int64_t ld;
+    int ld;
     Rows out;
     const float* factor;
     int first, last;
-    __device__ __forceinline__ void operator()(int row, int col, int nv, float (&v)[8]) const {
+    __device__ __forceinline__ SumEpi from(int64_t r) const {
+        return {sum ? sum + r * ld : sum, ld, out.from(r), factor, first, last};
+    }
+    struct Before {
+        floatx4 lo, hi;
+    };
+    template <class Run>
+    __device__ __forceinline__ void with(Run&& run) const {
+        run(*this);
+    }
+    __device__ __forceinline__ float column(int, int) const { return factor[0]; }
+    __device__ __forceinline__ Before load(int row, int col, int) const {
+        if (!sum || first) return {};
+        const float* p = sum + (uint32_t)(row * ld + col);
+        return {*reinterpret_cast<const floatx4*>(p), *reinterpret_cast<const floatx4*>(p + 4)};
+    }
+    __device__ __forceinline__ void operator()(int row, int col, int nv, float (&v)[8], float f,
+                                               const Before& b) const {
         if (sum) {
-            float* p = sum + (int64_t)row * ld + col;
+            float* p = sum + (uint32_t)(row * ld + col);
             floatx4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
             if (!first) {
-                lo += *reinterpret_cast<const floatx4*>(p);
-                hi += *reinterpret_cast<const floatx4*>(p + 4);
+                lo += b.lo;
+                hi += b.hi;
             }
             if (!last) {
                 *reinterpret_cast<floatx4*>(p) = lo;
@@ -233,7 +286,6 @@ struct SumEpi {
                 v[4 + q] = hi[q];
             }
         }
-        const float f = factor[0];
 #pragma unroll
         for (int q = 0; q < 8; ++q) v[q] *= f;
         store8<E>(out, row, col, nv, v);
@@ -244,10 +296,11 @@ struct SumEpi {
 // size and whole tiles.
 constexpr int64_t kPieceBytes = (int64_t)1 << 29;
 constexpr int64_t kPieceLeast = 1024;
+constexpr int64_t kPieceMost = (int64_t)1 << 21;  // a row pitch of dl
 constexpr int64_t kPackRows = 32768;  // rows of W padded at a time
 
 int64_t piece_rows(int64_t V, int64_t most) {
-    most = std::max(most / 256 * 256, kPieceLeast);
+    most = std::min(std::max(most / 256 * 256, kPieceLeast), kPieceMost);
     const int64_t n = (V + most - 1) / most;
     return n <= 1 ? V : round_up((V + n - 1) / n, 256);
 }
@@ -291,7 +344,7 @@ struct Xent {
             if ((rc = piece(c.w, c.ldw, v0, n, c.D, room, false, stream, w)) != hipSuccess)
                 return rc;
             const Args g = args(x, w, c.M, n, c.D, cut, ar);
-            const StatsEpi epi = {part, logit, c.target, v0, c.M, used};
+            const StatsEpi epi = {part, logit, c.target, v0, c.M, (int)n, used};
             using T = lp::Tiles<E, true, true>;
             rc = cut.big ? lp::launch_tiles<typename T::Big, StatsEpi, false>(g, 1, epi, stream)
                          : lp::launch_tiles<typename T::Small, StatsEpi, false>(g, 1, epi, stream);
@@ -356,12 +409,12 @@ struct Xent {
                 return rc;
             const View dv = {dl, (int)s8};
             if (c.M > 0) {
-                const DlogitEpi<E> epi = {{dl, s8, 1}, c.lse, weight, c.target, v0};
+                const DlogitEpi<E> epi = {{dl, (int)s8}, c.lse, weight, c.target, v0};
                 rc = lp::launch_product<E, true, true>(product(x, w, c.M, n, c.D), cl, epi, stream);
                 if (rc != hipSuccess) return rc;
             }
             if (c.dx && c.M > 0 && c.D > 0) {
-                const SumEpi<E> epi = {sum, d8, make_rows(c.dx, c.lddx), factor, first, last};
+                const SumEpi<E> epi = {sum, (int)d8, make_rows(c.dx, c.lddx), factor, first, last};
                 // the last piece may be shorter: its own contraction, the same cut
                 Cut cut = cx;
                 if (cut.splits > 1) cut.splits = (int)((n + cut.chunk - 1) / cut.chunk);
