@@ -85,13 +85,16 @@ def build(verbose: bool = False, extra_flags=None) -> str:
         cmd = ([HIPCC] + FLAGS + PER_FILE.get(name, []) + list(extra_flags or [])
                + ["-c", src, "-o", obj])
         jobs.append((cmd, obj))
-    with ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
-        list(ex.map(lambda j: _run(j[0], verbose), jobs))
-    tmp = LIB + ".tmp%d" % os.getpid()
     objs = [o for _, o in jobs]
-    _run([HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC"] + objs + ["-o", tmp], verbose)
-    for o in objs:
-        os.remove(o)
+    tmp = LIB + ".tmp%d" % os.getpid()
+    try:
+        with ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
+            list(ex.map(lambda j: _run(j[0], verbose), jobs))
+        _run([HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC"] + objs + ["-o", tmp], verbose)
+    finally:
+        for o in objs:
+            if os.path.exists(o):
+                os.remove(o)
     os.replace(tmp, LIB)
     return LIB
 

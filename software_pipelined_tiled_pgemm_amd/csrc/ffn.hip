@@ -27,6 +27,7 @@ namespace {
 template <class E>
 struct GluEpi {
     static constexpr lp::EpiKind kind = lp::kPaired;
+    static constexpr bool kWalk = false;
     static constexpr int kAhead = 1;
     Rows h;  // padded rows: whole chunks
     Rows gate, up;
@@ -57,6 +58,7 @@ struct GluEpi {
 template <class E>
 struct GluGradEpi {
     static constexpr lp::EpiKind kind = lp::kPlain;
+    static constexpr bool kWalk = false;
     static constexpr int kAhead = 4;
     Rows gate, up;       // as the forward pass kept them
     Rows h, dgate, dup;  // padded rows: whole chunks, zeros past F
@@ -123,6 +125,12 @@ struct Ffn {
         const int64_t f8 = round_up(c.F, 8);
         hipError_t rc;
         uint16_t* h = static_cast<uint16_t*>(ar.take(c.M * f8 * 2));
+        const Sink s = {c.y, c.ldy, c.residual, c.ldr, nullptr, 0, nullptr, 0, 0};
+        uint16_t* gu = static_cast<uint16_t*>(c.gate_up);
+        const GluEpi<E> epi = {{h, (int)f8},
+                               make_rows(gu, c.ldgu),
+                               make_rows(gu ? gu + c.F : nullptr, c.ldgu),
+                               c.act};
         if (c.F > 0) {
             View x, w;
             if ((rc = operand(c.x, c.ldx, c.M, c.D, ar, stream, x)) != hipSuccess) return rc;
@@ -132,11 +140,6 @@ struct Ffn {
             g.N = (int)c.F;
             g.pair_shift = (int)f8;
             if (!ar.dry()) {
-                uint16_t* gu = static_cast<uint16_t*>(c.gate_up);
-                const GluEpi<E> epi = {{h, (int)f8},
-                                       make_rows(gu, c.ldgu),
-                                       make_rows(gu ? gu + c.F : nullptr, c.ldgu),
-                                       c.act};
                 rc = lp::launch_product<E, true, false>(g, cut, epi, stream);
                 if (rc != hipSuccess) return rc;
             }
@@ -146,7 +149,6 @@ struct Ffn {
         const Cut cut = choose_cut(c.M, c.N, c.F, cus, 16);
         const Args g = args({h, (int)f8}, wo, c.M, c.N, c.F, cut, ar);
         if (ar.dry()) return hipSuccess;
-        const Sink s = {c.y, c.ldy, c.residual, c.ldr, nullptr, 0, nullptr, 0, 0};
         return launch_linear(dtype, kNN, g, cut, s, stream);
     }
 

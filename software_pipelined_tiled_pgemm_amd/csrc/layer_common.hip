@@ -29,7 +29,9 @@ __global__ __launch_bounds__(256) void pack_kernel(const uint16_t* __restrict__ 
         } else {
             uint16_t e[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) e[q] = c + q < cols ? p[q] : (uint16_t)0;
+            for (int q = 0; q < 8; ++q) e[q] = p[c + q < cols ? q : 0];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) e[q] = c + q < cols ? e[q] : (uint16_t)0;
 #pragma unroll
             for (int q = 0; q < 4; ++q) w[q] = e[2 * q] | ((uint32_t)e[2 * q + 1] << 16);
         }
@@ -37,25 +39,38 @@ __global__ __launch_bounds__(256) void pack_kernel(const uint16_t* __restrict__ 
     }
 }
 
-// out[c] = sum over r of part[r][c] in ascending r inside each of 4 row
-// groups, the groups added in order: 64 columns per workgroup.
+// out[c] = sum over r of part[r][c]: 64 columns per workgroup, its 16 waves
+// each adding a sixteenth of the rows in ascending order (8 loads in flight),
+// the sixteenths then in order.
+constexpr int kSegs = 16;
 template <class E>
-__global__ __launch_bounds__(256) void column_sum_kernel(const float* __restrict__ part,
-                                                         int64_t parts, int64_t cols,
-                                                         uint16_t* __restrict__ out) {
-    __shared__ float sums[4][64];
+__global__ __launch_bounds__(64 * kSegs) void column_sum_kernel(const float* __restrict__ part,
+                                                                int64_t parts, int64_t cols,
+                                                                uint16_t* __restrict__ out) {
+    __shared__ float sums[kSegs][64];
     const int lane = threadIdx.x & 63, seg = threadIdx.x >> 6;
     const int64_t c = (int64_t)blockIdx.x * 64 + lane;
     float s = 0.0f;
     if (c < cols) {
-        const int64_t per = (parts + 3) / 4;
+        const int64_t per = (parts + kSegs - 1) / kSegs;
         const int64_t r1 = parts < (seg + 1) * per ? parts : (seg + 1) * per;
-        for (int64_t r = seg * per; r < r1; ++r) s += part[r * cols + c];
+        int64_t r = seg * per;
+        for (; r + 8 <= r1; r += 8) {
+            float v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = part[(r + u) * cols + c];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) s += v[u];
+        }
+        for (; r < r1; ++r) s += part[r * cols + c];
     }
     sums[seg][lane] = s;
     __syncthreads();
-    if (seg == 0 && c < cols)
-        out[c] = E::put(((sums[0][lane] + sums[1][lane]) + sums[2][lane]) + sums[3][lane]);
+    if (seg == 0 && c < cols) {
+        float t = sums[0][lane];
+        for (int k = 1; k < kSegs; ++k) t += sums[k][lane];
+        out[c] = E::put(t);
+    }
 }
 
 }  // namespace
@@ -74,28 +89,29 @@ hipError_t launch_column_sum(int dtype, const float* part, int64_t parts, int64_
                              hipStream_t stream) {
     const dim3 grid((unsigned)((cols + 63) / 64));
     if (dtype == kBF16)
-        hipLaunchKernelGGL(column_sum_kernel<BF16>, grid, dim3(256), 0, stream, part, parts, cols,
+        hipLaunchKernelGGL(column_sum_kernel<BF16>, grid, dim3(64 * kSegs), 0, stream, part, parts, cols,
                            static_cast<uint16_t*>(out));
     else
-        hipLaunchKernelGGL(column_sum_kernel<F16>, grid, dim3(256), 0, stream, part, parts, cols,
+        hipLaunchKernelGGL(column_sum_kernel<F16>, grid, dim3(64 * kSegs), 0, stream, part, parts, cols,
                            static_cast<uint16_t*>(out));
     return hipGetLastError();
 }
 
 namespace {
-// Estimated microseconds of a cut.  A 256x256 tile takes about 0.5 us per K
-// step of 32, two 128x128 tiles on a CU about 0.6 of that, one alone 0.35;
-// every round of workgroups adds its prologue and epilogue (about 4 us), and a
+// Estimated microseconds of a cut, with the constants measured on MI355X: a
+// 256x256 tile takes 0.65 us per K step of 32, two 128x128 tiles on a CU 0.57
+// (their LDS reads bound them: half the product for nearly the time), one
+// alone 0.33; a round of workgroups adds its prologue and epilogue, and a
 // split a second launch and the partials' traffic.
 double cut_time(int64_t M, int64_t N, int64_t K, int cus, bool big, int splits) {
     const int64_t b = big ? 256 : 128;
     const int64_t wgs = ((M + b - 1) / b) * ((N + b - 1) / b) * splits;
     const int64_t slots = big ? cus : 2 * cus;
-    const double step = big ? 0.5 : wgs <= cus ? 0.175 : 0.3;
+    const double step = big ? 0.65 : wgs <= cus ? 0.33 : 0.57;
     const double rounds = (double)((wgs + slots - 1) / slots);
-    const double steps = (double)((K + splits * 32 - 1) / (splits * 32)) + 4;
-    double t = rounds * (steps * step + 4.0);
-    if (splits > 1) t += 4.0 + (double)splits * M * N * 8.0 / 4.0e6;
+    const double steps = (double)((K + splits * 32 - 1) / (splits * 32)) + 2;
+    double t = rounds * (steps * step + (big ? 6.0 : 3.0));
+    if (splits > 1) t += 3.0 + (double)splits * M * N * 8.0 / 4.0e6;
     return t;
 }
 }  // namespace

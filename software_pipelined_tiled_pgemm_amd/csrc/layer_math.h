@@ -187,16 +187,21 @@ __device__ __forceinline__ void unpack8(const u4_t& w, float (&v)[8]) {
     }
 }
 
-// The bits of 8 values, zeros from nv on; row < 256.
+// The bits of 8 values, zeros from nv >= 1 on; row < 256.  At the edge the
+// loads past nv take the first value's address, so that all are issued at once
+// instead of one behind the other's branch.
 __device__ __forceinline__ u4_t load8_bits(const Rows& m, int row, int col, int nv) {
     const uint16_t* p = m.ptr + (uint32_t)(row * m.ld + col);
     u4_t w = {};
     if (nv == 8) {
         __builtin_memcpy(&w, p, 16);
     } else {
+        uint32_t e[8];
 #pragma unroll
-        for (int q = 0; q < 7; ++q)
-            if (q < nv) w[q >> 1] |= (uint32_t)p[q] << (16 * (q & 1));
+        for (int q = 0; q < 8; ++q) e[q] = p[q < nv ? q : 0];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            w[q >> 1] |= (q < nv ? e[q] : 0u) << (16 * (q & 1));
     }
     return w;
 }

@@ -99,7 +99,7 @@ struct Operand {
         if constexpr (KC) {
             base = v.ptr + (int64_t)origin * ld;
             rows_valid = min(ROWS, extent - origin);
-            fix = scalar4(rsrc_words(base, (int64_t)rows_valid * ld * 2));
+            fix = rsrc_words(base, (int64_t)rows_valid * ld * 2);
         } else {
             base = v.ptr + origin;
             col0 = origin;
@@ -124,7 +124,7 @@ struct Operand {
                                          uint32_t stage, int wave) const {
         const uint32_t dst = stage + (wave * CP + t) * 1024;
         if constexpr (KC) {
-            dma16s(fix, off[t], k_byte, dst);
+            dma16s(scalar4(fix), off[t], k_byte, dst);
         } else {
             const uint64_t a = reinterpret_cast<uint64_t>(row);
             u32x4 r;
@@ -223,9 +223,10 @@ struct Product {
     // order of half16 in gemm_kernels.h (the same sums, bit for bit).
     template <int CALL, int NC, class CopyFn>
     __device__ __forceinline__ void half(const char* rst, CopyFn copy) {
-        // TN: 16 blocks' offsets for every slot of the ring would not fit in
-        // registers; hiding the offsets' value keeps their derivation here.
-        if constexpr (!TL::AKC) asm volatile("" : "+v"(oa), "+v"(ob));
+        // A KR operand's block offsets for every slot of the ring would not fit
+        // in registers; hiding the offset's value keeps their derivation here.
+        if constexpr (!TL::AKC) asm volatile("" : "+v"(oa));
+        if constexpr (!TL::BKC) asm volatile("" : "+v"(ob));
         constexpr int HALF = CALL & 1, b = CALL >> 1;
         constexpr int FM = TL::FM, JH = TL::FN / 2;
         constexpr int NS = JH * FM;
@@ -291,69 +292,94 @@ struct Plan {
     }
 };
 
-// One output tile's K loop: the prologue, the periods and the drain of the
-// copies past K.  a and b have been initialised; place(): recomputes their
-// per-lane offsets (so that the unrolled loop need not keep the tail's).
-template <class TL, int PH, class Place>
-__device__ __forceinline__ void run_k(Product<TL>& pr, typename TL::OpA& a, typename TL::OpB& b,
-                                      char* smem, int K, int wave, int tid, Place&& place) {
-    constexpr int S = TL::S;
-    const uint32_t ring = lds_addr(smem);
-    const int nk = (K + BK - 1) / BK;
-    const int64_t astep = (int64_t)BK * a.ld, bstep = (int64_t)BK * b.ld;
+// The copies of a tile, a and b having been initialised for it.
+template <class TL>
+struct Copies {
+    typename TL::OpA a;
+    typename TL::OpB b;
+    int64_t astep, bstep;  // elements per step (KR)
 
-    // Copies of call CALL for steps (s, s+1) at slots (se, so), general form.
-    auto general = [&](auto call, int c, int s, uint32_t se, uint32_t so)
-                       __attribute__((always_inline)) {
-        using P = Plan<TL, decltype(call)::value>;
+    __device__ __forceinline__ void init(int lane, int wave, View va, View vb, int m0, int M, int n0,
+                                         int N, int shift) {
+        a.init(lane, wave, va, m0, M, 0);
+        b.init(lane, wave, vb, n0, N, shift);
+        astep = (int64_t)BK * va.ld;
+        bstep = (int64_t)BK * vb.ld;
+    }
+    // Copy c of call CALL for steps (s, s+1) into the stages at LDS addresses
+    // se and so; any part may lie past K.
+    template <int CALL>
+    __device__ __forceinline__ void general(int c, int K, int s, uint32_t se, uint32_t so,
+                                            int wave) const {
+        using P = Plan<TL, CALL>;
         const int t = P::t(c), h = P::h(c);
         const uint32_t st = h ? so : se;
         if constexpr (P::B)
             b.general(t, K, (s + h) * BK, st + TL::A_BYTES, wave);
         else
             a.general(t, K, (s + h) * BK, st, wave);
-    };
-    auto fast = [&](auto call, int c, uint32_t k_byte, const uint16_t* ar, const uint16_t* br,
-                    uint32_t se, uint32_t so) __attribute__((always_inline)) {
-        using P = Plan<TL, decltype(call)::value>;
+    }
+    // The same for steps inside K: k_byte, ar, br belong to step s.
+    template <int CALL>
+    __device__ __forceinline__ void fast(int c, uint32_t k_byte, const uint16_t* ar,
+                                         const uint16_t* br, uint32_t se, uint32_t so,
+                                         int wave) const {
+        using P = Plan<TL, CALL>;
         const int t = P::t(c), h = P::h(c);
         const uint32_t st = h ? so : se;
         if constexpr (P::B)
             b.fast(t, k_byte + h * (BK * 2), br + h * bstep, st + TL::A_BYTES, wave);
         else
             a.fast(t, k_byte + h * (BK * 2), ar + h * astep, st, wave);
-    };
-    auto calls = [&](auto&& f) __attribute__((always_inline)) {
-        f(std::integral_constant<int, 0>{});
-        f(std::integral_constant<int, 1>{});
-        f(std::integral_constant<int, 2>{});
-        f(std::integral_constant<int, 3>{});
-    };
-    // ---- prologue: steps 0 .. S-2
+    }
+    template <int CALL, bool FAST>
+    __device__ __forceinline__ void start_call(int e, int K, uint32_t se, uint32_t so,
+                                               int wave) const {
 #pragma unroll
-    for (int e = 0; e < S - 1; e += 2) {
-        const uint32_t se = ring + e * TL::STAGE, so = se + TL::STAGE;
-        if (K >= (S - 1) * BK) {
-            calls([&](auto call) __attribute__((always_inline)) {
-#pragma unroll
-                for (int c = 0; c < Plan<TL, decltype(call)::value>::NC; ++c)
-                    fast(call, c, (uint32_t)(e * BK * 2), a.base + e * astep, b.base + e * bstep,
-                         se, so);
-            });
-        } else {
-            calls([&](auto call) __attribute__((always_inline)) {
-#pragma unroll
-                for (int c = 0; c < Plan<TL, decltype(call)::value>::NC; ++c)
-                    general(call, c, e, se, so);
-            });
+        for (int c = 0; c < Plan<TL, CALL>::NC; ++c) {
+            if constexpr (FAST)
+                fast<CALL>(c, (uint32_t)(e * BK * 2), a.base + e * astep, b.base + e * bstep, se, so,
+                           wave);
+            else
+                general<CALL>(c, K, e, se, so, wave);
         }
     }
+    template <bool FAST>
+    __device__ __forceinline__ void start_all(int K, uint32_t ring, int wave) const {
+#pragma unroll
+        for (int e = 0; e < TL::S - 1; e += 2) {
+            const uint32_t se = ring + e * TL::STAGE, so = se + TL::STAGE;
+            start_call<0, FAST>(e, K, se, so, wave);
+            start_call<1, FAST>(e, K, se, so, wave);
+            start_call<2, FAST>(e, K, se, so, wave);
+            start_call<3, FAST>(e, K, se, so, wave);
+        }
+    }
+    // The prologue: steps 0 .. S-2 into slots 0 .. S-2.
+    __device__ __forceinline__ void start(int K, uint32_t ring, int wave) const {
+        if (K >= (TL::S - 1) * BK)
+            start_all<true>(K, ring, wave);
+        else
+            start_all<false>(K, ring, wave);
+    }
+};
+
+// One output tile's K loop, its prologue copies having been issued: the
+// periods, and the wait for the copies past K.  place(): recomputes the
+// copies' per-lane offsets (so that the unrolled loop need not keep them for
+// the tail).
+template <class TL, int PH, class Place>
+__device__ __forceinline__ void run_k(Product<TL>& pr, Copies<TL>& cp, char* smem, int K, int wave,
+                                      int tid, Place&& place) {
+    constexpr int S = TL::S;
+    const uint32_t ring = lds_addr(smem);
+    const int nk = (K + BK - 1) / BK;
     wait_vmcnt<TL::W0>();
     __syncthreads();
     pr.first_reads(smem);
 
-    const uint16_t* ar = a.base + (S - 1) * astep;  // rows of step kt+S-1
-    const uint16_t* br = b.base + (S - 1) * bstep;
+    const uint16_t* ar = cp.a.base + (S - 1) * cp.astep;  // rows of step kt+S-1
+    const uint16_t* br = cp.b.base + (S - 1) * cp.bstep;
     uint32_t k_byte = (S - 1) * BK * 2;
     auto period = [&](int kt, auto is_fast, auto slot) __attribute__((always_inline)) {
         constexpr bool F = decltype(is_fast)::value;
@@ -362,11 +388,12 @@ __device__ __forceinline__ void run_k(Product<TL>& pr, typename TL::OpA& a, type
         const int s4 = dm::wrap_slot<S>(se + S - 1);
         const uint32_t st4 = ring + s4 * TL::STAGE, st5 = ring + se * TL::STAGE;
         auto copy = [&](auto call) __attribute__((always_inline)) {
-            return [&, call](int c) __attribute__((always_inline)) {
+            constexpr int CALL = decltype(call)::value;
+            return [&](int c) __attribute__((always_inline)) {
                 if constexpr (F)
-                    fast(call, c, k_byte, ar, br, st4, st5);
+                    cp.template fast<CALL>(c, k_byte, ar, br, st4, st5, wave);
                 else
-                    general(call, c, kt + S - 1, st4, st5);
+                    cp.template general<CALL>(c, K, kt + S - 1, st4, st5, wave);
             };
         };
         const std::integral_constant<int, 0> c0;
@@ -393,8 +420,8 @@ __device__ __forceinline__ void run_k(Product<TL>& pr, typename TL::OpA& a, type
         }
         dm::half_priority<PH, 3>();
         pr.template half<3, Plan<TL, 3>::NC>(smem + s2 * TL::STAGE, copy(c3));
-        ar += 2 * astep;
-        br += 2 * bstep;
+        ar += 2 * cp.astep;
+        br += 2 * cp.bstep;
         k_byte += 2 * BK * 2;
         return s2;
     };
@@ -560,6 +587,7 @@ __device__ __forceinline__ void drain_rows(char* smem, const Product<TL>& pr, in
 // Functor of a split-K launch: the partial product, rows of part_ld floats.
 struct StorePart {
     static constexpr EpiKind kind = kPlain;
+    static constexpr bool kWalk = false;
     static constexpr int kAhead = 1;
     float* part;
     int ld;
@@ -579,18 +607,24 @@ struct StorePart {
     }
 };
 
+// One workgroup per tile; with a functor that says kWalk, a workgroup takes the
+// tiles blockIdx.x, blockIdx.x + gridDim.x, ...: as many workgroups as the chip
+// holds walk the tiles of a large product (see launch_tiles).  The copies of a tile's first steps are issued before the
+// epilogue of the one before it, which needs no LDS (kRows: 8 KiB in the slot
+// that the prologue leaves free), so they land meanwhile.  On gfx9 the wait
+// for step 0 counts the epilogue's stores too, which were issued later: it
+// then waits for more than it has to.
 template <class TL, class Epi, bool SPLIT>
 __global__ __launch_bounds__(TL::T, 1) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void product_kernel(const Args g, const Epi epi) {
     __shared__ __attribute__((aligned(1024))) char smem[TL::LDS];
-    int tm, tn;
-    tile_of_block(blockIdx.x, g.tiles_m * g.tiles_n, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
     constexpr int COLS = Epi::kind == kPaired ? TL::BN / 2 : TL::BN;
-    const int m0 = tm * TL::BM, n0 = tn * COLS;
+    const int tiles = g.tiles_m * g.tiles_n;
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / TL::WN, wn = wave % TL::WN;
+    const uint32_t ring = lds_addr(smem);
 
     View va = g.a, vb = g.b;
     int K = g.K;
@@ -602,36 +636,58 @@ void product_kernel(const Args g, const Epi epi) {
     }
     const int shift = Epi::kind == kPaired ? g.pair_shift : 0;
 
+    int blk = blockIdx.x, tm, tn;
+    tile_of_block(blk, tiles, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
     Product<TL> pr;
-    pr.zero();
     pr.place(wm, wn, lane);
+    Copies<TL> cp;
     if (K > 0) {
-        typename TL::OpA a;
-        typename TL::OpB b;
-        a.init(lane, wave, va, m0, g.M, 0);
-        b.init(lane, wave, vb, n0, g.N, shift);
-        dm::with_priority_group<TL>(wave, [&](auto ph) __attribute__((always_inline)) {
-            run_k<TL, decltype(ph)::value>(pr, a, b, smem, K, wave, tid,
-                                           [&]() __attribute__((always_inline)) {
-                                               int l = lane;
-                                               asm volatile("" : "+v"(l));
-                                               a.place(l, wave, va, m0, g.M, 0);
-                                               b.place(l, wave, vb, n0, g.N, shift);
-                                           });
-        });
+        cp.init(lane, wave, va, vb, tm * TL::BM, g.M, tn * COLS, g.N, shift);
+        cp.start(K, ring, wave);
     }
-    // The epilogue derives its lane addresses afresh, so that none is kept
-    // live across the K loop.
-    int tid_d = tid;
-    asm volatile("" : "+v"(tid_d));
-    if constexpr (SPLIT) {
-        const StorePart sp = {g.part + (int64_t)blockIdx.y * g.M * g.part_ld, g.part_ld};
-        drain_epi<TL>(pr, g.M, g.N, m0, n0, tid_d, wm, wn, sp);
-    } else if constexpr (Epi::kind == kRows) {
-        __syncthreads();  // every wave is done with the ring
-        drain_rows<TL>(smem, pr, g.M, g.N, m0, tn, tid_d, wm, wn, epi);
-    } else {
-        drain_epi<TL>(pr, g.M, g.N, m0, n0, tid_d, wm, wn, epi);
+    for (;;) {
+        const int m0 = tm * TL::BM, n0 = tn * COLS;
+        const int tn_now = tn;
+        pr.zero();
+        if (K > 0) {
+            dm::with_priority_group<TL>(wave, [&](auto ph) __attribute__((always_inline)) {
+                run_k<TL, decltype(ph)::value>(
+                    pr, cp, smem, K, wave, tid, [&]() __attribute__((always_inline)) {
+                        int l = lane;
+                        asm volatile("" : "+v"(l));
+                        cp.a.place(l, wave, va, m0, g.M, 0);
+                        cp.b.place(l, wave, vb, n0, g.N, shift);
+                    });
+            });
+        }
+        bool more = false;
+        if constexpr (Epi::kWalk) {
+            blk += gridDim.x;
+            more = blk < tiles;
+        }
+        if constexpr (Epi::kWalk || Epi::kind == kRows)
+            __syncthreads();  // every wave is done with the ring
+        // What follows derives its lane values afresh, so that none is kept
+        // live across the K loop.
+        int tid_d = tid;
+        asm volatile("" : "+v"(tid_d));
+        if (Epi::kWalk && more) {
+            tile_of_block(blk, tiles, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
+            if (K > 0) {
+                cp.init(tid_d & 63, wave, va, vb, tm * TL::BM, g.M, tn * COLS, g.N, shift);
+                cp.start(K, ring, wave);
+            }
+        }
+        if constexpr (SPLIT) {
+            const StorePart sp = {g.part + (int64_t)blockIdx.y * g.M * g.part_ld, g.part_ld};
+            drain_epi<TL>(pr, g.M, g.N, m0, n0, tid_d, wm, wn, sp);
+        } else if constexpr (Epi::kind == kRows) {
+            drain_rows<TL>(smem + (TL::S - 1) * TL::STAGE, pr, g.M, g.N, m0, tn_now, tid_d, wm, wn,
+                           epi);
+        } else {
+            drain_epi<TL>(pr, g.M, g.N, m0, n0, tid_d, wm, wn, epi);
+        }
+        if (!more) break;
     }
 }
 
@@ -702,8 +758,16 @@ hipError_t launch_tiles(Args g, int splits, const Epi& epi, hipStream_t stream) 
     g.tiles_n = (g.N + COLS - 1) / COLS;
     // Bands of 4 tile rows, as in the plain GEMM's launch.
     g.group_m = g.tiles_m < 4 ? g.tiles_m : 4;
-    hipLaunchKernelGGL((product_kernel<TL, Epi, SPLIT>), dim3(g.tiles_m * g.tiles_n, splits),
-                       dim3(TL::T), 0, stream, g, epi);
+    // One 256x256 workgroup fills a CU's LDS: at most one per CU, each walking
+    // several tiles (a multiple of 8 workgroups keeps tile_of_block's map of
+    // tiles to XCDs).
+    int grid = g.tiles_m * g.tiles_n;
+    if (TL::BM == 256 && Epi::kWalk) {
+        const int cus = compute_units();
+        if (cus >= 8) grid = std::min(grid, cus & ~7);
+    }
+    hipLaunchKernelGGL((product_kernel<TL, Epi, SPLIT>), dim3(grid, splits), dim3(TL::T), 0, stream,
+                       g, epi);
     return hipGetLastError();
 }
 

@@ -20,6 +20,7 @@ namespace {
 template <class E>
 struct LinearEpi {
     static constexpr lp::EpiKind kind = lp::kPlain;
+    static constexpr bool kWalk = false;
     static constexpr int kAhead = 4;
     Rows y, res, pre;
     const uint16_t* bias;
@@ -65,6 +66,7 @@ struct LinearEpi {
 template <class E>
 struct GradEpi {
     static constexpr lp::EpiKind kind = lp::kPlain;
+    static constexpr bool kWalk = false;
     static constexpr int kAhead = 4;
     Rows y, add;
     int half;
@@ -205,8 +207,11 @@ struct Linear {
             dzw = static_cast<uint16_t*>(ar.take(c.M * n8 * 2));
             dz = {dzw, (int)n8};
         }
-        const int64_t per = kDzRows * std::max<int64_t>(1, (c.M + kDzRows * kDzBlocks - 1) /
-                                                              (kDzRows * kDzBlocks));
+        // Rows per workgroup: fewer where there would be too few workgroups.
+        const int64_t strips = (n8 + 511) / 512;
+        int64_t per = kDzRows * std::max<int64_t>(1, (c.M + kDzRows * kDzBlocks - 1) /
+                                                        (kDzRows * kDzBlocks));
+        while (per > 16 && strips * ((c.M + per - 1) / per) < 1024) per /= 2;
         const int64_t blocks = (c.M + per - 1) / per;
         float* part = nullptr;
         if (c.dbias) part = static_cast<float*>(ar.take(std::max<int64_t>(blocks, 1) * c.N * 4));

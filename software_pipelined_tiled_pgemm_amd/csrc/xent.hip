@@ -36,6 +36,7 @@ constexpr float grad_scale() {
 // from whichever lane holds it.
 struct StatsEpi {
     static constexpr lp::EpiKind kind = lp::kRows;
+    static constexpr bool kWalk = true;
     float2* part;  // [tile][M]
     float* target_logit;
     const int64_t* target;
@@ -83,17 +84,18 @@ struct StatsEpi {
     }
 };
 
-// Joins a row's tiles: 64 rows per workgroup, 4 waves taking every fourth
-// tile.  A target outside the vocabulary that is not ignore_index gives NaN.
-__global__ __launch_bounds__(256) void join_kernel(const float2* __restrict__ part, int tiles,
-                                                   const float* __restrict__ target_logit,
-                                                   const int64_t* __restrict__ target,
-                                                   int64_t ignore_index, int64_t V, int64_t M,
-                                                   float* __restrict__ lse,
-                                                   float* __restrict__ row_loss) {
-    __shared__ float2 seg[4][64];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t r = (int64_t)blockIdx.x * 64 + lane;
+// Joins a row's tiles: 16 rows per workgroup, 64 lanes taking every 64th tile
+// of a row each (4 loads in flight), then the lanes in order through LDS.  A
+// target outside the vocabulary that is not ignore_index gives NaN.
+__global__ __launch_bounds__(1024) void join_kernel(const float2* __restrict__ part, int tiles,
+                                                    const float* __restrict__ target_logit,
+                                                    const int64_t* __restrict__ target,
+                                                    int64_t ignore_index, int64_t V, int64_t M,
+                                                    float* __restrict__ lse,
+                                                    float* __restrict__ row_loss) {
+    __shared__ float2 seg[64][16];
+    const int row = threadIdx.x & 15, w = threadIdx.x >> 4;
+    const int64_t r = (int64_t)blockIdx.x * 16 + row;
     float m = -INFINITY, s = 0.0f;
     auto join = [&](float2 p) {
         const float top = fmaxf(m, p.x);
@@ -101,12 +103,26 @@ __global__ __launch_bounds__(256) void join_kernel(const float2* __restrict__ pa
         s = s * exp_fast(m - base) + p.y * exp_fast(p.x - base);
         m = top;
     };
-    if (r < M)
-        for (int t = w; t < tiles; t += 4) join(part[(int64_t)t * M + r]);
-    seg[w][lane] = float2{m, s};
-    __syncthreads();
+    if (r < M) {
+        int t = w;
+        for (; t + 192 < tiles; t += 256) {
+            float2 p[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) p[u] = part[(int64_t)(t + 64 * u) * M + r];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) join(p[u]);
+        }
+        for (; t < tiles; t += 64) join(part[(int64_t)t * M + r]);
+    }
+    seg[w][row] = float2{m, s};
+    for (int h = 32; h > 0; h >>= 1) {
+        __syncthreads();
+        if (w < h) {
+            join(seg[w + h][row]);
+            seg[w][row] = float2{m, s};
+        }
+    }
     if (w == 0 && r < M) {
-        for (int k = 1; k < 4; ++k) join(seg[k][lane]);
         const float l = (m == -INFINITY ? 0.0f : m) + logf(s);
         lse[r] = l;
         const int64_t t = target[r];
@@ -204,6 +220,7 @@ __global__ __launch_bounds__(1024) void weights_kernel(const int64_t* __restrict
 template <class E>
 struct DlogitEpi {
     static constexpr lp::EpiKind kind = lp::kPlain;
+    static constexpr bool kWalk = false;
     static constexpr int kAhead = 8;
     Rows dl;
     const float* lse;
@@ -244,6 +261,7 @@ struct DlogitEpi {
 template <class E>
 struct SumEpi {
     static constexpr lp::EpiKind kind = lp::kPlain;
+    static constexpr bool kWalk = false;
     static constexpr int kAhead = 4;
     float* sum;  // [M][ld], NULL where there is one piece only
     int ld;
@@ -352,7 +370,7 @@ struct Xent {
             used += (int)((n + bn - 1) / bn);
         }
         if (c.M > 0) {
-            hipLaunchKernelGGL(join_kernel, dim3((unsigned)((c.M + 63) / 64)), dim3(256), 0, stream,
+            hipLaunchKernelGGL(join_kernel, dim3((unsigned)((c.M + 15) / 16)), dim3(1024), 0, stream,
                                part, used, logit, c.target, c.ignore_index, c.V, c.M, c.lse,
                                row_loss);
             if ((rc = hipGetLastError()) != hipSuccess) return rc;

@@ -9,58 +9,68 @@ dimension is contiguous; their rows may be strided.
 """
 from __future__ import annotations
 
+import ctypes
+import sys
+
 from . import _lib
 from ._lib import PgemmError, lib
+
+_pkg = sys.modules[__package__]  # its helpers, defined before this module is imported
+_new, _invoke = _pkg._new, _pkg._invoke
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 REDUCTIONS = {"none": 0, "mean": 1, "sum": 2}
 
 
+# torch, looked up at the first call (importing the package does not import
+# torch).  A token's kernels take a few microseconds, so what a call does here
+# is kept short: the checks are single expressions in the common case, and
+# the sizes of workspaces are remembered by what they depend on.
+_torch = None
+_TENSOR = None
+_F16 = _BF16 = _F32 = None
+
+
 def _base():
-    from . import _torch
-    return _torch()
-
-
-def _new(shape, dtype, device, stream):
-    from . import _new as new
-    return new(shape, dtype, device, stream)
-
-
-def _invoke(t, stream, fn):
-    from . import _invoke as invoke
-    return invoke(t, stream, fn)
+    global _torch, _TENSOR, _F16, _BF16, _F32
+    if _torch is None:
+        t = _pkg._torch()
+        _TENSOR, _F16, _BF16, _F32 = t.Tensor, t.float16, t.bfloat16, t.float32
+        _torch = t
+    return _torch
 
 
 def _act(act):
-    try:
-        return ACTIVATIONS[act]
-    except (KeyError, TypeError):
-        raise ValueError("act must be one of %s, got %r" % (", ".join(ACTIVATIONS), act)) from None
+    a = ACTIVATIONS.get(act) if isinstance(act, str) else None
+    if a is None:
+        raise ValueError("act must be one of %s, got %r" % (", ".join(ACTIVATIONS), act))
+    return a
 
 
 def _dtype(t, name):
-    torch = _base()
+    torch = _torch or _base()
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if t.dtype is torch.float16:
+    dt = t.dtype
+    if dt is _F16:
         return 0
-    if t.dtype is torch.bfloat16:
+    if dt is _BF16:
         return 1
-    raise TypeError("%s must be float16 or bfloat16, got %s" % (name, t.dtype))
+    raise TypeError("%s must be float16 or bfloat16, got %s" % (name, dt))
 
 
 def _mat(t, name, like, rows=None, cols=None):
     """Checks a matrix against the call's first tensor `like` (type, device)
     and a shape; returns its row pitch in elements."""
-    torch = _base()
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _TENSOR):
         raise TypeError("%s must be a torch.Tensor" % name)
     if not t.is_cuda:
         raise ValueError("%s must be a device (HIP) tensor, got %s" % (name, t.device))
-    if t.dtype is not like.dtype:
-        raise TypeError("%s must be %s, got %s" % (name, like.dtype, t.dtype))
-    if t.get_device() != like.get_device():
-        raise ValueError("%s is on another device than the other tensors" % name)
+    if t is not like:
+        if t.dtype is not like.dtype:
+            raise TypeError("%s must be %s, got %s" % (name, like.dtype, t.dtype))
+        if t.get_device() != like.get_device():
+            raise ValueError("%s is on another device than the other tensors" % name)
     if t.dim() != 2:
         raise ValueError("%s must have 2 dimensions" % name)
     r, c = t.shape
@@ -75,12 +85,11 @@ def _mat(t, name, like, rows=None, cols=None):
         raise ValueError("%s must be contiguous along its rows" % name)
     if r > 1 and s0 < c:
         raise ValueError("%s must not have overlapping rows" % name)
-    return s0 if r > 1 else max(c, 1)
+    return s0 if r > 1 else c
 
 
 def _vec(t, name, like, n):
-    torch = _base()
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _TENSOR):
         raise TypeError("%s must be a torch.Tensor" % name)
     if not t.is_cuda or t.get_device() != like.get_device():
         raise ValueError("%s must be on the other tensors' device" % name)
@@ -96,22 +105,45 @@ def _ptr(t):
 
 def _out(t, name, like, shape, stream):
     if t is None:
-        t = _new(shape, like.dtype, like.device, stream)
+        return _new(shape, like.dtype, like.device, stream), max(shape[1], 1)
     return t, _mat(t, name, like, *shape)
 
 
-def _workspace(need, given, like, stream, what):
+_needs = {}
+
+
+def _need(fn, like, *args):
+    """fn(*args), a workspace size, remembered: it depends on the arguments
+    (pointers: on their alignment alone, which is what is passed) and on the
+    device."""
+    key = (fn.__name__, like.get_device()) + args
+    need = _needs.get(key)
+    if need is None:
+        with _base().cuda.device(key[1]):
+            need = fn(*args)
+        if need < 0:
+            raise PgemmError(int(need), fn.__name__)
+        if len(_needs) >= 4096:
+            _needs.clear()
+        _needs[key] = need
+    return need
+
+
+def _at(t):
+    """An address of t's alignment."""
+    return 16 + (t.data_ptr() & 15)
+
+
+def _workspace(need, given, like, stream):
     """(pointer, bytes, tensor to keep alive) of a call's workspace."""
-    if need < 0:
-        raise PgemmError(int(need), what)
     if given is not None:
         if given.device != like.device or not given.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on %s" % like.device)
         return given.data_ptr(), given.numel() * given.element_size(), given
     if need == 0:
         return None, 0, None
-    w = _new(int(need), _base().uint8, like.device, stream)
-    return w.data_ptr(), int(need), w
+    w = _new(need, _torch.uint8, like.device, stream)
+    return w.data_ptr(), need, w
 
 
 def _call(rc, what):
@@ -139,9 +171,10 @@ def plinear(x, w, bias=None, residual=None, act="none", preact=None, out=None, w
     out, ldy = _out(out, "out", x, (M, N), stream)
     L = lib()
 
+    need = _need(L.plinear_workspace_bytes, x, dt, _at(x), ldx, _at(w), ldw, M, N, K)
+    ws, nws, keep = _workspace(need, workspace, x, stream)
+
     def run(h):
-        need = L.plinear_workspace_bytes(dt, x.data_ptr(), ldx, w.data_ptr(), ldw, M, N, K)
-        ws, nws, keep = _workspace(need, workspace, x, stream, "plinear")
         return L.plinear(dt, x.data_ptr(), ldx, w.data_ptr(), ldw, _ptr(bias), _ptr(residual), ldr,
                          out.data_ptr(), ldy, _ptr(preact), ldp, M, N, K, a, ws, nws, h)
     _call(_invoke(x, stream, run), "plinear")
@@ -177,10 +210,11 @@ def plinear_bwd(dy, x, w, preact=None, act="none", dx_residual=None, needs=(True
     dx, dw, dbias = (t if n else None for t, n in zip((dx, dw, dbias), needs))
     L = lib()
 
+    need = _need(L.plinear_bwd_workspace_bytes, dy, dt, _at(dy), lddy, _at(x), ldx, _at(w), ldw, M,
+                 N, K, a, *map(int, map(bool, needs)))
+    ws, nws, keep = _workspace(need, workspace, dy, stream)
+
     def run(h):
-        need = L.plinear_bwd_workspace_bytes(dt, dy.data_ptr(), lddy, x.data_ptr(), ldx,
-                                             w.data_ptr(), ldw, M, N, K, a, *map(int, map(bool, needs)))
-        ws, nws, keep = _workspace(need, workspace, dy, stream, "plinear_bwd")
         return L.plinear_bwd(dt, dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(), ldw,
                              _ptr(preact), ldp, _ptr(dx_residual), lda, _ptr(dx), lddx, _ptr(dw),
                              lddw, _ptr(dbias), M, N, K, a, ws, nws, h)
@@ -210,10 +244,11 @@ def pffn(x, w_in, w_out, residual=None, act="silu", gate_up=None, out=None, work
     out, ldy = _out(out, "out", x, (M, N), stream)
     L = lib()
 
+    need = _need(L.pffn_workspace_bytes, x, dt, _at(x), ldx, _at(w_in), ldwi, _at(w_out), ldwo, M,
+                 D, F, N)
+    ws, nws, keep = _workspace(need, workspace, x, stream)
+
     def run(h):
-        need = L.pffn_workspace_bytes(dt, x.data_ptr(), ldx, w_in.data_ptr(), ldwi,
-                                      w_out.data_ptr(), ldwo, M, D, F, N)
-        ws, nws, keep = _workspace(need, workspace, x, stream, "pffn")
         return L.pffn(dt, x.data_ptr(), ldx, w_in.data_ptr(), ldwi, w_out.data_ptr(), ldwo,
                       _ptr(residual), ldr, out.data_ptr(), ldy, _ptr(gate_up), ldgu, M, D, F, N, a,
                       ws, nws, h)
@@ -250,11 +285,11 @@ def pffn_bwd(dy, x, w_in, w_out, gate_up, act="silu", dx_residual=None, needs=(T
     dx, dw_in, dw_out = (t if n else None for t, n in zip((dx, dw_in, dw_out), needs))
     L = lib()
 
+    need = _need(L.pffn_bwd_workspace_bytes, dy, dt, _at(dy), lddy, _at(x), ldx, _at(w_in), ldwi,
+                 _at(w_out), ldwo, M, D, F, N, *map(int, map(bool, needs)))
+    ws, nws, keep = _workspace(need, workspace, dy, stream)
+
     def run(h):
-        need = L.pffn_bwd_workspace_bytes(dt, dy.data_ptr(), lddy, x.data_ptr(), ldx,
-                                          w_in.data_ptr(), ldwi, w_out.data_ptr(), ldwo, M, D, F,
-                                          N, *map(int, map(bool, needs)))
-        ws, nws, keep = _workspace(need, workspace, dy, stream, "pffn_bwd")
         return L.pffn_bwd(dt, dy.data_ptr(), lddy, x.data_ptr(), ldx, w_in.data_ptr(), ldwi,
                           w_out.data_ptr(), ldwo, gate_up.data_ptr(), ldgu, _ptr(dx_residual), lda,
                           _ptr(dx), lddx, _ptr(dw_in), lddwi, _ptr(dw_out), lddwo, M, D, F, N, a,
@@ -311,9 +346,10 @@ def pxent(x, w, target, ignore_index=-100, reduction="mean", loss=None, lse=None
     _flat(lse, "lse", x, torch.float32, (M,))
     L = lib()
 
+    need = _need(L.pxent_workspace_bytes, x, dt, _at(x), ldx, _at(w), ldw, red, M, V, D)
+    ws, nws, keep = _workspace(need, workspace, x, stream)
+
     def run(h):
-        need = L.pxent_workspace_bytes(dt, x.data_ptr(), ldx, w.data_ptr(), ldw, red, M, V, D)
-        ws, nws, keep = _workspace(need, workspace, x, stream, "pxent")
         return L.pxent(dt, x.data_ptr(), ldx, w.data_ptr(), ldw, target.data_ptr(),
                        int(ignore_index), red, loss.data_ptr(), lse.data_ptr(), M, V, D, ws, nws, h)
     _call(_invoke(x, stream, run), "pxent")
@@ -340,10 +376,11 @@ def pxent_bwd(x, w, target, lse, dloss=None, ignore_index=-100, reduction="mean"
     dx, dw = (t if n else None for t, n in zip((dx, dw), needs))
     L = lib()
 
+    need = _need(L.pxent_bwd_workspace_bytes, x, dt, _at(x), ldx, _at(w), ldw, M, V, D,
+                 *map(int, map(bool, needs)))
+    ws, nws, keep = _workspace(need, workspace, x, stream)
+
     def run(h):
-        need = L.pxent_bwd_workspace_bytes(dt, x.data_ptr(), ldx, w.data_ptr(), ldw, M, V, D,
-                                           *map(int, map(bool, needs)))
-        ws, nws, keep = _workspace(need, workspace, x, stream, "pxent_bwd")
         return L.pxent_bwd(dt, x.data_ptr(), ldx, w.data_ptr(), ldw, target.data_ptr(),
                            int(ignore_index), red, lse.data_ptr(), _ptr(dloss), _ptr(dx), lddx,
                            _ptr(dw), lddw, M, V, D, ws, nws, h)
@@ -356,50 +393,47 @@ def pclip_grad_norm(tensors, max_norm, out=None, norm=None, workspace=None, stre
     they come) by min(1, max_norm / (norm + 1e-6)), norm being that of all
     their elements together: in place, or into the list `out`.  Returns the
     norm before clipping as a float32 scalar tensor on the device."""
-    import ctypes
-    torch = _base()
+    torch = _torch or _base()
     tensors = list(tensors)
-    if not tensors:
+    n = len(tensors)
+    if not n:
         raise ValueError("tensors must not be empty")
     first = tensors[0]
-    codes = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
-    kinds = []
-
-    def check(t, name):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("%s must be torch.Tensors" % name)
-        if not t.is_cuda or t.get_device() != index:
-            raise ValueError("%s must be on one HIP device" % name)
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
-        code = codes.get(t.dtype)
-        if code is None:
-            raise TypeError("%s must be float16, bfloat16 or float32, got %s" % (name, t.dtype))
-        return code
-    index = first.get_device() if isinstance(first, torch.Tensor) and first.is_cuda else -1
-    for t in tensors:
-        kinds.append(check(t, "tensors"))
-    n = len(tensors)
     outs = None
+    every = tensors
     if out is not None:
         out = list(out)
         if len(out) != n:
             raise ValueError("out must have %d tensors" % n)
-        for t, o, k in zip(tensors, out, kinds):
-            if check(o, "out") != k or o.numel() != t.numel():
-                raise ValueError("out must have the tensors' types and sizes")
-        outs = (ctypes.c_void_p * n)(*[o.data_ptr() for o in out])
+        every = tensors + out
+    if not all([type(t) is _TENSOR or isinstance(t, _TENSOR) for t in every]):
+        raise TypeError("tensors and out must be torch.Tensors")
+    if len({t.get_device() for t in every}) != 1 or not first.is_cuda:
+        raise ValueError("tensors and out must be on one HIP device")
+    if not all([t.is_contiguous() for t in every]):
+        raise ValueError("tensors and out must be contiguous")
+    codes = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+    try:
+        kinds = [codes[t.dtype] for t in tensors]
+    except KeyError as e:
+        raise TypeError("tensors must be float16, bfloat16 or float32, got %s" % e) from None
+    counts = [t.numel() for t in tensors]
+    if out is not None:
+        if [codes.get(t.dtype) for t in out] != kinds or [t.numel() for t in out] != counts:
+            raise ValueError("out must have the tensors' types and sizes")
+        outs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in out])
     if norm is None:
         norm = _new((), torch.float32, first.device, stream)
-    _flat(norm, "norm", first, torch.float32, ())
+    else:
+        _flat(norm, "norm", first, torch.float32, ())
     grads = (ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors])
-    sizes = (ctypes.c_int64 * n)(*[t.numel() for t in tensors])
+    sizes = (ctypes.c_int64 * n)(*counts)
     dtypes = (ctypes.c_int * n)(*kinds)
     L = lib()
+    ws, nws, keep = _workspace(_need(L.pclip_grad_norm_workspace_bytes, first, n), workspace, first,
+                               stream)
 
     def run(h):
-        need = L.pclip_grad_norm_workspace_bytes(n)
-        ws, nws, keep = _workspace(need, workspace, first, stream, "pclip_grad_norm")
         return L.pclip_grad_norm(grads, outs, sizes, dtypes, n, float(max_norm), norm.data_ptr(),
                                  ws, nws, h)
     _call(_invoke(first, stream, run), "pclip_grad_norm")
