@@ -59,7 +59,7 @@ template <class E>
 struct GluGradEpi {
     static constexpr lp::EpiKind kind = lp::kPlain;
     static constexpr bool kWalk = false;
-    static constexpr int kAhead = 4;
+    static constexpr int kAhead = 2;
     Rows gate, up;       // as the forward pass kept them
     Rows h, dgate, dup;  // padded rows: whole chunks, zeros past F
     int act;
@@ -88,11 +88,9 @@ struct GluGradEpi {
                     u[q] *= v;                                        // h
                     d[q] *= v;                                        // du
                 }
-                if (h) store8<E>(h, row, col, 8, u);
-                if (dgate) {
-                    store8<E>(dgate, row, col, 8, s);
-                    store8<E>(dup, row, col, 8, d);
-                }
+                store8<E>(h, row, col, 8, u);
+                store8<E>(dgate, row, col, 8, s);
+                store8<E>(dup, row, col, 8, d);
             });
         });
     }
@@ -155,14 +153,11 @@ struct Ffn {
     static hipError_t backward(const FfnGradCall& c, Arena& ar, hipStream_t stream) {
         const int cus = compute_units();
         const int64_t f8 = round_up(c.F, 8);
-        const bool need_d = c.dx || c.dw_in;
         hipError_t rc;
         View dy = {}, wo = {};
         if ((rc = operand(c.dy, c.lddy, c.M, c.N, ar, stream, dy)) != hipSuccess) return rc;
-        uint16_t* h = nullptr;
-        if (c.dw_out) h = static_cast<uint16_t*>(ar.take(c.M * f8 * 2));
-        uint16_t* d = nullptr;
-        if (need_d) d = static_cast<uint16_t*>(ar.take(c.M * 2 * f8 * 2));
+        uint16_t* h = static_cast<uint16_t*>(ar.take(c.M * f8 * 2));
+        uint16_t* d = static_cast<uint16_t*>(ar.take(c.M * 2 * f8 * 2));
         if (c.M > 0 && c.F > 0) {
             if ((rc = operand(c.w_out, c.ldwo, c.F, c.N, ar, stream, wo)) != hipSuccess) return rc;
             const Cut cut = choose_cut(c.M, c.F, c.N, cus, 16);
@@ -171,7 +166,7 @@ struct Ffn {
                 const uint16_t* gu = static_cast<const uint16_t*>(c.gate_up);
                 const GluGradEpi<E> epi = {make_rows(gu, c.ldgu), make_rows(gu + c.F, c.ldgu),
                                            {h, (int)f8}, {d, (int)(2 * f8)},
-                                           {d ? d + f8 : d, (int)(2 * f8)}, c.act};
+                                           {d + f8, (int)(2 * f8)}, c.act};
                 rc = lp::launch_product<E, true, true>(g, cut, epi, stream);
                 if (rc != hipSuccess) return rc;
             }

@@ -446,8 +446,8 @@ __device__ __forceinline__ void run_k(Product<TL>& pr, Copies<TL>& cp, char* sme
 // wave's part.  Exchanging the odd 16-lane rows of block j with the even ones
 // of block j + 1 (one v_permlane16_swap per register) leaves every lane with
 // 8 consecutive columns, 16 (j + g % 2) + 8 (g / 2) .. + 7, of one row: a
-// functor's loads and stores are 16 bytes a lane, 64 bytes a row.  No LDS and
-// no barrier, so the ring is free for the next tile's copies meanwhile.
+// functor's loads and stores are 16 bytes a lane, 64 bytes a row, with no LDS
+// and no barrier.
 //
 // Functors on chunks of 8 fp32 values (columns col .. col + nv - 1 of a row, nv <
 // 8 only at the matrix's edge).  epi.from(m0) is the functor for the tile whose
@@ -482,10 +482,10 @@ __device__ __forceinline__ void chunk8(const floatx4& a, const floatx4& b, float
     }
 }
 
-// The chunks of one tile; FULL: the tile lies inside the matrix.
-template <class TL, class Epi, bool FULL>
-__device__ __forceinline__ void drain_chunks(const Product<TL>& pr, int M, int N, int row0, int col0,
-                                             const Epi epi) {
+// A tile inside the matrix.
+template <class TL, class Epi>
+__device__ __forceinline__ void drain_full(const Product<TL>& pr, int row0, int col0,
+                                           const Epi epi) {
     constexpr bool PAIR = Epi::kind == kPaired;
     constexpr int JP = TL::FN / (PAIR ? 4 : 2);  // column chunks per lane
     constexpr int FM = TL::FM;
@@ -495,28 +495,23 @@ __device__ __forceinline__ void drain_chunks(const Product<TL>& pr, int M, int N
 #pragma unroll
         for (int jp = 0; jp < JP; ++jp) {
             const int col = col0 + 32 * jp;
-            const int nv = FULL ? 8 : min(8, N - col);
-            const int rows = nv > 0 ? M : 0;  // a lane past the last column has no rows
-            decltype(epi.column(0, 0)) column = {};
-            if (nv > 0) column = epi.column(col, nv);
+            const auto column = epi.column(col, 8);
             decltype(epi.load(0, 0, 0)) aux[AHEAD];
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i)
-                if (FULL || row0 + 16 * i < rows) aux[i] = epi.load(row0 + 16 * i, col, nv);
+            for (int i = 0; i < AHEAD; ++i) aux[i] = epi.load(row0 + 16 * i, col, 8);
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
                 const int row = row0 + 16 * i;
                 const auto now = aux[i % AHEAD];
-                if (i + AHEAD < FM && (FULL || row + 16 * AHEAD < rows))
-                    aux[i % AHEAD] = epi.load(row + 16 * AHEAD, col, nv);
-                float v[8];  // every lane takes part in the exchange
+                if (i + AHEAD < FM) aux[i % AHEAD] = epi.load(row + 16 * AHEAD, col, 8);
+                float v[8];
                 chunk8(pr.acc[2 * jp][i], pr.acc[2 * jp + 1][i], v);
                 if constexpr (PAIR) {
                     float u[8];
                     chunk8(pr.acc[2 * jp + 2][i], pr.acc[2 * jp + 3][i], u);
-                    if (FULL || row < rows) f(row, col, nv, v, u, column, now);
+                    f(row, col, 8, v, u, column, now);
                 } else {
-                    if (FULL || row < rows) f(row, col, nv, v, column, now);
+                    f(row, col, 8, v, column, now);
                 }
                 __builtin_amdgcn_sched_barrier(0);  // bounds what is in registers at once
             }
@@ -524,18 +519,86 @@ __device__ __forceinline__ void drain_chunks(const Product<TL>& pr, int M, int N
     });
 }
 
+// A tile at the matrix's edge: the accumulators go through the ring in bands
+// of rows (half of each wave's at a time where the tile does not fit), and a
+// loop over the band's chunks checks each against the edge.  (Checked chunks
+// unrolled like drain_full's made the code of both so large that the
+// registers of the K loop suffered.)  16-byte chunk c of LDS row r sits at
+// (c & 1) * CH/2 + ((c >> 1) ^ (r mod CH/2)): the two halves of 8 columns are
+// read from the two halves of the row, consecutive lanes consecutive chunks.
 template <class TL, class Epi>
-__device__ __forceinline__ void drain_epi(const Product<TL>& pr, int M, int N, int m0, int n0,
-                                          int tid, int wm, int wn, const Epi& epi) {
+__device__ __forceinline__ void drain_edge(char* smem, const Product<TL>& pr, int rows, int N,
+                                           int n0, int tid, int wm, int wn, const Epi epi) {
+    constexpr bool PAIR = Epi::kind == kPaired;
+    constexpr int CH = TL::BN / 4, ROWB = TL::BN * 4;
+    constexpr int NB = TL::BM * ROWB <= TL::LDS ? 1 : 2;
+    constexpr int RB = TL::BM / NB, WR = TL::TM / NB, IB = TL::FM / NB;
+    static_assert(RB * ROWB <= TL::LDS && TL::FM % NB == 0, "a band fits in the ring");
+    constexpr int LPR = (PAIR ? TL::BN / 2 : TL::BN) / 8;  // threads per row
+    constexpr int STEP = TL::T / LPR;                      // rows per pass
+    auto pos = [](int c, int row) {
+        return row * ROWB + ((c & 1) * (CH / 2) + ((c >> 1) ^ (row & (CH / 2 - 1)))) * 16;
+    };
+    auto read8 = [&](int c, int row, float(&v)[8]) __attribute__((always_inline)) {
+        const floatx4 lo = *reinterpret_cast<const floatx4*>(smem + pos(2 * c, row));
+        const floatx4 hi = *reinterpret_cast<const floatx4*>(smem + pos(2 * c + 1, row));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            v[q] = lo[q];
+            v[4 + q] = hi[q];
+        }
+    };
+    const int r = tid & 15, g = (tid >> 4) & 3;
+    const int cl = tid % LPR;
+    const int col = n0 + cl * 8, nv = min(8, N - col);
+    epi.with([&](const auto& f) __attribute__((always_inline)) {
+#pragma unroll
+        for (int p = 0; p < NB; ++p) {
+            __syncthreads();  // the ring, or the band before, has been read
+#pragma unroll
+            for (int j = 0; j < TL::FN; ++j)
+#pragma unroll
+                for (int ii = 0; ii < IB; ++ii)
+                    *reinterpret_cast<floatx4*>(
+                        smem + pos((wn * TL::TN + 16 * j) / 4 + g, wm * WR + 16 * ii + r)) =
+                        pr.acc[j][p * IB + ii];
+            __syncthreads();
+            if (nv > 0) {
+                const auto column = epi.column(col, nv);
+#pragma unroll 1
+                for (int l = tid / LPR; l < RB; l += STEP) {
+                    const int row = (l / WR) * TL::TM + p * WR + l % WR;
+                    if (row >= rows) continue;
+                    const auto aux = epi.load(row, col, nv);
+                    float v[8];
+                    if constexpr (PAIR) {
+                        const int c = (cl >> 2) * 8 + (cl & 3);  // the first half's chunk
+                        float u[8];
+                        read8(c, l, v);
+                        read8(c + 4, l, u);
+                        f(row, col, nv, v, u, column, aux);
+                    } else {
+                        read8(cl, l, v);
+                        f(row, col, nv, v, column, aux);
+                    }
+                }
+            }
+        }
+    });
+}
+
+template <class TL, class Epi>
+__device__ __forceinline__ void drain_epi(char* smem, const Product<TL>& pr, int M, int N, int m0,
+                                          int n0, int tid, int wm, int wn, const Epi& epi) {
     constexpr bool PAIR = Epi::kind == kPaired;
     constexpr int COLS = PAIR ? TL::BN / 2 : TL::BN;
-    const int r = tid & 15, g = (tid >> 4) & 3;
-    const int row0 = wm * TL::TM + r;
-    const int col0 = n0 + wn * (PAIR ? 32 : TL::TN) + 16 * (g & 1) + 8 * (g >> 1);
-    if (m0 + TL::BM <= M && n0 + COLS <= N)
-        drain_chunks<TL, Epi, true>(pr, M - m0, N, row0, col0, epi.from(m0));
-    else
-        drain_chunks<TL, Epi, false>(pr, M - m0, N, row0, col0, epi.from(m0));
+    if (m0 + TL::BM <= M && n0 + COLS <= N) {
+        const int r = tid & 15, g = (tid >> 4) & 3;
+        drain_full<TL>(pr, wm * TL::TM + r,
+                       n0 + wn * (PAIR ? 32 : TL::TN) + 16 * (g & 1) + 8 * (g >> 1), epi.from(m0));
+    } else {
+        drain_edge<TL>(smem, pr, M - m0, N, n0, tid, wm, wn, epi.from(m0));
+    }
 }
 
 // Row functors: each row of the tile is reduced over its columns, first in
@@ -680,12 +743,12 @@ void product_kernel(const Args g, const Epi epi) {
         }
         if constexpr (SPLIT) {
             const StorePart sp = {g.part + (int64_t)blockIdx.y * g.M * g.part_ld, g.part_ld};
-            drain_epi<TL>(pr, g.M, g.N, m0, n0, tid_d, wm, wn, sp);
+            drain_epi<TL>(smem, pr, g.M, g.N, m0, n0, tid_d, wm, wn, sp);
         } else if constexpr (Epi::kind == kRows) {
             drain_rows<TL>(smem + (TL::S - 1) * TL::STAGE, pr, g.M, g.N, m0, tn_now, tid_d, wm, wn,
                            epi);
         } else {
-            drain_epi<TL>(pr, g.M, g.N, m0, n0, tid_d, wm, wn, epi);
+            drain_epi<TL>(smem, pr, g.M, g.N, m0, n0, tid_d, wm, wn, epi);
         }
         if (!more) break;
     }
