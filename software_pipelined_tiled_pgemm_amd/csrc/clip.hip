@@ -58,13 +58,23 @@ __device__ __forceinline__ int locate(const Table& t, int chunk, int& index) {
 }
 
 // Loads and stores of 8 values from any element-aligned address (the
-// compiler's unaligned 16-byte accesses).
+// compiler's unaligned 16-byte accesses).  STREAM: past the caches, for data
+// that is not used again.
+typedef u4_t u4_any __attribute__((aligned(2)));
+template <bool STREAM>
+__device__ __forceinline__ u4_t get16(const void* p) {
+    const u4_any* q = static_cast<const u4_any*>(p);
+    return *q;
+}
+__device__ __forceinline__ void put16(void* p, u4_t w) {
+    __builtin_nontemporal_store(w, static_cast<u4_any*>(p));
+}
 template <class E>
 struct Vec8 {
     typedef uint16_t elem;
+    template <bool STREAM>
     __device__ static __forceinline__ void load(const elem* p, float (&v)[8]) {
-        u4_t w;
-        __builtin_memcpy(&w, p, 16);
+        const u4_t w = get16<STREAM>(p);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             v[2 * q] = E::get((uint16_t)w[q]);
@@ -74,7 +84,7 @@ struct Vec8 {
     __device__ static __forceinline__ void store(elem* p, const float (&v)[8]) {
         const u4_t w = {E::put2(v[0], v[1]), E::put2(v[2], v[3]), E::put2(v[4], v[5]),
                         E::put2(v[6], v[7])};
-        __builtin_memcpy(p, &w, 16);
+        put16(p, w);
     }
     __device__ static __forceinline__ float get(const elem* p) { return E::get(*p); }
     __device__ static __forceinline__ void put(elem* p, float v) { *p = E::put(v); }
@@ -83,11 +93,18 @@ struct F32 {};
 template <>
 struct Vec8<F32> {
     typedef float elem;
+    template <bool STREAM>
     __device__ static __forceinline__ void load(const elem* p, float (&v)[8]) {
-        __builtin_memcpy(v, p, 32);
+        const u4_t lo = get16<STREAM>(p), hi = get16<STREAM>(p + 4);
+        __builtin_memcpy(v, &lo, 16);
+        __builtin_memcpy(v + 4, &hi, 16);
     }
     __device__ static __forceinline__ void store(elem* p, const float (&v)[8]) {
-        __builtin_memcpy(p, v, 32);
+        u4_t lo, hi;
+        __builtin_memcpy(&lo, v, 16);
+        __builtin_memcpy(&hi, v + 4, 16);
+        put16(p, lo);
+        put16(p + 4, hi);
     }
     __device__ static __forceinline__ float get(const elem* p) { return *p; }
     __device__ static __forceinline__ void put(elem* p, float v) { *p = v; }
@@ -116,14 +133,14 @@ __device__ __forceinline__ double chunk_squares(const void* in, int64_t from, in
     for (; i + 3 * 8 * kThreads + 8 <= to; i += 4 * 8 * kThreads) {
         float v[4][8];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) Vec8<E>::load(p + i + u * 8 * kThreads, v[u]);
+        for (int u = 0; u < 4; ++u) Vec8<E>::template load<false>(p + i + u * 8 * kThreads, v[u]);
 #pragma unroll
         for (int u = 0; u < 4; ++u) s += squares<E>(v[u]);
     }
     for (; i < to; i += 8 * kThreads) {
         float v[8];
         if (i + 8 <= to) {
-            Vec8<E>::load(p + i, v);
+            Vec8<E>::template load<false>(p + i, v);
         } else {
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] = i + q < to ? Vec8<E>::get(p + i + q) : 0.0f;
@@ -187,7 +204,7 @@ __device__ __forceinline__ void chunk_scale(const void* in, void* out, int64_t f
     for (; i + 3 * 8 * kThreads + 8 <= to; i += 4 * 8 * kThreads) {
         float v[4][8];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) Vec8<E>::load(p + i + u * 8 * kThreads, v[u]);
+        for (int u = 0; u < 4; ++u) Vec8<E>::template load<true>(p + i + u * 8 * kThreads, v[u]);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
 #pragma unroll
@@ -198,7 +215,7 @@ __device__ __forceinline__ void chunk_scale(const void* in, void* out, int64_t f
     for (; i < to; i += 8 * kThreads) {
         if (i + 8 <= to) {
             float v[8];
-            Vec8<E>::load(p + i, v);
+            Vec8<E>::template load<true>(p + i, v);
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] *= f;
             Vec8<E>::store(o + i, v);

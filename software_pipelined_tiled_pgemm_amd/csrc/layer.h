@@ -21,11 +21,14 @@ struct View {
 struct Args {
     View a, b;
     int M, N, K;
-    int tiles_m, tiles_n, group_m;
+    int tiles_m, tiles_n;
     int pair_shift;  // > 0: B's columns are paired (see Operand::place); N counts one half
     int chunk;       // split-K: contraction indices per split
     float* part;     // split-K: partials [split][M][part_ld]
     int part_ld;
+    // Where not NULL, device memory with the number of rows in use, at most M
+    // (NN, NT) or K (TN): the others are left out.
+    const int* live;
 };
 
 // Layout of a product's operands (K-contiguous or K-rows).

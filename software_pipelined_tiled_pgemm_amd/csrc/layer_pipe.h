@@ -682,7 +682,19 @@ __global__ __launch_bounds__(TL::T, 1) __attribute__((amdgpu_waves_per_eu(2, 2))
 void product_kernel(const Args g, const Epi epi) {
     __shared__ __attribute__((aligned(1024))) char smem[TL::LDS];
     constexpr int COLS = Epi::kind == kPaired ? TL::BN / 2 : TL::BN;
-    const int tiles = g.tiles_m * g.tiles_n;
+    int M = g.M, Kfull = g.K, tiles_m = g.tiles_m;
+    if (g.live) {
+        const int n = *g.live;
+        if constexpr (TL::AKC) {
+            M = min(M, n);
+            tiles_m = (M + TL::BM - 1) / TL::BM;
+        } else {
+            Kfull = min(Kfull, n);
+        }
+    }
+    const int tiles = tiles_m * g.tiles_n;
+    if ((int)blockIdx.x >= tiles) return;
+    const int group_m = min(tiles_m, 4);  // bands of 4 tile rows, as in the plain GEMM
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -690,22 +702,22 @@ void product_kernel(const Args g, const Epi epi) {
     const uint32_t ring = lds_addr(smem);
 
     View va = g.a, vb = g.b;
-    int K = g.K;
+    int K = Kfull;
     if constexpr (SPLIT) {
         const int kb = blockIdx.y * g.chunk;
-        K = min(g.chunk, g.K - kb);
+        K = min(g.chunk, Kfull - kb);
         va.ptr += TL::AKC ? (int64_t)kb : (int64_t)kb * va.ld;
         vb.ptr += TL::BKC ? (int64_t)kb : (int64_t)kb * vb.ld;
     }
     const int shift = Epi::kind == kPaired ? g.pair_shift : 0;
 
     int blk = blockIdx.x, tm, tn;
-    tile_of_block(blk, tiles, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
+    tile_of_block(blk, tiles, tiles_m, g.tiles_n, group_m, tm, tn);
     Product<TL> pr;
     pr.place(wm, wn, lane);
     Copies<TL> cp;
     if (K > 0) {
-        cp.init(lane, wave, va, vb, tm * TL::BM, g.M, tn * COLS, g.N, shift);
+        cp.init(lane, wave, va, vb, tm * TL::BM, M, tn * COLS, g.N, shift);
         cp.start(K, ring, wave);
     }
     for (;;) {
@@ -718,7 +730,7 @@ void product_kernel(const Args g, const Epi epi) {
                     pr, cp, smem, K, wave, tid, [&]() __attribute__((always_inline)) {
                         int l = lane;
                         asm volatile("" : "+v"(l));
-                        cp.a.place(l, wave, va, m0, g.M, 0);
+                        cp.a.place(l, wave, va, m0, M, 0);
                         cp.b.place(l, wave, vb, n0, g.N, shift);
                     });
             });
@@ -735,20 +747,20 @@ void product_kernel(const Args g, const Epi epi) {
         int tid_d = tid;
         asm volatile("" : "+v"(tid_d));
         if (Epi::kWalk && more) {
-            tile_of_block(blk, tiles, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
+            tile_of_block(blk, tiles, tiles_m, g.tiles_n, group_m, tm, tn);
             if (K > 0) {
-                cp.init(tid_d & 63, wave, va, vb, tm * TL::BM, g.M, tn * COLS, g.N, shift);
+                cp.init(tid_d & 63, wave, va, vb, tm * TL::BM, M, tn * COLS, g.N, shift);
                 cp.start(K, ring, wave);
             }
         }
         if constexpr (SPLIT) {
             const StorePart sp = {g.part + (int64_t)blockIdx.y * g.M * g.part_ld, g.part_ld};
-            drain_epi<TL>(smem, pr, g.M, g.N, m0, n0, tid_d, wm, wn, sp);
+            drain_epi<TL>(smem, pr, M, g.N, m0, n0, tid_d, wm, wn, sp);
         } else if constexpr (Epi::kind == kRows) {
-            drain_rows<TL>(smem + (TL::S - 1) * TL::STAGE, pr, g.M, g.N, m0, tn_now, tid_d, wm, wn,
+            drain_rows<TL>(smem + (TL::S - 1) * TL::STAGE, pr, M, g.N, m0, tn_now, tid_d, wm, wn,
                            epi);
         } else {
-            drain_epi<TL>(smem, pr, g.M, g.N, m0, n0, tid_d, wm, wn, epi);
+            drain_epi<TL>(smem, pr, M, g.N, m0, n0, tid_d, wm, wn, epi);
         }
         if (!more) break;
     }
@@ -759,9 +771,9 @@ void product_kernel(const Args g, const Epi epi) {
 template <class Epi>
 __global__ __launch_bounds__(256) void finish_kernel(const float* __restrict__ part, int64_t part_ld,
                                                      int splits, int M, int N, int pair_shift,
-                                                     const Epi epi) {
+                                                     const int* live, const Epi epi) {
     const int cpr = (N + 7) / 8;
-    const int64_t total = (int64_t)M * cpr;
+    const int64_t total = (int64_t)(live ? min(M, *live) : M) * cpr;
     const int64_t slice = (int64_t)M * part_ld;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
          i += (int64_t)gridDim.x * 256) {
@@ -819,8 +831,6 @@ hipError_t launch_tiles(Args g, int splits, const Epi& epi, hipStream_t stream) 
     constexpr int COLS = Epi::kind == kPaired ? TL::BN / 2 : TL::BN;
     g.tiles_m = (g.M + TL::BM - 1) / TL::BM;
     g.tiles_n = (g.N + COLS - 1) / COLS;
-    // Bands of 4 tile rows, as in the plain GEMM's launch.
-    g.group_m = g.tiles_m < 4 ? g.tiles_m : 4;
     // One 256x256 workgroup fills a CU's LDS: at most one per CU, each walking
     // several tiles (a multiple of 8 workgroups keeps tile_of_block's map of
     // tiles to XCDs).
@@ -843,12 +853,12 @@ struct Tiles {
 };
 
 template <class Epi>
-hipError_t launch_finish(const Args& g, int splits, int pair_shift, const Epi& epi,
-                         hipStream_t stream) {
+hipError_t launch_finish(const Args& g, int splits, int pair_shift, const int* live,
+                         const Epi& epi, hipStream_t stream) {
     const int64_t chunks = (int64_t)g.M * ((g.N + 7) / 8);
     const int64_t blocks = std::min<int64_t>((chunks + 255) / 256, 4096);
     hipLaunchKernelGGL((finish_kernel<Epi>), dim3((unsigned)blocks), dim3(256), 0, stream, g.part,
-                       (int64_t)g.part_ld, splits, g.M, g.N, pair_shift, epi);
+                       (int64_t)g.part_ld, splits, g.M, g.N, pair_shift, live, epi);
     return hipGetLastError();
 }
 
@@ -867,7 +877,8 @@ hipError_t launch_product(const Args& g, const layer::Cut& cut, const Epi& epi,
                                                                            : layer::kF16,
                                               layout, p, cut, stream);
     if (rc != hipSuccess) return rc;
-    return launch_finish(g, cut.splits, Epi::kind == kPaired ? g.pair_shift : 0, epi, stream);
+    return launch_finish(g, cut.splits, Epi::kind == kPaired ? g.pair_shift : 0,
+                         AKC ? g.live : nullptr, epi, stream);
 }
 
 }  // namespace lp

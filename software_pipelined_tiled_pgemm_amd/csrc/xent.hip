@@ -11,7 +11,8 @@
 // joins the tiles of a row.  Backward, piece by piece of the vocabulary: the
 // piece's logits again, turned into dl in the epilogue and kept in 16 bits;
 // then the piece's part of dx (summed over the pieces in fp32) and its rows
-// of dW.  8 M V D flops in all, 2 of them for the logits that were not kept.
+// of dW, all over the rows that are not ignored alone.  8 M V D flops in all, 2
+// of them for the logits that were not kept.
 //
 // dl in 16 bits: |exp(l - lse) - [.]| <= 1, and a softmax over V entries is
 // mostly values near 1/V, which fp16 holds with few bits or none.  So dl is kept
@@ -162,57 +163,113 @@ __global__ __launch_bounds__(1024) void total_kernel(const float* __restrict__ r
     }
 }
 
-// Row weights of the backward pass: c_m in [-1, 1] and the factor of the
-// sums, by one workgroup.  Ignored rows weigh 0; a weight that is not finite,
-// or belongs to an invalid target (NaN), stands for its row alone.
+// Row weights of the backward pass: c_m in [-1, 1], the factor of the sums,
+// and the rows that count (c_m not 0) packed together, by one workgroup whose
+// threads take consecutive runs of rows.  Ignored rows weigh 0; a weight that
+// is not finite, or belongs to an invalid target (NaN), stands for its row
+// alone.
+//   rank[m]: place of row m among the rows that count, -1 where it does not;
+//   row[j]: the j-th row that counts; live: how many there are.
+struct Kept {
+    int* rank;
+    int* row;
+    int* live;
+    float* weight;    // [j]
+    float* lse;       // [j]
+    int64_t* target;  // [j]
+    float* factor;
+};
+
 __global__ __launch_bounds__(1024) void weights_kernel(const int64_t* __restrict__ target,
                                                        int64_t ignore_index, int64_t V, int64_t M,
                                                        int reduction,
-                                                       const float* __restrict__ dloss, float scale,
-                                                       float* __restrict__ weight,
-                                                       float* __restrict__ factor) {
+                                                       const float* __restrict__ dloss,
+                                                       const float* __restrict__ lse, float scale,
+                                                       const Kept k) {
     __shared__ float tops[1024];
-    __shared__ int64_t counts[1024];
-    const bool each = reduction == PGEMM_REDUCE_NONE;
+    __shared__ int counts[1024];
+    __shared__ int places[1024];
+    const int t = threadIdx.x;
+    const bool each = reduction == PGEMM_REDUCE_NONE && dloss;
+    const int64_t per = (M + 1023) / 1024;
+    const int64_t r0 = t * per, r1 = r0 + per < M ? r0 + per : M;
     float top = 0.0f;
-    int64_t n = 0;
-    for (int64_t r = threadIdx.x; r < M; r += 1024) {
+    int n = 0;
+    for (int64_t r = r0; r < r1; ++r) {
         if (target[r] == ignore_index) continue;
         ++n;
-        if (each && dloss) {
+        if (each) {
             const float a = fabsf(dloss[r]);
             if (a < INFINITY) top = fmaxf(top, a);
         }
     }
-    tops[threadIdx.x] = top;
-    counts[threadIdx.x] = n;
+    tops[t] = top;
+    counts[t] = n;
     for (int h = 512; h > 0; h >>= 1) {
         __syncthreads();
-        if (threadIdx.x < h) {
-            tops[threadIdx.x] = fmaxf(tops[threadIdx.x], tops[threadIdx.x + h]);
-            counts[threadIdx.x] += counts[threadIdx.x + h];
+        if (t < h) {
+            tops[t] = fmaxf(tops[t], tops[t + h]);
+            counts[t] += counts[t + h];
         }
     }
     __syncthreads();
     top = tops[0];
-    n = counts[0];
-    for (int64_t r = threadIdx.x; r < M; r += 1024) {
-        const int64_t t = target[r];
-        float c = 1.0f;
-        if (each && dloss) {
-            const float g = dloss[r];
-            c = fabsf(g) < INFINITY ? (top > 0.0f ? g / top : 0.0f) : g;
-        }
-        if (t == ignore_index)
-            c = 0.0f;
-        else if (t < 0 || t >= V)
-            c = __builtin_nanf("");
-        weight[r] = c;
+    auto weight = [&](int64_t r) {
+        const int64_t at = target[r];
+        if (at == ignore_index) return 0.0f;
+        if (at < 0 || at >= V) return __builtin_nanf("");
+        if (!each) return 1.0f;
+        const float g = dloss[r];
+        return fabsf(g) < INFINITY ? (top > 0.0f ? g / top : 0.0f) : g;
+    };
+    int mine = 0;
+    for (int64_t r = r0; r < r1; ++r) mine += weight(r) != 0.0f;
+    places[t] = mine;
+    for (int h = 1; h < 1024; h <<= 1) {  // running sums
+        __syncthreads();
+        const int before = t >= h ? places[t - h] : 0;
+        __syncthreads();
+        places[t] += before;
     }
-    if (threadIdx.x == 0) {
-        float f = each ? (dloss ? top : 1.0f) : (dloss ? dloss[0] : 1.0f);
-        if (reduction == PGEMM_REDUCE_MEAN) f /= (float)(n > 0 ? n : 1);
-        factor[0] = f / scale;
+    int j = places[t] - mine;
+    for (int64_t r = r0; r < r1; ++r) {
+        const float c = weight(r);
+        k.rank[r] = c != 0.0f ? j : -1;
+        if (c != 0.0f) {
+            k.row[j] = (int)r;
+            k.weight[j] = c;
+            k.lse[j] = lse[r];
+            k.target[j] = target[r];
+            ++j;
+        }
+    }
+    if (t == 1023) k.live[0] = places[1023];
+    if (t == 0) {
+        float f = each ? top : (dloss ? dloss[0] : 1.0f);
+        if (reduction == PGEMM_REDUCE_MEAN) f /= (float)(counts[0] > 0 ? counts[0] : 1);
+        k.factor[0] = f / scale;
+    }
+}
+
+// The rows of x that count, packed together in padded rows of whole chunks;
+// the rows of dx (where asked for) that do not are zeroed.
+__global__ __launch_bounds__(256) void gather_kernel(const Rows x, const Rows dx, uint16_t* kept,
+                                                     int kept_ld, const int* __restrict__ rank,
+                                                     int64_t M, int D) {
+    const int cpr = (D + 7) / 8;
+    const int64_t total = M * cpr;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
+         i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / cpr;
+        const int col = (int)(i - r * cpr) * 8, nv = min(8, D - col);
+        const int j = rank[r];
+        if (j >= 0) {
+            *reinterpret_cast<u4_t*>(kept + (int64_t)j * kept_ld + col) =
+                load8_bits(x.from(r), 0, col, nv);
+        } else if (dx) {
+            const float zero[8] = {};
+            store8<F16>(dx.from(r), 0, col, nv, zero);
+        }
     }
 }
 
@@ -250,14 +307,14 @@ struct DlogitEpi {
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             const float p = exp_fast(v[q] - l) - (t == q ? 1.0f : 0.0f);
-            // an ignored row is 0 whatever its logits are
-            v[q] = (q < nv && c != 0.0f) ? c * p : 0.0f;
+            v[q] = q < nv ? c * p : 0.0f;
         }
         store8<E>(dl, row, col, 8, v);
     }
 };
 
-// dx over the pieces: fp32 sums in the workspace, the last piece rounds.
+// The gradients' epilogue.  dx over the pieces: fp32 sums in the workspace, the
+// last piece rounds; its rows go where the rows that count came from (map).
 template <class E>
 struct SumEpi {
     static constexpr lp::EpiKind kind = lp::kPlain;
@@ -266,13 +323,16 @@ struct SumEpi {
     float* sum;  // [M][ld], NULL where there is one piece only
     int ld;
     Rows out;
+    const int* map;  // NULL: rows as they are
     const float* factor;
     int first, last;
     __device__ __forceinline__ SumEpi from(int64_t r) const {
-        return {sum ? sum + r * ld : sum, ld, out.from(r), factor, first, last};
+        return {sum ? sum + r * ld : sum, ld,   map ? out : out.from(r), map ? map + r : map,
+                factor,                   first, last};
     }
     struct Before {
         floatx4 lo, hi;
+        int row;
     };
     template <class Run>
     __device__ __forceinline__ void with(Run&& run) const {
@@ -280,9 +340,13 @@ struct SumEpi {
     }
     __device__ __forceinline__ float column(int, int) const { return factor[0]; }
     __device__ __forceinline__ Before load(int row, int col, int) const {
-        if (!sum || first) return {};
+        Before b = {};
+        if (map && last) b.row = map[row];
+        if (!sum || first) return b;
         const float* p = sum + (uint32_t)(row * ld + col);
-        return {*reinterpret_cast<const floatx4*>(p), *reinterpret_cast<const floatx4*>(p + 4)};
+        b.lo = *reinterpret_cast<const floatx4*>(p);
+        b.hi = *reinterpret_cast<const floatx4*>(p + 4);
+        return b;
     }
     __device__ __forceinline__ void operator()(int row, int col, int nv, float (&v)[8], float f,
                                                const Before& b) const {
@@ -306,7 +370,10 @@ struct SumEpi {
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q) v[q] *= f;
-        store8<E>(out, row, col, nv, v);
+        if (map)
+            store8<E>(out.from(b.row), 0, col, nv, v);
+        else
+            store8<E>(out, row, col, nv, v);
     }
 };
 
@@ -386,15 +453,24 @@ struct Xent {
     static hipError_t backward(const XentGradCall& c, Arena& ar, hipStream_t stream) {
         const int cus = compute_units();
         hipError_t rc;
-        View x, w;
-        if ((rc = operand(c.x, c.ldx, c.M, c.D, ar, stream, x)) != hipSuccess) return rc;
+        View w;
         const int64_t step = piece_rows(c.V, kPieceBytes / (2 * std::max<int64_t>(c.M, 1)));
         const int64_t s8 = round_up(step, 8), d8 = round_up(c.D, 8);
         const int64_t pieces = (c.V + step - 1) / step;
         uint16_t* room = nullptr;
         if (!direct(c.w, c.ldw, c.D)) room = static_cast<uint16_t*>(ar.take(step * d8 * 2));
-        float* weight = static_cast<float*>(ar.take(c.M * 4));
-        float* factor = static_cast<float*>(ar.take(4));
+        // The rows that count are packed together: the products take them
+        // alone, and nothing of an ignored row (it may hold anything) reaches
+        // a gradient.  The copy also serves as x in whole chunks.
+        Kept k;
+        k.rank = static_cast<int*>(ar.take(c.M * 4));
+        k.row = static_cast<int*>(ar.take(c.M * 4));
+        k.weight = static_cast<float*>(ar.take(c.M * 4));
+        k.lse = static_cast<float*>(ar.take(c.M * 4));
+        k.target = static_cast<int64_t*>(ar.take(c.M * 8));
+        k.live = static_cast<int*>(ar.take(4));
+        k.factor = static_cast<float*>(ar.take(4));
+        uint16_t* kept = static_cast<uint16_t*>(ar.take(c.M * d8 * 2));
         uint16_t* dl = static_cast<uint16_t*>(ar.take(c.M * s8 * 2));
         float* sum = nullptr;
         if (c.dx && pieces > 1) sum = static_cast<float*>(ar.take(c.M * d8 * 4));
@@ -415,11 +491,21 @@ struct Xent {
             g.K = (int)K;
             g.part = part;
             g.part_ld = (int)round_up(N, 8);
+            g.live = k.live;
             return g;
         };
         hipLaunchKernelGGL(weights_kernel, dim3(1), dim3(1024), 0, stream, c.target, c.ignore_index,
-                           c.V, c.M, c.reduction, c.dloss, grad_scale<E>(), weight, factor);
+                           c.V, c.M, c.reduction, c.dloss, c.lse, grad_scale<E>(), k);
         if ((rc = hipGetLastError()) != hipSuccess) return rc;
+        if (c.M > 0 && c.D > 0) {
+            const int64_t chunks = c.M * (d8 / 8);
+            hipLaunchKernelGGL(gather_kernel,
+                               dim3((unsigned)std::min<int64_t>((chunks + 255) / 256, 1 << 16)),
+                               dim3(256), 0, stream, make_rows(c.x, c.ldx),
+                               make_rows(c.dx, c.lddx), kept, (int)d8, k.rank, c.M, (int)c.D);
+            if ((rc = hipGetLastError()) != hipSuccess) return rc;
+        }
+        const View x = {kept, (int)d8};
         for (int64_t v0 = 0; v0 < c.V; v0 += step) {
             const int64_t n = std::min(step, c.V - v0);
             const bool first = v0 == 0, last = v0 + n == c.V;
@@ -427,12 +513,13 @@ struct Xent {
                 return rc;
             const View dv = {dl, (int)s8};
             if (c.M > 0) {
-                const DlogitEpi<E> epi = {{dl, (int)s8}, c.lse, weight, c.target, v0};
+                const DlogitEpi<E> epi = {{dl, (int)s8}, k.lse, k.weight, k.target, v0};
                 rc = lp::launch_product<E, true, true>(product(x, w, c.M, n, c.D), cl, epi, stream);
                 if (rc != hipSuccess) return rc;
             }
             if (c.dx && c.M > 0 && c.D > 0) {
-                const SumEpi<E> epi = {sum, (int)d8, make_rows(c.dx, c.lddx), factor, first, last};
+                const SumEpi<E> epi = {sum,      (int)d8, make_rows(c.dx, c.lddx), k.row,
+                                       k.factor, first,   last};
                 // the last piece may be shorter: its own contraction, the same cut
                 Cut cut = cx;
                 if (cut.splits > 1) cut.splits = (int)((n + cut.chunk - 1) / cut.chunk);
@@ -442,7 +529,7 @@ struct Xent {
             }
             if (c.dw && c.D > 0) {
                 uint16_t* out = static_cast<uint16_t*>(c.dw) + v0 * c.lddw;
-                const SumEpi<E> epi = {nullptr, 0, make_rows(out, c.lddw), factor, 1, 1};
+                const SumEpi<E> epi = {nullptr, 0, make_rows(out, c.lddw), nullptr, k.factor, 1, 1};
                 rc = lp::launch_product<E, false, false>(product(dv, x, n, c.D, c.M), cw, epi,
                                                          stream);
                 if (rc != hipSuccess) return rc;

@@ -9,7 +9,7 @@ dimension is contiguous; their rows may be strided.
 """
 from __future__ import annotations
 
-import ctypes
+import array
 import sys
 
 from . import _lib
@@ -398,43 +398,39 @@ def pclip_grad_norm(tensors, max_norm, out=None, norm=None, workspace=None, stre
     n = len(tensors)
     if not n:
         raise ValueError("tensors must not be empty")
+    every = tensors if out is None else tensors + list(out)
+    if out is not None and len(every) != 2 * n:
+        raise ValueError("out must have %d tensors" % n)
+    # Unbound methods over the whole list: a model has hundreds of gradients,
+    # and the calls' own time is most of the host's.
+    T = _TENSOR
+    devices = set(map(T.get_device, every))  # (TypeError if one is no tensor)
     first = tensors[0]
-    outs = None
-    every = tensors
-    if out is not None:
-        out = list(out)
-        if len(out) != n:
-            raise ValueError("out must have %d tensors" % n)
-        every = tensors + out
-    if not all([type(t) is _TENSOR or isinstance(t, _TENSOR) for t in every]):
-        raise TypeError("tensors and out must be torch.Tensors")
-    if len({t.get_device() for t in every}) != 1 or not first.is_cuda:
+    if len(devices) != 1 or not first.is_cuda:
         raise ValueError("tensors and out must be on one HIP device")
-    if not all([t.is_contiguous() for t in every]):
+    if not all(map(T.is_contiguous, every)):
         raise ValueError("tensors and out must be contiguous")
-    codes = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
-    try:
-        kinds = [codes[t.dtype] for t in tensors]
-    except KeyError as e:
-        raise TypeError("tensors must be float16, bfloat16 or float32, got %s" % e) from None
-    counts = [t.numel() for t in tensors]
-    if out is not None:
-        if [codes.get(t.dtype) for t in out] != kinds or [t.numel() for t in out] != counts:
-            raise ValueError("out must have the tensors' types and sizes")
-        outs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in out])
+    kinds = list(map({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}.get,
+                     [t.dtype for t in every]))
+    if None in kinds:
+        raise TypeError("tensors must be float16, bfloat16 or float32")
+    counts = list(map(T.numel, every))
+    if out is not None and (kinds[:n] != kinds[n:] or counts[:n] != counts[n:]):
+        raise ValueError("out must have the tensors' types and sizes")
+    pointers = array.array("Q", map(T.data_ptr, every))
+    sizes, dtypes = array.array("q", counts), array.array("i", kinds)
+    grads = pointers.buffer_info()[0]
+    outs = None if out is None else grads + n * pointers.itemsize
     if norm is None:
         norm = _new((), torch.float32, first.device, stream)
     else:
         _flat(norm, "norm", first, torch.float32, ())
-    grads = (ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors])
-    sizes = (ctypes.c_int64 * n)(*counts)
-    dtypes = (ctypes.c_int * n)(*kinds)
     L = lib()
     ws, nws, keep = _workspace(_need(L.pclip_grad_norm_workspace_bytes, first, n), workspace, first,
                                stream)
 
     def run(h):
-        return L.pclip_grad_norm(grads, outs, sizes, dtypes, n, float(max_norm), norm.data_ptr(),
-                                 ws, nws, h)
+        return L.pclip_grad_norm(grads, outs, sizes.buffer_info()[0], dtypes.buffer_info()[0], n,
+                                 float(max_norm), norm.data_ptr(), ws, nws, h)
     _call(_invoke(first, stream, run), "pclip_grad_norm")
     return norm
