@@ -357,8 +357,12 @@ int64_t plinear_bwd_workspace_bytes(int dtype, const void* dy, int64_t lddy, con
  * y = h W_out + residual.
  *   x [M,D], W_in [D,2F] (the F gate columns, then the F up columns),
  *   W_out [F,N], residual [M,N] (may be NULL), y [M,N].
- *   gate_up [M,2F] (may be NULL) receives [g | u] rounded to dtype, which the
- *   backward pass needs.  h is rounded once, as the operand of W_out.
+ *   gate_up [M,2F] (may be NULL) receives [g | u] for the backward pass, in 16
+ *   bits each: fp16 as they are; bf16 as 1 sign, 6 exponent (bias 31) and 9
+ *   fraction bits, a quarter of bf16's rounding, which would show in the
+ *   gradients (exponent field 0 is 0, the topmost code NaN: magnitudes below
+ *   2^-30 become 0, those from about 2^33 on NaN).  h is rounded once, as the
+ *   operand of W_out.
  *   y may be exactly residual or x.
  * Both projections, the activation and the product are one kernel.  The
  * workspace holds h (and what operands that need padding, and products cut

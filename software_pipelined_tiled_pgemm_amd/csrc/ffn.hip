@@ -14,7 +14,7 @@
 // W_in lie side by side, dx and dW_in are one product each.
 //
 // Roundings beyond one per output: h and [dg | du], once each, as operands of
-// the next product; g and u as kept for the backward pass.
+// the next product; g and u as kept for the backward pass (Kept16).
 #include "ffn.h"
 
 #include "layer_pipe.h"
@@ -43,8 +43,8 @@ struct GluEpi {
             run([&](int row, int col, int nv, float(&g)[8], float(&u)[8], lp::Nothing, lp::Nothing)
                     __attribute__((always_inline)) {
                 if (gate) {
-                    store8<E>(gate, row, col, nv, g);
-                    store8<E>(up, row, col, nv, u);
+                    store8<Kept16<E>>(gate, row, col, nv, g);
+                    store8<Kept16<E>>(up, row, col, nv, u);
                 }
                 // past F both are 0, and so is h
 #pragma unroll
@@ -79,8 +79,8 @@ struct GluGradEpi {
             run([&](int row, int col, int nv, float(&d)[8], lp::Nothing, const Kept& k)
                     __attribute__((always_inline)) {
                 float g[8], u[8], s[8];
-                unpack8<E>(k.g, g);
-                unpack8<E>(k.u, u);
+                unpack8_kept<E>(k.g, g);
+                unpack8_kept<E>(k.u, u);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     float v;

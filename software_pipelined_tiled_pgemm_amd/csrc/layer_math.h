@@ -52,6 +52,39 @@ struct BF16 {
     }
 };
 
+// How pffn keeps g and u for its backward pass, in 16 bits.  The gradients
+// take products of them, so their rounding shows there: rounded to bf16 they
+// double the error of dW_out (2.1 roundings of its size in all, against 1.4
+// for h and the output alone).  fp16 keeps the values themselves.  bf16 keeps
+// them with 6 exponent and 9 fraction bits (bias 31), a quarter of bf16's
+// rounding (1.5 in all): magnitudes below 2^-30 become 0, those that round to
+// 2^33 - 2^23 and more, infinities and NaN become NaN (the topmost code).
+template <class E>
+struct Kept16 {
+    __device__ static __forceinline__ uint32_t put2(float a, float b) { return E::put2(a, b); }
+    __device__ static __forceinline__ float get(uint16_t u) { return E::get(u); }
+};
+template <>
+struct Kept16<BF16> {
+    static constexpr uint32_t kRebias = 96u << 23;  // 127 - 31
+    // Rounds to nearest, ties away from zero.
+    __device__ static __forceinline__ uint32_t put(float f) {
+        const uint32_t bits = __builtin_bit_cast(uint32_t, f);
+        const uint32_t a = max(bits & 0x7FFFFFFFu, kRebias) - kRebias + 0x2000u;
+        return (min(a, 0x7FFFu << 14) >> 14) | ((bits >> 16) & 0x8000u);
+    }
+    __device__ static __forceinline__ uint32_t put2(float a, float b) {
+        return put(a) | (put(b) << 16);
+    }
+    __device__ static __forceinline__ float get(uint16_t u) {
+        const uint32_t c = u & 0x7FFFu;
+        uint32_t m = (c << 14) + kRebias;
+        m = c < 0x200u ? 0u : m;  // exponent field 0
+        m = c == 0x7FFFu ? 0x7FC00000u : m;
+        return __builtin_bit_cast(float, m | ((uint32_t)(u & 0x8000u) << 16));
+    }
+};
+
 // ---- activations -----------------------------------------------------------
 // exp2 and reciprocal are the hardware's (1 ulp), so an activation costs two
 // quarter-rate instructions and a few ordinary ones per value.
@@ -187,6 +220,15 @@ __device__ __forceinline__ void unpack8(const u4_t& w, float (&v)[8]) {
     }
 }
 
+template <class E>
+__device__ __forceinline__ void unpack8_kept(const u4_t& w, float (&v)[8]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        v[2 * q] = Kept16<E>::get((uint16_t)w[q]);
+        v[2 * q + 1] = Kept16<E>::get((uint16_t)(w[q] >> 16));
+    }
+}
+
 // The bits of 8 values, zeros from nv >= 1 on; row < 256.  At the edge the
 // loads past nv take the first value's address, so that all are issued at once
 // instead of one behind the other's branch.
@@ -211,12 +253,8 @@ __device__ __forceinline__ void load8(const Rows& m, int row, int col, int nv, f
     unpack8<E>(load8_bits(m, row, col, nv), v);
 }
 
-template <class E>
-__device__ __forceinline__ void store8(const Rows& m, int row, int col, int nv,
-                                       const float (&v)[8]) {
+__device__ __forceinline__ void store8_bits(const Rows& m, int row, int col, int nv, u4_t w) {
     uint16_t* p = m.ptr + (uint32_t)(row * m.ld + col);
-    const u4_t w = {E::put2(v[0], v[1]), E::put2(v[2], v[3]), E::put2(v[4], v[5]),
-                    E::put2(v[6], v[7])};
     if (nv == 8) {
         __builtin_memcpy(p, &w, 16);
     } else {
@@ -224,6 +262,14 @@ __device__ __forceinline__ void store8(const Rows& m, int row, int col, int nv,
         for (int q = 0; q < 7; ++q)
             if (q < nv) p[q] = (uint16_t)(w[q >> 1] >> (16 * (q & 1)));
     }
+}
+
+// F: how a pair of values is put (an element type, or Kept16 of one).
+template <class F>
+__device__ __forceinline__ void store8(const Rows& m, int row, int col, int nv,
+                                       const float (&v)[8]) {
+    store8_bits(m, row, col, nv, u4_t{F::put2(v[0], v[1]), F::put2(v[2], v[3]),
+                                      F::put2(v[4], v[5]), F::put2(v[6], v[7])});
 }
 
 }  // namespace

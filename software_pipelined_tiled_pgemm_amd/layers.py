@@ -227,8 +227,8 @@ def pffn(x, w_in, w_out, residual=None, act="silu", gate_up=None, out=None, work
     """(act(g) * u) @ w_out + residual with [g | u] = x @ w_in: the gated
     feed-forward block for x [M,D], w_in [D,2F], w_out [F,N].
 
-    gate_up: an [M,2F] tensor that receives [g | u], which pffn_bwd needs.
-    out may be residual or x."""
+    gate_up: an [M,2F] tensor that receives [g | u] for pffn_bwd (for bfloat16 in
+    a 16-bit form of its own, see include/pgemm.h).  out may be residual or x."""
     dt = _dtype(x, "x")
     a = _act(act)
     ldx = _mat(x, "x", x)

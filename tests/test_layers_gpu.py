@@ -182,6 +182,33 @@ FFN = [(1, 1, 1, 1), (1, 64, 96, 64), (5, 37, 51, 29), (130, 72, 129, 72), (64, 
        (129, 4096, 136, 24)]
 
 
+def kept(t):
+    """The values that pffn kept in gate_up: float16 as they are, for bfloat16
+    1 sign, 6 exponent (bias 31) and 9 fraction bits."""
+    if t.dtype is torch.float16:
+        return f64(t)
+    torch.cuda.synchronize()
+    c = t.contiguous().view(torch.int16).cpu().numpy().astype(np.int64) & 0xFFFF
+    exponent, fraction = (c >> 9) & 63, c & 511
+    v = np.where(exponent > 0, np.ldexp(1.0 + fraction / 512.0, exponent - 31), 0.0)
+    v = np.where((c & 0x7FFF) == 0x7FFF, np.nan, v)
+    return np.where(c >> 15, -v, v)
+
+
+def test_ffn_kept_range():
+    """Kept values of every size: g = x * w_in with one input and x = 1."""
+    v = np.array([0.0, 1.0, -1.5, 2.0 ** -30, 2.0 ** -31, -(2.0 ** 32), 2.0 ** 34, 1e38, np.inf,
+                  np.nan, 255.0, -(2.0 ** -29)])
+    w = torch.from_numpy(np.concatenate([v, v])[None]).to(torch.bfloat16).cuda()
+    gu = torch.empty((1, 24), dtype=torch.bfloat16, device="cuda")
+    pg.pffn(torch.ones((1, 1), dtype=torch.bfloat16, device="cuda"), w,
+            torch.zeros((12, 1), dtype=torch.bfloat16, device="cuda"), gate_up=gu)
+    exact = f64(w)[0]
+    a = np.abs(exact)
+    exact = np.where(a < 2.0 ** -30, 0.0, np.where(a < 2.0 ** 33, exact, np.nan))
+    assert np.array_equal(kept(gu)[0], exact, equal_nan=True)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("shape", FFN)
 def test_ffn(shape, dtype):
@@ -197,7 +224,9 @@ def test_ffn(shape, dtype):
     X, WI, WO, R = f64(x), f64(wi), f64(wo), f64(r)
     G, U = (X @ WI)[:, :F], (X @ WI)[:, F:]
     S = np.abs(X) @ np.abs(WI)
-    assert_near(gu, X @ WI, S, dtype, D, 0, "gate_up")
+    KU = UNIT[dtype] / (1 if dtype is torch.float16 else 4)  # the kept form's rounding
+    GU = kept(gu)
+    assert (np.abs(GU - X @ WI) <= KU * np.abs(X @ WI) + (D + 16) * 2.0 ** -23 * S + 2.0 ** -30).all()
     H = act_exact(G, act) * U
     # an error of g or u (fp32 accumulation) reaches h through the product
     e32 = (D + 16) * 2.0 ** -23
@@ -214,7 +243,7 @@ def test_ffn(shape, dtype):
     dy = rand((M, N), dtype, 35)
     a = rand((M, D), dtype, 36)
     dx, dwi, dwo = pg.pffn_bwd(dy, x, wi, wo, gu, act=act, dx_residual=a)
-    GU, DY, A = f64(gu), f64(dy), f64(a)
+    DY, A = f64(dy), f64(a)
     G, U = GU[:, :F], GU[:, F:]
     DH = DY @ WO.T
     DHS = np.abs(DY) @ np.abs(WO).T
