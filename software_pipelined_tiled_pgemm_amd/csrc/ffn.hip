@@ -88,9 +88,9 @@ struct GluGradEpi {
                     u[q] *= v;                                        // h
                     d[q] *= v;                                        // du
                 }
-                store8<E>(h, row, col, 8, u);
-                store8<E>(dgate, row, col, 8, s);
-                store8<E>(dup, row, col, 8, d);
+                store8<E, false>(h, row, col, 8, u);
+                store8<E, false>(dgate, row, col, 8, s);
+                store8<E, false>(dup, row, col, 8, d);
             });
         });
     }
