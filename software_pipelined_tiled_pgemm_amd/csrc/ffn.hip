@@ -37,19 +37,22 @@ struct GluEpi {
     }
     __device__ __forceinline__ lp::Nothing column(int, int) const { return {}; }
     __device__ __forceinline__ lp::Nothing load(int, int, int) const { return {}; }
-    template <class Run>
+    __device__ __forceinline__ bool aligned() const {
+        return !gate || (gate.aligned && up.aligned);
+    }
+    template <bool STREAM, class Run>
     __device__ __forceinline__ void with(Run&& run) const {
         with_act(act, [&](auto a) __attribute__((always_inline)) {
             run([&](int row, int col, int nv, float(&g)[8], float(&u)[8], lp::Nothing, lp::Nothing)
                     __attribute__((always_inline)) {
                 if (gate) {
-                    store8<Kept16<E>>(gate, row, col, nv, g);
-                    store8<Kept16<E>>(up, row, col, nv, u);
+                    store8<Kept16<E>, false>(gate, row, col, nv, g);
+                    store8<Kept16<E>, false>(up, row, col, nv, u);
                 }
                 // past F both are 0, and so is h
 #pragma unroll
                 for (int q = 0; q < 8; ++q) u[q] *= decltype(a)::value(g[q]);
-                store8<E>(h, row, col, 8, u);
+                store8<E, STREAM>(h, row, col, 8, u);
             });
         });
     }
@@ -59,7 +62,7 @@ template <class E>
 struct GluGradEpi {
     static constexpr lp::EpiKind kind = lp::kPlain;
     static constexpr bool kWalk = false;
-    static constexpr int kAhead = 2;
+    static constexpr int kAhead = 1;
     Rows gate, up;       // as the forward pass kept them
     Rows h, dgate, dup;  // padded rows: whole chunks, zeros past F
     int act;
@@ -73,7 +76,8 @@ struct GluGradEpi {
     __device__ __forceinline__ Kept load(int row, int col, int nv) const {
         return {load8_bits(gate, row, col, nv), load8_bits(up, row, col, nv)};
     }
-    template <class Run>
+    __device__ __forceinline__ bool aligned() const { return true; }
+    template <bool STREAM, class Run>
     __device__ __forceinline__ void with(Run&& run) const {
         with_act(act, [&](auto a) __attribute__((always_inline)) {
             run([&](int row, int col, int nv, float(&d)[8], lp::Nothing, const Kept& k)
@@ -125,7 +129,7 @@ struct Ffn {
         uint16_t* h = static_cast<uint16_t*>(ar.take(c.M * f8 * 2));
         const Sink s = {c.y, c.ldy, c.residual, c.ldr, nullptr, 0, nullptr, 0, 0};
         uint16_t* gu = static_cast<uint16_t*>(c.gate_up);
-        const GluEpi<E> epi = {{h, (int)f8},
+        const GluEpi<E> epi = {{h, (int)f8, 1},
                                make_rows(gu, c.ldgu),
                                make_rows(gu ? gu + c.F : nullptr, c.ldgu),
                                c.act};
@@ -165,8 +169,8 @@ struct Ffn {
             if (!ar.dry()) {
                 const uint16_t* gu = static_cast<const uint16_t*>(c.gate_up);
                 const GluGradEpi<E> epi = {make_rows(gu, c.ldgu), make_rows(gu + c.F, c.ldgu),
-                                           {h, (int)f8}, {d, (int)(2 * f8)},
-                                           {d + f8, (int)(2 * f8)}, c.act};
+                                           {h, (int)f8, 1}, {d, (int)(2 * f8), 1},
+                                           {d + f8, (int)(2 * f8), 1}, c.act};
                 rc = lp::launch_product<E, true, true>(g, cut, epi, stream);
                 if (rc != hipSuccess) return rc;
             }

@@ -196,17 +196,19 @@ __device__ __forceinline__ void with_act(int act, Run&& run) {
 // (nv < 8).
 struct Rows {
     uint16_t* ptr;
-    int ld;  // below 2^22
+    int ld;        // below 2^22
+    int aligned;  // whole chunks are 16-byte aligned
     __host__ __device__ explicit operator bool() const { return ptr != nullptr; }
     // The same matrix from row r on.  Kernels address the rows of a tile (at
     // most 256) from its first one: a uniform 64-bit base and a 32-bit offset.
     __device__ __forceinline__ Rows from(int64_t r) const {
-        return {ptr ? ptr + r * ld : ptr, ld};
+        return {ptr ? ptr + r * ld : ptr, ld, aligned};
     }
 };
 
 inline Rows make_rows(const void* p, int64_t ld) {
-    return {static_cast<uint16_t*>(const_cast<void*>(p)), (int)ld};
+    return {static_cast<uint16_t*>(const_cast<void*>(p)), (int)ld,
+            (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0};
 }
 
 typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
@@ -256,8 +258,11 @@ __device__ __forceinline__ void load8(const Rows& m, int row, int col, int nv, f
 // F: how a pair of values is put (an element type, or Kept16 of one).  STREAM:
 // past the caches, which keeps them for the operands that other workgroups
 // still fetch (4096^3 with its epilogue 118 -> 114 us, the vocabulary
-// gradients 1.6% faster); not for what the next launch reads at once.
-template <class F, bool STREAM = true>
+// gradients 1.6% faster); not for what the block's next products or its
+// backward pass read again (1% of its step), and not for chunks that straddle
+// lines, whose halves the caches join (a step of 2039 x 1025 x 2047: 86 us, past
+// the caches 94).
+template <class F, bool STREAM>
 __device__ __forceinline__ void store8(const Rows& m, int row, int col, int nv,
                                        const float (&v)[8]) {
     typedef u4_t u4_any __attribute__((aligned(2)));

@@ -457,9 +457,10 @@ __device__ __forceinline__ void run_k(Product<TL>& pr, Copies<TL>& cp, char* sme
 // with column = epi.column(col, nv), what a column chunk needs (bias), and aux
 // = epi.load(row, col, nv), what the functor reads of memory for the chunk;
 // these loads are issued kAhead chunks before their use, since a wait for
-// memory per chunk would dominate.  epi.with(run) calls run(f) once with the
-// functor proper, so that what is the same for all chunks (the activation) is
-// decided before the first one.
+// memory per chunk would dominate.  epi.with<STREAM>(run) calls run(f) once with
+// the functor proper, so that what is the same for all chunks (the activation,
+// whether stores go past the caches) is decided before the first one;
+// epi.aligned() says that chunks do not straddle 16-byte boundaries.
 // Functors on rows (kRows) see the accumulators themselves (see drain_rows).
 enum EpiKind { kPlain, kPaired, kRows };
 struct Nothing {};
@@ -482,7 +483,7 @@ __device__ __forceinline__ void chunk8(const floatx4& a, const floatx4& b, float
     }
 }
 
-// A tile inside the matrix.
+// A tile inside the matrix whose chunks are aligned.
 template <class TL, class Epi>
 __device__ __forceinline__ void drain_full(const Product<TL>& pr, int row0, int col0,
                                            const Epi epi) {
@@ -491,7 +492,7 @@ __device__ __forceinline__ void drain_full(const Product<TL>& pr, int row0, int 
     constexpr int FM = TL::FM;
     constexpr int AHEAD = Epi::kAhead < FM ? Epi::kAhead : FM;
     static_assert(!PAIR || TL::TN == 64, "32 columns of each half per wave");
-    epi.with([&](const auto& f) __attribute__((always_inline)) {
+    epi.template with<true>([&](const auto& f) __attribute__((always_inline)) {
 #pragma unroll
         for (int jp = 0; jp < JP; ++jp) {
             const int col = col0 + 32 * jp;
@@ -519,7 +520,7 @@ __device__ __forceinline__ void drain_full(const Product<TL>& pr, int row0, int 
     });
 }
 
-// A tile at the matrix's edge: the accumulators go through the ring in bands
+// A tile at the matrix's edge, or of unaligned rows: the accumulators go through the ring in bands
 // of rows (half of each wave's at a time where the tile does not fit), and a
 // loop over the band's chunks checks each against the edge.  (Checked chunks
 // unrolled like drain_full's made the code of both so large that the
@@ -551,7 +552,7 @@ __device__ __forceinline__ void drain_edge(char* smem, const Product<TL>& pr, in
     const int r = tid & 15, g = (tid >> 4) & 3;
     const int cl = tid % LPR;
     const int col = n0 + cl * 8, nv = min(8, N - col);
-    epi.with([&](const auto& f) __attribute__((always_inline)) {
+    epi.template with<false>([&](const auto& f) __attribute__((always_inline)) {
 #pragma unroll
         for (int p = 0; p < NB; ++p) {
             __syncthreads();  // the ring, or the band before, has been read
@@ -592,7 +593,7 @@ __device__ __forceinline__ void drain_epi(char* smem, const Product<TL>& pr, int
                                           int n0, int tid, int wm, int wn, const Epi& epi) {
     constexpr bool PAIR = Epi::kind == kPaired;
     constexpr int COLS = PAIR ? TL::BN / 2 : TL::BN;
-    if (m0 + TL::BM <= M && n0 + COLS <= N) {
+    if (m0 + TL::BM <= M && n0 + COLS <= N && epi.aligned()) {
         const int r = tid & 15, g = (tid >> 4) & 3;
         drain_full<TL>(pr, wm * TL::TM + r,
                        n0 + wn * (PAIR ? 32 : TL::TN) + 16 * (g & 1) + 8 * (g >> 1), epi.from(m0));
@@ -655,7 +656,8 @@ struct StorePart {
     float* part;
     int ld;
     __device__ __forceinline__ StorePart from(int64_t r) const { return {part + r * ld, ld}; }
-    template <class Run>
+    __device__ __forceinline__ bool aligned() const { return true; }
+    template <bool STREAM, class Run>
     __device__ __forceinline__ void with(Run&& run) const {
         run(*this);
     }
@@ -812,7 +814,7 @@ __global__ __launch_bounds__(256) void finish_kernel(const float* __restrict__ p
         const auto aux = at.load(0, col, nv);
         float v[8];
         sum(p, v);
-        at.with([&](const auto& f) __attribute__((always_inline)) {
+        at.template with<false>([&](const auto& f) __attribute__((always_inline)) {
             if constexpr (Epi::kind == kPaired) {
                 float u[8];
                 sum(p + pair_shift, u);

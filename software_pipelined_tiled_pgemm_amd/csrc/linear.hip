@@ -33,20 +33,21 @@ struct LinearEpi {
     };
     __device__ __forceinline__ Column column(int col, int nv) const {
         Column c = {};
-        if (bias) load8<E>(Rows{const_cast<uint16_t*>(bias), 0}, 0, col, nv, c.bias);
+        if (bias) load8<E>(Rows{const_cast<uint16_t*>(bias), 0, 0}, 0, col, nv, c.bias);
         return c;
     }
     __device__ __forceinline__ u4_t load(int row, int col, int nv) const {
         return res ? load8_bits(res, row, col, nv) : u4_t{};
     }
-    template <class Run>
+    __device__ __forceinline__ bool aligned() const { return y.aligned && (!pre || pre.aligned); }
+    template <bool STREAM, class Run>
     __device__ __forceinline__ void with(Run&& run) const {
         with_act(act, [&](auto a) __attribute__((always_inline)) {
             run([&](int row, int col, int nv, float(&v)[8], const Column& c, u4_t r)
                     __attribute__((always_inline)) {
 #pragma unroll
                 for (int q = 0; q < 8; ++q) v[q] += c.bias[q];
-                if (pre) store8<E>(pre, row, col, nv, v);
+                if (pre) store8<E, STREAM>(pre, row, col, nv, v);
                 float t[8];
                 unpack8<E>(r, t);
 #pragma unroll
@@ -55,7 +56,7 @@ struct LinearEpi {
 #pragma unroll
                     for (int q = 0; q < 8; ++q) v[q] += t[q];
                 }
-                store8<E>(y, row, col, nv, v);
+                store8<E, STREAM>(y, row, col, nv, v);
             });
         });
     }
@@ -77,7 +78,8 @@ struct GradEpi {
     __device__ __forceinline__ u4_t load(int row, int col, int nv) const {
         return add ? load8_bits(add, row, col, nv) : u4_t{};
     }
-    template <class Run>
+    __device__ __forceinline__ bool aligned() const { return y.aligned && half % 8 == 0; }
+    template <bool STREAM, class Run>
     __device__ __forceinline__ void with(Run&& run) const {
         run([&](int row, int col, int nv, float(&v)[8], lp::Nothing, u4_t r)
                 __attribute__((always_inline)) {
@@ -94,7 +96,7 @@ struct GradEpi {
                 nv = min(8, half - c);
                 col = c + (second ? half : 0);
             }
-            store8<E>(y, row, col, nv, v);
+            store8<E, STREAM>(y, row, col, nv, v);
         });
     }
 };
@@ -130,7 +132,7 @@ __global__ __launch_bounds__(256) void dz_kernel(const Rows dy0, const Rows pre0
                     s[q] += d[q];
                 }
                 // dz rows are padded with zeros to whole chunks
-                if (dz) store8<E>(dz, r, col, 8, d);
+                if (dz) store8<E, true>(dz, r, col, 8, d);
             };
             // kDzRows rows at a time, 4 rows' loads in flight per lane
             for (int64_t rb = r0; rb < end; rb += kDzRows) {
@@ -218,8 +220,8 @@ struct Linear {
         if (!ar.dry() && c.M > 0 && c.N > 0 && (need_dz || c.dbias)) {
             const dim3 grid((unsigned)((n8 + 511) / 512), (unsigned)blocks);
             hipLaunchKernelGGL(dz_kernel<E>, grid, dim3(256), 0, stream, make_rows(c.dy, c.lddy),
-                               act ? make_rows(c.preact, c.ldp) : Rows{nullptr, 0},
-                               need_dz ? Rows{dzw, (int)n8} : Rows{nullptr, 0}, part, c.M,
+                               act ? make_rows(c.preact, c.ldp) : Rows{nullptr, 0, 0},
+                               need_dz ? Rows{dzw, (int)n8, 1} : Rows{nullptr, 0, 0}, part, c.M,
                                (int)c.N, need_dz ? (int)n8 : (int)c.N, per, c.act);
             if ((rc = hipGetLastError()) != hipSuccess) return rc;
         }

@@ -268,7 +268,7 @@ __global__ __launch_bounds__(256) void gather_kernel(const Rows x, const Rows dx
                 load8_bits(x.from(r), 0, col, nv);
         } else if (dx) {
             const float zero[8] = {};
-            store8<F16>(dx.from(r), 0, col, nv, zero);
+            store8<F16, false>(dx.from(r), 0, col, nv, zero);
         }
     }
 }
@@ -291,7 +291,8 @@ struct DlogitEpi {
         float weight, lse;
         int64_t target;
     };
-    template <class Run>
+    __device__ __forceinline__ bool aligned() const { return true; }
+    template <bool STREAM, class Run>
     __device__ __forceinline__ void with(Run&& run) const {
         run(*this);
     }
@@ -309,7 +310,7 @@ struct DlogitEpi {
             const float p = exp_fast(v[q] - l) - (t == q ? 1.0f : 0.0f);
             v[q] = q < nv ? c * p : 0.0f;
         }
-        store8<E>(dl, row, col, 8, v);
+        store8<E, true>(dl, row, col, 8, v);
     }
 };
 
@@ -334,9 +335,11 @@ struct SumEpi {
         floatx4 lo, hi;
         int row;
     };
-    template <class Run>
+    __device__ __forceinline__ bool aligned() const { return out.aligned; }
+    template <bool STREAM, class Run>
     __device__ __forceinline__ void with(Run&& run) const {
-        run(*this);
+        run([this](int row, int col, int nv, float(&v)[8], float f, const Before& b)
+                __attribute__((always_inline)) { put<STREAM>(row, col, nv, v, f, b); });
     }
     __device__ __forceinline__ float column(int, int) const { return factor[0]; }
     __device__ __forceinline__ Before load(int row, int col, int) const {
@@ -348,8 +351,9 @@ struct SumEpi {
         b.hi = *reinterpret_cast<const floatx4*>(p + 4);
         return b;
     }
-    __device__ __forceinline__ void operator()(int row, int col, int nv, float (&v)[8], float f,
-                                               const Before& b) const {
+    template <bool STREAM>
+    __device__ __forceinline__ void put(int row, int col, int nv, float (&v)[8], float f,
+                                        const Before& b) const {
         if (sum) {
             float* p = sum + (uint32_t)(row * ld + col);
             floatx4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
@@ -371,9 +375,9 @@ struct SumEpi {
 #pragma unroll
         for (int q = 0; q < 8; ++q) v[q] *= f;
         if (map)
-            store8<E>(out.from(b.row), 0, col, nv, v);
+            store8<E, STREAM>(out.from(b.row), 0, col, nv, v);
         else
-            store8<E>(out, row, col, nv, v);
+            store8<E, STREAM>(out, row, col, nv, v);
     }
 };
 
@@ -513,7 +517,7 @@ struct Xent {
                 return rc;
             const View dv = {dl, (int)s8};
             if (c.M > 0) {
-                const DlogitEpi<E> epi = {{dl, (int)s8}, k.lse, k.weight, k.target, v0};
+                const DlogitEpi<E> epi = {{dl, (int)s8, 1}, k.lse, k.weight, k.target, v0};
                 rc = lp::launch_product<E, true, true>(product(x, w, c.M, n, c.D), cl, epi, stream);
                 if (rc != hipSuccess) return rc;
             }
