@@ -62,7 +62,7 @@ template <class E>
 struct GluGradEpi {
     static constexpr lp::EpiKind kind = lp::kPlain;
     static constexpr bool kWalk = false;
-    static constexpr int kAhead = 1;
+    static constexpr int kAhead = 2;
     Rows gate, up;       // as the forward pass kept them
     Rows h, dgate, dup;  // padded rows: whole chunks, zeros past F
     int act;

@@ -198,6 +198,10 @@ struct Rows {
     uint16_t* ptr;
     int ld;        // below 2^22
     int aligned;  // whole chunks are 16-byte aligned
+    // Element (row, col): row < 256 and ld < 2^24, a full-rate 24-bit product.
+    __device__ __forceinline__ uint32_t at(int row, int col) const {
+        return __umul24((uint32_t)row, (uint32_t)ld) + (uint32_t)col;
+    }
     __host__ __device__ explicit operator bool() const { return ptr != nullptr; }
     // The same matrix from row r on.  Kernels address the rows of a tile (at
     // most 256) from its first one: a uniform 64-bit base and a 32-bit offset.
@@ -235,7 +239,7 @@ __device__ __forceinline__ void unpack8_kept(const u4_t& w, float (&v)[8]) {
 // loads past nv take the first value's address, so that all are issued at once
 // instead of one behind the other's branch.
 __device__ __forceinline__ u4_t load8_bits(const Rows& m, int row, int col, int nv) {
-    const uint16_t* p = m.ptr + (uint32_t)(row * m.ld + col);
+    const uint16_t* p = m.ptr + m.at(row, col);
     u4_t w = {};
     if (nv == 8) {
         __builtin_memcpy(&w, p, 16);
@@ -266,7 +270,7 @@ template <class F, bool STREAM>
 __device__ __forceinline__ void store8(const Rows& m, int row, int col, int nv,
                                        const float (&v)[8]) {
     typedef u4_t u4_any __attribute__((aligned(2)));
-    uint16_t* p = m.ptr + (uint32_t)(row * m.ld + col);
+    uint16_t* p = m.ptr + m.at(row, col);
     const u4_t w = {F::put2(v[0], v[1]), F::put2(v[2], v[3]), F::put2(v[4], v[5]),
                     F::put2(v[6], v[7])};
     if (nv == 8) {

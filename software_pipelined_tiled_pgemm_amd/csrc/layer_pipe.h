@@ -485,7 +485,7 @@ __device__ __forceinline__ void chunk8(const floatx4& a, const floatx4& b, float
 
 // A tile inside the matrix whose chunks are aligned.
 template <class TL, class Epi>
-__device__ __forceinline__ void drain_full(const Product<TL>& pr, int row0, int col0,
+__device__ __forceinline__ void drain_full(const Product<TL>& pr, const int row00, int col0,
                                            const Epi epi) {
     constexpr bool PAIR = Epi::kind == kPaired;
     constexpr int JP = TL::FN / (PAIR ? 4 : 2);  // column chunks per lane
@@ -499,9 +499,13 @@ __device__ __forceinline__ void drain_full(const Product<TL>& pr, int row0, int 
             const auto column = epi.column(col, 8);
             decltype(epi.load(0, 0, 0)) aux[AHEAD];
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) aux[i] = epi.load(row0 + 16 * i, col, 8);
+            for (int i = 0; i < AHEAD; ++i) aux[i] = epi.load(row00 + 16 * i, col, 8);
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
+                // Hidden from the compiler, so that it does not keep the
+                // addresses of all chunks in registers.
+                int row0 = row00;
+                asm volatile("" : "+v"(row0));
                 const int row = row0 + 16 * i;
                 const auto now = aux[i % AHEAD];
                 if (i + AHEAD < FM) aux[i % AHEAD] = epi.load(row + 16 * AHEAD, col, 8);
