@@ -12,7 +12,8 @@ namespace {
 // Packing an operand whose rows are not whole 16-byte pieces: one thread
 // writes 16 bytes of the padded copy.  Reads are 16 bytes from any 2-byte
 // boundary (the compiler's unaligned global load), element by element at
-// the row's end.  Bound by memory: each value is read and written once.
+// the row's end.  Bound by memory: each value is read and written once (2039
+// x 1025: 2.4-5 us for 8 MB, mostly the launch).
 __global__ __launch_bounds__(256) void pack_kernel(const uint16_t* __restrict__ src, int64_t ld,
                                                    uint16_t* __restrict__ dst, int64_t dst_ld,
                                                    int64_t rows, int cols) {
@@ -41,7 +42,8 @@ __global__ __launch_bounds__(256) void pack_kernel(const uint16_t* __restrict__ 
 
 // out[c] = sum over r of part[r][c]: 64 columns per workgroup, its 16 waves
 // each adding a sixteenth of the rows in ascending order (8 loads in flight),
-// the sixteenths then in order.
+// the sixteenths then in order.  Bound by latency: 128 rows of 4096 in 4 us
+// (with 4 waves and one load in flight 12).
 constexpr int kSegs = 16;
 template <class E>
 __global__ __launch_bounds__(64 * kSegs) void column_sum_kernel(const float* __restrict__ part,

@@ -34,7 +34,9 @@ constexpr float grad_scale() {
 }
 
 // Rows of a tile to (maximum, sum of exponentials), and the target's logit
-// from whichever lane holds it.
+// from whichever lane holds it.  In registers, and with workgroups that walk
+// the tiles: 8192 x 2048 x 65536 bf16 1575-1730 us (1270-1400 TFLOP/s); through LDS,
+// one workgroup per tile, 1913.
 struct StatsEpi {
     static constexpr lp::EpiKind kind = lp::kRows;
     static constexpr bool kWalk = true;
@@ -86,7 +88,8 @@ struct StatsEpi {
 };
 
 // Joins a row's tiles: 16 rows per workgroup, 64 lanes taking every 64th tile
-// of a row each (4 loads in flight), then the lanes in order through LDS.  A
+// of a row each (4 loads in flight), then the lanes in order through LDS; 8192
+// rows of 256 tiles in 6 us (with 4 lanes a row 28).  A
 // target outside the vocabulary that is not ignore_index gives NaN.
 __global__ __launch_bounds__(1024) void join_kernel(const float2* __restrict__ part, int tiles,
                                                     const float* __restrict__ target_logit,
@@ -167,7 +170,7 @@ __global__ __launch_bounds__(1024) void total_kernel(const float* __restrict__ r
 // and the rows that count (c_m not 0) packed together, by one workgroup whose
 // threads take consecutive runs of rows.  Ignored rows weigh 0; a weight that
 // is not finite, or belongs to an invalid target (NaN), stands for its row
-// alone.
+// alone.  Bound by latency: 8192 rows 25 us, of 4.5 ms that follow.
 //   rank[m]: place of row m among the rows that count, -1 where it does not;
 //   row[j]: the j-th row that counts; live: how many there are.
 struct Kept {
@@ -252,7 +255,8 @@ __global__ __launch_bounds__(1024) void weights_kernel(const int64_t* __restrict
 }
 
 // The rows of x that count, packed together in padded rows of whole chunks;
-// the rows of dx (where asked for) that do not are zeroed.
+// the rows of dx (where asked for) that do not are zeroed.  Bound by memory
+// (8192 x 2048: 11.5 us for 63 MB, 5.5 TB/s).
 __global__ __launch_bounds__(256) void gather_kernel(const Rows x, const Rows dx, uint16_t* kept,
                                                      int kept_ld, const int* __restrict__ rank,
                                                      int64_t M, int D) {
@@ -273,7 +277,9 @@ __global__ __launch_bounds__(256) void gather_kernel(const Rows x, const Rows dx
     }
 }
 
-// dl of a piece: whole chunks, zeros past its last column.
+// dl of a piece: whole chunks, zeros past its last column.  7372 x 2048 x 32768
+// bf16 780-810 us (1220-1270 TFLOP/s): an exponential and the weight a value, and
+// 16 bits written.
 template <class E>
 struct DlogitEpi {
     static constexpr lp::EpiKind kind = lp::kPlain;
@@ -315,7 +321,8 @@ struct DlogitEpi {
 };
 
 // The gradients' epilogue.  dx over the pieces: fp32 sums in the workspace, the
-// last piece rounds; its rows go where the rows that count came from (map).
+// last piece rounds; its rows go where the rows that count came from (map).  dx
+// of a piece of 32768 at 7372 x 2048 675-710 us, its dW 717-746 (1330-1470 TFLOP/s).
 template <class E>
 struct SumEpi {
     static constexpr lp::EpiKind kind = lp::kPlain;
