@@ -303,8 +303,8 @@ int pgemm_test_iota_f32(float* o, int64_t n, pgemm_stream_t stream);
  *    and return a negative status for arguments that the call would refuse.
  *  - Results are the same bits call after call for the same arguments.
  *  - PGEMM_EUNSUPPORTED: unknown dtype or activation, an odd address, a row
- *    length or pitch of 2^22 or more, 2^31 - 256 rows or more, or an output of
- *    more than 2^37 elements.
+ *    length or pitch of 2^22 or more, 2^31 - 256 rows or more, or a matrix
+ *    (the block's M x 2F intermediate among them) of more than 2^37 elements.
  * ======================================================================== */
 enum pgemm_dtype { PGEMM_F16 = 0, PGEMM_BF16 = 1, PGEMM_F32 = 2 };
 

@@ -116,7 +116,9 @@ int check_ffn(int dtype, int act, int64_t M, int64_t D, int64_t F, int64_t N) {
     if (F < 0 || N < 0) return PGEMM_EINVAL;
     const int rc = check_linear(dtype, act, M, D, N);
     if (rc != PGEMM_OK) return rc;
-    return F >= kMaxCols / 2 ? PGEMM_EUNSUPPORTED : PGEMM_OK;
+    // [g | u] in padded halves is a matrix like the others
+    if (F > kMaxCols / 2 - 8 || (F > 0 && M > kMaxElems / (2 * F))) return PGEMM_EUNSUPPORTED;
+    return PGEMM_OK;
 }
 
 // Gradient clipping.

@@ -93,6 +93,7 @@ def test_ffn_checks(L):
     assert call(y=None) == EINVAL
     assert call(ldwi=95) == EINVAL and call(gu=P, ldgu=95) == EINVAL
     assert call(F=1 << 21, ldwi=(1 << 22) - 8) == EUNSUP
+    assert call(M=1 << 28, F=1 << 10, ldwi=1 << 11) == EUNSUP   # M 2F above 2^37
     assert call(dtype=F32) == EUNSUP and call(act=17) == EUNSUP
     assert call(gu=Y, ldgu=96) == EINVAL and call(gu=X, ldgu=96) == EINVAL
     assert call(y=W) == EINVAL
