@@ -132,8 +132,13 @@ __device__ __forceinline__ float gelu_tanh_of(float z) {
 __device__ __forceinline__ float silu_of(float z) { return z * sigmoid(z); }
 
 // The derivative, and with it the value (for the gated product, which needs
-// both).  Far out the derivative of the tanh form is 0 or 1 to the last bit;
-// its polynomial is evaluated at z held to +-30, so that it stays finite.
+// both).  z is as a forward pass stored it, so in fp16 it is infinite where
+// the sum was beyond 65504: the smooth activations' limits there are the
+// values 0 and z, the derivatives 0 and 1.  They come from a distribution
+// function that is exactly 0 or 1, which takes z itself (so NaN stays NaN),
+// and from factors of z that are held to finite values.
+__device__ __forceinline__ float not_minus_inf(float z) { return fmaxf(z, -1e30f); }
+
 __device__ __forceinline__ float relu_grad(float z, float& value) {
     value = relu_of(z);
     return z > 0.0f ? 1.0f : 0.0f;
@@ -141,19 +146,22 @@ __device__ __forceinline__ float relu_grad(float z, float& value) {
 __device__ __forceinline__ float gelu_grad(float z, float& value) {
     float c, d;
     normal_cdf_pdf(z, c, d);
-    value = z * c;
+    value = not_minus_inf(z) * c;
     return d > 0.0f ? fmaf(z, d, c) : c;
 }
+// Far out the polynomial of the derivative is evaluated at +-30, where it is
+// multiplied by 0.
 __device__ __forceinline__ float gelu_tanh_grad(float z, float& value) {
     const float h = fminf(fmaxf(z, -30.0f), 30.0f);
-    const float s = sigmoid(kGeluA * (h + kGeluB * h * h * h));
-    value = z * s;
+    const float s = sigmoid(kGeluA * (z + kGeluB * z * z * z));
+    value = not_minus_inf(z) * s;
     return s + h * s * (1.0f - s) * kGeluA * (1.0f + 3.0f * kGeluB * h * h);
 }
 __device__ __forceinline__ float silu_grad(float z, float& value) {
     const float s = sigmoid(z);
-    value = z * s;
-    return s * fmaf(z, 1.0f - s, 1.0f);
+    const float h = not_minus_inf(z);
+    value = h * s;
+    return s * fmaf(fminf(h, 1e30f), 1.0f - s, 1.0f);
 }
 
 // An activation as a compile-time choice.
