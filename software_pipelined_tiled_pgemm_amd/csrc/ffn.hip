@@ -51,9 +51,9 @@ struct GluEpi {
                     store8<Kept16<E>, false>(gate, row, col, nv, g);
                     store8<Kept16<E>, false>(up, row, col, nv, u);
                 }
-                // past F both are 0, and so is h
+                // 0 past F, where an infinite row of x has NaN
 #pragma unroll
-                for (int q = 0; q < 8; ++q) u[q] *= decltype(a)::value(g[q]);
+                for (int q = 0; q < 8; ++q) u[q] = q < nv ? u[q] * decltype(a)::value(g[q]) : 0.0f;
                 store8<E, STREAM>(h, row, col, 8, u);
             });
         });
@@ -98,6 +98,7 @@ struct GluGradEpi {
                     s[q] = decltype(a)::grad(g[q], v) * d[q] * u[q];  // dg
                     u[q] *= v;                                        // h
                     d[q] *= v;                                        // du
+                    if (q >= nv) s[q] = d[q] = 0.0f;  // where an infinite row of dy has NaN
                 }
                 store8<E, false>(h, row, col, 8, u);
                 store8<E, false>(dgate, row, col, 8, s);

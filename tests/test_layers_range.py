@@ -105,3 +105,20 @@ def test_ffn_gate_below_the_range(act):
     dy = torch.tensor([[2.0], [0.0]], device="cuda").half()
     for grad in pg.pffn_bwd(dy, x, wi, wo, gu, act=act):
         assert not bool(grad.any()) and bool(torch.isfinite(grad).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("F", [1, 8])
+def test_ffn_infinite_rows(F, dtype):
+    """An infinite row of x or dy gives the formula's infinities, also where F
+    is padded to whole 16-byte pieces."""
+    x = torch.tensor([[inf], [1.0]], dtype=dtype, device="cuda")
+    wi = torch.ones((1, 2 * F), dtype=dtype, device="cuda")
+    wo = torch.full((F, 1), 2.0, dtype=dtype, device="cuda")
+    assert pg.pffn(x, wi, wo, act="relu").tolist() == [[inf], [2.0 * F]]
+    one = torch.ones((2, 1), dtype=dtype, device="cuda")
+    gu = torch.empty((2, 2 * F), dtype=dtype, device="cuda")
+    pg.pffn(one, wi, wo, act="relu", gate_up=gu)
+    dx, dwi, dwo = pg.pffn_bwd(x, one, wi, wo, gu, act="relu")
+    assert dx.tolist() == [[inf], [4.0 * F]]
+    assert dwi.tolist() == [[inf] * (2 * F)] and dwo.tolist() == [[inf]] * F
