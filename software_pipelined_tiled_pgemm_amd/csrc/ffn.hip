@@ -154,6 +154,7 @@ struct Ffn {
                 if (rc != hipSuccess) return rc;
             }
         }
+        if (c.N == 0) return hipSuccess;  // only gate_up was asked for
         View wo;
         if ((rc = operand(c.w_out, c.ldwo, c.F, c.N, ar, stream, wo)) != hipSuccess) return rc;
         const Cut cut = choose_cut(c.M, c.N, c.F, cus, 16);

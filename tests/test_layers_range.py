@@ -122,3 +122,22 @@ def test_ffn_infinite_rows(F, dtype):
     dx, dwi, dwo = pg.pffn_bwd(x, one, wi, wo, gu, act="relu")
     assert dx.tolist() == [[inf], [4.0 * F]]
     assert dwi.tolist() == [[inf] * (2 * F)] and dwo.tolist() == [[inf]] * F
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("F", [0, 6, 24])
+def test_ffn_without_outputs(F, dtype):
+    """N = 0: gate_up is written all the same, and the gradients are 0."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x = torch.randn(5, 8, generator=g, device="cuda").to(dtype)
+    wi = torch.randn(8, 2 * F, generator=g, device="cuda").to(dtype)
+    wo = torch.empty((F, 0), dtype=dtype, device="cuda")
+    gu = torch.full((5, 2 * F), nan, dtype=dtype, device="cuda")
+    y = pg.pffn(x, wi, wo, gate_up=gu)
+    assert y.shape == (5, 0)
+    full = torch.full((5, 2 * F), nan, dtype=dtype, device="cuda")
+    pg.pffn(x, wi, torch.ones((F, 3), dtype=dtype, device="cuda"), gate_up=full)
+    assert torch.equal(gu.view(torch.int16), full.view(torch.int16))
+    assert not bool(torch.isnan(gu).any())
+    dx, dwi, dwo = pg.pffn_bwd(torch.empty((5, 0), dtype=dtype, device="cuda"), x, wi, wo, gu)
+    assert not bool(dx.any()) and not bool(dwi.any()) and dwo.shape == (F, 0)
