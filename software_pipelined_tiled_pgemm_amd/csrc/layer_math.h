@@ -98,17 +98,23 @@ __device__ __forceinline__ float sigmoid(float x) {
 }
 
 // Standard normal distribution and density at z.  The tail
-// Phi(-|z|) = erfc(|z| / sqrt 2) / 2 is Abramowitz and Stegun 7.1.26 (absolute
-// error of erfc at most 1.5e-7, and its error shrinks with the factor
-// exp(-z^2 / 2)); the exponential serves the density too.
+// Phi(-|z|) = exp(-x^2) t P(t), x = |z| / sqrt 2, t = 1 / (1 + 0.375 x): the form
+// of Abramowitz and Stegun 7.1.26, with a P of degree 6 fitted here for the
+// relative error, since the activation's value for z < 0 is this tail (least
+// squares on exp(x^2) erfc(x) / 2 for x <= 9.6, reweighted towards the largest
+// relative error: 6.4e-7; in fp32 1.8e-6 at z = -4, 2e-5 at -13, where the
+// argument of the exponential is rounded).  It serves the density too.
 __device__ __forceinline__ void normal_cdf_pdf(float z, float& cdf, float& pdf) {
     const float x = fabsf(z) * 0.70710678f;
-    const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * x);
+    const float t = __builtin_amdgcn_rcpf(fmaf(x, 0.375f, 1.0f));
     const float e = exp_fast(-x * x);
-    const float poly =
-        t * (0.254829592f +
-             t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
-    const float tail = 0.5f * poly * e;
+    float p = fmaf(t, -0.067547955f, 0.19396894f);
+    p = fmaf(t, p, -0.064798675f);
+    p = fmaf(t, p, 0.14153078f);
+    p = fmaf(t, p, 0.08333228f);
+    p = fmaf(t, p, 0.10784459f);
+    p = fmaf(t, p, 0.10566972f);
+    const float tail = t * p * e;
     cdf = z < 0.0f ? tail : 1.0f - tail;
     pdf = 0.3989422804f * e;
 }

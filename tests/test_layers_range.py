@@ -141,3 +141,24 @@ def test_ffn_without_outputs(F, dtype):
     assert not bool(torch.isnan(gu).any())
     dx, dwi, dwo = pg.pffn_bwd(torch.empty((5, 0), dtype=dtype, device="cuda"), x, wi, wo, gu)
     assert not bool(dx.any()) and not bool(dwi.any()) and dwo.shape == (F, 0)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gelu_tail(dtype):
+    """z Phi(z) and its derivative to one rounding of the type down the tail: the
+    fp32 evaluation adds 2^-19 and, by the rounded argument of exp(-z^2 / 2), z^2
+    2^-22 of the value (of each term of the derivative)."""
+    z = torch.linspace(-13.0, 6.0, 3001, dtype=torch.float64).to(dtype).cuda()[None]
+    n = z.shape[1]
+    one = torch.ones((1, 1), dtype=dtype, device="cuda")
+    y = pg.plinear(one, z, act="gelu")
+    Z = z.double()
+    rel = UNIT[dtype] + 2.0 ** -19 + Z * Z * 2.0 ** -22
+    cdf = torch.special.erfc(-Z.cpu() * 0.5 ** 0.5).cuda() / 2   # (ndtr cancels in the tail)
+    E = Z * cdf
+    ratio = ((y.double() - E).abs() - TINY[dtype]) / (rel * E.abs() + 1e-300)
+    assert float(ratio.max()) <= 1, (float(ratio.max()), float(Z[0, int(ratio.argmax())]))
+    db = pg.plinear_bwd(torch.ones_like(z), one, torch.ones_like(z), preact=z, act="gelu")[2]
+    a, b = cdf, Z * torch.exp(-Z * Z / 2) / (2 * np.pi) ** 0.5
+    tol = UNIT[dtype] * (a + b).abs() + (rel - UNIT[dtype]) * (a + b.abs()) + TINY[dtype]
+    assert bool(((db.double() - (a + b)[0]).abs() <= tol[0]).all())
