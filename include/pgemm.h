@@ -360,8 +360,11 @@ int64_t plinear_bwd_workspace_bytes(int dtype, const void* dy, int64_t lddy, con
  *   gate_up [M,2F] (may be NULL) receives [g | u] for the backward pass, in 16
  *   bits each: fp16 as they are; bf16 as 1 sign, 6 exponent (bias 31) and 9
  *   fraction bits, a quarter of bf16's rounding, which would show in the
- *   gradients (exponent field 0 is 0, the topmost code NaN: magnitudes below
- *   2^-30 become 0, those from about 2^33 on NaN).  h is rounded once, as the
+ *   gradients.  Values that these forms do not hold are marked, and pffn_bwd
+ *   computes them again: in fp16 the infinities; in bf16 what has exponent
+ *   field 0 (magnitudes below 2^-30, with gradual underflow; nothing but 0 has
+ *   code 0) and the topmost code (magnitudes from about 2^33 on, and NaN).  The
+ *   bf16 form is not bf16: only pffn_bwd reads it.  h is rounded once, as the
  *   operand of W_out.
  *   y may be exactly residual or x.
  * Both projections, the activation and the product are one kernel.  The
@@ -385,6 +388,10 @@ int64_t pffn_workspace_bytes(int dtype, const void* x, int64_t ldx, const void* 
  * instance dy where x was also the residual; dx may be exactly add.  dx,
  * dW_in and dW_out may each be NULL: that gradient is not computed, and x
  * (without dW_in) and W_in (without dx) may be NULL too.
+ * The values of gate_up that its form does not hold are summed again from x and
+ * W_in, in fp32, one dot product a value (4096 x 2048 -> 2 x 8192, 1 ms: 64-135
+ * ms where every value is such a one); without x or W_in fp16's infinities stand
+ * as they are, bf16's topmost code for NaN and its small values as kept.
  */
 int pffn_bwd(int dtype, const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w_in,
              int64_t ldwi, const void* w_out, int64_t ldwo, const void* gate_up, int64_t ldgu,

@@ -30,6 +30,7 @@ template <class E>
 struct GluEpi {
     static constexpr lp::EpiKind kind = lp::kPaired;
     static constexpr bool kWalk = false;
+    static constexpr bool kRedo = false;
     static constexpr int kAhead = 1;
     Rows h;  // padded rows: whole chunks
     Rows gate, up;
@@ -60,21 +61,71 @@ struct GluEpi {
     }
 };
 
-// dg, du and h from dh and the kept g and u.  Bound by the epilogue itself: 52
-// instructions a value (8 each to decode g and u, about 20 for the
-// activation's derivative) and five streams of memory; 4093 x 8192 at K = 2048
-// 209 us, of which the product takes 95.  128x128 tiles, whose two workgroups
-// per CU overlap better, took 40 us more.
+// g and u summed again in fp32, for the kept codes that do not hold them: one
+// dot product of a row of x and a column of W_in per value, by one lane.  At
+// ordinary scales a block has no such values; NaN takes the same way, and ends
+// its sum at once.
+template <class E>
+struct Source {
+    const uint16_t* x;  // NULL where x or W_in is not at hand
+    int64_t ldx;
+    const uint16_t* w;
+    int64_t ldw;
+    int D, F;
+    __device__ __forceinline__ Source from(int64_t r) const {
+        return {x ? x + r * ldx : x, ldx, w, ldw, D, F};
+    }
+    __device__ __forceinline__ void again(int row, int col, const u4_t& gc, const u4_t& uc,
+                                          float (&g)[8], float (&u)[8]) const {
+        uint32_t todo = 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const uint32_t cg = gc[q >> 1] >> (16 * (q & 1)), cu = uc[q >> 1] >> (16 * (q & 1));
+            todo |= Kept16<E>::beyond(cg) << q | Kept16<E>::beyond(cu) << (8 + q);
+            if (!x) {
+                g[q] = Kept16<E>::as_kept(cg);
+                u[q] = Kept16<E>::as_kept(cu);
+            }
+        }
+        if (!x) return;
+        while (todo) {
+            const int q = __builtin_ctz(todo);
+            todo &= todo - 1;
+            const uint16_t* px = x + row * ldx;
+            const uint16_t* pw = w + col + (q & 7) + (q >= 8 ? F : 0);
+            float sum = 0.0f;
+            for (int d = 0; d < D && sum == sum; d += 32) {  // a NaN stays one
+                const int end = min(D, d + 32);
+#pragma unroll 4
+                for (int e = d; e < end; ++e, pw += ldw) sum = fmaf(E::get(px[e]), E::get(*pw), sum);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                g[k] = q == k ? sum : g[k];
+                u[k] = q == k + 8 ? sum : u[k];
+            }
+        }
+    }
+};
+
+// dg, du and h from dh and the kept g and u.  Bound by the epilogue itself:
+// about 50 instructions a value (4 each to decode g and u, 4 to look for marked
+// codes, 20 for the activation's derivative) and five streams of memory; 4093 x
+// 8192 at K = 2048 209 us, of which the product takes 95.  128x128 tiles, whose
+// two workgroups per CU overlap better, took 40 us more.
 template <class E>
 struct GluGradEpi {
     static constexpr lp::EpiKind kind = lp::kPlain;
     static constexpr bool kWalk = false;
+    static constexpr bool kRedo = true;
     static constexpr int kAhead = 2;
     Rows gate, up;       // as the forward pass kept them
     Rows h, dgate, dup;  // padded rows: whole chunks, zeros past F
     int act;
+    Source<E> source;
     __device__ __forceinline__ GluGradEpi from(int64_t r) const {
-        return {gate.from(r), up.from(r), h.from(r), dgate.from(r), dup.from(r), act};
+        return {gate.from(r), up.from(r), h.from(r), dgate.from(r), dup.from(r), act,
+                source.from(r)};
     }
     struct Kept {
         u4_t g, u;
@@ -84,14 +135,19 @@ struct GluGradEpi {
         return {load8_bits(gate, row, col, nv), load8_bits(up, row, col, nv)};
     }
     __device__ __forceinline__ bool aligned() const { return true; }
+    // STREAM (whole tiles): a chunk with a code that does not hold its value
+    // only says so, and its tile is done again in the other form.
     template <bool STREAM, class Run>
     __device__ __forceinline__ void with(Run&& run) const {
         with_act(act, [&](auto a) __attribute__((always_inline)) {
             run([&](int row, int col, int nv, float(&d)[8], lp::Nothing, const Kept& k)
                     __attribute__((always_inline)) {
+                const uint32_t odd = Kept16<E>::any_beyond(k.g, k.u);
                 float g[8], u[8], s[8];
                 unpack8_kept<E>(k.g, g);
                 unpack8_kept<E>(k.u, u);
+                if constexpr (!STREAM)
+                    if (odd) source.again(row, col, k.g, k.u, g, u);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     float v;
@@ -103,6 +159,7 @@ struct GluGradEpi {
                 store8<E, false>(h, row, col, 8, u);
                 store8<E, false>(dgate, row, col, 8, s);
                 store8<E, false>(dup, row, col, 8, d);
+                return odd;
             });
         });
     }
@@ -177,9 +234,12 @@ struct Ffn {
             const Args g = args(dy, wo, c.M, c.F, c.N, cut, ar);
             if (!ar.dry()) {
                 const uint16_t* gu = static_cast<const uint16_t*>(c.gate_up);
-                const GluGradEpi<E> epi = {make_rows(gu, c.ldgu), make_rows(gu + c.F, c.ldgu),
-                                           {h, (int)f8, 1}, {d, (int)(2 * f8), 1},
-                                           {d + f8, (int)(2 * f8), 1}, c.act};
+                const bool source = c.x && c.w_in;
+                const GluGradEpi<E> epi = {
+                    make_rows(gu, c.ldgu), make_rows(gu + c.F, c.ldgu), {h, (int)f8, 1},
+                    {d, (int)(2 * f8), 1}, {d + f8, (int)(2 * f8), 1}, c.act,
+                    {source ? static_cast<const uint16_t*>(c.x) : nullptr, c.ldx,
+                     static_cast<const uint16_t*>(c.w_in), c.ldwi, (int)c.D, (int)c.F}};
                 rc = lp::launch_product<E, true, true>(g, cut, epi, stream);
                 if (rc != hipSuccess) return rc;
             }

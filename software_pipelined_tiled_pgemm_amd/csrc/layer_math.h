@@ -57,31 +57,79 @@ struct BF16 {
 // double the error of dW_out (2.1 roundings of its size in all, against 1.4
 // for h and the output alone).  fp16 keeps the values themselves.  bf16 keeps
 // them with 6 exponent and 9 fraction bits (bias 31), a quarter of bf16's
-// rounding (1.5 in all): magnitudes below 2^-30 become 0, those that round to
-// 2^33 - 2^23 and more, infinities and NaN become NaN (the topmost code).
+// rounding (1.5 in all).
+//
+// What a form does not hold is marked, and the backward pass computes it again
+// from x and W_in: in fp16 the infinities; in bf16 exponent field 0 (magnitudes
+// below 2^-30, with gradual underflow; only 0 itself is code 0) and the
+// topmost code (those that round to 2^33 - 2^23 and more, infinities, NaN).
+// beyond(c) is 1 for a marked code, any_beyond(g, u) where one of 16 is (or, in
+// fp16, is NaN); as_kept(c) is what it stands for where x or W_in is not at
+// hand.  Both are computed as integers: 16 lane masks would not fit in scalar
+// registers beside those of the copies.
+typedef uint16_t us2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
+
 template <class E>
 struct Kept16 {
     __device__ static __forceinline__ uint32_t put2(float a, float b) { return E::put2(a, b); }
-    __device__ static __forceinline__ float get(uint16_t u) { return E::get(u); }
+    __device__ static __forceinline__ void unpack2(uint32_t w, float& a, float& b) {
+        a = E::get((uint16_t)w);
+        b = E::get((uint16_t)(w >> 16));
+    }
+    __device__ static __forceinline__ uint32_t beyond(uint32_t c) {
+        return 1u - min((c & 0x7FFFu) ^ 0x7C00u, 1u);
+    }
+    __device__ static __forceinline__ uint32_t any_beyond(const u4_t& g, const u4_t& u) {
+        us2_t top = {};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            top = __builtin_elementwise_max(top, __builtin_bit_cast(us2_t, g[q] & 0x7FFF7FFFu));
+            top = __builtin_elementwise_max(top, __builtin_bit_cast(us2_t, u[q] & 0x7FFF7FFFu));
+        }
+        return ((uint32_t)max(top[0], top[1]) + 0x400u) >> 15;
+    }
+    __device__ static __forceinline__ float as_kept(uint32_t c) { return E::get((uint16_t)c); }
 };
 template <>
 struct Kept16<BF16> {
-    static constexpr uint32_t kRebias = 96u << 23;  // 127 - 31
-    // Rounds to nearest, ties away from zero.
+    // The code is the top of an fp32 pattern 2^96 below the value: exact both
+    // ways in the normal range.  Rounds to nearest, ties away from zero.
     __device__ static __forceinline__ uint32_t put(float f) {
-        const uint32_t bits = __builtin_bit_cast(uint32_t, f);
-        const uint32_t a = max(bits & 0x7FFFFFFFu, kRebias) - kRebias + 0x2000u;
+        const uint32_t bits = __builtin_bit_cast(uint32_t, f * 0x1p-96f);
+        const uint32_t least = f != 0.0f ? 1u << 14 : 0u;
+        const uint32_t a = max((bits & 0x7FFFFFFFu) + 0x2000u, least);
         return (min(a, 0x7FFFu << 14) >> 14) | ((bits >> 16) & 0x8000u);
     }
     __device__ static __forceinline__ uint32_t put2(float a, float b) {
         return put(a) | (put(b) << 16);
     }
-    __device__ static __forceinline__ float get(uint16_t u) {
-        const uint32_t c = u & 0x7FFFu;
-        uint32_t m = (c << 14) + kRebias;
-        m = c < 0x200u ? 0u : m;  // exponent field 0
-        m = c == 0x7FFFu ? 0x7FC00000u : m;
-        return __builtin_bit_cast(float, m | ((uint32_t)(u & 0x8000u) << 16));
+    // A code in the high half of w; the topmost one comes out as a number.
+    __device__ static __forceinline__ float high(uint32_t w) {
+        return __builtin_bit_cast(float, (uint32_t)((int32_t)w >> 2) & 0x9FFFC000u) * 0x1p96f;
+    }
+    __device__ static __forceinline__ void unpack2(uint32_t w, float& a, float& b) {
+        a = high(w << 16);
+        b = high(w);
+    }
+    __device__ static __forceinline__ uint32_t beyond(uint32_t c) {
+        c &= 0x7FFFu;
+        return ((c + 1u) >> 15) | (((c - 0x200u) >> 31) & min(c, 1u));
+    }
+    __device__ static __forceinline__ uint32_t any_beyond(const u4_t& g, const u4_t& u) {
+        const us2_t one = {1, 1};
+        us2_t top = {}, low = {0xFFFF, 0xFFFF};  // low: of code - 1, so that 0 passes
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const us2_t c = __builtin_bit_cast(us2_t, (q < 4 ? g[q & 3] : u[q & 3]) & 0x7FFF7FFFu);
+            top = __builtin_elementwise_max(top, c);
+            low = __builtin_elementwise_min(low, (us2_t)(c - one));
+        }
+        return (((uint32_t)max(top[0], top[1]) + 1u) >> 15) |
+               (((uint32_t)min(low[0], low[1]) - 0x1FFu) >> 31);
+    }
+    __device__ static __forceinline__ float as_kept(uint32_t c) {
+        return (c & 0x7FFFu) == 0x7FFFu ? __builtin_nanf("") : high(c << 16);
     }
 };
 
@@ -229,8 +277,6 @@ inline Rows make_rows(const void* p, int64_t ld) {
             (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0};
 }
 
-typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
-
 template <class E>
 __device__ __forceinline__ void unpack8(const u4_t& w, float (&v)[8]) {
 #pragma unroll
@@ -243,10 +289,7 @@ __device__ __forceinline__ void unpack8(const u4_t& w, float (&v)[8]) {
 template <class E>
 __device__ __forceinline__ void unpack8_kept(const u4_t& w, float (&v)[8]) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        v[2 * q] = Kept16<E>::get((uint16_t)w[q]);
-        v[2 * q + 1] = Kept16<E>::get((uint16_t)(w[q] >> 16));
-    }
+    for (int q = 0; q < 4; ++q) Kept16<E>::unpack2(w[q], v[2 * q], v[2 * q + 1]);
 }
 
 // The bits of 8 values, zeros from nv >= 1 on; row < 256.  At the edge the

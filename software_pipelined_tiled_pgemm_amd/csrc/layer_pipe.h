@@ -462,7 +462,9 @@ __device__ __forceinline__ void run_k(Product<TL>& pr, Copies<TL>& cp, char* sme
 // memory per chunk would dominate.  epi.with<STREAM>(run) calls run(f) once with
 // the functor proper, so that what is the same for all chunks (the activation,
 // whether stores go past the caches) is decided before the first one;
-// epi.aligned() says that chunks do not straddle 16-byte boundaries.
+// epi.aligned() says that chunks do not straddle 16-byte boundaries.  With kRedo f
+// returns whether the chunk needs more than the functor of whole tiles
+// (STREAM) does: such a tile is done again with the other one, in drain_edge.
 // Functors on rows (kRows) see the accumulators themselves (see drain_rows).
 enum EpiKind { kPlain, kPaired, kRows };
 struct Nothing {};
@@ -485,15 +487,17 @@ __device__ __forceinline__ void chunk8(const floatx4& a, const floatx4& b, float
     }
 }
 
-// A tile inside the matrix whose chunks are aligned.
+// A tile inside the matrix whose chunks are aligned.  Not 0 where the functor
+// (kRedo) found a chunk that it cannot do here.
 template <class TL, class Epi>
-__device__ __forceinline__ void drain_full(const Product<TL>& pr, const int row00, int col0,
+__device__ __forceinline__ uint32_t drain_full(const Product<TL>& pr, const int row00, int col0,
                                            const Epi epi) {
     constexpr bool PAIR = Epi::kind == kPaired;
     constexpr int JP = TL::FN / (PAIR ? 4 : 2);  // column chunks per lane
     constexpr int FM = TL::FM;
     constexpr int AHEAD = Epi::kAhead < FM ? Epi::kAhead : FM;
     static_assert(!PAIR || TL::TN == 64, "32 columns of each half per wave");
+    uint32_t redo = 0;
     epi.template with<true>([&](const auto& f) __attribute__((always_inline)) {
 #pragma unroll
         for (int jp = 0; jp < JP; ++jp) {
@@ -517,6 +521,9 @@ __device__ __forceinline__ void drain_full(const Product<TL>& pr, const int row0
                     float u[8];
                     chunk8(pr.acc[2 * jp + 2][i], pr.acc[2 * jp + 3][i], u);
                     f(row, col, 8, v, u, column, now);
+                } else if constexpr (Epi::kRedo) {
+                    redo |= f(row, col, 8, v, column, now);
+                    asm volatile("" : "+v"(redo));
                 } else {
                     f(row, col, 8, v, column, now);
                 }
@@ -524,6 +531,7 @@ __device__ __forceinline__ void drain_full(const Product<TL>& pr, const int row0
             }
         }
     });
+    return redo;
 }
 
 // A tile at the matrix's edge, or of unaligned rows: the accumulators go through the ring in bands
@@ -601,8 +609,24 @@ __device__ __forceinline__ void drain_epi(char* smem, const Product<TL>& pr, int
     constexpr int COLS = PAIR ? TL::BN / 2 : TL::BN;
     if (m0 + TL::BM <= M && n0 + COLS <= N && epi.aligned()) {
         const int r = tid & 15, g = (tid >> 4) & 3;
-        drain_full<TL>(pr, wm * TL::TM + r,
-                       n0 + wn * (PAIR ? 32 : TL::TN) + 16 * (g & 1) + 8 * (g >> 1), epi.from(m0));
+        const uint32_t redo =
+            drain_full<TL>(pr, wm * TL::TM + r,
+                           n0 + wn * (PAIR ? 32 : TL::TN) + 16 * (g & 1) + 8 * (g >> 1), epi.from(m0));
+        if constexpr (Epi::kRedo) {
+            // Does any wave ask for the tile once more?  A word per wave in LDS.
+            uint32_t* const asked = reinterpret_cast<uint32_t*>(smem);
+            const bool mine = __any(redo != 0);
+            __syncthreads();  // every wave is done with the ring
+            if ((tid & 63) == 0) asked[tid >> 6] = mine;
+            __syncthreads();
+            bool any = false;
+#pragma unroll
+            for (int w = 0; w < TL::NW; ++w) any |= asked[w] != 0;
+            if (any) {
+                wait_vmcnt<0>();  // the first pass's stores, before any wave's second ones
+                drain_edge<TL>(smem, pr, M - m0, N, n0, tid, wm, wn, epi.from(m0));
+            }
+        }
     } else {
         drain_edge<TL>(smem, pr, M - m0, N, n0, tid, wm, wn, epi.from(m0));
     }
@@ -658,6 +682,7 @@ __device__ __forceinline__ void drain_rows(char* smem, const Product<TL>& pr, in
 struct StorePart {
     static constexpr EpiKind kind = kPlain;
     static constexpr bool kWalk = false;
+    static constexpr bool kRedo = false;
     static constexpr int kAhead = 1;
     float* part;
     int ld;

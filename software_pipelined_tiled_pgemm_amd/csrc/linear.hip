@@ -23,6 +23,7 @@ template <class E>
 struct LinearEpi {
     static constexpr lp::EpiKind kind = lp::kPlain;
     static constexpr bool kWalk = false;
+    static constexpr bool kRedo = false;
     static constexpr int kAhead = 4;
     Rows y, res, pre;
     const uint16_t* bias;
@@ -70,6 +71,7 @@ template <class E>
 struct GradEpi {
     static constexpr lp::EpiKind kind = lp::kPlain;
     static constexpr bool kWalk = false;
+    static constexpr bool kRedo = false;
     static constexpr int kAhead = 4;
     Rows y, add;
     int half;

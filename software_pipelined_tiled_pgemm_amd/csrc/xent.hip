@@ -284,6 +284,7 @@ template <class E>
 struct DlogitEpi {
     static constexpr lp::EpiKind kind = lp::kPlain;
     static constexpr bool kWalk = false;
+    static constexpr bool kRedo = false;
     static constexpr int kAhead = 8;
     Rows dl;
     const float* lse;
@@ -327,6 +328,7 @@ template <class E>
 struct SumEpi {
     static constexpr lp::EpiKind kind = lp::kPlain;
     static constexpr bool kWalk = false;
+    static constexpr bool kRedo = false;
     static constexpr int kAhead = 4;
     float* sum;  // [M][ld], NULL where there is one piece only
     int ld;

@@ -162,3 +162,131 @@ def test_gelu_tail(dtype):
     a, b = cdf, Z * torch.exp(-Z * Z / 2) / (2 * np.pi) ** 0.5
     tol = UNIT[dtype] * (a + b).abs() + (rel - UNIT[dtype]) * (a + b.abs()) + TINY[dtype]
     assert bool(((db.double() - (a + b)[0]).abs() <= tol[0]).all())
+
+
+# (M, D, F, N): an edge, whole and broken 16-byte rows, a split contraction
+# (dh through the finish kernel), whole 128x128 and 256x256 tiles
+BEYOND = [(3, 16, 5, 4), (70, 40, 136, 72), (130, 72, 129, 600), (256, 64, 256, 64),
+          (4096, 64, 4096, 128)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("shape", BEYOND)
+def test_ffn_gradients_beyond_the_kept_range(shape, act, dtype):
+    """Columns of g and u whose values the 16 bits that they are kept in do not
+    hold (fp16: beyond 65504; bf16: beyond 2^33 and below 2^-30), in a block
+    whose activations and gradients are of ordinary size: gate column c is scaled by
+    a, up column c by b and row c of W_out by 1 / (a b).
+
+    Bound: a kept value carries its rounding (2^-11, for bf16 2^-10, fp16
+    subnormals 2^-25) and the fp32 sum's error, a value computed again the
+    latter; |act'| and |act''| are at most 1.13; relu' may differ where |g| is
+    below its error.  Entries of [dg | du] and h are rounded once (u, subnormals
+    TINY)."""
+    M, D, F, N = shape
+    print("beyond", shape, act, dtype, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(7)
+
+    def rnd(*s):
+        return torch.randn(*s, generator=g, device="cuda", dtype=torch.float64)
+    x = rnd(M, D).to(dtype)
+    x[M // 2] = 0.0  # g and u of exactly 0
+    a, b = (torch.ones(F, dtype=torch.float64, device="cuda") for _ in range(2))
+    if dtype is torch.float16:
+        a[1::5], b[1::5], a[3::5], b[3::5] = 5e4, 1e-2, 1e-2, 5e4
+    else:
+        a[1::5], b[1::5], a[3::5], b[3::5], a[4::5] = 1e14, 1e-13, 1e-20, 1e16, 1e-12
+    wi = (rnd(D, 2 * F) * D ** -0.5 * torch.cat([a, b])).to(dtype)
+    wo = (rnd(F, N) * F ** -0.5 / (a * b)[:, None]).to(dtype)
+    dy = rnd(M, N).to(dtype)
+    gu = torch.empty((M, 2 * F), dtype=dtype, device="cuda")
+    y = pg.pffn(x, wi, wo, act=act, gate_up=gu)
+    assert bool(torch.isfinite(y).all())
+    dx, dwi, dwo = pg.pffn_bwd(dy, x, wi, wo, gu, act=act)
+
+    X, WI, WO, DY = x.double(), wi.double(), wo.double(), dy.double()
+    Z, S = X @ WI, X.abs() @ WI.abs()
+    u, tiny = UNIT[dtype], TINY[dtype]
+    KU = u if dtype is torch.float16 else u / 4
+    E = KU * Z.abs() + (D + 16) * E32 * S + (2.0 ** -25 if dtype is torch.float16 else 0.0)
+    if dtype is torch.float16:
+        assert int((Z.abs() > 65520).sum()) > 0
+    else:
+        assert int((Z.abs() > 2.0 ** 34).sum()) > 0 and int((Z.abs() < 2.0 ** -31).sum()) > F
+    G, U, EG, EU = Z[:, :F], Z[:, F:], E[:, :F], E[:, F:]
+    DH = DY @ WO.t()
+    EDH = (N + 17) * E32 * (DY.abs() @ WO.abs().t())
+    A, P = value(G, act), slope(G, act)
+    DIN = torch.cat([DH * U * P, DH * A], 1)
+    H = A * U
+    unsure = (G.abs() <= EG) * (DH * U).abs() if act == "relu" else 0.0
+    # the activations' own fp32 evaluation: 1e-6 of their argument
+    EDIN = torch.cat([1.13 * (EDH * U.abs() + DH.abs() * (EU + U.abs() * EG)) + unsure + 1e-6 * (DH * U).abs(),
+                      EDH * A.abs() + DH.abs() * (1.13 * EG + 1e-6 * G.abs())], 1)
+    EH = A.abs() * EU + U.abs() * (1.13 * EG + 1e-6 * G.abs())
+    EDIN = 1.01 * EDIN + u * DIN.abs() + tiny
+    EH = 1.01 * EH + u * H.abs() + tiny
+    for name, got, exact, err, scale, n in (
+            ("dx", dx, DIN @ WI.t(), EDIN @ WI.abs().t(), DIN.abs() @ WI.abs().t(), 2 * F),
+            ("dw_in", dwi, X.t() @ DIN, X.abs().t() @ EDIN, X.abs().t() @ DIN.abs(), M),
+            ("dw_out", dwo, H.t() @ DY, EH.t() @ DY.abs(), H.abs().t() @ DY.abs(), M)):
+        bound = u * exact.abs() + 1.01 * err + (n + 16) * E32 * scale + tiny
+        bad = ~((got.double() - exact).abs() <= bound)
+        # sums beyond the output type's own range are its infinity
+        bad &= ~((exact.abs() + bound > torch.finfo(dtype).max) & (got == exact.sign() * inf))
+        assert not bool(bad.any()), (name, int(bad.sum()), got[bad][:4], exact[bad][:4], bound[bad][:4])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,F", [(70, 51), (256, 256)])
+def test_ffn_gradients_keep_nan(M, F, dtype):
+    """A NaN row of x: its own row of dx is NaN, the others keep their bits."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    x = torch.randn(M, 40, generator=g, device="cuda").to(dtype)
+    wi = torch.randn(40, 2 * F, generator=g, device="cuda").mul(0.16).to(dtype)
+    wo = torch.randn(F, 24, generator=g, device="cuda").mul(0.1).to(dtype)
+    dy = torch.randn(M, 24, generator=g, device="cuda").to(dtype)
+    gu = torch.empty((M, 2 * F), dtype=dtype, device="cuda")
+    pg.pffn(x, wi, wo, gate_up=gu)
+    ref = pg.pffn_bwd(dy, x, wi, wo, gu)[0]
+    x[5] = nan
+    pg.pffn(x, wi, wo, gate_up=gu)
+    dx, dwi, dwo = pg.pffn_bwd(dy, x, wi, wo, gu)
+    assert bool(torch.isnan(dx[5]).all()) and bool(torch.isnan(dwi).all()) and bool(torch.isnan(dwo).all())
+    dx[5] = ref[5]
+    assert torch.equal(dx, ref)
+
+
+def test_ffn_kept_codes():
+    """bf16's kept form: gradual underflow below 2^-30, nothing but 0 becomes 0,
+    and without x the topmost code stands for NaN."""
+    v = [0.0, 2.0 ** -30, 2.0 ** -31, -(2.0 ** -33), 2.0 ** -39, 1e-30, -1e-37, 2.0 ** 34, -1e38, inf, nan, 1.0]
+    w = torch.tensor([v + v], dtype=torch.float64).to(torch.bfloat16).cuda()
+    one = torch.ones((1, 1), dtype=torch.bfloat16, device="cuda")
+    wo = torch.ones((12, 1), dtype=torch.bfloat16, device="cuda")
+    gu = torch.empty((1, 24), dtype=torch.bfloat16, device="cuda")
+    pg.pffn(one, w, wo, gate_up=gu)
+    codes = [c & 0xFFFF for c in gu.view(torch.int16)[0, :12].tolist()]
+    assert codes[:7] == [0, 1 << 9, 1 << 8, 0x8000 | 1 << 6, 1, 1, 0x8001]
+    assert all(c & 0x7FFF == 0x7FFF for c in codes[7:11]) and codes[11] == 31 << 9
+
+    # dW_out = h^T dy alone, without x: act "none", h = g u
+    L = pg.lib()
+    dwo = torch.empty((12, 1), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    for x in (None, one.data_ptr()):
+        rc = L.pffn_bwd(1, one.data_ptr(), 1, x, 1, w.data_ptr(), 24, wo.data_ptr(), 1, gu.data_ptr(), 24,
+                        None, 0, None, 0, None, 0, dwo.data_ptr(), 1, 1, 1, 12, 1, 0, ws.data_ptr(),
+                        ws.numel(), torch.cuda.current_stream().cuda_stream)
+        assert rc == pg.PGEMM_OK
+        got = dwo.double().cpu()[:, 0]
+        exact = w[0, :12].double().cpu() ** 2
+        if x is None:
+            assert torch.isnan(got[7:11]).all()
+            assert bool(((got - exact)[:7].abs() <= 2.0 ** -8 * exact[:7] + 2.0 ** -78).all())
+        else:
+            assert float(got[7]) == 2.0 ** 68 and got[8] == inf and got[9] == inf and torch.isnan(got[10])
+            fits = exact > 2.0 ** -126   # (-1e-37 squared is below the type's range)
+            fits[7:] = False
+            assert bool(((got - exact).abs() <= 2.0 ** -8 * exact)[fits].all())
