@@ -59,7 +59,9 @@ class Model:
             z = gate_up = None
             if keep is not None:
                 z = torch.empty(len(x), w.shape[1], dtype=x.dtype, device=x.device)
-                gate_up = torch.empty(len(x), w_in.shape[1], dtype=x.dtype, device=x.device)
+                # bf16's kept form is no bf16: 16 bits that only pffn_bwd reads
+                form = torch.int16 if x.dtype is torch.bfloat16 else x.dtype
+                gate_up = torch.empty(len(x), w_in.shape[1], dtype=form, device=x.device)
             y = pg.plinear(x, w, bias=b, residual=x, act="gelu", preact=z)
             out = pg.pffn(y, w_in, w_out, residual=y, act="silu", gate_up=gate_up)
             if keep is not None:

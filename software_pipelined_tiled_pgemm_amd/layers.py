@@ -62,15 +62,16 @@ def _dtype(t, name):
     raise TypeError("%s must be float16 or bfloat16, got %s" % (name, dt))
 
 
-def _mat(t, name, like, rows=None, cols=None):
+def _mat(t, name, like, rows=None, cols=None, also=None):
     """Checks a matrix against the call's first tensor `like` (type, device)
-    and a shape; returns its row pitch in elements."""
+    and a shape; returns its row pitch in elements.  `also`: another type that
+    it may have."""
     if not isinstance(t, _TENSOR):
         raise TypeError("%s must be a torch.Tensor" % name)
     if not t.is_cuda:
         raise ValueError("%s must be a device (HIP) tensor, got %s" % (name, t.device))
     if t is not like:
-        if t.dtype is not like.dtype:
+        if t.dtype is not like.dtype and (also is None or t.dtype is not also):
             raise TypeError("%s must be %s, got %s" % (name, like.dtype, t.dtype))
         if t.get_device() != like.get_device():
             raise ValueError("%s is on another device than the other tensors" % name)
@@ -225,13 +226,23 @@ def plinear_bwd(dy, x, w, preact=None, act="none", dx_residual=None, needs=(True
     return dx, dw, dbias
 
 
+def _gate_up(t, like, rows, cols):
+    """gate_up's row pitch.  bfloat16's kept form is not bfloat16, so it may be
+    held as what it is to everyone but pffn_bwd: 16 bits."""
+    return _mat(t, "gate_up", like, rows, cols,
+                _torch.int16 if like.dtype is _BF16 else None)
+
+
 def pffn(x, w_in, w_out, residual=None, act="silu", gate_up=None, out=None, workspace=None,
          stream=None):
     """(act(g) * u) @ w_out + residual with [g | u] = x @ w_in: the gated
     feed-forward block for x [M,D], w_in [D,2F], w_out [F,N].
 
-    gate_up: an [M,2F] tensor that receives [g | u] for pffn_bwd (for bfloat16 in
-    a 16-bit form of its own, see include/pgemm.h).  out may be residual or x."""
+    gate_up: an [M,2F] tensor that receives [g | u] for pffn_bwd, of x's type; for
+    bfloat16 in a 16-bit form of its own (include/pgemm.h), whose numbers mean
+    nothing as bfloat16, so an int16 tensor is taken too, and is the better
+    choice: it cannot be read, or passed on, as activations by mistake.
+    out may be residual or x."""
     dt = _dtype(x, "x")
     a = _act(act)
     ldx = _mat(x, "x", x)
@@ -243,7 +254,7 @@ def pffn(x, w_in, w_out, residual=None, act="silu", gate_up=None, out=None, work
     ldwo = _mat(w_out, "w_out", x, rows=F)
     N = w_out.shape[1]
     ldr = _mat(residual, "residual", x, M, N) if residual is not None else 0
-    ldgu = _mat(gate_up, "gate_up", x, M, 2 * F) if gate_up is not None else 0
+    ldgu = _gate_up(gate_up, x, M, 2 * F) if gate_up is not None else 0
     out, ldy = _out(out, "out", x, (M, N), stream)
     L = lib()
 
@@ -262,7 +273,8 @@ def pffn(x, w_in, w_out, residual=None, act="silu", gate_up=None, out=None, work
 def pffn_bwd(dy, x, w_in, w_out, gate_up, act="silu", dx_residual=None, needs=(True, True, True),
              dx=None, dw_in=None, dw_out=None, workspace=None, stream=None):
     """(dx, dw_in, dw_out) of pffn for the gradient dy [M,N] of its output
-    (which is also the gradient of its residual).  `needs` says which are
+    (which is also the gradient of its residual).  gate_up: as pffn wrote it, with
+    the same x and w_in (not a product of the caller's own).  `needs` says which are
     computed; the others are None.  dx_residual [M,D] is added to dx (dy, where
     x was also the residual)."""
     dt = _dtype(dy, "dy")
@@ -276,7 +288,7 @@ def pffn_bwd(dy, x, w_in, w_out, gate_up, act="silu", dx_residual=None, needs=(T
         raise ValueError("w_in must have an even number of columns (gate, then up)")
     F = w_in.shape[1] // 2
     ldwo = _mat(w_out, "w_out", dy, F, N)
-    ldgu = _mat(gate_up, "gate_up", dy, M, 2 * F)
+    ldgu = _gate_up(gate_up, dy, M, 2 * F)
     lda = _mat(dx_residual, "dx_residual", dy, M, D) if dx_residual is not None else 0
     lddx = lddwi = lddwo = 0
     if needs[0]:

@@ -290,3 +290,24 @@ def test_ffn_kept_codes():
             fits = exact > 2.0 ** -126   # (-1e-37 squared is below the type's range)
             fits[7:] = False
             assert bool(((got - exact).abs() <= 2.0 ** -8 * exact)[fits].all())
+
+
+def test_gate_up_as_int16():
+    """bfloat16's kept form in an int16 tensor: the same bits and gradients;
+    float16 keeps its values in float16 alone."""
+    g = torch.Generator(device="cuda").manual_seed(10)
+    x, wi, wo = (torch.randn(*s, generator=g, device="cuda").bfloat16() for s in ((9, 8), (8, 12), (6, 4)))
+    kept = [torch.empty((9, 12), dtype=t, device="cuda") for t in (torch.bfloat16, torch.int16)]
+    for gu in kept:
+        pg.pffn(x, wi, wo, gate_up=gu)
+    assert torch.equal(kept[0].view(torch.int16), kept[1])
+    dy = torch.randn(9, 4, generator=g, device="cuda").bfloat16()
+    for a, b in zip(*(pg.pffn_bwd(dy, x, wi, wo, gu) for gu in kept)):
+        assert torch.equal(a, b)
+    for bad in (torch.float16, torch.float32, torch.int32):
+        with pytest.raises(TypeError):
+            pg.pffn(x, wi, wo, gate_up=torch.empty((9, 12), dtype=bad, device="cuda"))
+        with pytest.raises(TypeError):
+            pg.pffn_bwd(dy, x, wi, wo, torch.empty((9, 12), dtype=bad, device="cuda"))
+    with pytest.raises(TypeError):
+        pg.pffn(x.half(), wi.half(), wo.half(), gate_up=kept[1])
