@@ -11,11 +11,11 @@
 // so that what the first pass read last is read again first, while it is
 // still in the last-level cache.
 //
-// Squares: fp16 ones are exact in fp32, where 8 of them are added before
-// joining an fp64 sum; bf16 and fp32 values are squared in fp64, where none
-// overflows or vanishes.  The order of all sums is fixed.  7e8 bf16 values: 826
-// us (4.2 GB, 5.1 TB/s; with stores through the caches 898); 60 tensors of 2^20
-// fp32 values in all: 12.5 us of kernels.
+// Squares: fp16 ones are exact in fp32, where 8 of them are added (rounding by
+// at most 7 2^-24 of the sum) before joining an fp64 sum; bf16 and fp32 values are
+// squared in fp64, where none overflows or vanishes.  The order of all sums is
+// fixed.  7e8 bf16 values: 826 us (4.2 GB, 5.1 TB/s; with stores through the
+// caches 898); 60 tensors of 2^20 fp32 values in all: 12.5 us of kernels.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -60,10 +60,8 @@ __device__ __forceinline__ int locate(const Table& t, int chunk, int& index) {
 }
 
 // Loads and stores of 8 values from any element-aligned address (the
-// compiler's unaligned 16-byte accesses).  STREAM: past the caches, for data
-// that is not used again.
+// compiler's unaligned 16-byte accesses); stores go past the caches.
 typedef u4_t u4_any __attribute__((aligned(2)));
-template <bool STREAM>
 __device__ __forceinline__ u4_t get16(const void* p) {
     const u4_any* q = static_cast<const u4_any*>(p);
     return *q;
@@ -74,9 +72,8 @@ __device__ __forceinline__ void put16(void* p, u4_t w) {
 template <class E>
 struct Vec8 {
     typedef uint16_t elem;
-    template <bool STREAM>
     __device__ static __forceinline__ void load(const elem* p, float (&v)[8]) {
-        const u4_t w = get16<STREAM>(p);
+        const u4_t w = get16(p);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             v[2 * q] = E::get((uint16_t)w[q]);
@@ -95,9 +92,8 @@ struct F32 {};
 template <>
 struct Vec8<F32> {
     typedef float elem;
-    template <bool STREAM>
     __device__ static __forceinline__ void load(const elem* p, float (&v)[8]) {
-        const u4_t lo = get16<STREAM>(p), hi = get16<STREAM>(p + 4);
+        const u4_t lo = get16(p), hi = get16(p + 4);
         __builtin_memcpy(v, &lo, 16);
         __builtin_memcpy(v + 4, &hi, 16);
     }
@@ -135,14 +131,14 @@ __device__ __forceinline__ double chunk_squares(const void* in, int64_t from, in
     for (; i + 3 * 8 * kThreads + 8 <= to; i += 4 * 8 * kThreads) {
         float v[4][8];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) Vec8<E>::template load<false>(p + i + u * 8 * kThreads, v[u]);
+        for (int u = 0; u < 4; ++u) Vec8<E>::load(p + i + u * 8 * kThreads, v[u]);
 #pragma unroll
         for (int u = 0; u < 4; ++u) s += squares<E>(v[u]);
     }
     for (; i < to; i += 8 * kThreads) {
         float v[8];
         if (i + 8 <= to) {
-            Vec8<E>::template load<false>(p + i, v);
+            Vec8<E>::load(p + i, v);
         } else {
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] = i + q < to ? Vec8<E>::get(p + i + q) : 0.0f;
@@ -206,7 +202,7 @@ __device__ __forceinline__ void chunk_scale(const void* in, void* out, int64_t f
     for (; i + 3 * 8 * kThreads + 8 <= to; i += 4 * 8 * kThreads) {
         float v[4][8];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) Vec8<E>::template load<true>(p + i + u * 8 * kThreads, v[u]);
+        for (int u = 0; u < 4; ++u) Vec8<E>::load(p + i + u * 8 * kThreads, v[u]);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
 #pragma unroll
@@ -217,7 +213,7 @@ __device__ __forceinline__ void chunk_scale(const void* in, void* out, int64_t f
     for (; i < to; i += 8 * kThreads) {
         if (i + 8 <= to) {
             float v[8];
-            Vec8<E>::template load<true>(p + i, v);
+            Vec8<E>::load(p + i, v);
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] *= f;
             Vec8<E>::store(o + i, v);

@@ -70,9 +70,8 @@ struct Cut {
     int splits;
     int64_t chunk;  // multiple of 64
 };
-// max_splits 1: no split (its output is not a plain sum, or no workspace).
-// Estimated time of a cut, in microseconds, and the cheapest one
-// (layer_common.hip).
+// The cheapest cut by an estimate of its time (layer_common.hip).  max_splits 1:
+// no split (the epilogue needs the whole sum of a tile at once).
 Cut choose_cut(int64_t M, int64_t N, int64_t K, int cus, int max_splits);
 // Bytes of the partials of a cut (0 without a split).
 inline int64_t part_bytes(const Cut& c, int64_t M, int64_t N) {
