@@ -67,13 +67,16 @@ struct StatsEpi {
             target_logit[r] = at;
         }
         const float base = m == -INFINITY ? 0.0f : m;  // a row of -inf has the sum 0
-        const float scaled = base * kLog2e;
+        // exp(v - base) = exp2(v k - base k), k = log2 e; near the end of fp32's range
+        // base k would overflow, and any k will do: what is not base is 0.
+        const float k = fabsf(base) > 2e38f ? 1.0f : kLog2e;
+        const float scaled = base * k;
         float s = 0.0f;
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                s += __builtin_amdgcn_exp2f(fmaf(v[j][q], kLog2e, -scaled));
+                s += __builtin_amdgcn_exp2f(fmaf(v[j][q], k, -scaled));
         return float2{m, s};
     }
     __device__ __forceinline__ void join(Acc& a, Acc b) const {

@@ -311,3 +311,22 @@ def test_gate_up_as_int16():
             pg.pffn_bwd(dy, x, wi, wo, torch.empty((9, 12), dtype=bad, device="cuda"))
     with pytest.raises(TypeError):
         pg.pffn(x.half(), wi.half(), wo.half(), gate_up=kept[1])
+
+
+@pytest.mark.parametrize("V", [3, 300])
+def test_xent_at_the_ends_of_fp32(V):
+    """Logits of bfloat16's lowest and largest values: a row of nothing but the
+    lowest, one with a single ordinary entry, one with the largest; lse to fp32's
+    rounding (log V is far below it at 3e38)."""
+    top = float(torch.finfo(torch.bfloat16).max)
+    w = torch.ones((V, 3), dtype=torch.float64)
+    w[1, 1], w[2, 2] = 0.0, 0.5
+    w = w.to(torch.bfloat16).cuda()
+    x = torch.tensor([[-top, 0, 0], [0, -top, 0], [0, 0, top]], dtype=torch.float64).to(torch.bfloat16).cuda()
+    t = torch.tensor([0, 1, 2], device="cuda")
+    loss, lse = pg.pxent(x, w, t, reduction="none")
+    logits = x.double() @ w.double().t()
+    exact = torch.logsumexp(logits, 1)
+    assert bool(((lse.double() - exact).abs() <= 2.0 ** -22 * exact.abs()).all()), (lse, exact)
+    each = exact - logits[torch.arange(3), t.cpu()]
+    assert bool(((loss.double() - each).abs() <= 2.0 ** -22 * (exact.abs() + each.abs())).all())
