@@ -302,6 +302,10 @@ int pgemm_test_iota_f32(float* o, int64_t n, pgemm_stream_t stream);
  *    has passed the call.  Those functions look at pointers' alignment only,
  *    and return a negative status for arguments that the call would refuse.
  *  - Results are the same bits call after call for the same arguments.
+ *  - What a backward pass computes as the operand of a product (dz, h, [dg |
+ *    du], dl) is rounded once to dtype, and so is what the forward pass keeps
+ *    for it (preact, gate_up): beside its own rounding a gradient carries one to
+ *    two of that size (norm of the error over its norm).
  *  - PGEMM_EUNSUPPORTED: unknown dtype or activation, an odd address, a row
  *    length or pitch of 2^22 or more, 2^31 - 256 rows or more, or a matrix
  *    (the block's M x 2F intermediate among them) of more than 2^37 elements.
@@ -367,9 +371,10 @@ int64_t plinear_bwd_workspace_bytes(int dtype, const void* dy, int64_t lddy, con
  *   bf16 form is not bf16: only pffn_bwd reads it.  h is rounded once, as the
  *   operand of W_out.
  *   y may be exactly residual or x.
- * Both projections, the activation and the product are one kernel.  The
- * workspace holds h (and what operands that need padding, and products cut
- * along their contraction, take).
+ * Both projections, the activation and the product are one kernel; where the
+ * contraction over D is cut, a second one adds its parts.  The workspace
+ * holds h (and what operands that need padding, and products cut along their
+ * contraction, take).
  */
 int pffn(int dtype, const void* x, int64_t ldx, const void* w_in, int64_t ldwi, const void* w_out,
          int64_t ldwo, const void* residual, int64_t ldr, void* y, int64_t ldy, void* gate_up,
@@ -434,6 +439,9 @@ int64_t pxent_workspace_bytes(int dtype, const void* x, int64_t ldx, const void*
  * The vocabulary is taken in pieces whose dl (rounded once to dtype, scaled
  * so that the largest |g| is 2^15 in fp16 and 1 in bf16) takes at most
  * 512 MiB of workspace, or 1024 entries; dx is summed over the pieces in fp32.
+ * The scale is one for all rows: in fp16 an entry of dl below 2^-29 of the
+ * largest |g| is subnormal there and keeps fewer bits (a softmax of 1e-5 in a
+ * row whose |g| is 2^-12 of the largest still keeps all).
  */
 int pxent_bwd(int dtype, const void* x, int64_t ldx, const void* w, int64_t ldw,
               const int64_t* target, int64_t ignore_index, int reduction, const float* lse,

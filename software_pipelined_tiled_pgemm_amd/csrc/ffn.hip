@@ -6,9 +6,10 @@
 //              dg = dh * u * act'(g),  du = dh * act(g)
 //              dx = [dg | du] W_in^T (+ a),  dW_in = x^T [dg | du],  dW_out = h^T dy
 //
-// Both projections, the activation and the product are one kernel: a tile's
-// columns are 32 gate columns and the same 32 up columns per wave, so g and u
-// of a value meet in the epilogue, and only h is written (and g, u for a
+// Both projections, the activation and the product are one kernel (the sums of
+// a split contraction are joined, and the rest done, by the finish kernel): a
+// tile's columns are 32 gate columns and the same 32 up columns per wave, so g
+// and u of a value meet in the epilogue, and only h is written (and g, u for a
 // backward pass).  The backward pass computes dg, du and h (again, from g
 // and u) in the epilogue of dh, which is never written.  Since [dg | du] and
 // W_in lie side by side, dx and dW_in are one product each.
@@ -109,9 +110,9 @@ struct Source {
 };
 
 // dg, du and h from dh and the kept g and u.  Bound by the epilogue itself:
-// about 50 instructions a value (4 each to decode g and u, 4 to look for marked
-// codes, 20 for the activation's derivative) and five streams of memory; 4093 x
-// 8192 at K = 2048 209 us, of which the product takes 95.  128x128 tiles, whose
+// 45 instructions a value (4 each to decode g and u, 4 to look for marked codes,
+// 20 for the activation's derivative) and five streams of memory; 4093 x 8192
+// at K = 2048 212-224 us, of which the product takes 95.  128x128 tiles, whose
 // two workgroups per CU overlap better, took 40 us more.
 template <class E>
 struct GluGradEpi {

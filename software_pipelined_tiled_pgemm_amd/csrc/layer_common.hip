@@ -100,11 +100,13 @@ hipError_t launch_column_sum(int dtype, const float* part, int64_t parts, int64_
 }
 
 namespace {
-// Estimated microseconds of a cut, with the constants measured on MI355X: a
-// 256x256 tile takes 0.65 us per K step of 32, two 128x128 tiles on a CU 0.57
+// Estimated microseconds of a cut, with the constants measured on MI355X at long
+// K: a 256x256 tile takes 0.65 us per K step of 32, two 128x128 tiles on a CU 0.57
 // (their LDS reads bound them: half the product for nearly the time), one
 // alone 0.33; a round of workgroups adds its prologue and epilogue, and a
-// split a second launch and the partials' traffic.
+// split a second launch and the partials' traffic.  It ranks cuts and is no
+// forecast: 2039 x 2047 x 1025, where launch and edges count, is 14.5 by it and
+// takes 20; reading the weights of a few rows has no term of its own.
 double cut_time(int64_t M, int64_t N, int64_t K, int cus, bool big, int splits) {
     const int64_t b = big ? 256 : 128;
     const int64_t wgs = ((M + b - 1) / b) * ((N + b - 1) / b) * splits;

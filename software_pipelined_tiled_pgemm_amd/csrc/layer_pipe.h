@@ -18,9 +18,15 @@
 //
 // What bounds it: the matrix cores (a 256x256 tile reads 32 B per clock and
 // CU against the 58 B a copy can sustain); at 4096^3 and above the loop runs
-// at the chip's power limit, as the plain GEMM does.  Measured, bf16 without
-// an epilogue's extras: 8192^3 722 us (1522 TFLOP/s); 8192 x 4096 x 4096 NN 188
-// us (1464), NT 189 (1453), TN 198 (1385).
+// at the chip's power limit, as the plain GEMM does, where a product's first
+// launches are 10-20% faster than steady ones.  Measured, bf16 without an
+// epilogue's extras, the fastest run of ten launches and the median: 8192^3 758
+// and 788 us (1451 and 1395 TFLOP/s); 8192 x 4096 x 4096 NN 198 and 212 (1388 and
+// 1297), NT 202 and 212, TN 202 and 214-222.
+//
+// Registers: the 256x256 tiles use all 256 vector registers of a wave, and some
+// spill: in NN 2 (LinearEpi fp16, SumEpi), 5 (GluEpi) or 22 (StorePart, with four
+// scratch loads in the loop of 10 steps), in NT the walking StatsEpi 1.
 
 #pragma once
 
@@ -534,9 +540,10 @@ __device__ __forceinline__ uint32_t drain_full(const Product<TL>& pr, const int 
     return redo;
 }
 
-// A tile at the matrix's edge, or of unaligned rows: the accumulators go through the ring in bands
-// of rows (half of each wave's at a time where the tile does not fit), and a
-// loop over the band's chunks checks each against the edge.  (Checked chunks
+// A tile at the matrix's edge, of unaligned rows, or done again (kRedo): the
+// accumulators go through the ring in bands of rows (half of each wave's at a
+// time where the tile does not fit), and a loop over the band's chunks checks
+// each against the edge.  (Checked chunks
 // unrolled like drain_full's made the code of both so large that the
 // registers of the K loop suffered.)  16-byte chunk c of LDS row r sits at
 // (c & 1) * CH/2 + ((c >> 1) ^ (r mod CH/2)): the two halves of 8 columns are
@@ -705,11 +712,13 @@ struct StorePart {
 
 // One workgroup per tile; with a functor that says kWalk, a workgroup takes the
 // tiles blockIdx.x, blockIdx.x + gridDim.x, ...: as many workgroups as the chip
-// holds walk the tiles of a large product (see launch_tiles).  The copies of a tile's first steps are issued before the
-// epilogue of the one before it, which needs no LDS (kRows: 8 KiB in the slot
-// that the prologue leaves free), so they land meanwhile.  On gfx9 the wait
-// for step 0 counts the epilogue's stores too, which were issued later: it
-// then waits for more than it has to.
+// holds walk the tiles of a large product (see launch_tiles).  The copies of a
+// tile's first steps are issued before the epilogue of the one before it, which
+// needs no LDS (kRows: 8 KiB in the slot that the prologue leaves free).  They
+// overlap only with what that epilogue does before its first load: loads return
+// in order, so a functor that reads memory (StatsEpi: a target per row block)
+// waits for these copies first.  The wait for step 0 counts the epilogue's
+// stores too, which were issued later, and waits for more than it has to.
 template <class TL, class Epi, bool SPLIT>
 __global__ __launch_bounds__(TL::T, 1) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void product_kernel(const Args g, const Epi epi) {

@@ -36,7 +36,8 @@ constexpr float grad_scale() {
 // Rows of a tile to (maximum, sum of exponentials), and the target's logit
 // from whichever lane holds it.  In registers, and with workgroups that walk
 // the tiles: 8192 x 2048 x 65536 bf16 1575-1730 us (1270-1400 TFLOP/s); through LDS,
-// one workgroup per tile, 1913.
+// one workgroup per tile, 1913.  Each row block's target is loaded where it is
+// used: eight waits for memory a tile.
 struct StatsEpi {
     static constexpr lp::EpiKind kind = lp::kRows;
     static constexpr bool kWalk = true;

@@ -5,7 +5,9 @@ entropy over a vocabulary and gradient clipping, each with its backward pass.
 As in the rest of the package the functions check arguments, allocate the
 outputs and workspaces that were not given (from the pool of the stream the
 call runs on) and pass pointers.  Matrices are 2-D tensors whose last
-dimension is contiguous; their rows may be strided.  With stream=None a call
+dimension is contiguous; their rows may be strided.  They know nothing of
+torch's autograd: a result carries no graph, also where an input requires
+grad, and gradients are what the _bwd functions return.  With stream=None a call
 runs on the current stream; on another one the caller orders it after the
 work that produces its inputs and keeps them alive, as for any torch tensor
 used on a stream that is not its own.
