@@ -1,0 +1,476 @@
+"""The operators around a language model's low-precision projections, as cases
+to measure: the root-mean-square norm with the residual's addition (its output
+in 16 bits or microscaled, and its gradients), microscaled quantisation to 4 and
+8 bits, the product of microscaled operands with its epilogue, and the sampling
+of tokens from logits.  `run` computes a case in plain torch (`own` false) or
+with the package's operators (`own` true)."""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+DTYPES = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def listed():
+    return [
+        # One token's residual stream through a norm: latency counts.
+        {"name": "norm_token", "op": "norm", "M": 1, "D": 4096, "dtype": "bf16", "residual": True,
+         "to": "same", "train": False},
+        # A prompt, normed straight into the 8-bit operand of the next projection.
+        {"name": "norm_prompt_8bit", "op": "norm", "M": 4096, "D": 4096, "dtype": "bf16",
+         "residual": True, "to": "e4m3", "train": False},
+        # A training step at a width that fits neither a tile nor a 16-byte row.
+        {"name": "norm_train_odd", "op": "norm", "M": 2039, "D": 1025, "dtype": "f16",
+         "residual": True, "to": "same", "train": True},
+        # A training step on a large batch of tokens.
+        {"name": "norm_train", "op": "norm", "M": 16384, "D": 4096, "dtype": "bf16",
+         "residual": True, "to": "same", "train": True},
+        # A layer's weights turned to 4 bits and read back.
+        {"name": "quant_weights", "op": "quant", "M": 16384, "D": 4096, "dtype": "bf16",
+         "to": "e2m1"},
+        # A few users' activations of an odd width turned to 8 bits.
+        {"name": "quant_users", "op": "quant", "M": 67, "D": 2050, "dtype": "f16", "to": "e4m3"},
+        # One token through a projection with 4-bit weights: decoding for one user.
+        {"name": "mx_token", "op": "mx", "M": 1, "K": 4096, "N": 8192, "dtype": "bf16",
+         "x": "e4m3", "given": "dtype", "w": "e2m1", "act": "none", "bias": False,
+         "residual": True},
+        # A batch of decoding users, sizes that fit nothing, both operands in 4 bits.
+        {"name": "mx_users", "op": "mx", "M": 37, "K": 2050, "N": 5001, "dtype": "f16",
+         "x": "e2m1", "given": "dtype", "w": "e2m1", "act": "gelu", "bias": True,
+         "residual": False},
+        # A prompt through a square projection, both operands in 4 bits.
+        {"name": "mx_prompt", "op": "mx", "M": 4096, "K": 4096, "N": 4096, "dtype": "bf16",
+         "x": "e2m1", "given": "mx", "w": "e2m1", "act": "silu", "bias": True, "residual": True},
+        # A long prompt through a wide projection, activations in 8 bits.
+        {"name": "mx_wide", "op": "mx", "M": 8192, "K": 4096, "N": 8192, "dtype": "bf16",
+         "x": "e4m3", "given": "mx", "w": "e2m1", "act": "none", "bias": False,
+         "residual": False},
+        # One user's next token out of a large vocabulary.
+        {"name": "sample_one", "op": "sample", "M": 1, "V": 131072, "dtype": "f32",
+         "top_k": 50, "top_p": 0.95, "min_p": 0.0, "each": False, "masked": 0.0},
+        # Many users, each with settings of their own, a part of the tokens barred.
+        {"name": "sample_batch", "op": "sample", "M": 256, "V": 65536, "dtype": "bf16",
+         "top_k": 0, "top_p": 0.9, "min_p": 0.01, "each": True, "masked": 0.02},
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def _size(rng, lo, hi):
+    """A size between lo and hi: even odds of a multiple of 32 and of any."""
+    n = _log_int(rng, lo, hi)
+    return max(32, n // 32 * 32) if rng.random() < 0.5 else n
+
+
+def draw(rng):
+    op = rng.choice(["norm", "quant", "mx", "sample"])
+    kind = rng.choice(["f16", "bf16"])
+    while op == "norm":
+        train = rng.random() < 0.5
+        c = {"op": op, "M": _log_int(rng, 1, 16384), "D": _size(rng, 32, 16384), "dtype": kind,
+             "residual": rng.random() < 0.7,
+             "to": "same" if train else rng.choice(["same", "same", "e4m3", "e2m1"]),
+             "train": train}
+        if c["M"] * c["D"] <= 16384 * 4096:
+            return c
+    while op == "quant":
+        c = {"op": op, "M": _log_int(rng, 1, 16384), "D": _size(rng, 32, 16384), "dtype": kind,
+             "to": rng.choice(["e4m3", "e2m1"])}
+        if c["M"] * c["D"] <= 16384 * 4096:
+            return c
+    while op == "mx":
+        x = rng.choice(["e4m3", "e2m1"])
+        c = {"op": op, "M": _log_int(rng, 1, 8192), "K": _size(rng, 100, 8192),
+             "N": _size(rng, 100, 8192), "dtype": kind, "x": x,
+             "given": rng.choice(["dtype", "mx"]), "w": rng.choice(["e2m1", "e2m1", x]),
+             "act": rng.choice(["none", "relu", "gelu", "gelu_tanh", "silu"]),
+             "bias": rng.random() < 0.5, "residual": rng.random() < 0.5}
+        if c["M"] * c["K"] * c["N"] <= 8192 * 4096 * 8192:
+            return c
+    while True:
+        c = {"op": op, "M": _log_int(rng, 1, 512), "V": _log_int(rng, 100, 131072),
+             "dtype": rng.choice(["f16", "bf16", "f32"]),
+             "top_k": rng.choice([0, 0, 1, 40, 1000]), "top_p": rng.choice([1.0, 0.95, 0.8]),
+             "min_p": rng.choice([0.0, 0.0, 0.05]), "each": rng.random() < 0.5,
+             "masked": rng.choice([0.0, 0.1])}
+        if c["M"] * c["V"] <= 256 * 65536:
+            return c
+
+
+# ---- microscaled numbers -----------------------------------------------------
+# Blocks of 32 consecutive values of a row share a scale 2^e, e the smallest whole
+# number (from -127 on) for which no element is beyond the element type's
+# largest, 6 or 448.  Rows are padded with zeros to whole groups of 128 values.
+
+def _padded(n):
+    return (n + 127) // 128 * 128
+
+
+def _power(e):
+    return (e.to(torch.int32).clamp(min=-126) + 127 << 23).view(torch.float32)
+
+
+def _grid(a, to):
+    """Magnitudes rounded to the nearest element, ties to the even one."""
+    if to == "e2m1":
+        step = torch.where(a < 2, 0.5, torch.where(a < 4, 1.0, 2.0))
+    else:
+        step = _power(torch.frexp(a).exponent.clamp(min=-5) - 4)
+    return torch.round(a / step) * step
+
+
+def _elements(v, to):
+    """(elements, exponents e) of the rows of v, padded."""
+    rows, cols = v.shape
+    v = torch.nn.functional.pad(v, (0, _padded(cols) - cols)).view(rows, -1, 32)
+    m, e = torch.frexp(v.abs().amax(dim=2))
+    e = e - 3 + (m > 0.75).int() if to == "e2m1" else e - 9 + (m > 0.875).int()
+    q = _grid(v.abs() * _power(-e)[:, :, None], to)
+    return torch.where(v < 0, -q, q), e
+
+
+def _rounded(v, to):
+    """The values that the microscaled form of v stands for."""
+    q, e = _elements(v, to)
+    return (q * _power(e)[:, :, None]).view(v.shape[0], -1)[:, :v.shape[1]]
+
+
+def _pack(v, to):
+    """(codes, scales) as the package holds them: rows of bytes, in 4 bits two
+    elements a byte, the first one in the low half; scales with a bias of 127."""
+    q, e = _elements(v, to)
+    q = q.view(v.shape[0], -1)
+    if to == "e4m3":
+        codes = q.to(torch.float8_e4m3fn).view(torch.uint8)
+    else:
+        a = q.abs()
+        code = torch.where(a < 2, 2 * a, torch.where(a < 4, a + 2, a * 0.5 + 4))
+        code = (code + 8.0 * (q < 0)).to(torch.uint8)
+        codes = code[:, 0::2] | (code[:, 1::2] << 4)
+    return codes.contiguous(), (e.clamp(min=-126) + 127).to(torch.uint8)
+
+
+def _unpack(codes, scales, to, cols):
+    rows = codes.shape[0]
+    if to == "e4m3":
+        q = codes.view(torch.float8_e4m3fn).float()
+    else:
+        c = torch.stack([codes & 15, codes >> 4], dim=2).view(rows, -1)
+        a = (c & 7).float()
+        a = torch.where(a < 4, 0.5 * a, torch.where(a < 6, a - 2, 2 * a - 8))
+        q = torch.where(c > 7, -a, a)
+    s = (scales.to(torch.int32) << 23).view(torch.float32)
+    return (q.view(rows, -1, 32) * s[:, :, None]).view(rows, -1)[:, :cols]
+
+
+def prepare(case, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    dt = DTYPES[case["dtype"]]
+
+    def normal(*shape, std=1.0, dtype=dt):
+        return (torch.randn(*shape, generator=g, device="cuda") * std).to(dtype)
+
+    s = {"case": case}
+    if case["op"] in ("norm", "quant"):
+        M, D = case["M"], case["D"]
+        # A few channels are far larger than the others, as in a residual stream.
+        spread = torch.where(torch.rand(D, generator=g, device="cuda") < 0.01, 12.0, 1.0)
+        s["x"] = (normal(M, D, dtype=torch.float32) * spread).to(dt)
+        if case["op"] == "norm":
+            s["w"] = (1.0 + 0.2 * normal(D, dtype=torch.float32)).to(dt)
+            s["r"] = normal(M, D, std=2.0) if case["residual"] else None
+            if case["train"]:
+                s["dy"], s["dh"] = normal(M, D, std=0.05), normal(M, D, std=0.05)
+    elif case["op"] == "mx":
+        M, K, N = case["M"], case["K"], case["N"]
+        x = normal(M, K)
+        s["x"] = x if case["given"] == "dtype" else _pack(x.float(), case["x"])
+        s["w"] = _pack(normal(N, K, std=K ** -0.5).float(), case["w"])
+        s["b"] = normal(N, std=0.2) if case["bias"] else None
+        s["r"] = normal(M, N) if case["residual"] else None
+    else:
+        M, V = case["M"], case["V"]
+        l = normal(M, V, std=3.0)
+        if case["masked"]:
+            barred = torch.rand(M, V, generator=g, device="cuda") < case["masked"]
+            barred[:, 0] = False
+            l = l.masked_fill_(barred, float("-inf"))
+        s["l"] = l
+        s["u"] = torch.rand(M, generator=g, device="cuda")
+        if case["each"]:
+            def between(lo, hi):
+                return lo + (hi - lo) * torch.rand(M, generator=g, device="cuda")
+            s["t"] = between(0.5, 1.3)
+            s["t"][::7] = 0.0  # greedy
+            k = torch.randint(1, case["top_k"] + 1, (M,), generator=g, device="cuda") \
+                if case["top_k"] else torch.zeros(M, device="cuda")
+            s["k"] = k.to(torch.int32)
+            s["p"] = between(case["top_p"] - 0.2, 1.0) if case["top_p"] < 1 else \
+                torch.ones(M, device="cuda")
+            s["m"] = between(0.0, 2.0 * case["min_p"])
+        else:
+            s["t"], s["k"] = 0.75, case["top_k"]
+            s["p"], s["m"] = case["top_p"], case["min_p"]
+    return s
+
+
+# ---- plain forms: 32 bits throughout (sampling: 64), one rounding at the end --
+
+def _act(z, act):
+    if act == "relu":
+        return torch.where(z > 0, z, torch.zeros_like(z))
+    if act == "gelu":
+        return 0.5 * z * (1.0 + torch.erf(z * math.sqrt(0.5)))
+    if act == "gelu_tanh":
+        return 0.5 * z * (1.0 + torch.tanh(math.sqrt(2.0 / math.pi) * (z + 0.044715 * z * z * z)))
+    if act == "silu":
+        return z / (1.0 + torch.exp(-z))
+    return z
+
+
+EPS = 1e-6
+
+
+def _column(v, rows):
+    """A setting (one number, or one of each row) as a column in 64 bits; a
+    number counts as rounded to 32 bits."""
+    if isinstance(v, torch.Tensor):
+        return v.double()[:, None]
+    return float(np.float32(v))
+
+
+def _plain(s):
+    case = s["case"]
+    dt = DTYPES[case["dtype"]]
+    if case["op"] == "norm":
+        h, w = s["x"].float(), s["w"].float()
+        if s["r"] is not None:
+            h = h + s["r"].float()
+        inv = torch.rsqrt((h * h).mean(dim=1, keepdim=True) + EPS)
+        n = h * inv
+        y = n * w
+        out = {"y": (y if case["to"] == "same" else _rounded(y, case["to"])).to(dt)}
+        if s["r"] is not None:
+            out["h"] = h.to(dt)
+        if case["train"]:
+            dy = s["dy"].float()
+            d = dy * w
+            dx = inv * (d - n * (d * n).mean(dim=1, keepdim=True)) + s["dh"].float()
+            out["dx"], out["dw"] = dx.to(dt), (dy * n).sum(dim=0).to(dt)
+        return out
+    if case["op"] == "quant":
+        return _rounded(s["x"].float(), case["to"]).to(dt)
+    if case["op"] == "mx":
+        K = case["K"]
+        if case["given"] == "dtype":
+            x = _rounded(s["x"].float(), case["x"])
+        else:
+            x = _unpack(*s["x"], case["x"], K)
+        z = x @ _unpack(*s["w"], case["w"], K).t()
+        if s["b"] is not None:
+            z = z + s["b"].float()
+        y = _act(z, case["act"])
+        if s["r"] is not None:
+            y = y + s["r"].float()
+        return y.to(dt)
+    M, V = case["M"], case["V"]
+    l, order = torch.sort(s["l"].double(), dim=1, descending=True, stable=True)
+    t = _column(s["t"], M)
+    x = (l - l[:, :1]) / t
+    if isinstance(t, torch.Tensor):
+        greedy = torch.where(l == l[:, :1], 0.0, float("-inf"))
+        x = torch.where(t > 0, x, greedy)
+        k = torch.where(s["k"] > 0, s["k"], V)[:, None]
+        k = torch.where(t > 0, k, 1)
+    else:
+        k = s["k"] if s["k"] > 0 else V
+    place = torch.arange(V, device="cuda")[None, :]
+    w = torch.where(place < k, torch.exp(x), 0.0)
+    below = torch.cumsum(w, dim=1)
+    p = _column(s["p"], M)
+    keep = (place < k) & (w >= _column(s["m"], M))
+    keep &= (below - w < p * below[:, -1:]) | (place == 0) | (p >= torch.ones_like(below[:, :1]))
+    w = torch.where(keep, w, 0.0)
+    below = torch.cumsum(w, dim=1)
+    total = below[:, -1:]
+    at = (below <= s["u"].double()[:, None] * total).sum(dim=1, keepdim=True)
+    at = torch.minimum(at, keep.sum(dim=1, keepdim=True) - 1)
+    return {"token": order.gather(1, at)[:, 0],
+            "logprob": (torch.log(w.gather(1, at) / total)[:, 0]).float()}
+
+
+def _own(s):
+    import software_pipelined_tiled_pgemm_amd as pg
+    case = s["case"]
+    dt = DTYPES[case["dtype"]]
+    if case["op"] == "norm":
+        x, w, r = s["x"], s["w"], s["r"]
+        h = torch.empty_like(x) if r is not None else None
+        out = {}
+        if case["to"] == "same":
+            out["y"] = pg.prmsnorm(x, w, residual=r, eps=EPS, h=h)
+        else:
+            m = pg.prmsnorm(x, w, residual=r, eps=EPS, h=h, format=case["to"])
+            out["y"] = pg.pmx_dequantize(m, dtype=dt)
+        if h is not None:
+            out["h"] = h
+        if case["train"]:
+            out["dx"], out["dw"] = pg.prmsnorm_bwd(s["dy"], x if h is None else h, w, eps=EPS,
+                                                   dh=s["dh"])
+        return out
+    if case["op"] == "quant":
+        return pg.pmx_dequantize(pg.pmx_quantize(s["x"], case["to"]), dtype=dt)
+    if case["op"] == "mx":
+        K = case["K"]
+        x = s["x"]
+        if case["given"] == "mx":
+            x = pg.MxMatrix(*x, K, case["x"])
+        w = pg.MxMatrix(*s["w"], K, case["w"])
+        return pg.pmx_linear(x, w, bias=s["b"], residual=s["r"], act=case["act"], format=case["x"],
+                             dtype=dt)
+    token, logprob = pg.psample(s["l"], s["u"], temperature=s["t"], top_k=s["k"], top_p=s["p"],
+                                min_p=s["m"])
+    return {"token": token, "logprob": logprob}
+
+
+def run(state):
+    return _own(state) if own else _plain(state)
+
+
+def work(case):
+    b = 4 if case["dtype"] == "f32" else 2
+    if case["op"] == "norm":
+        M, D = case["M"], case["D"]
+        values = 2 * M * D + D
+        if case["residual"]:
+            values += 2 * M * D  # the residual in, the sum out
+        if case["train"]:  # dy, dh in; dx, dw out
+            values += 3 * M * D + D
+        return {"bytes": values * b, "flops": (15 if case["train"] else 6) * M * D}
+    if case["op"] == "quant":
+        return {"bytes": 2 * case["M"] * case["D"] * b, "flops": 3 * case["M"] * case["D"]}
+    if case["op"] == "mx":
+        M, K, N = case["M"], case["K"], case["N"]
+        size = {"e2m1": 0.5 + 1 / 32, "e4m3": 1 + 1 / 32}
+        x = M * K * (b if case["given"] == "dtype" else size[case["x"]])
+        y = M * N * b * (2 if case["residual"] else 1) + (N * b if case["bias"] else 0)
+        return {"bytes": x + N * K * size[case["w"]] + y, "flops": 2 * M * K * N}
+    M, V = case["M"], case["V"]
+    return {"bytes": M * V * b + M * (4 + 8 + 4) + (16 * M if case["each"] else 0),
+            "flops": 2 * M * V}
+
+
+# ---- the definitions in 64 bits ----------------------------------------------
+
+ELEMENTS = {"e2m1": [0, 0.5, 1, 1.5, 2, 3, 4, 6],
+            "e4m3": [i * 2.0 ** -9 for i in range(8)] +
+                    [(8 + i) * 2.0 ** (e - 10) for e in range(1, 16) for i in range(8)][:-1]}
+
+
+def _nearest(v, to):
+    """Rows of v to the nearest of the elements that the format has, ties to
+    the one with the even code, under the smallest scale that holds a block."""
+    grid = torch.tensor(ELEMENTS[to], dtype=torch.float64, device=v.device)
+    out = torch.empty_like(v)
+    for c in range(0, v.shape[1], 32):
+        block = v[:, c:c + 32]
+        most = block.abs().max(dim=1, keepdim=True).values
+        e = torch.ceil(torch.log2(most / grid[-1]))
+        e = torch.where(most > 0, e, torch.zeros_like(e))
+        # a logarithm next to a whole number may have come out on either side
+        e = torch.where(most > grid[-1] * torch.exp2(e), e + 1, e)
+        e = torch.where((most <= grid[-1] * torch.exp2(e - 1)) & (most > 0), e - 1, e)
+        a = block.abs() / torch.exp2(e)
+        hi = torch.searchsorted(grid, a.contiguous()).clamp(max=len(grid) - 1)
+        lo = (hi - 1).clamp(min=0)
+        up, down = grid[hi] - a, a - grid[lo]
+        code = torch.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, lo)
+        out[:, c:c + 32] = torch.sign(block) * grid[code] * torch.exp2(e)
+    return out
+
+
+def _values(codes, scales, to, cols):
+    """What codes and scales stand for."""
+    grid = torch.tensor(ELEMENTS[to] + ([0.0] if to == "e4m3" else []), dtype=torch.float64,
+                        device="cuda")
+    if to == "e4m3":
+        q = grid[(codes & 127).long()] * torch.where(codes > 127, -1.0, 1.0).double()
+    else:
+        c = torch.empty(codes.shape[0], 2 * codes.shape[1], dtype=torch.uint8, device="cuda")
+        c[:, 0::2], c[:, 1::2] = codes & 15, codes >> 4
+        q = grid[(c & 7).long()] * torch.where(c > 7, -1.0, 1.0).double()
+    return (q * torch.exp2(scales.double() - 127).repeat_interleave(32, dim=1))[:, :cols]
+
+
+def _definition(z, act):
+    if act == "none":
+        return z
+    if act == "relu":
+        return z.clamp(min=0)
+    if act == "silu":
+        return z * torch.sigmoid(z)
+    if act == "gelu":  # z times the standard normal distribution function
+        return z * torch.special.ndtr(z)
+    return z * torch.sigmoid(2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3))
+
+
+def _chosen(l, u, t, k, p, m):
+    """(token, log probability) of one row, in descending order of its logits,
+    on the host."""
+    order = np.argsort(-l, kind="stable")
+    if t <= 0:
+        return order[0], 0.0
+    n = int(np.isfinite(l).sum())
+    n = min(n, k) if k > 0 else n
+    kept = l[order[:n]]
+    w = np.exp((kept - kept[0]) / t)
+    if p < 1:
+        n = 1 + int(np.searchsorted(np.cumsum(w), p * w.sum(), side="left"))
+    n = max(1, min(n, int(np.count_nonzero(w >= m)), len(w)))
+    w = w[:n] / w[:n].sum()
+    at = min(int(np.searchsorted(np.cumsum(w), u, side="right")), n - 1)
+    return order[at], math.log(w[at])
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["op"] == "norm":
+        train = case["train"]
+        x, w = s["x"].double().requires_grad_(train), s["w"].double().requires_grad_(train)
+        h = x if s["r"] is None else x + s["r"].double()
+        y = h / torch.sqrt(torch.mean(h ** 2, dim=1, keepdim=True) + EPS) * w
+        out = {"y": y.detach() if case["to"] == "same" else _nearest(y, case["to"])}
+        if s["r"] is not None:
+            out["h"] = h.detach()
+        if train:
+            torch.autograd.backward([y, h], [s["dy"].double(), s["dh"].double()])
+            out["dx"], out["dw"] = x.grad, w.grad
+        return out
+    if case["op"] == "quant":
+        return _nearest(s["x"].double(), case["to"])
+    if case["op"] == "mx":
+        K = case["K"]
+        x = (_nearest(s["x"].double(), case["x"]) if case["given"] == "dtype"
+             else _values(*s["x"], case["x"], K))
+        w = _values(*s["w"], case["w"], K).t()
+        z = torch.matmul(x, w) if s["b"] is None else torch.addmm(s["b"].double(), x, w)
+        y = _definition(z, case["act"])
+        return y if s["r"] is None else y + s["r"].double()
+    M = case["M"]
+
+    def each(v):
+        if isinstance(v, torch.Tensor):
+            return v.double().cpu().numpy()
+        return np.full(M, np.float32(v), dtype=np.float64)
+    l = s["l"].double().cpu().numpy()
+    u, t, p, m = (each(s[n]) for n in "utpm")
+    k = each(s["k"]).astype(np.int64)
+    found = [_chosen(l[i], u[i], t[i], k[i], p[i], m[i]) for i in range(M)]
+    return {"token": torch.tensor([int(f[0]) for f in found]),
+            "logprob": torch.tensor([float(f[1]) for f in found], dtype=torch.float64)}
