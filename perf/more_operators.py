@@ -142,7 +142,8 @@ def _rounded(v, to):
 
 def _pack(v, to):
     """(codes, scales) as the package holds them: rows of bytes, in 4 bits two
-    elements a byte, the first one in the low half; scales with a bias of 127."""
+    elements a byte, the first one in the low half; scales with a bias of 127,
+    their rows padded to whole 16 bytes."""
     q, e = _elements(v, to)
     q = q.view(v.shape[0], -1)
     if to == "e4m3":
@@ -152,7 +153,8 @@ def _pack(v, to):
         code = torch.where(a < 2, 2 * a, torch.where(a < 4, a + 2, a * 0.5 + 4))
         code = (code + 8.0 * (q < 0)).to(torch.uint8)
         codes = code[:, 0::2] | (code[:, 1::2] << 4)
-    return codes.contiguous(), (e.clamp(min=-126) + 127).to(torch.uint8)
+    scales = (e.clamp(min=-126) + 127).to(torch.uint8)
+    return codes.contiguous(), torch.nn.functional.pad(scales, (0, -e.shape[1] % 16))
 
 
 def _unpack(codes, scales, to, cols):
@@ -164,7 +166,7 @@ def _unpack(codes, scales, to, cols):
         a = (c & 7).float()
         a = torch.where(a < 4, 0.5 * a, torch.where(a < 6, a - 2, 2 * a - 8))
         q = torch.where(c > 7, -a, a)
-    s = (scales.to(torch.int32) << 23).view(torch.float32)
+    s = (scales[:, :_padded(cols) // 32].to(torch.int32) << 23).view(torch.float32)
     return (q.view(rows, -1, 32) * s[:, :, None]).view(rows, -1)[:, :cols]
 
 
@@ -405,7 +407,8 @@ def _values(codes, scales, to, cols):
         c = torch.empty(codes.shape[0], 2 * codes.shape[1], dtype=torch.uint8, device="cuda")
         c[:, 0::2], c[:, 1::2] = codes & 15, codes >> 4
         q = grid[(c & 7).long()] * torch.where(c > 7, -1.0, 1.0).double()
-    return (q * torch.exp2(scales.double() - 127).repeat_interleave(32, dim=1))[:, :cols]
+    scale = torch.exp2(scales.double() - 127).repeat_interleave(32, dim=1)
+    return q[:, :cols] * scale[:, :cols]
 
 
 def _definition(z, act):
