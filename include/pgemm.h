@@ -473,6 +473,134 @@ int pclip_grad_norm(const void* const* grads, void* const* outs, const int64_t* 
                     int64_t workspace_bytes, pgemm_stream_t stream);
 int64_t pclip_grad_norm_workspace_bytes(int64_t count);
 
+/* ===========================================================================
+ * Around a model's low-precision projections: the root-mean-square norm,
+ * microscaled matrices and their product, and sampling.  What the layers'
+ * section says of types, matrices, overlap, workspaces and refusals holds here
+ * too; sums and statistics are fp32 unless said otherwise.
+ *
+ * A microscaled matrix [rows, cols] is a matrix of codes and one of scales, both
+ * row-major with pitches in bytes:
+ *  - codes: each row cut into blocks of 32 columns and padded with zeros to whole
+ *    groups of 128; PMX_E2M1 holds two 4-bit elements a byte, the first one in
+ *    the low half (64 bytes a group), PMX_E4M3 one 8-bit element a byte (128
+ *    bytes a group).  e2m1: 1 sign, 2 exponent (bias 1), 1 fraction bit, up to 6;
+ *    e4m3: 1 sign, 4 exponent (bias 7), 3 fraction bits, up to 448, no
+ *    infinities.
+ *  - scales: one byte s per block, which stands for 2^(s - 127), 255 for NaN; 4
+ *    bytes a group, 0 in the padding.  A row takes whole 16 bytes (a single or last
+ *    row too); those behind its last group mean nothing.
+ *  - both 16-byte aligned, with pitches that are multiples of 16 and below 2^22;
+ *    anything else is PGEMM_EUNSUPPORTED.
+ * A value is its element times its block's scale.
+ * ======================================================================== */
+enum pmx_format { PMX_NONE = -1, PMX_E2M1 = 0, PMX_E4M3 = 1 };
+
+/* Bytes that the codes and the scales of a row of `cols` columns take (the
+ * smallest pitches); PGEMM_EINVAL / PGEMM_EUNSUPPORTED (negative). */
+int64_t pmx_codes_pitch(int format, int64_t cols);
+int64_t pmx_scales_pitch(int64_t cols);
+
+/*
+ * Root-mean-square norm with the residual's addition:
+ *   s = x + residual,  y = s / sqrt(mean over the row of s^2 + eps) * weight.
+ *   x, residual (may be NULL: 0) [M,D], weight [D] (may be NULL: 1).
+ *   h [M,D] (may be NULL) receives s rounded to dtype: the residual stream, and
+ *   what the backward pass takes.  y is normed from s as it is in fp32.
+ *   format PMX_NONE: y [M,D] of dtype, pitch ldy in elements, scales unused.
+ *   Otherwise y and scales are the codes and scales of a microscaled matrix (as
+ *   pmx_quantize makes them, of y in fp32), ldy and lds their pitches.
+ *   h may be exactly x or residual; so may y, without a format, where h is not
+ *   the same.
+ * eps is finite and at least 0 (PGEMM_EINVAL).  A row's squares may leave fp32's
+ * range (|s| beyond about 2^64, or far below 1 with an eps as small): they are
+ * summed scaled then.
+ */
+int prmsnorm(int dtype, const void* x, int64_t ldx, const void* residual, int64_t ldr,
+             const void* weight, void* h, int64_t ldh, int format, void* y, int64_t ldy,
+             void* scales, int64_t lds, int64_t M, int64_t D, float eps, pgemm_stream_t stream);
+
+/*
+ * Backward pass of the norm: with n = h / sqrt(mean(h^2) + eps) and g = dy *
+ * weight,
+ *   dx = (g - n mean(g n)) / sqrt(mean(h^2) + eps) + dh,  dweight = sum over rows
+ *   of dy n.
+ * dx is the gradient of x and of residual.  h as the forward pass wrote it (x where
+ * there was no residual); dh [M,D] (may be NULL) is the gradient that reaches s by
+ * other ways (the residual stream's), and dx may be exactly dh.  dx and dweight [D]
+ * may each be NULL.
+ */
+int prmsnorm_bwd(int dtype, const void* dy, int64_t lddy, const void* h, int64_t ldh,
+                 const void* weight, const void* dh, int64_t lddh, void* dx, int64_t lddx,
+                 void* dweight, int64_t M, int64_t D, float eps, void* workspace,
+                 int64_t workspace_bytes, pgemm_stream_t stream);
+int64_t prmsnorm_bwd_workspace_bytes(int dtype, int64_t M, int64_t D, int need_dx,
+                                     int need_dweight);
+
+/*
+ * x [M,K] of dtype as a microscaled matrix.  The scale of a block is the
+ * smallest 2^e, e >= -127, with which none of its elements is beyond the format's
+ * largest; elements are rounded to nearest even.  A block of zeros has scale code
+ * 0.  A block that holds an infinity or a NaN becomes NaN: scale code 255, elements
+ * 0.
+ */
+int pmx_quantize(int dtype, const void* x, int64_t ldx, int format, void* codes, int64_t ldc,
+                 void* scales, int64_t lds, int64_t M, int64_t K, pgemm_stream_t stream);
+
+/* The values of a microscaled matrix, rounded once to dtype: y [M,K]. */
+int pmx_dequantize(int format, const void* codes, int64_t ldc, const void* scales, int64_t lds,
+                   int dtype, void* y, int64_t ldy, int64_t M, int64_t K, pgemm_stream_t stream);
+
+/*
+ * Linear layer on microscaled matrices: y = act(x w^T + bias) + residual.
+ *   x [M,K] and w [N,K] (one row per output, as it is quantised along K), each in
+ *   either format.  x: codes and scales; or, with xscales NULL, a matrix of dtype
+ *   (pitch ldx in elements) that is quantised to xformat first.
+ *   bias [N], residual [M,N] and y [M,N] of dtype; bias and residual may be NULL; y
+ *   may be exactly residual.
+ * The products are added by the matrix cores in fp32; with 8-bit elements on
+ * either side an addend below 2^-11 of the largest of its 128 columns may lose
+ * bits (2^-16 of the result for normally distributed values).
+ */
+int pmx_linear(int dtype, int xformat, const void* x, int64_t ldx, const void* xscales,
+               int64_t ldxs, int wformat, const void* w, int64_t ldw, const void* wscales,
+               int64_t ldws, const void* bias, const void* residual, int64_t ldr, void* y,
+               int64_t ldy, int64_t M, int64_t N, int64_t K, int act, void* workspace,
+               int64_t workspace_bytes, pgemm_stream_t stream);
+/* quantizes: whether the call will have xscales NULL. */
+int64_t pmx_linear_workspace_bytes(int dtype, int xformat, int quantizes, int wformat, int64_t M,
+                                   int64_t N, int64_t K);
+
+/*
+ * Samples a token from each row of logits [M,V] (PGEMM_F16, PGEMM_BF16 or PGEMM_F32)
+ * with the random number u[m] in [0, 1) (device memory).  In descending order of
+ * the logits, equal ones by index, with w = exp((l - largest) / temperature):
+ *  - top_k > 0 keeps the first top_k tokens;
+ *  - top_p < 1 keeps the fewest of those whose sum of w is at least top_p times the
+ *    sum of those, at least one;
+ *  - min_p keeps of them the ones with w >= min_p, at least one;
+ *  - the token is the first one up to which the sum of w exceeds u times the kept
+ *    ones' sum.
+ * temperature 0 takes the first of the largest logits.  Each setting is one number
+ * for all rows, or, where its array is not NULL, a number per row in device memory.
+ * tokens: M int64; logprobs (may be NULL): M floats, the logarithm of the token's
+ * w over the kept ones' sum.
+ * A logit of -infinity is never drawn.  Several of +infinity share the row.  A row
+ * with a NaN, or with nothing but -infinity, gives the token -1 and the logprob
+ * NaN.
+ * w is held as a multiple of 2^-40 (below half of that: never drawn) and added
+ * exactly.  PGEMM_EINVAL: V < 1, a temperature, top_p or min_p that is negative or
+ * NaN, a min_p beyond 1; of the arrays' numbers a temperature that is not above 0
+ * counts as 0, a NaN in top_p or min_p as off, a min_p beyond 1 as 1, a u outside
+ * [0, 1) as the nearest number in it.  PGEMM_EUNSUPPORTED: V of 2^22 and more.
+ */
+int psample(int dtype, const void* logits, int64_t ld, const float* u, float temperature,
+            const float* temperatures, int32_t top_k, const int32_t* top_ks, float top_p,
+            const float* top_ps, float min_p, const float* min_ps, int64_t* tokens,
+            float* logprobs, int64_t M, int64_t V, void* workspace, int64_t workspace_bytes,
+            pgemm_stream_t stream);
+int64_t psample_workspace_bytes(int dtype, int64_t M, int64_t V);
+
 /* Static English text for a status code (never NULL). */
 const char* pgemm_status_string(int status);
 

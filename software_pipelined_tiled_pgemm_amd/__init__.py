@@ -21,6 +21,8 @@ __all__ = [
     "pgemm_test_fill_f32", "pgemm_test_iota_f32",
     "plinear", "plinear_bwd", "pffn", "pffn_bwd",
     "pxent", "pxent_bwd", "pclip_grad_norm",
+    "prmsnorm", "prmsnorm_bwd", "MxMatrix", "pmx_quantize", "pmx_dequantize", "pmx_linear",
+    "psample",
     "lib", "status_string", "PgemmError",
     "PGEMM_OK", "PGEMM_EINVAL", "PGEMM_EUNSUPPORTED", "PGEMM_EHIP", "PGEMM_ESCRATCH",
     "STATIC_SCRATCH_BYTES",
@@ -323,3 +325,5 @@ def pgemm_test_iota_f32(n, device="cuda", out=None, stream=None):
 
 from .layers import (pclip_grad_norm, pffn, pffn_bwd, plinear,  # noqa: E402  (uses the helpers above)
                      plinear_bwd, pxent, pxent_bwd)
+from .serving import (MxMatrix, pmx_dequantize, pmx_linear, pmx_quantize, prmsnorm,  # noqa: E402
+                      prmsnorm_bwd, psample)

@@ -68,6 +68,21 @@ def _declare(lib):
         "pxent_bwd_workspace_bytes": (i64, [i32, p, i64, p, i64, i64, i64, i64, i32, i32]),
         "pclip_grad_norm": (i32, [p, p, p, p, i64, ctypes.c_float, p, p, i64, p]),
         "pclip_grad_norm_workspace_bytes": (i64, [i64]),
+        "pmx_codes_pitch": (i64, [i32, i64]),
+        "pmx_scales_pitch": (i64, [i64]),
+        "prmsnorm": (i32, [i32, p, i64, p, i64, p, p, i64, i32, p, i64, p, i64, i64, i64,
+                           ctypes.c_float, p]),
+        "prmsnorm_bwd": (i32, [i32, p, i64, p, i64, p, p, i64, p, i64, p, i64, i64,
+                               ctypes.c_float, p, i64, p]),
+        "prmsnorm_bwd_workspace_bytes": (i64, [i32, i64, i64, i32, i32]),
+        "pmx_quantize": (i32, [i32, p, i64, i32, p, i64, p, i64, i64, i64, p]),
+        "pmx_dequantize": (i32, [i32, p, i64, p, i64, i32, p, i64, i64, i64, p]),
+        "pmx_linear": (i32, [i32, i32, p, i64, p, i64, i32, p, i64, p, i64, p, p, i64, p, i64, i64,
+                             i64, i64, i32, p, i64, p]),
+        "pmx_linear_workspace_bytes": (i64, [i32, i32, i32, i32, i64, i64, i64]),
+        "psample": (i32, [i32, p, i64, p, ctypes.c_float, p, ctypes.c_int32, p, ctypes.c_float, p,
+                          ctypes.c_float, p, p, p, i64, i64, p, i64, p]),
+        "psample_workspace_bytes": (i64, [i32, i64, i64]),
         "pgemm_status_string": (ctypes.c_char_p, [i32]),
         "pgemm_last_hip_error": (i32, []),
         "pgemm_version": (i32, []),

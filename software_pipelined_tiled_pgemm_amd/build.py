@@ -53,6 +53,7 @@ PER_FILE = {
     "layer_split.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "ffn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "xent.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "mx_linear.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
 }
 
 
