@@ -53,7 +53,9 @@ PER_FILE = {
     "layer_split.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "ffn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "xent.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
-    "mx_linear.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "mx_product_f16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "mx_product_bf16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "mx_split.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
 }
 
 

@@ -495,9 +495,9 @@ __device__ __forceinline__ void chunk8(const floatx4& a, const floatx4& b, float
 
 // A tile inside the matrix whose chunks are aligned.  Not 0 where the functor
 // (kRedo) found a chunk that it cannot do here.
-template <class TL, class Epi>
-__device__ __forceinline__ uint32_t drain_full(const Product<TL>& pr, const int row00, int col0,
-                                           const Epi epi) {
+template <class TL, class Acc, class Epi>
+__device__ __forceinline__ uint32_t drain_full(const Acc& pr, const int row00, int col0,
+                                               const Epi epi) {
     constexpr bool PAIR = Epi::kind == kPaired;
     constexpr int JP = TL::FN / (PAIR ? 4 : 2);  // column chunks per lane
     constexpr int FM = TL::FM;
@@ -548,8 +548,8 @@ __device__ __forceinline__ uint32_t drain_full(const Product<TL>& pr, const int 
 // registers of the K loop suffered.)  16-byte chunk c of LDS row r sits at
 // (c & 1) * CH/2 + ((c >> 1) ^ (r mod CH/2)): the two halves of 8 columns are
 // read from the two halves of the row, consecutive lanes consecutive chunks.
-template <class TL, class Epi>
-__device__ __forceinline__ void drain_edge(char* smem, const Product<TL>& pr, int rows, int N,
+template <class TL, class Acc, class Epi>
+__device__ __forceinline__ void drain_edge(char* smem, const Acc& pr, int rows, int N,
                                            int n0, int tid, int wm, int wn, const Epi epi) {
     constexpr bool PAIR = Epi::kind == kPaired;
     constexpr int CH = TL::BN / 4, ROWB = TL::BN * 4;
@@ -609,9 +609,10 @@ __device__ __forceinline__ void drain_edge(char* smem, const Product<TL>& pr, in
     });
 }
 
-template <class TL, class Epi>
-__device__ __forceinline__ void drain_epi(char* smem, const Product<TL>& pr, int M, int N, int m0,
-                                          int n0, int tid, int wm, int wn, const Epi& epi) {
+// Acc: what holds the accumulators acc[FN][FM] of a wave.
+template <class TL, class Acc, class Epi>
+__device__ __forceinline__ void drain_epi(char* smem, const Acc& pr, int M, int N, int m0, int n0,
+                                          int tid, int wm, int wn, const Epi& epi) {
     constexpr bool PAIR = Epi::kind == kPaired;
     constexpr int COLS = PAIR ? TL::BN / 2 : TL::BN;
     if (m0 + TL::BM <= M && n0 + COLS <= N && epi.aligned()) {

@@ -455,6 +455,38 @@ def test_mx_linear(shape, xf, wf, dtype):
     assert torch.equal(r, y)
 
 
+@pytest.mark.parametrize("xf,wf", [("e2m1", "e2m1"), ("e4m3", "e2m1"), ("e4m3", "e4m3"), ("e2m1", "e4m3")])
+@pytest.mark.parametrize("shape", [(4100, 4110, 1200), (8200, 2040, 130), (300, 20000, 4224)])
+def test_mx_linear_many_tiles(shape, xf, wf):
+    """More 256-row tiles than compute units, edges and steps that fill nothing:
+    every output against the product of the same values in fp32, some rows
+    against binary64."""
+    M, N, K = shape
+    dtype = torch.bfloat16 if M > 5000 else torch.float16
+    say("mx linear, many tiles", shape, xf, wf)
+    x, w = rand((M, K), dtype, 1), rand((N, K), dtype, 2, std=K ** -0.5)
+    q, w = pg.pmx_quantize(x, xf), pg.pmx_quantize(w, wf)
+    b, r = rand((N,), dtype, 3, std=0.3), rand((M, N), dtype, 4)
+    y = pg.pmx_linear(q, w, bias=b, residual=r, act="gelu")
+    rows = np.unique(np.concatenate([[0, 15, 16, 127, 128, 255, 256, M - 1, M - 2],
+                                     np.random.default_rng(1).integers(0, M, 20)]))
+    some = pg.MxMatrix(q.codes[rows].contiguous(), q.scales[rows].contiguous(), K, xf)
+    check_mx(y[rows], some, w, b, r[rows], "gelu", dtype, "rows")
+    X = torch.from_numpy(values_of(q)).float().cuda()
+    W = torch.from_numpy(values_of(w)).float().cuda()
+    Z = X @ W.t() + b.float()
+    ref = torch.nn.functional.gelu(Z) + r.float()
+    # as in check_mx, the reference's own fp32 sum added; |products| by their norms
+    size = X.norm(dim=1)[:, None] * W.norm(dim=1)[None, :]
+    drop = 0.0
+    if "e4m3" in (xf, wf):
+        drop = -(-K // 128) * 2.0 ** -10 * X.abs().amax(dim=1)[:, None] * W.abs().amax(dim=1)[None, :]
+    bound = UNIT[dtype] * ref.abs() + 1.13 * (2 * (K + 16) * 2.0 ** -23 * size + drop) \
+        + 2.0 ** -17 * (Z.abs() + r.float().abs() + ref.abs()) + TINY[dtype]
+    bad = ~((y.float() - ref).abs() <= bound)
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[0].tolist())
+
+
 def test_mx_linear_wide_scales():
     """Scales over their whole range in one product: the ends of fp32 and NaN."""
     K, N = 256, 40
