@@ -16,11 +16,20 @@
 // row of 10^5 tokens gives another token than the definition for one u in about a
 // hundred.)
 //
-// The search: a histogram of counts and sums over bins of 1/64 in (max - l) /
-// temperature, in LDS; the bin that holds the wanted place is gathered and its
-// elements ranked by comparison with each other.  A bin of more elements than
-// the list takes is cut into bins of its own, down to equal logits, which are
-// taken by index.
+// The search: a histogram over bins of 1/64 in (max - l) / temperature, in LDS;
+// the bins that hold the wanted places are gathered and sorted.  Three ways:
+//  - up to 512 kept by top-k (the usual case): counts alone find the bin of the
+//    k-th; everything up to it is gathered, weighed and sorted.  No other
+//    logit is weighed.
+//  - no top-k: sums of the weights; the bin where top-p ends and those where the
+//    token may lie are gathered and sorted.
+//  - more than 512, or more elements in those bins than the list takes (many
+//    logits next to each other): one search after the other, each cutting its
+//    bin into bins of its own until the list takes what is left, down to equal
+//    logits, which are taken by index.
+// A row stays in the registers of a workgroup where it fits; few long rows are cut
+// into pieces, a workgroup each, with the histogram and the list in the
+// workspace.
 #include "sample.h"
 
 #include "layer_math.h"
@@ -46,7 +55,10 @@ struct Logits<F32> {
 
 constexpr int kT = 1024;       // lanes of a row's workgroup
 constexpr int kBins = 2048;    // bins of a histogram
-constexpr int kList = 1024;    // elements that are ranked at once
+constexpr int kList = 1024;    // elements that are sorted at once
+constexpr int kSmallK = 512;   // most of top-k for the way of counts alone
+// Bins from here on hold no weight: exp(-28.5) 2^40 is below a half.
+constexpr int kLightBin = 1824;
 constexpr float kPerUnit = 64.0f;  // bins per unit of (max - l) / temperature
 constexpr double kOne = 1099511627776.0;  // 2^40, the largest weight
 
@@ -65,56 +77,128 @@ struct Found {
     float logit;
 };
 
+// LDS: what every way needs, and the histograms; a kept row takes the place of those
+// of the searches, which read the row from memory.
 struct Shared {
-    Histogram all, part;
-    float logit[kList];
-    uint32_t index[kList];
-    u64 weight[kList];
+    double power[64];  // 2^(i / 64)
+    u64 list[kList];   // sorted keys (key_of)
     u64 wave_sum[kT / 64];
     uint32_t wave_count[kT / 64];
     float wave_min[kT / 64], wave_max[kT / 64];
-    int flag;
-    uint32_t listed;
-    int bin;
-    u64 before_sum, before_count;
+    u64 before_sum, before_count, bin_sum;
     Found found;
+    uint32_t listed;
+    int flag, bin;
+};
+struct Searches {
+    Histogram all, part;
+};
+// A histogram of sums or of counts alone.
+union Single {
+    u64 sum[kBins];
+    uint32_t count[kBins];
 };
 
-// A row's logits and what its weights are made with.
-template <class E>
-struct Row {
-    typedef Logits<E> L;
-    const typename L::Bits* ptr;
-    int V;
+// What a row's weights are made with.
+struct Scale {
     float most;
-    double inverse;  // 1 / temperature
-    float per;       // bins per unit of max - l
+    double inverse;       // 1 / temperature
+    float per;            // bins per unit of max - l
+    const double* power;  // 2^(i / 64) in LDS
 
-    // f(index, logit) for this lane's elements.
-    template <class Fn>
-    __device__ __forceinline__ void each(Fn&& f) const {
-        for (int64_t c = (int64_t)threadIdx.x * L::kWidth; c < V; c += kT * L::kWidth) {
-            typename L::Bits b[L::kWidth];
-            if (c + L::kWidth <= V) {
-                __builtin_memcpy(b, ptr + c, 16);
-#pragma unroll
-                for (int q = 0; q < L::kWidth; ++q) f((int)c + q, L::get(b[q]));
-            } else {
-                for (int q = 0; c + q < V; ++q) f((int)c + q, L::get(ptr[c + q]));
-            }
-        }
-    }
-    // exp((l - max) / temperature); 0 where it is below 2^-41.
+    // exp((l - max) / temperature), 2^-44 off; 0 where it is below 2^-41.  With n =
+    // 64 x / log 2 rounded: 2^(n / 64) from the table times e^r, |r| < 0.0055, to r^4.
     __device__ __forceinline__ double weight(float l) const {
-        if (l == most) return 1.0;
-        const double x = ((double)l - (double)most) * inverse;
-        return x > -28.5 ? exp(x) : 0.0;  // NaN (a masked logit, no temperature): 0
+        double x = ((double)l - (double)most) * inverse;
+        if (l == most) x = 0.0;
+        const bool some = x > -28.5;  // NaN (a masked logit, no temperature): none
+        x = some ? x : 0.0;
+        const double shift = 0x1.8p52;
+        const double s = fma(x, 0x1.71547652b82fep+6, shift);  // 64 / log 2
+        const int n = (int)(uint32_t)__builtin_bit_cast(u64, s);
+        const double r = fma(s - shift, -0x1.62e42fefa39efp-7, x);  // log 2 / 64
+        const double p = r * fma(r, fma(r, fma(r, 1.0 / 24, 1.0 / 6), 0.5), 1.0);
+        const double t = power[n & 63];
+        const double e = __builtin_amdgcn_ldexp(fma(t, p, t), n >> 6);
+        return some ? e : 0.0;
     }
     __device__ __forceinline__ int bin(float l) const {
         return l == most ? 0 : (int)fminf((most - l) * per, (float)(kBins - 1));
     }
 };
-__device__ __forceinline__ u64 whole(double w) { return (u64)__builtin_rint(w * kOne); }
+__device__ __forceinline__ u64 whole(double w) {
+    // below 2^52: the rounded value is the low half of w 2^40 + 2^52
+    return __builtin_bit_cast(u64, fma(w, kOne, 0x1p52)) - 0x4330000000000000ull;
+}
+
+// Logits and indices as keys in the order of the search (ascending), and back.
+__device__ __forceinline__ u64 key_of(float l, uint32_t index) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, l + 0.0f);  // -0 is 0
+    const uint32_t up = b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+    return ((u64)~up << 32) | index;
+}
+__device__ __forceinline__ float logit_of(u64 key) {
+    const uint32_t up = ~(uint32_t)(key >> 32);
+    return __builtin_bit_cast(float, up ^ ((up >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+// A row's elements, 16 bytes at a time, read from memory for each pass, or (HELD)
+// kept in LDS by the first one.
+template <class E, bool HELD>
+struct Row {
+    typedef Logits<E> L;
+    typedef typename L::Bits Bits;
+    static constexpr int W = L::kWidth;
+    const Bits* ptr;
+    int V;
+    u4_t* kept;
+
+    __device__ __forceinline__ u4_t piece(int c) const {
+        u4_t w = {};
+        if (c + W <= V) {
+            __builtin_memcpy(&w, ptr + c, 16);
+        } else if (c < V) {
+            Bits b[W] = {};
+#pragma unroll
+            for (int q = 0; q < W - 1; ++q) b[q] = ptr[c + q < V ? c + q : c];
+            __builtin_memcpy(&w, b, 16);
+        }
+        return w;
+    }
+    // Calls that take long expressions are kept apart two by two: with all of a
+    // piece's at once in registers they would not fit.
+    template <class Fn>
+    __device__ __forceinline__ void visit(u4_t w, int c, Fn&& f) const {
+        Bits b[W];
+        __builtin_memcpy(b, &w, 16);
+#pragma unroll
+        for (int q = 0; q < W; ++q) {
+            if (c + q < V) f(c + q, L::get(b[q]));
+            if (q & 1) __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    // f(index, logit) for this lane's elements.
+    template <class Fn>
+    __device__ __forceinline__ void each(Fn&& f) const {
+#pragma unroll 1
+        for (int p = threadIdx.x; p * W < V; p += kT) visit(HELD ? kept[p] : piece(p * W), p * W, f);
+    }
+    // The first pass: 4 pieces are on their way at once.
+    template <class Fn>
+    __device__ __forceinline__ void each_first(Fn&& f) const {
+#pragma unroll 1
+        for (int p = threadIdx.x; p * W < V; p += 4 * kT) {
+            u4_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = piece((p + i * kT) * W);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (HELD && (p + i * kT) * W < V) kept[p + i * kT] = w[i];
+                visit(w[i], (p + i * kT) * W, f);
+            }
+        }
+    }
+};
 
 template <class V, class Op>
 __device__ __forceinline__ V over_block(V v, V* slots, Op op) {
@@ -135,23 +219,29 @@ __device__ __forceinline__ void clear(Histogram& h) {
         h.count[i] = 0;
     }
 }
+__device__ __forceinline__ void clear(Single& h) {
+    for (int i = threadIdx.x; i < kBins; i += kT) h.sum[i] = 0;
+}
 
 // The bin in which the running sum (by_count: count) first reaches `goal`, and
-// what comes before it: s.bin, s.before_sum, s.before_count.  Bins run in
-// descending order of the logits.
-__device__ __forceinline__ void find_bin(Shared& s, const Histogram& h, bool by_count, u64 goal,
-                                         u64 sum0, u64 count0) {
+// what comes before it: s.bin, s.before_sum, s.before_count, s.bin_sum.  Bins run
+// in descending order of the logits.  sum_of and count_of: a bin's.
+template <class Sum, class Count>
+__device__ __forceinline__ void find_bin(Shared& s, Sum&& sum_of, Count&& count_of, bool by_count,
+                                         u64 goal, u64 sum0, u64 count0) {
     constexpr int PER = kBins / kT;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    u64 sum = 0;
-    uint32_t count = 0;
+    u64 sum[PER];
+    uint32_t count[PER];
+    u64 sums = 0;
+    uint32_t counts = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        sum += h.sum[threadIdx.x * PER + i];
-        count += h.count[threadIdx.x * PER + i];
+        sums += sum[i] = sum_of(threadIdx.x * PER + i);
+        counts += count[i] = count_of(threadIdx.x * PER + i);
     }
-    u64 sums = sum;
-    uint32_t counts = count;
+    const u64 own_sum = sums;
+    const uint32_t own_count = counts;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
         const u64 a = __shfl_up(sums, o, 64);
@@ -167,42 +257,106 @@ __device__ __forceinline__ void find_bin(Shared& s, const Histogram& h, bool by_
         s.wave_count[wave] = counts;
     }
     __syncthreads();
-    u64 bs = sum0 + sums - sum, bc = count0 + counts - count;
+    u64 bs = sum0 + sums - own_sum, bc = count0 + counts - own_count;
     for (int i = 0; i < wave; ++i) {
         bs += s.wave_sum[i];
         bc += s.wave_count[i];
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const u64 hs = h.sum[threadIdx.x * PER + i];
-        const uint32_t hc = h.count[threadIdx.x * PER + i];
-        const u64 before = by_count ? bc : bs, own = by_count ? hc : hs;
+        const u64 before = by_count ? bc : bs, own = by_count ? count[i] : sum[i];
         if (before < goal && goal <= before + own) {
             s.bin = threadIdx.x * PER + i;
             s.before_sum = bs;
             s.before_count = bc;
+            s.bin_sum = sum[i];
         }
-        bs += hs;
-        bc += hc;
+        bs += sum[i];
+        bc += count[i];
     }
+    __syncthreads();
+}
+__device__ __forceinline__ void find_bin(Shared& s, const Histogram& h, bool by_count, u64 goal,
+                                         u64 sum0, u64 count0) {
+    find_bin(s, [&](int i) { return h.sum[i]; }, [&](int i) { return h.count[i]; }, by_count, goal,
+             sum0, count0);
+}
+__device__ __forceinline__ void find_bin(Shared& s, const Single& h, bool by_count, u64 goal) {
+    if (by_count)
+        find_bin(s, [](int) { return (u64)0; }, [&](int i) { return h.count[i]; }, true, goal, 0, 0);
+    else
+        find_bin(s, [&](int i) { return h.sum[i]; }, [](int) { return 0u; }, false, goal, 0, 0);
+}
+
+// The sum of v over the lanes up to and with this one.
+__device__ __forceinline__ u64 running_sum(Shared& s, u64 v) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const u64 a = __shfl_up(v, o, 64);
+        if (lane >= o) v += a;
+    }
+    __syncthreads();
+    if (lane == 63) s.wave_sum[wave] = v;
+    __syncthreads();
+    for (int i = 0; i < wave; ++i) v += s.wave_sum[i];
+    return v;
+}
+
+// Appends the row's elements that `in` takes to the list (s.listed is 0); those
+// that it has no room for are counted.
+template <class R, class In>
+__device__ __forceinline__ void gather(Shared& s, const R& row, In&& in) {
+    row.each([&](int i, float l) __attribute__((always_inline)) {
+        if (in(l)) {
+            const uint32_t at = atomicAdd(&s.listed, 1u);
+            if (at < kList) s.list[at] = key_of(l, (uint32_t)i);
+        }
+    });
+    __syncthreads();
+}
+
+// Sorts the first n (at most kList) keys of the list: a bitonic network, a key a
+// lane, between lanes of a wave by exchanges and between waves through LDS.
+__device__ __forceinline__ void sort_list(Shared& s, uint32_t n) {
+    static_assert(kList == kT, "a key a lane");
+    const uint32_t t = threadIdx.x;
+    u64 key = t < n ? s.list[t] : ~0ull;
+    for (uint32_t size = 2; size < 2 * n; size <<= 1)
+        for (uint32_t half = size / 2; half > 0; half >>= 1) {
+            u64 other;
+            if (half < 64) {
+                other = __shfl_xor(key, (int)half, 64);
+            } else {
+                __syncthreads();
+                s.list[t] = key;
+                __syncthreads();
+                other = s.list[t ^ half];
+            }
+            const bool least = ((t & half) == 0) == ((t & size) == 0);
+            key = least == (key < other) ? key : other;
+        }
+    __syncthreads();
+    s.list[t] = key;
     __syncthreads();
 }
 
 // The first element, in the order, at which the running sum (by_count: count)
 // reaches `goal`, which lies between 1 and the whole row's.
-template <class E>
-__device__ __forceinline__ void search(Shared& s, const Row<E>& row, bool by_count, u64 goal) {
-    find_bin(s, s.all, by_count, goal, 0, 0);
+template <class R>
+__device__ __forceinline__ void search(Shared& s, Searches& h, const R& row, const Scale& sc,
+                                       bool by_count, u64 goal) {
+    find_bin(s, h.all, by_count, goal, 0, 0);
     const int bin = s.bin;
     u64 before_sum = s.before_sum, before_count = s.before_count;
-    uint32_t count = s.all.count[bin];
+    uint32_t count = h.all.count[bin];
     // The elements looked at: those of the bin, then those of lo <= l <= hi.
     float lo = 0.0f, hi = 0.0f;
     bool ranged = false;
     auto in = [&](float l) __attribute__((always_inline)) {
         if (ranged) return l >= lo && l <= hi;
         // a bin far out may hold logits without weight, which do not count
-        return row.bin(l) == bin && (bin < kBins * 7 / 8 || whole(row.weight(l)) != 0);
+        return sc.bin(l) == bin && (bin < kBins * 7 / 8 || whole(sc.weight(l)) != 0);
     };
     // fp32's range holds 278 doublings, and a pass takes off almost 11: the bound
     // is never reached.
@@ -228,19 +382,19 @@ __device__ __forceinline__ void search(Shared& s, const Row<E>& row, bool by_cou
             return (int)fmin(((double)hi - (double)l) * scale, (double)(kBins - 1));
         };
         __syncthreads();
-        clear(s.part);
+        clear(h.part);
         __syncthreads();
         row.each([&](int, float l) __attribute__((always_inline)) {
             if (l >= lo && l <= hi) {
                 const int b = sub(l);
-                atomicAdd(&s.part.sum[b], whole(row.weight(l)));
-                atomicAdd(&s.part.count[b], 1u);
+                atomicAdd(&h.part.sum[b], whole(sc.weight(l)));
+                atomicAdd(&h.part.count[b], 1u);
             }
         });
         __syncthreads();
-        find_bin(s, s.part, by_count, goal, before_sum, before_count);
+        find_bin(s, h.part, by_count, goal, before_sum, before_count);
         before_sum = s.before_sum, before_count = s.before_count;
-        count = s.part.count[s.bin];
+        count = h.part.count[s.bin];
         // the ends of that bin's logits
         const int want = s.bin;
         least = INFINITY, top = -INFINITY;
@@ -257,13 +411,13 @@ __device__ __forceinline__ void search(Shared& s, const Row<E>& row, bool by_cou
     __syncthreads();
     if (count > kList) {
         // `count` equal logits: the r-th of them by index.
-        const u64 w = whole(row.weight(lo));
+        const u64 w = whole(sc.weight(lo));
         const u64 r = by_count ? goal - before_count : (goal - before_sum + w - 1) / w;
         // Lane t looks at the t-th stretch of the row.
         const int64_t per = ((int64_t)row.V + kT - 1) / kT;
         const int64_t i0 = threadIdx.x * per, i1 = min(i0 + per, (int64_t)row.V);
         uint32_t mine = 0;
-        for (int64_t i = i0; i < i1; ++i) mine += Logits<E>::get(row.ptr[i]) == lo;
+        for (int64_t i = i0; i < i1; ++i) mine += R::L::get(row.ptr[i]) == lo;
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
         uint32_t upto = mine;
 #pragma unroll
@@ -277,7 +431,7 @@ __device__ __forceinline__ void search(Shared& s, const Row<E>& row, bool by_cou
         for (int i = 0; i < wave; ++i) n += s.wave_count[i];
         if (n < r && r <= n + mine)
             for (int64_t i = i0; i < i1; ++i)
-                if (Logits<E>::get(row.ptr[i]) == lo && ++n == r) {
+                if (R::L::get(row.ptr[i]) == lo && ++n == r) {
                     s.found.sum = before_sum + r * w;
                     s.found.index = i;
                     s.found.logit = lo;
@@ -287,35 +441,19 @@ __device__ __forceinline__ void search(Shared& s, const Row<E>& row, bool by_cou
     }
     if (threadIdx.x == 0) s.listed = 0;
     __syncthreads();
-    row.each([&](int i, float l) __attribute__((always_inline)) {
-        if (in(l)) {
-            const uint32_t at = atomicAdd(&s.listed, 1u);
-            if (at < kList) {
-                s.logit[at] = l;
-                s.index[at] = (uint32_t)i;
-                s.weight[at] = whole(row.weight(l));
-            }
-        }
-    });
-    __syncthreads();
-    if (threadIdx.x < count) {
-        const float l = s.logit[threadIdx.x];
-        const uint32_t i = s.index[threadIdx.x];
-        u64 bs = before_sum, bc = before_count;
-        for (uint32_t j = 0; j < count; ++j) {
-            const float lj = s.logit[j];
-            if (lj > l || (lj == l && s.index[j] < i)) {
-                bs += s.weight[j];
-                ++bc;
-            }
-        }
-        const u64 w = s.weight[threadIdx.x];
-        const u64 before = by_count ? bc : bs, own = by_count ? 1 : w;
-        if (before < goal && goal <= before + own) {
-            s.found.sum = bs + w;
-            s.found.index = i;
-            s.found.logit = l;
-        }
+    gather(s, row, in);
+    sort_list(s, count);
+    // the running sums over the list
+    const bool mine = threadIdx.x < count;
+    const u64 key = mine ? s.list[threadIdx.x] : 0;
+    const float l = logit_of(key);
+    const u64 w = mine ? whole(sc.weight(l)) : 0;
+    const u64 upto = before_sum + running_sum(s, w);
+    const u64 reach = by_count ? before_count + threadIdx.x + 1 : upto;
+    if (mine && reach >= goal && reach - (by_count ? 1 : w) < goal) {
+        s.found.sum = upto;
+        s.found.index = (uint32_t)key;
+        s.found.logit = l;
     }
     __syncthreads();
 }
@@ -334,38 +472,261 @@ __device__ __forceinline__ V at(const Setting<V>& s, int64_t row) {
     return s.each ? s.each[row] : s.value;
 }
 
-template <class E>
-__global__ __launch_bounds__(kT) void sample_kernel(
-    const typename Logits<E>::Bits* __restrict__ logits, int64_t ld, const float* __restrict__ u,
-    const Setting<float> temperature, const Setting<float> top_p, const Setting<float> min_p,
-    const Setting<int32_t> top_k, int64_t* __restrict__ tokens, float* __restrict__ logprobs,
-    int64_t M, int V) {
+struct Settings {
+    float u, temperature, top_p, min_p;
+    int32_t top_k;
+};
+
+// The row by one search after the other.
+template <class R>
+__device__ __forceinline__ void sample_searching(Shared& s, Searches& h, const R& row, const Scale& sc,
+                                                 const Settings& set) {
+    __syncthreads();
+    clear(h.all);
+    __syncthreads();
+    const double bound = set.min_p > 0.0f ? fmin((double)set.min_p, 1.0) : 0.0;
+    u64 kept = 0, total = 0;
+    uint32_t n = 0;
+    row.each([&](int, float l) __attribute__((always_inline)) {
+        const double e = sc.weight(l);
+        const u64 w = whole(e);
+        if (w != 0) {
+            const int b = sc.bin(l);
+            atomicAdd(&h.all.sum[b], w);
+            atomicAdd(&h.all.count[b], 1u);
+            total += w;
+            ++n;
+            if (e >= bound) kept += w;
+        }
+    });
+    auto add = [](auto a, auto b) { return a + b; };
+    kept = over_block(kept, s.wave_sum, add);
+    total = over_block(total, s.wave_sum, add);
+    n = over_block(n, s.wave_count, add);
+    u64 Z = total;
+    // top-k, top-p, the token
+#pragma unroll 1
+    for (int step = 0; step < 3; ++step) {
+        u64 goal = (u64)set.top_k;
+        if (step == 0 && !(set.top_k > 0 && (uint32_t)set.top_k < n)) continue;
+        if (step == 1) {
+            if (!(set.top_p < 1.0f)) continue;
+            goal = least_sum((double)set.top_p * (double)Z, false, Z);
+        }
+        if (step == 2) {
+            Z = min(Z, kept);
+            goal = least_sum((double)set.u * (double)Z, true, Z);
+        }
+        search(s, h, row, sc, step == 0, goal);
+        if (step < 2) Z = min(Z, s.found.sum);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) s.found.sum = Z;
+    __syncthreads();
+}
+
+// Which bins a row's token and the end of top-p lie in: those of first .. last, and
+// `end` (behind them, or -1), and the sums before first and before end.
+struct Wanted {
+    int first, last, end;
+    u64 before, before_end;
+    u64 total, kept;  // the sums of all and of what min-p keeps (without top-k)
+};
+
+__device__ __forceinline__ bool by_counts(const Settings& set, int V) {
+    return set.top_k > 0 && set.top_k <= kSmallK && set.top_k < V;
+}
+
+// From the histogram: of counts (`counts`: the bins up to the k-th's), or of sums.
+__device__ __forceinline__ Wanted wanted_bins(Shared& s, const Single& h, bool counts,
+                                              const Settings& set, u64 total, u64 kept) {
+    Wanted w = {0, 0, -1, 0, 0, total, kept};
+    if (counts) {
+        // fewer with weight than k: all of them
+        w.last = kLightBin - 1;
+        if ((u64)set.top_k <= total) {
+            find_bin(s, h, true, (u64)set.top_k);
+            w.last = s.bin;
+        }
+        return w;
+    }
+    u64 low = total, high = total;  // bounds of what top-p keeps
+    if (set.top_p < 1.0f) {
+        find_bin(s, h, false, least_sum((double)set.top_p * (double)total, false, total));
+        w.end = s.bin;
+        w.before_end = s.before_sum;
+        low = s.before_sum + 1, high = s.before_sum + s.bin_sum;
+    }
+    low = min(low, kept), high = min(high, kept);
+    find_bin(s, h, false, least_sum((double)set.u * (double)low, true, low));
+    w.first = s.bin;
+    w.before = s.before_sum;
+    w.last = w.first;
+    if (high != low) {
+        find_bin(s, h, false, least_sum((double)set.u * (double)high, true, high));
+        w.last = s.bin;
+    }
+    if (w.end <= w.last) w.last = max(w.last, w.end);
+    return w;
+}
+__device__ __forceinline__ bool wants(const Wanted& w, int bin) {
+    return (bin >= w.first && bin <= w.last) || bin == w.end;
+}
+
+// The token of a row whose wanted elements are the first n of the list (n at most
+// kList): s.found, with the sum kept for found.sum.
+__device__ __forceinline__ void sample_list(Shared& s, uint32_t n, bool counts, const Wanted& want,
+                                            const Scale& sc, const Settings& set) {
+    sort_list(s, n);
+    const uint32_t t = threadIdx.x;
+    const bool mine = t < n;
+    const u64 key = mine ? s.list[t] : 0;
+    const float l = logit_of(key);
+    const double e = mine ? sc.weight(l) : 0.0;
+    const u64 w = whole(e);
+    u64 upto = running_sum(s, w);
+    u64 Z;
+    if (counts) {
+        // the list is the beginning of the order
+        const uint32_t k = min((uint32_t)set.top_k, n);
+        if (t == k - 1) s.before_sum = upto;
+        __syncthreads();
+        Z = s.before_sum;
+        const double bound = set.min_p > 0.0f ? fmin((double)set.min_p, 1.0) : 0.0;
+        const u64 kept = over_block(t < k && e >= bound ? w : (u64)0, s.wave_sum,
+                                    [](u64 a, u64 b) { return a + b; });
+        if (set.top_p < 1.0f) {
+            const u64 goal = least_sum((double)set.top_p * (double)Z, false, Z);
+            if (mine && upto >= goal && upto - w < goal) s.bin_sum = upto;
+            __syncthreads();
+            Z = min(Z, s.bin_sum);
+        }
+        Z = min(Z, kept);
+    } else {
+        // The bins first .. last, then `end`: the sums before them come from the
+        // histogram.
+        const bool behind = want.end > want.last;
+        const int bin = mine ? sc.bin(l) : 0;
+        if (t == 0) s.before_count = 0;
+        __syncthreads();
+        if (mine && bin <= want.last && (t == n - 1 || sc.bin(logit_of(s.list[t + 1])) > want.last))
+            s.before_count = upto;  // the sum of first .. last
+        __syncthreads();
+        upto = behind && bin > want.last ? want.before_end + (upto - s.before_count)
+                                         : want.before + upto;
+        Z = want.total;
+        if (set.top_p < 1.0f) {
+            const u64 goal = least_sum((double)set.top_p * (double)Z, false, Z);
+            if (mine && upto >= goal && upto - w < goal && bin == want.end) s.bin_sum = upto;
+            __syncthreads();
+            Z = min(Z, s.bin_sum);
+        }
+        Z = min(Z, want.kept);
+    }
+    const u64 goal = least_sum((double)set.u * (double)Z, true, Z);
+    if (mine && upto >= goal && upto - w < goal) {
+        s.found.sum = Z;
+        s.found.index = (uint32_t)key;
+        s.found.logit = l;
+    }
+    __syncthreads();
+}
+
+struct SampleArgs {
+    const void* logits;
+    int64_t ld;
+    const float* u;
+    Setting<float> temperature, top_p, min_p;
+    Setting<int32_t> top_k;
+    int64_t* tokens;
+    float* logprobs;
+    int64_t M;
+    int V;
+    __device__ __forceinline__ Settings settings(int64_t m) const {
+        return {u[m], at(temperature, m), at(top_p, m), at(min_p, m), at(top_k, m)};
+    }
+    __device__ __forceinline__ void put(int64_t m, int64_t token, float logprob) const {
+        tokens[m] = token;
+        if (logprobs) logprobs[m] = logprob;
+    }
+    __device__ __forceinline__ void put_found(int64_t m, const Found& f, const Scale& sc) const {
+        const double x =
+            f.logit == sc.most ? 0.0 : ((double)f.logit - (double)sc.most) * sc.inverse;
+        put(m, f.index, (float)(x - log((double)f.sum / kOne)));
+    }
+};
+
+__device__ __forceinline__ Scale scale_for(const Shared& s, float most, float temperature) {
+    return {most, 1.0 / (double)temperature, kPerUnit / temperature, s.power};
+}
+__device__ __forceinline__ void fill_powers(Shared& s) {
+    if (threadIdx.x < 64) s.power[threadIdx.x] = exp2(threadIdx.x / 64.0);
+}
+
+// This lane's part of the histogram: of counts, or of sums, whose totals it adds.
+template <class R>
+__device__ __forceinline__ void add_to_histogram(Single& h, const R& row, const Scale& sc,
+                                                 const Settings& set, bool counts, u64& total,
+                                                 u64& kept) {
+    const double bound = set.min_p > 0.0f ? fmin((double)set.min_p, 1.0) : 0.0;
+    if (counts) {
+        row.each([&](int, float l) __attribute__((always_inline)) {
+            const int b = sc.bin(l);
+            if (b < kLightBin) {
+                atomicAdd(&h.count[b], 1u);
+                ++total;
+            }
+        });
+    } else {
+        row.each([&](int, float l) __attribute__((always_inline)) {
+            const double e = sc.weight(l);
+            const u64 w = whole(e);
+            if (w != 0) {
+                atomicAdd(&h.sum[sc.bin(l)], w);
+                total += w;
+                if (e >= bound) kept += w;
+            }
+        });
+    }
+}
+
+// A workgroup per row.  HELD: bytes of LDS that keep the row (0: none).
+template <class E, int HELD>
+__global__ __launch_bounds__(kT) void sample_kernel(const SampleArgs a) {
     __shared__ Shared s;
-    for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
-        Row<E> row = {logits + m * ld, V, 0.0f, 0.0, 0.0f};
+    __shared__ union {
+        Searches searches;
+        struct {
+            Single single;
+            u4_t row[HELD > 0 ? HELD / 16 : 1];
+        };
+    } h;
+    typedef Row<E, (HELD > 0)> R;
+    fill_powers(s);
+    for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
+        const R row = {static_cast<const typename R::Bits*>(a.logits) + m * a.ld, a.V, h.row};
+        const Settings set = a.settings(m);
+        __syncthreads();  // the row before is done
         // The largest logit, and whether there is a NaN.
         float most = -INFINITY;
         int bad = 0;
-        row.each([&](int, float l) __attribute__((always_inline)) {
+        row.each_first([&](int, float l) __attribute__((always_inline)) {
             most = fmaxf(most, l);
             bad |= l != l;
         });
-        __syncthreads();  // the row before is done
-        if (threadIdx.x == 0) s.flag = 0;
-        clear(s.all);
+        if (threadIdx.x == 0) {
+            s.flag = 0;
+            s.listed = 0;
+        }
+        clear(h.single);
         most = over_block(most, s.wave_max, [](float a, float b) { return fmaxf(a, b); });
         if (bad) s.flag = 1;
         __syncthreads();
         if (s.flag || most == -INFINITY) {
-            if (threadIdx.x == 0) {
-                tokens[m] = -1;
-                if (logprobs) logprobs[m] = __builtin_nanf("");
-            }
+            if (threadIdx.x == 0) a.put(m, -1, __builtin_nanf(""));
             continue;
         }
-        const float t = at(temperature, m);
-        row.most = most;
-        if (!(t > 0.0f)) {
+        if (!(set.temperature > 0.0f)) {
             // Greedy: the first of the largest.
             uint32_t first = 0xFFFFFFFFu;
             row.each([&](int i, float l) __attribute__((always_inline)) {
@@ -373,71 +734,49 @@ __global__ __launch_bounds__(kT) void sample_kernel(
             });
             first = over_block(first, s.wave_count,
                                [](uint32_t a, uint32_t b) { return a < b ? a : b; });
-            if (threadIdx.x == 0) {
-                tokens[m] = first;
-                if (logprobs) logprobs[m] = 0.0f;
-            }
+            if (threadIdx.x == 0) a.put(m, first, 0.0f);
             continue;
         }
-        row.inverse = 1.0 / (double)t;
-        row.per = kPerUnit / t;
-        // The histogram; the sum of what min-p keeps.
-        const float least = at(min_p, m);
-        const double bound = least > 0.0f ? fmin((double)least, 1.0) : 0.0;
-        u64 kept = 0;
-        row.each([&](int, float l) __attribute__((always_inline)) {
-            const double e = row.weight(l);
-            const u64 w = whole(e);
-            if (w != 0) {
-                const int b = row.bin(l);
-                atomicAdd(&s.all.sum[b], w);
-                atomicAdd(&s.all.count[b], 1u);
-                if (e >= bound) kept += w;
-            }
-        });
-        __syncthreads();
-        u64 total = 0;
-        uint32_t n = 0;
-        for (int i = threadIdx.x; i < kBins; i += kT) {
-            total += s.all.sum[i];
-            n += s.all.count[i];
-        }
-        auto add = [](auto a, auto b) { return a + b; };
-        kept = over_block(kept, s.wave_sum, add);
-        total = over_block(total, s.wave_sum, add);
-        n = over_block(n, s.wave_count, add);
-        u64 Z = total;
-        const int32_t k = at(top_k, m);
-        if (k > 0 && (uint32_t)k < n) {
-            search(s, row, true, (u64)k);
-            Z = s.found.sum;
-        }
-        const float p = at(top_p, m);
-        if (p < 1.0f) {
-            search(s, row, false, least_sum((double)p * (double)Z, false, Z));
-            Z = min(Z, s.found.sum);
-        }
-        Z = min(Z, kept);
-        search(s, row, false, least_sum((double)u[m] * (double)Z, true, Z));
-        if (threadIdx.x == 0) {
-            tokens[m] = s.found.index;
-            if (logprobs) {
-                const double x = s.found.logit == most
-                                     ? 0.0
-                                     : ((double)s.found.logit - (double)most) * row.inverse;
-                logprobs[m] = (float)(x - log((double)Z / kOne));
+        const Scale sc = scale_for(s, most, set.temperature);
+        const bool counts = by_counts(set, a.V);
+        bool done = false;
+        if (counts || !(set.top_k > 0 && set.top_k < a.V)) {
+            u64 total = 0, kept = 0;
+            add_to_histogram(h.single, row, sc, set, counts, total, kept);
+            auto add = [](u64 x, u64 y) { return x + y; };
+            total = over_block(total, s.wave_sum, add);
+            kept = over_block(kept, s.wave_sum, add);
+            const Wanted want = wanted_bins(s, h.single, counts, set, total, kept);
+            gather(s, row, [&](float l) __attribute__((always_inline)) {
+                return wants(want, sc.bin(l));
+            });
+            const uint32_t n = s.listed;
+            if (n <= kList) {
+                sample_list(s, n, counts, want, sc, set);
+                done = true;
             }
         }
+        if (!done) {
+            const Row<E, false> all = {row.ptr, a.V, nullptr};
+            sample_searching(s, h.searches, all, sc, set);
+        }
+        if (threadIdx.x == 0) a.put_found(m, s.found, sc);
     }
 }
 
 template <class E>
 hipError_t launch(const SampleCall& c, hipStream_t stream) {
     const unsigned blocks = (unsigned)(c.M < (1 << 20) ? c.M : 1 << 20);
-    hipLaunchKernelGGL(sample_kernel<E>, dim3(blocks), dim3(kT), 0, stream,
-                       static_cast<const typename Logits<E>::Bits*>(c.logits), c.ld, c.u,
-                       c.temperature, c.top_p, c.min_p, c.top_k, c.tokens, c.logprobs, c.M,
-                       (int)c.V);
+    const SampleArgs a = {c.logits, c.ld, c.u, c.temperature, c.top_p, c.min_p, c.top_k,
+                          c.tokens, c.logprobs, c.M, (int)c.V};
+    const int64_t bytes = (c.V + Logits<E>::kWidth - 1) / Logits<E>::kWidth * 16;
+    auto go = [&](auto held) {
+        hipLaunchKernelGGL((sample_kernel<E, decltype(held)::value>), dim3(blocks), dim3(kT), 0,
+                           stream, a);
+    };
+    if (bytes <= 32768) go(std::integral_constant<int, 32768>{});
+    else if (bytes <= 131072) go(std::integral_constant<int, 131072>{});
+    else go(std::integral_constant<int, 0>{});
     return hipGetLastError();
 }
 

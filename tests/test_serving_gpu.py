@@ -567,7 +567,8 @@ def uniform(M, seed):
 
 SETTINGS = [dict(), dict(t=0.7, k=1), dict(t=0.0), dict(k=40), dict(p=0.9), dict(m=0.05),
             dict(t=1.3, k=200, p=0.8, m=0.01), dict(t=0.05, p=0.5), dict(t=50.0, k=3000, p=0.99),
-            dict(p=0.0), dict(m=1.0), dict(k=10 ** 6)]
+            dict(p=0.0), dict(m=1.0), dict(k=10 ** 6), dict(k=512), dict(k=513, p=0.95),
+            dict(t=0.02, k=30), dict(t=20.0, p=0.999), dict(p=0.97, m=0.3), dict(t=3.0, k=7, m=0.2)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES + [torch.float32])
