@@ -125,6 +125,25 @@ struct Scale {
     __device__ __forceinline__ int bin(float l) const {
         return l == most ? 0 : (int)fminf((most - l) * per, (float)(kBins - 1));
     }
+    // Where the largest logit and the bins' width are finite numbers above 0 the
+    // difference needs no second look: bins from the quotient alone (-infinity:
+    // the last one), weights held to 2^-43, which rounds to none.
+    __device__ __forceinline__ bool ordinary() const {
+        return fabsf(most) < INFINITY && per < INFINITY && per > 0.0f;
+    }
+    __device__ __forceinline__ float place(float l) const { return (most - l) * per; }
+    __device__ __forceinline__ u64 whole_weight(float l) const {
+        const double x = fmax(((double)l - (double)most) * inverse, -30.0);
+        const double shift = 0x1.8p52;
+        const double s = fma(x, 0x1.71547652b82fep+6, shift);
+        const int n = (int)(uint32_t)__builtin_bit_cast(u64, s);
+        const double r = fma(s - shift, -0x1.62e42fefa39efp-7, x);
+        const double p = r * fma(r, fma(r, fma(r, 1.0 / 24, 1.0 / 6), 0.5), 1.0);
+        const double t = power[n & 63];
+        // 2^40 2^(n / 64's whole part)
+        const double up = __builtin_bit_cast(double, (u64)(uint32_t)((n >> 6) + 1063) << 52);
+        return __builtin_bit_cast(u64, fma(fma(t, p, t), up, 0x1p52)) - 0x4330000000000000ull;
+    }
 };
 __device__ __forceinline__ u64 whole(double w) {
     // below 2^52: the rounded value is the low half of w 2^40 + 2^52
@@ -569,10 +588,6 @@ __device__ __forceinline__ Wanted wanted_bins(Shared& s, const Single& h, bool c
     if (w.end <= w.last) w.last = max(w.last, w.end);
     return w;
 }
-__device__ __forceinline__ bool wants(const Wanted& w, int bin) {
-    return (bin >= w.first && bin <= w.last) || bin == w.end;
-}
-
 // The token of a row whose wanted elements are the first n of the list (n at most
 // kList): s.found, with the sum kept for found.sum.
 __device__ __forceinline__ void sample_list(Shared& s, uint32_t n, bool counts, const Wanted& want,
@@ -606,10 +621,10 @@ __device__ __forceinline__ void sample_list(Shared& s, uint32_t n, bool counts, 
         // The bins first .. last, then `end`: the sums before them come from the
         // histogram.
         const bool behind = want.end > want.last;
-        const int bin = mine ? sc.bin(l) : 0;
+        const int bin = mine ? (int)sc.place(l) : 0;
         if (t == 0) s.before_count = 0;
         __syncthreads();
-        if (mine && bin <= want.last && (t == n - 1 || sc.bin(logit_of(s.list[t + 1])) > want.last))
+        if (mine && bin <= want.last && (t == n - 1 || (int)sc.place(logit_of(s.list[t + 1])) > want.last))
             s.before_count = upto;  // the sum of first .. last
         __syncthreads();
         upto = behind && bin > want.last ? want.before_end + (upto - s.before_count)
@@ -663,31 +678,61 @@ __device__ __forceinline__ void fill_powers(Shared& s) {
     if (threadIdx.x < 64) s.power[threadIdx.x] = exp2(threadIdx.x / 64.0);
 }
 
-// This lane's part of the histogram: of counts, or of sums, whose totals it adds.
+// This lane's part of the histogram, of counts or of sums, and of the sum that min-p
+// keeps.  An ordinary row's (Scale).
 template <class R>
 __device__ __forceinline__ void add_to_histogram(Single& h, const R& row, const Scale& sc,
-                                                 const Settings& set, bool counts, u64& total,
-                                                 u64& kept) {
-    const double bound = set.min_p > 0.0f ? fmin((double)set.min_p, 1.0) : 0.0;
+                                                 const Settings& set, bool counts, u64& kept) {
     if (counts) {
         row.each([&](int, float l) __attribute__((always_inline)) {
-            const int b = sc.bin(l);
-            if (b < kLightBin) {
-                atomicAdd(&h.count[b], 1u);
-                ++total;
+            const float d = sc.place(l);
+            if (d < (float)kLightBin) atomicAdd(&h.count[(int)d], 1u);
+        });
+    } else if (set.min_p > 0.0f) {
+        const double bound = fmin((double)set.min_p, 1.0);
+        row.each([&](int, float l) __attribute__((always_inline)) {
+            const float d = sc.place(l);
+            if (d < (float)kLightBin) {
+                const double e = sc.weight(l);
+                const u64 w = whole(e);
+                atomicAdd(&h.sum[(int)d], w);
+                if (e >= bound) kept += w;
             }
         });
     } else {
         row.each([&](int, float l) __attribute__((always_inline)) {
-            const double e = sc.weight(l);
-            const u64 w = whole(e);
-            if (w != 0) {
-                atomicAdd(&h.sum[sc.bin(l)], w);
-                total += w;
-                if (e >= bound) kept += w;
-            }
+            const float d = sc.place(l);
+            if (d < (float)kLightBin) atomicAdd(&h.sum[(int)d], sc.whole_weight(l));
         });
     }
+}
+// The sum over a histogram, in every lane.
+__device__ __forceinline__ u64 histogram_total(Shared& s, const Single& h, bool counts) {
+    u64 total = 0;
+    for (int i = threadIdx.x; i < kBins; i += kT) total += counts ? h.count[i] : h.sum[i];
+    return over_block(total, s.wave_sum, [](u64 x, u64 y) { return x + y; });
+}
+
+// Whether a row's settings and scale allow the ways of one histogram.
+__device__ __forceinline__ bool one_histogram(const Scale& sc, const Settings& set, int V) {
+    return sc.ordinary() && (by_counts(set, V) || !(set.top_k > 0 && set.top_k < V));
+}
+
+template <class R>
+__device__ __forceinline__ void gather_wanted(Shared& s, const R& row, const Scale& sc,
+                                              const Wanted& want) {
+    const float lo = (float)want.first, hi = (float)(want.last + 1), lo2 = (float)want.end,
+                hi2 = (float)(want.end + 1);
+    if (want.end > want.last)
+        gather(s, row, [&](float l) __attribute__((always_inline)) {
+            const float d = sc.place(l);
+            return (d >= lo && d < hi) || (d >= lo2 && d < hi2);
+        });
+    else
+        gather(s, row, [&](float l) __attribute__((always_inline)) {
+            const float d = sc.place(l);
+            return d >= lo && d < hi;
+        });
 }
 
 // A workgroup per row.  HELD: bytes of LDS that keep the row (0: none).
@@ -740,16 +785,16 @@ __global__ __launch_bounds__(kT) void sample_kernel(const SampleArgs a) {
         const Scale sc = scale_for(s, most, set.temperature);
         const bool counts = by_counts(set, a.V);
         bool done = false;
-        if (counts || !(set.top_k > 0 && set.top_k < a.V)) {
-            u64 total = 0, kept = 0;
-            add_to_histogram(h.single, row, sc, set, counts, total, kept);
-            auto add = [](u64 x, u64 y) { return x + y; };
-            total = over_block(total, s.wave_sum, add);
-            kept = over_block(kept, s.wave_sum, add);
+        if (one_histogram(sc, set, a.V)) {
+            u64 kept = 0;
+            add_to_histogram(h.single, row, sc, set, counts, kept);
+            __syncthreads();
+            const u64 total = histogram_total(s, h.single, counts);
+            kept = set.min_p > 0.0f ? over_block(kept, s.wave_sum,
+                                                 [](u64 x, u64 y) { return x + y; })
+                                    : total;
             const Wanted want = wanted_bins(s, h.single, counts, set, total, kept);
-            gather(s, row, [&](float l) __attribute__((always_inline)) {
-                return wants(want, sc.bin(l));
-            });
+            gather_wanted(s, row, sc, want);
             const uint32_t n = s.listed;
             if (n <= kList) {
                 sample_list(s, n, counts, want, sc, set);
@@ -764,11 +809,219 @@ __global__ __launch_bounds__(kT) void sample_kernel(const SampleArgs a) {
     }
 }
 
+// Few long rows: pieces of kT * 16 bytes, a workgroup each, in four launches, with a
+// row's histogram and list in the workspace.
+struct Space {
+    Single hist;
+    u64 list[kList];
+    Wanted want;
+    u64 kept;
+    uint32_t listed, first;  // first: of the largest logits (greedy)
+    float most;
+    int unused;
+};
+struct Spaces {
+    Space* rows;
+    float* most;  // of each piece: [M][pieces], NaN for a piece that has one
+    int pieces;
+};
+
+// A piece of a row.
 template <class E>
-hipError_t launch(const SampleCall& c, hipStream_t stream) {
+struct Piece {
+    typedef Row<E, false> R;
+    typedef typename R::L L;
+    R row;
+    u4_t bits;
+    int c;
+    __device__ __forceinline__ Piece(const SampleArgs& a, int64_t m, int p)
+        : row{static_cast<const typename R::Bits*>(a.logits) + m * a.ld, a.V, nullptr},
+          c((p * kT + (int)threadIdx.x) * R::W) {
+        bits = row.piece(c);
+    }
+    template <class Fn>
+    __device__ __forceinline__ void each(Fn&& f) const {
+        row.visit(bits, c, f);
+    }
+};
+
+// The largest logit of each piece; the spaces cleared.
+template <class E>
+__global__ __launch_bounds__(kT) void piece_most_kernel(const SampleArgs a, const Spaces ws) {
+    __shared__ float slots[kT / 64];
+    __shared__ int flag;
+    const int p = blockIdx.x;
+    const int64_t m = blockIdx.y;
+    const Piece<E> piece(a, m, p);
+    Space& space = ws.rows[m];
+    if (threadIdx.x == 0) flag = 0;
+    for (int i = p * kT + threadIdx.x; i < kBins; i += ws.pieces * kT) space.hist.sum[i] = 0;
+    if (p == 0 && threadIdx.x == 0) {
+        space.kept = 0;
+        space.listed = 0;
+        space.first = 0xFFFFFFFFu;
+    }
+    float most = -INFINITY;
+    bool bad = false;
+    piece.each([&](int, float l) __attribute__((always_inline)) {
+        most = fmaxf(most, l);
+        bad |= l != l;
+    });
+    most = over_block(most, slots, [](float a, float b) { return fmaxf(a, b); });
+    if (bad) flag = 1;
+    __syncthreads();
+    if (threadIdx.x == 0) ws.most[m * ws.pieces + p] = flag ? __builtin_nanf("") : most;
+}
+
+// The largest logit of a row, NaN where it has one.
+__device__ __forceinline__ float most_of_row(float* slots, const Spaces& ws, int64_t m) {
+    float most = -INFINITY;
+    bool bad = false;
+    for (int i = threadIdx.x; i < ws.pieces; i += kT) {
+        const float v = ws.most[m * ws.pieces + i];
+        most = fmaxf(most, v);
+        bad |= v != v;
+    }
+    // a NaN as +infinity's successor in the order of the bits
+    uint32_t key = bad ? 0xFFFFFFFFu : (uint32_t)(~(key_of(most, 0) >> 32));
+    key = over_block(key, reinterpret_cast<uint32_t*>(slots),
+                     [](uint32_t a, uint32_t b) { return max(a, b); });
+    return key == 0xFFFFFFFFu ? __builtin_nanf("") : logit_of((u64)~key << 32);
+}
+
+template <class E>
+__global__ __launch_bounds__(kT) void piece_histogram_kernel(const SampleArgs a, const Spaces ws) {
+    __shared__ Shared s;
+    __shared__ Single h;
+    const int64_t m = blockIdx.y;
+    const Piece<E> piece(a, m, blockIdx.x);
+    Space& space = ws.rows[m];
+    const Settings set = a.settings(m);
+    fill_powers(s);
+    clear(h);
+    const float most = most_of_row(s.wave_max, ws, m);
+    if (blockIdx.x == 0 && threadIdx.x == 0) space.most = most;
+    if (!(most > -INFINITY)) return;
+    if (!(set.temperature > 0.0f)) {
+        uint32_t first = 0xFFFFFFFFu;
+        piece.each([&](int i, float l) __attribute__((always_inline)) {
+            if (l == most) first = min(first, (uint32_t)i);
+        });
+        if (first != 0xFFFFFFFFu) atomicMin(&space.first, first);
+        return;
+    }
+    const Scale sc = scale_for(s, most, set.temperature);
+    if (!one_histogram(sc, set, a.V)) return;
+    const bool counts = by_counts(set, a.V);
+    u64 kept = 0;
+    add_to_histogram(h, piece, sc, set, counts, kept);
+    if (set.min_p > 0.0f && !counts) {
+        kept = over_block(kept, s.wave_sum, [](u64 x, u64 y) { return x + y; });
+        if (threadIdx.x == 0 && kept != 0) atomicAdd(&space.kept, kept);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < kBins; i += kT) {
+        if (counts) {
+            if (h.count[i] != 0) atomicAdd(&space.hist.count[i], h.count[i]);
+        } else if (h.sum[i] != 0) {
+            atomicAdd(&space.hist.sum[i], h.sum[i]);
+        }
+    }
+}
+
+template <class E>
+__global__ __launch_bounds__(kT) void piece_gather_kernel(const SampleArgs a, const Spaces ws) {
+    __shared__ Shared s;
+    __shared__ Single h;
+    const int64_t m = blockIdx.y;
+    const Piece<E> piece(a, m, blockIdx.x);
+    Space& space = ws.rows[m];
+    const Settings set = a.settings(m);
+    const float most = space.most;
+    if (!(most > -INFINITY) || !(set.temperature > 0.0f)) return;
+    const Scale sc = scale_for(s, most, set.temperature);
+    if (!one_histogram(sc, set, a.V)) return;
+    const bool counts = by_counts(set, a.V);
+    for (int i = threadIdx.x; i < kBins; i += kT) h.sum[i] = space.hist.sum[i];
+    if (threadIdx.x == 0) s.listed = 0;
+    __syncthreads();
+    const u64 total = histogram_total(s, h, counts);
+    const u64 kept = set.min_p > 0.0f ? space.kept : total;
+    const Wanted want = wanted_bins(s, h, counts, set, total, kept);
+    if (blockIdx.x == 0 && threadIdx.x == 0) space.want = want;
+    gather_wanted(s, piece, sc, want);
+    const uint32_t n = s.listed;
+    if (n == 0) return;
+    if (threadIdx.x == 0) s.flag = (int)atomicAdd(&space.listed, n);
+    __syncthreads();
+    const uint32_t to = (uint32_t)s.flag;
+    for (uint32_t i = threadIdx.x; i < min(n, (uint32_t)kList); i += kT)
+        if (to + i < kList) space.list[to + i] = s.list[i];
+}
+
+template <class E>
+__global__ __launch_bounds__(kT) void finish_row_kernel(const SampleArgs a, const Spaces ws) {
+    __shared__ Shared s;
+    __shared__ Searches h;
+    const int64_t m = blockIdx.x;
+    const Space& space = ws.rows[m];
+    const Settings set = a.settings(m);
+    const float most = space.most;
+    if (!(most > -INFINITY) || !(set.temperature > 0.0f)) {
+        if (threadIdx.x == 0) {
+            if (most > -INFINITY)
+                a.put(m, space.first, 0.0f);
+            else
+                a.put(m, -1, __builtin_nanf(""));
+        }
+        return;
+    }
+    fill_powers(s);
+    const Scale sc = scale_for(s, most, set.temperature);
+    const uint32_t n = space.listed;
+    if (one_histogram(sc, set, a.V) && n <= kList) {
+        if (threadIdx.x < n) s.list[threadIdx.x] = space.list[threadIdx.x];
+        const Wanted want = space.want;
+        __syncthreads();
+        sample_list(s, n, by_counts(set, a.V), want, sc, set);
+    } else {
+        const Row<E, false> row = {
+            static_cast<const typename Logits<E>::Bits*>(a.logits) + m * a.ld, a.V, nullptr};
+        sample_searching(s, h, row, sc, set);
+    }
+    if (threadIdx.x == 0) a.put_found(m, s.found, sc);
+}
+
+// Whether rows are cut into pieces.
+bool cuts(int dtype, int64_t M, int64_t V) {
+    const int64_t bytes = V * (dtype == PGEMM_F32 ? 4 : 2);
+    return bytes > 32768 && M <= 64;
+}
+
+template <class E>
+hipError_t launch_pieces(const SampleArgs& a, const Spaces& ws, hipStream_t stream) {
+    const dim3 grid((unsigned)ws.pieces, (unsigned)a.M);
+    hipLaunchKernelGGL(piece_most_kernel<E>, grid, dim3(kT), 0, stream, a, ws);
+    hipLaunchKernelGGL(piece_histogram_kernel<E>, grid, dim3(kT), 0, stream, a, ws);
+    hipLaunchKernelGGL(piece_gather_kernel<E>, grid, dim3(kT), 0, stream, a, ws);
+    hipLaunchKernelGGL(finish_row_kernel<E>, dim3((unsigned)a.M), dim3(kT), 0, stream, a, ws);
+    return hipGetLastError();
+}
+
+template <class E>
+hipError_t launch(const SampleCall& c, Arena& ar, hipStream_t stream) {
+    Spaces ws = {};
+    const bool cut = cuts(c.dtype, c.M, c.V);
+    if (cut) {
+        ws.pieces = (int)((c.V + kT * Logits<E>::kWidth - 1) / (kT * Logits<E>::kWidth));
+        ws.rows = static_cast<Space*>(ar.take(c.M * (int64_t)sizeof(Space)));
+        ws.most = static_cast<float*>(ar.take(c.M * ws.pieces * 4));
+    }
+    if (ar.dry()) return hipSuccess;
     const unsigned blocks = (unsigned)(c.M < (1 << 20) ? c.M : 1 << 20);
     const SampleArgs a = {c.logits, c.ld, c.u, c.temperature, c.top_p, c.min_p, c.top_k,
                           c.tokens, c.logprobs, c.M, (int)c.V};
+    if (cut) return launch_pieces<E>(a, ws, stream);
     const int64_t bytes = (c.V + Logits<E>::kWidth - 1) / Logits<E>::kWidth * 16;
     auto go = [&](auto held) {
         hipLaunchKernelGGL((sample_kernel<E, decltype(held)::value>), dim3(blocks), dim3(kT), 0,
@@ -783,9 +1036,9 @@ hipError_t launch(const SampleCall& c, hipStream_t stream) {
 }  // namespace
 
 hipError_t sample(const SampleCall& c, Arena& ar, hipStream_t stream) {
-    if (ar.dry() || c.M == 0) return hipSuccess;
-    if (c.dtype == PGEMM_F32) return launch<F32>(c, stream);
-    return c.dtype == PGEMM_BF16 ? launch<BF16>(c, stream) : launch<F16>(c, stream);
+    if (c.M == 0) return hipSuccess;
+    if (c.dtype == PGEMM_F32) return launch<F32>(c, ar, stream);
+    return c.dtype == PGEMM_BF16 ? launch<BF16>(c, ar, stream) : launch<F16>(c, ar, stream);
 }
 
 }  // namespace layer

@@ -584,6 +584,24 @@ def test_sample(V, dtype):
         check_sample(l, u, got, (V, dtype, s), **s)
 
 
+@pytest.mark.parametrize("M,V,dtype", [(66, 40000, torch.float32), (65, 33001, torch.float16),
+                                       (65, 70003, torch.bfloat16), (65, 16385, torch.bfloat16)])
+def test_sample_many_rows(M, V, dtype):
+    """Long rows of a workgroup each: kept in LDS and read again."""
+    l = rand((M, V), dtype, V, std=3.0, pitch=V + 1)
+    u = uniform(M, V)
+    for s in (dict(), dict(k=50, p=0.9), dict(p=0.8, m=0.02), dict(k=2000), dict(t=0.0)):
+        say("sample, many rows", M, V, dtype, s)
+        got = pg.psample(l, u, temperature=s.get("t", 1.0), top_k=s.get("k", 0), top_p=s.get("p", 1.0),
+                         min_p=s.get("m", 0.0))
+        check_sample(l, u, got, s, **s)
+    # ties and crowds
+    l[:, ::3] = 2.0
+    for s in (dict(), dict(k=V // 2, p=0.9), dict(k=100)):
+        got = pg.psample(l, u, top_k=s.get("k", 0), top_p=s.get("p", 1.0))
+        check_sample(l, u, got, s, **s)
+
+
 @pytest.mark.parametrize("M,V", [(300, 1000), (70, 20000), (513, 130)])
 def test_sample_settings_by_row(M, V):
     rng = np.random.default_rng(M)
