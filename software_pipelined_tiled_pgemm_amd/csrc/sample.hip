@@ -32,6 +32,8 @@
 // workspace.
 #include "sample.h"
 
+#include <type_traits>
+
 #include "layer_math.h"
 
 namespace pgemm {
@@ -40,17 +42,60 @@ namespace {
 
 struct F32 {};  // logits of 32 bits
 
+// Pieces of 16 bytes; the largest and the smallest of many pieces, as whole numbers
+// in the logits' order, two at a time in 16 bits (NaN come out beyond the
+// infinities).
+typedef int16_t s2_t __attribute__((ext_vector_type(2)));
 template <class E>
 struct Logits {
     static constexpr int kWidth = 8;  // logits of 16 bytes
     typedef uint16_t Bits;
     __device__ static __forceinline__ float get(uint16_t b) { return E::get(b); }
+    static constexpr bool kBrain = std::is_same<E, BF16>::value;
+    static constexpr uint32_t kLeast = kBrain ? 0xFF80FF80u : 0xFC00FC00u;  // -infinity, twice
+    struct Ends {
+        static constexpr int16_t kTop = (int16_t)((uint16_t)kLeast ^ 0x7FFF),
+                                 kLow = (int16_t)((uint16_t)kLeast & 0x7FFF);  // +- infinity
+        s2_t top = {kTop, kTop}, low = {kLow, kLow};
+        __device__ __forceinline__ void add(u4_t w) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t word = w[q];  // (a bit_cast of an element takes element 0)
+                const s2_t b = __builtin_bit_cast(s2_t, word);
+                const s2_t flip = (b >> 15) & 0x7FFF;
+                top = __builtin_elementwise_max(top, (s2_t)(b ^ flip));
+                low = __builtin_elementwise_min(low, (s2_t)(b ^ flip));
+            }
+        }
+        __device__ static __forceinline__ float value(int v) {
+            return E::get((uint16_t)(v < 0 ? v ^ 0x7FFF : v));
+        }
+        __device__ __forceinline__ float most() const { return value(max(top[0], top[1])); }
+        __device__ __forceinline__ float least() const { return value(min(low[0], low[1])); }
+    };
 };
 template <>
 struct Logits<F32> {
     static constexpr int kWidth = 4;
     typedef uint32_t Bits;
     __device__ static __forceinline__ float get(uint32_t b) { return __builtin_bit_cast(float, b); }
+    static constexpr uint32_t kLeast = 0xFF800000u;
+    struct Ends {
+        int top = (int)(kLeast ^ 0x7FFFFFFFu), low = (int)(kLeast & 0x7FFFFFFFu);
+        __device__ __forceinline__ void add(u4_t w) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int b = (int)w[q], v = b ^ ((b >> 31) & 0x7FFFFFFF);
+                top = max(top, v);
+                low = min(low, v);
+            }
+        }
+        __device__ static __forceinline__ float value(int v) {
+            return __builtin_bit_cast(float, v < 0 ? v ^ 0x7FFFFFFF : v);
+        }
+        __device__ __forceinline__ float most() const { return value(top); }
+        __device__ __forceinline__ float least() const { return value(low); }
+    };
 };
 
 constexpr int kT = 1024;       // lanes of a row's workgroup
@@ -60,6 +105,7 @@ constexpr int kSmallK = 512;   // most of top-k for the way of counts alone
 // Bins from here on hold no weight: exp(-28.5) 2^40 is below a half.
 constexpr int kLightBin = 1824;
 constexpr float kPerUnit = 64.0f;  // bins per unit of (max - l) / temperature
+constexpr int kStepBits = 8, kSteps = 1 << kStepBits;  // of the exponential's table
 constexpr double kOne = 1099511627776.0;  // 2^40, the largest weight
 
 typedef unsigned long long u64;
@@ -80,7 +126,7 @@ struct Found {
 // LDS: what every way needs, and the histograms; a kept row takes the place of those
 // of the searches, which read the row from memory.
 struct Shared {
-    double power[64];  // 2^(i / 64)
+    double power[kSteps];  // 2^(i / kSteps)
     u64 list[kList];   // sorted keys (key_of)
     u64 wave_sum[kT / 64];
     uint32_t wave_count[kT / 64];
@@ -104,44 +150,47 @@ struct Scale {
     float most;
     double inverse;       // 1 / temperature
     float per;            // bins per unit of max - l
-    const double* power;  // 2^(i / 64) in LDS
+    const double* power;  // 2^(i / kSteps) in LDS
 
-    // exp((l - max) / temperature), 2^-44 off; 0 where it is below 2^-41.  With n =
-    // 64 x / log 2 rounded: 2^(n / 64) from the table times e^r, |r| < 0.0055, to r^4.
+    // exp((l - max) / temperature), 2^-42 of it off; 0 where it is below 2^-41.  With
+    // n = 256 x / log 2 rounded: 2^(n / 256) from the table times e^r, |r| < 0.00136, to
+    // r^3.
     __device__ __forceinline__ double weight(float l) const {
         double x = ((double)l - (double)most) * inverse;
         if (l == most) x = 0.0;
         const bool some = x > -28.5;  // NaN (a masked logit, no temperature): none
         x = some ? x : 0.0;
         const double shift = 0x1.8p52;
-        const double s = fma(x, 0x1.71547652b82fep+6, shift);  // 64 / log 2
+        const double s = fma(x, kSteps / 0.693147180559945309417232, shift);
         const int n = (int)(uint32_t)__builtin_bit_cast(u64, s);
-        const double r = fma(s - shift, -0x1.62e42fefa39efp-7, x);  // log 2 / 64
-        const double p = r * fma(r, fma(r, fma(r, 1.0 / 24, 1.0 / 6), 0.5), 1.0);
-        const double t = power[n & 63];
-        const double e = __builtin_amdgcn_ldexp(fma(t, p, t), n >> 6);
+        const double r = fma(s - shift, -0.693147180559945309417232 / kSteps, x);
+        const double p = r * fma(r, fma(r, 1.0 / 6, 0.5), 1.0);
+        const double t = power[n & (kSteps - 1)];
+        const double e = __builtin_amdgcn_ldexp(fma(t, p, t), n >> kStepBits);
         return some ? e : 0.0;
     }
     __device__ __forceinline__ int bin(float l) const {
         return l == most ? 0 : (int)fminf((most - l) * per, (float)(kBins - 1));
     }
     // Where the largest logit and the bins' width are finite numbers above 0 the
-    // difference needs no second look: bins from the quotient alone (-infinity:
-    // the last one), weights held to 2^-43, which rounds to none.
+    // difference needs no second look: a logit's place in bins is the quotient
+    // (-infinity: infinity), and what lies past kLightBin has no weight.
     __device__ __forceinline__ bool ordinary() const {
         return fabsf(most) < INFINITY && per < INFINITY && per > 0.0f;
     }
     __device__ __forceinline__ float place(float l) const { return (most - l) * per; }
+    // Of a logit whose place is below kLightBin: no clamp.
     __device__ __forceinline__ u64 whole_weight(float l) const {
-        const double x = fmax(((double)l - (double)most) * inverse, -30.0);
+        const double x = ((double)l - (double)most) * inverse;
         const double shift = 0x1.8p52;
-        const double s = fma(x, 0x1.71547652b82fep+6, shift);
+        const double s = fma(x, kSteps / 0.693147180559945309417232, shift);
         const int n = (int)(uint32_t)__builtin_bit_cast(u64, s);
-        const double r = fma(s - shift, -0x1.62e42fefa39efp-7, x);
-        const double p = r * fma(r, fma(r, fma(r, 1.0 / 24, 1.0 / 6), 0.5), 1.0);
-        const double t = power[n & 63];
-        // 2^40 2^(n / 64's whole part)
-        const double up = __builtin_bit_cast(double, (u64)(uint32_t)((n >> 6) + 1063) << 52);
+        const double r = fma(s - shift, -0.693147180559945309417232 / kSteps, x);
+        const double p = r * fma(r, fma(r, 1.0 / 6, 0.5), 1.0);
+        const double t = power[n & (kSteps - 1)];
+        // 2^40 2^(n / kSteps's whole part)
+        const double up =
+            __builtin_bit_cast(double, (u64)(uint32_t)((n >> kStepBits) + 1063) << 52);
         return __builtin_bit_cast(u64, fma(fma(t, p, t), up, 0x1p52)) - 0x4330000000000000ull;
     }
 };
@@ -172,14 +221,18 @@ struct Row {
     int V;
     u4_t* kept;
 
+    // Past the row's end: -infinity, which no pass takes.
     __device__ __forceinline__ u4_t piece(int c) const {
-        u4_t w = {};
+        u4_t w = {L::kLeast, L::kLeast, L::kLeast, L::kLeast};
         if (c + W <= V) {
             __builtin_memcpy(&w, ptr + c, 16);
         } else if (c < V) {
-            Bits b[W] = {};
+            Bits b[W];
 #pragma unroll
-            for (int q = 0; q < W - 1; ++q) b[q] = ptr[c + q < V ? c + q : c];
+            for (int q = 0; q < W; ++q) {
+                const Bits v = ptr[c + q < V ? c + q : c];
+                b[q] = c + q < V ? v : (Bits)L::kLeast;
+            }
             __builtin_memcpy(&w, b, 16);
         }
         return w;
@@ -192,19 +245,21 @@ struct Row {
         __builtin_memcpy(b, &w, 16);
 #pragma unroll
         for (int q = 0; q < W; ++q) {
-            if (c + q < V) f(c + q, L::get(b[q]));
+            f(c + q, L::get(b[q]));
             if (q & 1) __builtin_amdgcn_sched_barrier(0);
         }
     }
-    // f(index, logit) for this lane's elements.
+    // f(index, logit) for this lane's elements, and for -infinity behind the row's
+    // end.
     template <class Fn>
     __device__ __forceinline__ void each(Fn&& f) const {
 #pragma unroll 1
         for (int p = threadIdx.x; p * W < V; p += kT) visit(HELD ? kept[p] : piece(p * W), p * W, f);
     }
-    // The first pass: 4 pieces are on their way at once.
-    template <class Fn>
-    __device__ __forceinline__ void each_first(Fn&& f) const {
+    // The first pass, 4 pieces on their way at once: keeps the row, and returns the
+    // ends of this lane's elements.
+    __device__ __forceinline__ typename L::Ends first_pass() const {
+        typename L::Ends ends;
 #pragma unroll 1
         for (int p = threadIdx.x; p * W < V; p += 4 * kT) {
             u4_t w[4];
@@ -213,9 +268,10 @@ struct Row {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (HELD && (p + i * kT) * W < V) kept[p + i * kT] = w[i];
-                visit(w[i], (p + i * kT) * W, f);
+                ends.add(w[i]);
             }
         }
+        return ends;
     }
 };
 
@@ -675,7 +731,7 @@ __device__ __forceinline__ Scale scale_for(const Shared& s, float most, float te
     return {most, 1.0 / (double)temperature, kPerUnit / temperature, s.power};
 }
 __device__ __forceinline__ void fill_powers(Shared& s) {
-    if (threadIdx.x < 64) s.power[threadIdx.x] = exp2(threadIdx.x / 64.0);
+    if (threadIdx.x < kSteps) s.power[threadIdx.x] = exp2(threadIdx.x / (double)kSteps);
 }
 
 // This lane's part of the histogram, of counts or of sums, and of the sum that min-p
@@ -753,12 +809,9 @@ __global__ __launch_bounds__(kT) void sample_kernel(const SampleArgs a) {
         const Settings set = a.settings(m);
         __syncthreads();  // the row before is done
         // The largest logit, and whether there is a NaN.
-        float most = -INFINITY;
-        int bad = 0;
-        row.each_first([&](int, float l) __attribute__((always_inline)) {
-            most = fmaxf(most, l);
-            bad |= l != l;
-        });
+        const auto ends = row.first_pass();
+        float most = ends.most();
+        const bool bad = most != most || ends.least() != ends.least();
         if (threadIdx.x == 0) {
             s.flag = 0;
             s.listed = 0;
@@ -861,12 +914,10 @@ __global__ __launch_bounds__(kT) void piece_most_kernel(const SampleArgs a, cons
         space.listed = 0;
         space.first = 0xFFFFFFFFu;
     }
-    float most = -INFINITY;
-    bool bad = false;
-    piece.each([&](int, float l) __attribute__((always_inline)) {
-        most = fmaxf(most, l);
-        bad |= l != l;
-    });
+    typename Logits<E>::Ends ends;
+    ends.add(piece.bits);
+    float most = ends.most();
+    const bool bad = most != most || ends.least() != ends.least();
     most = over_block(most, slots, [](float a, float b) { return fmaxf(a, b); });
     if (bad) flag = 1;
     __syncthreads();
