@@ -42,6 +42,15 @@ namespace {
 
 struct F32 {};  // logits of 32 bits
 
+// Logits as whole numbers of the same order (-0 as 0), and back.
+__device__ __forceinline__ uint32_t order_of(float l) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, l + 0.0f);
+    return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float logit_in_order(uint32_t o) {
+    return __builtin_bit_cast(float, o ^ ((o >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+
 // Pieces of 16 bytes; the largest and the smallest of many pieces, as whole numbers
 // in the logits' order, two at a time in 16 bits (NaN come out beyond the
 // infinities).
@@ -70,8 +79,11 @@ struct Logits {
         __device__ static __forceinline__ float value(int v) {
             return E::get((uint16_t)(v < 0 ? v ^ 0x7FFF : v));
         }
-        __device__ __forceinline__ float most() const { return value(max(top[0], top[1])); }
-        __device__ __forceinline__ float least() const { return value(min(low[0], low[1])); }
+        // The largest as order_of() has it; a NaN's is above all.
+        __device__ __forceinline__ uint32_t order() const {
+            const float most = value(max(top[0], top[1])), least = value(min(low[0], low[1]));
+            return most != most || least != least ? 0xFFFFFFFFu : order_of(most);
+        }
     };
 };
 template <>
@@ -93,8 +105,10 @@ struct Logits<F32> {
         __device__ static __forceinline__ float value(int v) {
             return __builtin_bit_cast(float, v < 0 ? v ^ 0x7FFFFFFF : v);
         }
-        __device__ __forceinline__ float most() const { return value(top); }
-        __device__ __forceinline__ float least() const { return value(low); }
+        __device__ __forceinline__ uint32_t order() const {
+            const float most = value(top), least = value(low);
+            return most != most || least != least ? 0xFFFFFFFFu : order_of(most);
+        }
     };
 };
 
@@ -131,7 +145,14 @@ struct Shared {
     u64 wave_sum[kT / 64];
     uint32_t wave_count[kT / 64];
     float wave_min[kT / 64], wave_max[kT / 64];
-    u64 before_sum, before_count, bin_sum;
+    u64 before_sum, before_count;
+    // of the ways of one histogram: each place is written once a row
+    u64 slots[4][kT / 64], picked[2];
+    struct At {
+        u64 before, own;
+        int bin;
+    } at[3];
+    uint32_t fewest[kT / 64];
     Found found;
     uint32_t listed;
     int flag, bin;
@@ -201,13 +222,10 @@ __device__ __forceinline__ u64 whole(double w) {
 
 // Logits and indices as keys in the order of the search (ascending), and back.
 __device__ __forceinline__ u64 key_of(float l, uint32_t index) {
-    const uint32_t b = __builtin_bit_cast(uint32_t, l + 0.0f);  // -0 is 0
-    const uint32_t up = b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
-    return ((u64)~up << 32) | index;
+    return ((u64)~order_of(l) << 32) | index;
 }
 __device__ __forceinline__ float logit_of(u64 key) {
-    const uint32_t up = ~(uint32_t)(key >> 32);
-    return __builtin_bit_cast(float, up ^ ((up >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+    return logit_in_order(~(uint32_t)(key >> 32));
 }
 
 // A row's elements, 16 bytes at a time, read from memory for each pass, or (HELD)
@@ -275,17 +293,75 @@ struct Row {
     }
 };
 
+// Sums and the like over the 64 lanes of a wave, by moves between neighbours,
+// rows of 16 and their ends (row_shr 1, 2, 4, 8, then row_bcast 15 and 31): each is a
+// few cycles where an exchange through LDS is a hundred.  Lanes without a source get
+// `none`.
+template <int CTRL, int ROWS, class V>
+__device__ __forceinline__ V moved(V none, V v) {
+    if constexpr (sizeof(V) == 8) {
+        const u64 n = __builtin_bit_cast(u64, none), w = __builtin_bit_cast(u64, v);
+        const uint32_t lo = moved<CTRL, ROWS>((uint32_t)n, (uint32_t)w);
+        const uint32_t hi = moved<CTRL, ROWS>((uint32_t)(n >> 32), (uint32_t)(w >> 32));
+        return __builtin_bit_cast(V, ((u64)hi << 32) | lo);
+    } else {
+        return __builtin_bit_cast(
+            V, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none), __builtin_bit_cast(int, v),
+                                           CTRL, ROWS, 0xF, false));
+    }
+}
+// v combined with those of the lanes before.
 template <class V, class Op>
-__device__ __forceinline__ V over_block(V v, V* slots, Op op) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) v = op(v, __shfl_xor(v, o, 64));
-    __syncthreads();  // the slots' last readers are done
+__device__ __forceinline__ V wave_scan(V v, V none, Op op) {
+    v = op(v, moved<0x111, 0xF>(none, v));
+    v = op(v, moved<0x112, 0xF>(none, v));
+    v = op(v, moved<0x114, 0xF>(none, v));
+    v = op(v, moved<0x118, 0xF>(none, v));
+    v = op(v, moved<0x142, 0xA>(none, v));
+    return op(v, moved<0x143, 0xC>(none, v));
+}
+template <class V>
+__device__ __forceinline__ V from_lane(V v, int lane) {
+    if constexpr (sizeof(V) == 8) {
+        const u64 w = __builtin_bit_cast(u64, v);
+        const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)w, lane);
+        const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(w >> 32), lane);
+        return __builtin_bit_cast(V, ((u64)hi << 32) | lo);
+    } else {
+        return __builtin_bit_cast(V, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+    }
+}
+struct Plus {
+    template <class V>
+    __device__ __forceinline__ V operator()(V a, V b) const { return a + b; }
+};
+struct Larger {
+    __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+    __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return max(a, b); }
+};
+struct Smaller {
+    __device__ __forceinline__ float operator()(float a, float b) const { return fminf(a, b); }
+    __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return min(a, b); }
+};
+
+constexpr int kWaves = kT / 64;
+
+// v combined over the workgroup.  The slots are free: nothing has read them since
+// the last barrier.
+template <class V, class Op>
+__device__ __forceinline__ V over_block_once(V v, V none, V* slots, Op op) {
+    v = from_lane(wave_scan(v, none, op), 63);
     if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = v;
     __syncthreads();
     v = slots[0];
 #pragma unroll
-    for (int i = 1; i < kT / 64; ++i) v = op(v, slots[i]);
+    for (int i = 1; i < kWaves; ++i) v = op(v, slots[i]);
     return v;
+}
+template <class V, class Op>
+__device__ __forceinline__ V over_block(V v, V none, V* slots, Op op) {
+    __syncthreads();
+    return over_block_once(v, none, slots, op);
 }
 
 __device__ __forceinline__ void clear(Histogram& h) {
@@ -299,35 +375,23 @@ __device__ __forceinline__ void clear(Single& h) {
 }
 
 // The bin in which the running sum (by_count: count) first reaches `goal`, and
-// what comes before it: s.bin, s.before_sum, s.before_count, s.bin_sum.  Bins run
-// in descending order of the logits.  sum_of and count_of: a bin's.
-template <class Sum, class Count>
-__device__ __forceinline__ void find_bin(Shared& s, Sum&& sum_of, Count&& count_of, bool by_count,
-                                         u64 goal, u64 sum0, u64 count0) {
+// what comes before it: s.bin, s.before_sum, s.before_count.  Bins run in
+// descending order of the logits.
+__device__ __forceinline__ void find_bin(Shared& s, const Histogram& h, bool by_count, u64 goal,
+                                         u64 sum0, u64 count0) {
     constexpr int PER = kBins / kT;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    u64 sum[PER];
-    uint32_t count[PER];
-    u64 sums = 0;
-    uint32_t counts = 0;
+    const int wave = threadIdx.x >> 6;
+    u64 own_sum = 0;
+    uint32_t own_count = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        sums += sum[i] = sum_of(threadIdx.x * PER + i);
-        counts += count[i] = count_of(threadIdx.x * PER + i);
+        own_sum += h.sum[threadIdx.x * PER + i];
+        own_count += h.count[threadIdx.x * PER + i];
     }
-    const u64 own_sum = sums;
-    const uint32_t own_count = counts;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const u64 a = __shfl_up(sums, o, 64);
-        const uint32_t b = __shfl_up(counts, o, 64);
-        if (lane >= o) {
-            sums += a;
-            counts += b;
-        }
-    }
+    const u64 sums = wave_scan(own_sum, (u64)0, Plus{});
+    const uint32_t counts = wave_scan(own_count, 0u, Plus{});
     __syncthreads();
-    if (lane == 63) {
+    if ((threadIdx.x & 63) == 63) {
         s.wave_sum[wave] = sums;
         s.wave_count[wave] = counts;
     }
@@ -339,42 +403,28 @@ __device__ __forceinline__ void find_bin(Shared& s, Sum&& sum_of, Count&& count_
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const u64 before = by_count ? bc : bs, own = by_count ? count[i] : sum[i];
+        const u64 hs = h.sum[threadIdx.x * PER + i];
+        const uint32_t hc = h.count[threadIdx.x * PER + i];
+        const u64 before = by_count ? bc : bs, own = by_count ? hc : hs;
         if (before < goal && goal <= before + own) {
             s.bin = threadIdx.x * PER + i;
             s.before_sum = bs;
             s.before_count = bc;
-            s.bin_sum = sum[i];
         }
-        bs += sum[i];
-        bc += count[i];
+        bs += hs;
+        bc += hc;
     }
     __syncthreads();
-}
-__device__ __forceinline__ void find_bin(Shared& s, const Histogram& h, bool by_count, u64 goal,
-                                         u64 sum0, u64 count0) {
-    find_bin(s, [&](int i) { return h.sum[i]; }, [&](int i) { return h.count[i]; }, by_count, goal,
-             sum0, count0);
-}
-__device__ __forceinline__ void find_bin(Shared& s, const Single& h, bool by_count, u64 goal) {
-    if (by_count)
-        find_bin(s, [](int) { return (u64)0; }, [&](int i) { return h.count[i]; }, true, goal, 0, 0);
-    else
-        find_bin(s, [&](int i) { return h.sum[i]; }, [](int) { return 0u; }, false, goal, 0, 0);
 }
 
-// The sum of v over the lanes up to and with this one.
-__device__ __forceinline__ u64 running_sum(Shared& s, u64 v) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// The sum of v over the lanes up to and with this one.  The slots are free.
+__device__ __forceinline__ u64 running_sum(u64 v, u64* slots) {
+    const int wave = threadIdx.x >> 6;
+    v = wave_scan(v, (u64)0, Plus{});
+    if ((threadIdx.x & 63) == 63) slots[wave] = v;
+    __syncthreads();
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const u64 a = __shfl_up(v, o, 64);
-        if (lane >= o) v += a;
-    }
-    __syncthreads();
-    if (lane == 63) s.wave_sum[wave] = v;
-    __syncthreads();
-    for (int i = 0; i < wave; ++i) v += s.wave_sum[i];
+    for (int i = 0; i < kWaves - 1; ++i) v += i < wave ? slots[i] : 0;
     return v;
 }
 
@@ -391,11 +441,29 @@ __device__ __forceinline__ void gather(Shared& s, const R& row, In&& in) {
     __syncthreads();
 }
 
-// Sorts the first n (at most kList) keys of the list: a bitonic network, a key a
-// lane, between lanes of a wave by exchanges and between waves through LDS.
+// Sorts the first n (at most kList) keys of the list.  Up to 256 each key counts the
+// smaller ones (n reads that all lanes of a wave share); more take a bitonic network,
+// a key a lane, between lanes of a wave by exchanges and between waves through LDS.
 __device__ __forceinline__ void sort_list(Shared& s, uint32_t n) {
     static_assert(kList == kT, "a key a lane");
     const uint32_t t = threadIdx.x;
+    if (n <= 256) {
+        if (t >= n && t < ((n + 7) & ~7u)) s.list[t] = ~0ull;
+        __syncthreads();
+        u64 key = 0;
+        uint32_t rank = 0;
+        if (t < n) {
+            key = s.list[t];
+            for (uint32_t j = 0; j < n; j += 8) {
+#pragma unroll
+                for (uint32_t i = 0; i < 8; ++i) rank += s.list[j + i] < key ? 1 : 0;
+            }
+        }
+        __syncthreads();
+        if (t < n) s.list[rank] = key;
+        __syncthreads();
+        return;
+    }
     u64 key = t < n ? s.list[t] : ~0ull;
     for (uint32_t size = 2; size < 2 * n; size <<= 1)
         for (uint32_t half = size / 2; half > 0; half >>= 1) {
@@ -443,8 +511,8 @@ __device__ __forceinline__ void search(Shared& s, Searches& h, const R& row, con
                 top = fmaxf(top, l);
             }
         });
-        least = over_block(least, s.wave_min, [](float a, float b) { return fminf(a, b); });
-        top = over_block(top, s.wave_max, [](float a, float b) { return fmaxf(a, b); });
+        least = over_block(least, (float)INFINITY, s.wave_min, Smaller{});
+        top = over_block(top, -(float)INFINITY, s.wave_max, Larger{});
         lo = least, hi = top;
         ranged = true;
         if (lo == hi) break;
@@ -479,8 +547,8 @@ __device__ __forceinline__ void search(Shared& s, Searches& h, const R& row, con
                 top = fmaxf(top, l);
             }
         });
-        lo = over_block(least, s.wave_min, [](float a, float b) { return fminf(a, b); });
-        hi = over_block(top, s.wave_max, [](float a, float b) { return fmaxf(a, b); });
+        lo = over_block(least, (float)INFINITY, s.wave_min, Smaller{});
+        hi = over_block(top, -(float)INFINITY, s.wave_max, Larger{});
         if (lo == hi) break;
     }
     __syncthreads();
@@ -523,7 +591,8 @@ __device__ __forceinline__ void search(Shared& s, Searches& h, const R& row, con
     const u64 key = mine ? s.list[threadIdx.x] : 0;
     const float l = logit_of(key);
     const u64 w = mine ? whole(sc.weight(l)) : 0;
-    const u64 upto = before_sum + running_sum(s, w);
+    __syncthreads();
+    const u64 upto = before_sum + running_sum(w, s.wave_sum);
     const u64 reach = by_count ? before_count + threadIdx.x + 1 : upto;
     if (mine && reach >= goal && reach - (by_count ? 1 : w) < goal) {
         s.found.sum = upto;
@@ -574,10 +643,9 @@ __device__ __forceinline__ void sample_searching(Shared& s, Searches& h, const R
             if (e >= bound) kept += w;
         }
     });
-    auto add = [](auto a, auto b) { return a + b; };
-    kept = over_block(kept, s.wave_sum, add);
-    total = over_block(total, s.wave_sum, add);
-    n = over_block(n, s.wave_count, add);
+    kept = over_block(kept, (u64)0, s.wave_sum, Plus{});
+    total = over_block(total, (u64)0, s.wave_sum, Plus{});
+    n = over_block(n, 0u, s.wave_count, Plus{});
     u64 Z = total;
     // top-k, top-p, the token
 #pragma unroll 1
@@ -612,93 +680,128 @@ __device__ __forceinline__ bool by_counts(const Settings& set, int V) {
     return set.top_k > 0 && set.top_k <= kSmallK && set.top_k < V;
 }
 
-// From the histogram: of counts (`counts`: the bins up to the k-th's), or of sums.
+// From the histogram: of counts (`counts`: the bins up to the k-th's), or of sums.  kept:
+// the sum that min-p keeps, where it is on.
 __device__ __forceinline__ Wanted wanted_bins(Shared& s, const Single& h, bool counts,
-                                              const Settings& set, u64 total, u64 kept) {
-    Wanted w = {0, 0, -1, 0, 0, total, kept};
+                                              const Settings& set, u64 kept) {
+    constexpr int PER = kBins / kT;
+    const int first_bin = threadIdx.x * PER, wave = threadIdx.x >> 6;
+    u64 own[PER], sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        sum += own[i] = counts ? h.count[first_bin + i] : h.sum[first_bin + i];
+    const u64 upto = wave_scan(sum, (u64)0, Plus{});
+    if ((threadIdx.x & 63) == 63) s.slots[0][wave] = upto;
+    __syncthreads();
+    u64 before = upto - sum, total = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+        const u64 v = s.slots[0][i];
+        before += i < wave ? v : 0;
+        total += v;
+    }
+    // The bin in which the running sum first reaches `goal`, to s.at[k].
+    auto find = [&](u64 goal, int k) __attribute__((always_inline)) {
+        u64 b = before;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (b < goal && goal <= b + own[i]) s.at[k] = {b, own[i], first_bin + i};
+            b += own[i];
+        }
+    };
+    Wanted w = {0, 0, -1, 0, 0, total, set.min_p > 0.0f ? kept : total};
     if (counts) {
         // fewer with weight than k: all of them
         w.last = kLightBin - 1;
         if ((u64)set.top_k <= total) {
-            find_bin(s, h, true, (u64)set.top_k);
-            w.last = s.bin;
+            find((u64)set.top_k, 0);
+            __syncthreads();
+            w.last = s.at[0].bin;
         }
         return w;
     }
     u64 low = total, high = total;  // bounds of what top-p keeps
     if (set.top_p < 1.0f) {
-        find_bin(s, h, false, least_sum((double)set.top_p * (double)total, false, total));
-        w.end = s.bin;
-        w.before_end = s.before_sum;
-        low = s.before_sum + 1, high = s.before_sum + s.bin_sum;
+        find(least_sum((double)set.top_p * (double)total, false, total), 0);
+        __syncthreads();
+        w.end = s.at[0].bin;
+        w.before_end = s.at[0].before;
+        low = w.before_end + 1, high = w.before_end + s.at[0].own;
     }
-    low = min(low, kept), high = min(high, kept);
-    find_bin(s, h, false, least_sum((double)set.u * (double)low, true, low));
-    w.first = s.bin;
-    w.before = s.before_sum;
-    w.last = w.first;
-    if (high != low) {
-        find_bin(s, h, false, least_sum((double)set.u * (double)high, true, high));
-        w.last = s.bin;
-    }
+    low = min(low, w.kept), high = min(high, w.kept);
+    find(least_sum((double)set.u * (double)low, true, low), 1);
+    if (high != low) find(least_sum((double)set.u * (double)high, true, high), 2);
+    __syncthreads();
+    w.first = s.at[1].bin;
+    w.before = s.at[1].before;
+    w.last = max(high != low ? s.at[2].bin : w.first, 0);
     if (w.end <= w.last) w.last = max(w.last, w.end);
     return w;
 }
+
 // The token of a row whose wanted elements are the first n of the list (n at most
-// kList): s.found, with the sum kept for found.sum.
+// kList): s.found, with the sum kept for found.sum.  Up to 64 are the first wave's
+// alone.
 __device__ __forceinline__ void sample_list(Shared& s, uint32_t n, bool counts, const Wanted& want,
                                             const Scale& sc, const Settings& set) {
     sort_list(s, n);
     const uint32_t t = threadIdx.x;
-    const bool mine = t < n;
-    const u64 key = mine ? s.list[t] : 0;
-    const float l = logit_of(key);
-    const double e = mine ? sc.weight(l) : 0.0;
-    const u64 w = whole(e);
-    u64 upto = running_sum(s, w);
-    u64 Z;
-    if (counts) {
-        // the list is the beginning of the order
-        const uint32_t k = min((uint32_t)set.top_k, n);
-        if (t == k - 1) s.before_sum = upto;
-        __syncthreads();
-        Z = s.before_sum;
-        const double bound = set.min_p > 0.0f ? fmin((double)set.min_p, 1.0) : 0.0;
-        const u64 kept = over_block(t < k && e >= bound ? w : (u64)0, s.wave_sum,
-                                    [](u64 a, u64 b) { return a + b; });
+    const bool alone = n <= 64;
+    if (!alone || t < 64) {
+        const bool mine = t < n;
+        const u64 key = mine ? s.list[t] : 0;
+        const float l = logit_of(key);
+        const double e = mine ? sc.weight(l) : 0.0;
+        const u64 w = whole(e);
+        u64 upto = alone ? wave_scan(w, (u64)0, Plus{}) : running_sum(w, s.slots[1]);
+        // v of the one lane that has `here`
+        auto pick = [&](bool here, u64 v, u64* slot) __attribute__((always_inline)) {
+            if (alone) {
+                const u64 lanes = __ballot(here);
+                return lanes != 0 ? from_lane(v, __builtin_ctzll(lanes)) : 0;
+            }
+            if (here) *slot = v;
+            __syncthreads();
+            return *slot;
+        };
+        auto reaches = [&](u64 goal) __attribute__((always_inline)) {
+            return mine && upto >= goal && upto - w < goal;
+        };
+        u64 Z = want.total, kept = want.kept;
+        bool ends = true;  // whether this element may be where top-p ends
+        if (counts) {
+            // the list is the beginning of the order
+            const uint32_t k = min((uint32_t)set.top_k, n);
+            Z = kept = pick(t == k - 1, upto, &s.picked[0]);
+            if (set.min_p > 0.0f) {
+                const double bound = fmin((double)set.min_p, 1.0);
+                const u64 v = t < k && e >= bound ? w : 0;
+                kept = alone ? from_lane(wave_scan(v, (u64)0, Plus{}), 63)
+                             : over_block_once(v, (u64)0, s.slots[2], Plus{});
+            }
+        } else {
+            // The bins first .. last, then `end`: the sums before them come from the
+            // histogram.
+            const int bin = mine ? (int)sc.place(l) : 0;
+            const bool behind = bin > want.last;
+            ends = bin == want.end;
+            u64 front = 0;
+            if (want.end > want.last)
+                front = pick(mine && !behind &&
+                                 (t == n - 1 || (int)sc.place(logit_of(s.list[t + 1])) > want.last),
+                             upto, &s.picked[0]);
+            upto += behind ? want.before_end - front : want.before;
+        }
         if (set.top_p < 1.0f) {
             const u64 goal = least_sum((double)set.top_p * (double)Z, false, Z);
-            if (mine && upto >= goal && upto - w < goal) s.bin_sum = upto;
-            __syncthreads();
-            Z = min(Z, s.bin_sum);
+            Z = min(Z, pick(ends && reaches(goal), upto, &s.picked[1]));
         }
         Z = min(Z, kept);
-    } else {
-        // The bins first .. last, then `end`: the sums before them come from the
-        // histogram.
-        const bool behind = want.end > want.last;
-        const int bin = mine ? (int)sc.place(l) : 0;
-        if (t == 0) s.before_count = 0;
-        __syncthreads();
-        if (mine && bin <= want.last && (t == n - 1 || (int)sc.place(logit_of(s.list[t + 1])) > want.last))
-            s.before_count = upto;  // the sum of first .. last
-        __syncthreads();
-        upto = behind && bin > want.last ? want.before_end + (upto - s.before_count)
-                                         : want.before + upto;
-        Z = want.total;
-        if (set.top_p < 1.0f) {
-            const u64 goal = least_sum((double)set.top_p * (double)Z, false, Z);
-            if (mine && upto >= goal && upto - w < goal && bin == want.end) s.bin_sum = upto;
-            __syncthreads();
-            Z = min(Z, s.bin_sum);
+        if (reaches(least_sum((double)set.u * (double)Z, true, Z))) {
+            s.found.sum = Z;
+            s.found.index = (uint32_t)key;
+            s.found.logit = l;
         }
-        Z = min(Z, want.kept);
-    }
-    const u64 goal = least_sum((double)set.u * (double)Z, true, Z);
-    if (mine && upto >= goal && upto - w < goal) {
-        s.found.sum = Z;
-        s.found.index = (uint32_t)key;
-        s.found.logit = l;
     }
     __syncthreads();
 }
@@ -762,13 +865,6 @@ __device__ __forceinline__ void add_to_histogram(Single& h, const R& row, const 
         });
     }
 }
-// The sum over a histogram, in every lane.
-__device__ __forceinline__ u64 histogram_total(Shared& s, const Single& h, bool counts) {
-    u64 total = 0;
-    for (int i = threadIdx.x; i < kBins; i += kT) total += counts ? h.count[i] : h.sum[i];
-    return over_block(total, s.wave_sum, [](u64 x, u64 y) { return x + y; });
-}
-
 // Whether a row's settings and scale allow the ways of one histogram.
 __device__ __forceinline__ bool one_histogram(const Scale& sc, const Settings& set, int V) {
     return sc.ordinary() && (by_counts(set, V) || !(set.top_k > 0 && set.top_k < V));
@@ -810,17 +906,11 @@ __global__ __launch_bounds__(kT) void sample_kernel(const SampleArgs a) {
         __syncthreads();  // the row before is done
         // The largest logit, and whether there is a NaN.
         const auto ends = row.first_pass();
-        float most = ends.most();
-        const bool bad = most != most || ends.least() != ends.least();
-        if (threadIdx.x == 0) {
-            s.flag = 0;
-            s.listed = 0;
-        }
+        if (threadIdx.x == 0) s.listed = 0;
         clear(h.single);
-        most = over_block(most, s.wave_max, [](float a, float b) { return fmaxf(a, b); });
-        if (bad) s.flag = 1;
-        __syncthreads();
-        if (s.flag || most == -INFINITY) {
+        const float most =
+            logit_in_order(over_block_once(ends.order(), 0u, s.fewest, Larger{}));
+        if (!(most > -INFINITY)) {
             if (threadIdx.x == 0) a.put(m, -1, __builtin_nanf(""));
             continue;
         }
@@ -830,8 +920,7 @@ __global__ __launch_bounds__(kT) void sample_kernel(const SampleArgs a) {
             row.each([&](int i, float l) __attribute__((always_inline)) {
                 if (l == most) first = min(first, (uint32_t)i);
             });
-            first = over_block(first, s.wave_count,
-                               [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+            first = over_block_once(first, 0xFFFFFFFFu, s.wave_count, Smaller{});
             if (threadIdx.x == 0) a.put(m, first, 0.0f);
             continue;
         }
@@ -841,12 +930,11 @@ __global__ __launch_bounds__(kT) void sample_kernel(const SampleArgs a) {
         if (one_histogram(sc, set, a.V)) {
             u64 kept = 0;
             add_to_histogram(h.single, row, sc, set, counts, kept);
-            __syncthreads();
-            const u64 total = histogram_total(s, h.single, counts);
-            kept = set.min_p > 0.0f ? over_block(kept, s.wave_sum,
-                                                 [](u64 x, u64 y) { return x + y; })
-                                    : total;
-            const Wanted want = wanted_bins(s, h.single, counts, set, total, kept);
+            if (set.min_p > 0.0f && !counts)
+                kept = over_block_once(kept, (u64)0, s.slots[3], Plus{});
+            else
+                __syncthreads();
+            const Wanted want = wanted_bins(s, h.single, counts, set, kept);
             gather_wanted(s, row, sc, want);
             const uint32_t n = s.listed;
             if (n <= kList) {
@@ -875,7 +963,7 @@ struct Space {
 };
 struct Spaces {
     Space* rows;
-    float* most;  // of each piece: [M][pieces], NaN for a piece that has one
+    uint32_t* most;  // of each piece (order_of): [M][pieces], the largest for a NaN
     int pieces;
 };
 
@@ -901,13 +989,11 @@ struct Piece {
 // The largest logit of each piece; the spaces cleared.
 template <class E>
 __global__ __launch_bounds__(kT) void piece_most_kernel(const SampleArgs a, const Spaces ws) {
-    __shared__ float slots[kT / 64];
-    __shared__ int flag;
+    __shared__ uint32_t slots[kT / 64];
     const int p = blockIdx.x;
     const int64_t m = blockIdx.y;
     const Piece<E> piece(a, m, p);
     Space& space = ws.rows[m];
-    if (threadIdx.x == 0) flag = 0;
     for (int i = p * kT + threadIdx.x; i < kBins; i += ws.pieces * kT) space.hist.sum[i] = 0;
     if (p == 0 && threadIdx.x == 0) {
         space.kept = 0;
@@ -916,28 +1002,15 @@ __global__ __launch_bounds__(kT) void piece_most_kernel(const SampleArgs a, cons
     }
     typename Logits<E>::Ends ends;
     ends.add(piece.bits);
-    float most = ends.most();
-    const bool bad = most != most || ends.least() != ends.least();
-    most = over_block(most, slots, [](float a, float b) { return fmaxf(a, b); });
-    if (bad) flag = 1;
-    __syncthreads();
-    if (threadIdx.x == 0) ws.most[m * ws.pieces + p] = flag ? __builtin_nanf("") : most;
+    const uint32_t most = over_block_once(ends.order(), 0u, slots, Larger{});
+    if (threadIdx.x == 0) ws.most[m * ws.pieces + p] = most;
 }
 
 // The largest logit of a row, NaN where it has one.
-__device__ __forceinline__ float most_of_row(float* slots, const Spaces& ws, int64_t m) {
-    float most = -INFINITY;
-    bool bad = false;
-    for (int i = threadIdx.x; i < ws.pieces; i += kT) {
-        const float v = ws.most[m * ws.pieces + i];
-        most = fmaxf(most, v);
-        bad |= v != v;
-    }
-    // a NaN as +infinity's successor in the order of the bits
-    uint32_t key = bad ? 0xFFFFFFFFu : (uint32_t)(~(key_of(most, 0) >> 32));
-    key = over_block(key, reinterpret_cast<uint32_t*>(slots),
-                     [](uint32_t a, uint32_t b) { return max(a, b); });
-    return key == 0xFFFFFFFFu ? __builtin_nanf("") : logit_of((u64)~key << 32);
+__device__ __forceinline__ float most_of_row(uint32_t* slots, const Spaces& ws, int64_t m) {
+    uint32_t most = 0;
+    for (int i = threadIdx.x; i < ws.pieces; i += kT) most = max(most, ws.most[m * ws.pieces + i]);
+    return logit_in_order(over_block_once(most, 0u, slots, Larger{}));
 }
 
 template <class E>
@@ -950,7 +1023,7 @@ __global__ __launch_bounds__(kT) void piece_histogram_kernel(const SampleArgs a,
     const Settings set = a.settings(m);
     fill_powers(s);
     clear(h);
-    const float most = most_of_row(s.wave_max, ws, m);
+    const float most = most_of_row(s.fewest, ws, m);
     if (blockIdx.x == 0 && threadIdx.x == 0) space.most = most;
     if (!(most > -INFINITY)) return;
     if (!(set.temperature > 0.0f)) {
@@ -967,7 +1040,7 @@ __global__ __launch_bounds__(kT) void piece_histogram_kernel(const SampleArgs a,
     u64 kept = 0;
     add_to_histogram(h, piece, sc, set, counts, kept);
     if (set.min_p > 0.0f && !counts) {
-        kept = over_block(kept, s.wave_sum, [](u64 x, u64 y) { return x + y; });
+        kept = over_block_once(kept, (u64)0, s.slots[3], Plus{});
         if (threadIdx.x == 0 && kept != 0) atomicAdd(&space.kept, kept);
     }
     __syncthreads();
@@ -996,9 +1069,7 @@ __global__ __launch_bounds__(kT) void piece_gather_kernel(const SampleArgs a, co
     for (int i = threadIdx.x; i < kBins; i += kT) h.sum[i] = space.hist.sum[i];
     if (threadIdx.x == 0) s.listed = 0;
     __syncthreads();
-    const u64 total = histogram_total(s, h, counts);
-    const u64 kept = set.min_p > 0.0f ? space.kept : total;
-    const Wanted want = wanted_bins(s, h, counts, set, total, kept);
+    const Wanted want = wanted_bins(s, h, counts, set, space.kept);
     if (blockIdx.x == 0 && threadIdx.x == 0) space.want = want;
     gather_wanted(s, piece, sc, want);
     const uint32_t n = s.listed;
@@ -1066,7 +1137,7 @@ hipError_t launch(const SampleCall& c, Arena& ar, hipStream_t stream) {
     if (cut) {
         ws.pieces = (int)((c.V + kT * Logits<E>::kWidth - 1) / (kT * Logits<E>::kWidth));
         ws.rows = static_cast<Space*>(ar.take(c.M * (int64_t)sizeof(Space)));
-        ws.most = static_cast<float*>(ar.take(c.M * ws.pieces * 4));
+        ws.most = static_cast<uint32_t*>(ar.take(c.M * ws.pieces * 4));
     }
     if (ar.dry()) return hipSuccess;
     const unsigned blocks = (unsigned)(c.M < (1 << 20) ? c.M : 1 << 20);
