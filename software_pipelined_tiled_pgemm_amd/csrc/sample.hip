@@ -611,6 +611,11 @@ __device__ __forceinline__ u64 least_sum(double goal, bool beyond, u64 Z) {
     return min(beyond ? (u64)goal + 1 : (u64)ceil(goal), Z);
 }
 
+// The least weight that min-p keeps.
+__device__ __forceinline__ u64 least_weight(float min_p) {
+    return min_p > 0.0f ? (u64)ceil(fmin((double)min_p, 1.0) * kOne) : 0;
+}
+
 template <class V>
 __device__ __forceinline__ V at(const Setting<V>& s, int64_t row) {
     return s.each ? s.each[row] : s.value;
@@ -628,19 +633,18 @@ __device__ __forceinline__ void sample_searching(Shared& s, Searches& h, const R
     __syncthreads();
     clear(h.all);
     __syncthreads();
-    const double bound = set.min_p > 0.0f ? fmin((double)set.min_p, 1.0) : 0.0;
+    const u64 bound = least_weight(set.min_p);
     u64 kept = 0, total = 0;
     uint32_t n = 0;
     row.each([&](int, float l) __attribute__((always_inline)) {
-        const double e = sc.weight(l);
-        const u64 w = whole(e);
+        const u64 w = whole(sc.weight(l));
         if (w != 0) {
             const int b = sc.bin(l);
             atomicAdd(&h.all.sum[b], w);
             atomicAdd(&h.all.count[b], 1u);
             total += w;
             ++n;
-            if (e >= bound) kept += w;
+            if (w >= bound) kept += w;
         }
     });
     kept = over_block(kept, (u64)0, s.wave_sum, Plus{});
@@ -751,8 +755,7 @@ __device__ __forceinline__ void sample_list(Shared& s, uint32_t n, bool counts, 
         const bool mine = t < n;
         const u64 key = mine ? s.list[t] : 0;
         const float l = logit_of(key);
-        const double e = mine ? sc.weight(l) : 0.0;
-        const u64 w = whole(e);
+        const u64 w = mine ? whole(sc.weight(l)) : 0;
         u64 upto = alone ? wave_scan(w, (u64)0, Plus{}) : running_sum(w, s.slots[1]);
         // v of the one lane that has `here`
         auto pick = [&](bool here, u64 v, u64* slot) __attribute__((always_inline)) {
@@ -774,8 +777,7 @@ __device__ __forceinline__ void sample_list(Shared& s, uint32_t n, bool counts, 
             const uint32_t k = min((uint32_t)set.top_k, n);
             Z = kept = pick(t == k - 1, upto, &s.picked[0]);
             if (set.min_p > 0.0f) {
-                const double bound = fmin((double)set.min_p, 1.0);
-                const u64 v = t < k && e >= bound ? w : 0;
+                const u64 v = t < k && w >= least_weight(set.min_p) ? w : 0;
                 kept = alone ? from_lane(wave_scan(v, (u64)0, Plus{}), 63)
                              : over_block_once(v, (u64)0, s.slots[2], Plus{});
             }
@@ -848,14 +850,13 @@ __device__ __forceinline__ void add_to_histogram(Single& h, const R& row, const 
             if (d < (float)kLightBin) atomicAdd(&h.count[(int)d], 1u);
         });
     } else if (set.min_p > 0.0f) {
-        const double bound = fmin((double)set.min_p, 1.0);
+        const u64 bound = least_weight(set.min_p);
         row.each([&](int, float l) __attribute__((always_inline)) {
             const float d = sc.place(l);
             if (d < (float)kLightBin) {
-                const double e = sc.weight(l);
-                const u64 w = whole(e);
+                const u64 w = sc.whole_weight(l);
                 atomicAdd(&h.sum[(int)d], w);
-                if (e >= bound) kept += w;
+                kept += w >= bound ? w : 0;
             }
         });
     } else {
@@ -950,16 +951,15 @@ __global__ __launch_bounds__(kT) void sample_kernel(const SampleArgs a) {
     }
 }
 
-// Few long rows: pieces of kT * 16 bytes, a workgroup each, in four launches, with a
+// Few long rows: pieces of kT * 16 bytes, a workgroup each, in three launches, with a
 // row's histogram and list in the workspace.
 struct Space {
     Single hist;
     u64 list[kList];
-    Wanted want;
     u64 kept;
-    uint32_t listed, first;  // first: of the largest logits (greedy)
+    uint32_t listed, done;  // entries of the list; workgroups that have added theirs
+    uint32_t first;         // of the largest logits (greedy)
     float most;
-    int unused;
 };
 struct Spaces {
     Space* rows;
@@ -998,6 +998,7 @@ __global__ __launch_bounds__(kT) void piece_most_kernel(const SampleArgs a, cons
     if (p == 0 && threadIdx.x == 0) {
         space.kept = 0;
         space.listed = 0;
+        space.done = 0;
         space.first = 0xFFFFFFFFu;
     }
     typename Logits<E>::Ends ends;
@@ -1053,44 +1054,22 @@ __global__ __launch_bounds__(kT) void piece_histogram_kernel(const SampleArgs a,
     }
 }
 
+// Gathers the wanted elements; the workgroup of a row that is done last takes the
+// token.
 template <class E>
 __global__ __launch_bounds__(kT) void piece_gather_kernel(const SampleArgs a, const Spaces ws) {
     __shared__ Shared s;
-    __shared__ Single h;
+    __shared__ union {
+        Single single;
+        Searches searches;
+    } h;
     const int64_t m = blockIdx.y;
     const Piece<E> piece(a, m, blockIdx.x);
     Space& space = ws.rows[m];
     const Settings set = a.settings(m);
     const float most = space.most;
-    if (!(most > -INFINITY) || !(set.temperature > 0.0f)) return;
-    const Scale sc = scale_for(s, most, set.temperature);
-    if (!one_histogram(sc, set, a.V)) return;
-    const bool counts = by_counts(set, a.V);
-    for (int i = threadIdx.x; i < kBins; i += kT) h.sum[i] = space.hist.sum[i];
-    if (threadIdx.x == 0) s.listed = 0;
-    __syncthreads();
-    const Wanted want = wanted_bins(s, h, counts, set, space.kept);
-    if (blockIdx.x == 0 && threadIdx.x == 0) space.want = want;
-    gather_wanted(s, piece, sc, want);
-    const uint32_t n = s.listed;
-    if (n == 0) return;
-    if (threadIdx.x == 0) s.flag = (int)atomicAdd(&space.listed, n);
-    __syncthreads();
-    const uint32_t to = (uint32_t)s.flag;
-    for (uint32_t i = threadIdx.x; i < min(n, (uint32_t)kList); i += kT)
-        if (to + i < kList) space.list[to + i] = s.list[i];
-}
-
-template <class E>
-__global__ __launch_bounds__(kT) void finish_row_kernel(const SampleArgs a, const Spaces ws) {
-    __shared__ Shared s;
-    __shared__ Searches h;
-    const int64_t m = blockIdx.x;
-    const Space& space = ws.rows[m];
-    const Settings set = a.settings(m);
-    const float most = space.most;
     if (!(most > -INFINITY) || !(set.temperature > 0.0f)) {
-        if (threadIdx.x == 0) {
+        if (threadIdx.x == 0 && blockIdx.x == 0) {
             if (most > -INFINITY)
                 a.put(m, space.first, 0.0f);
             else
@@ -1100,16 +1079,48 @@ __global__ __launch_bounds__(kT) void finish_row_kernel(const SampleArgs a, cons
     }
     fill_powers(s);
     const Scale sc = scale_for(s, most, set.temperature);
-    const uint32_t n = space.listed;
-    if (one_histogram(sc, set, a.V) && n <= kList) {
-        if (threadIdx.x < n) s.list[threadIdx.x] = space.list[threadIdx.x];
-        const Wanted want = space.want;
+    const bool counts = by_counts(set, a.V);
+    bool searching = !one_histogram(sc, set, a.V);
+    Wanted want = {};
+    uint32_t n = 0;
+    if (!searching) {
+        for (int i = threadIdx.x; i < kBins; i += kT) h.single.sum[i] = space.hist.sum[i];
+        if (threadIdx.x == 0) s.listed = 0;
         __syncthreads();
-        sample_list(s, n, by_counts(set, a.V), want, sc, set);
+        want = wanted_bins(s, h.single, counts, set, space.kept);
+        gather_wanted(s, piece, sc, want);
+        n = s.listed;
+        if (n > 0) {
+            if (threadIdx.x == 0) s.flag = (int)atomicAdd(&space.listed, n);
+            __syncthreads();
+            const uint32_t to = (uint32_t)s.flag;
+            if (threadIdx.x < n && threadIdx.x + to < kList)
+                __hip_atomic_store(&space.list[to + threadIdx.x], s.list[threadIdx.x],
+                                   __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+    }
+    // This workgroup's entries are written before it counts itself, and the last
+    // one's reads come after its count.  (One lane's fence for all: a fence of every
+    // wave took 10 us.)
+    __syncthreads();
+    if (threadIdx.x == 0)
+        s.bin = __hip_atomic_fetch_add(&space.done, 1u, __ATOMIC_ACQ_REL,
+                                       __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)ws.pieces - 1;
+    __syncthreads();
+    if (!s.bin) return;
+    if (!searching) {
+        n = __hip_atomic_load(&space.listed, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        searching = n > kList;
+    }
+    if (searching) {
+        const Row<E, false> row = {piece.row.ptr, a.V, nullptr};
+        sample_searching(s, h.searches, row, sc, set);
     } else {
-        const Row<E, false> row = {
-            static_cast<const typename Logits<E>::Bits*>(a.logits) + m * a.ld, a.V, nullptr};
-        sample_searching(s, h, row, sc, set);
+        if (threadIdx.x < n)
+            s.list[threadIdx.x] = __hip_atomic_load(&space.list[threadIdx.x], __ATOMIC_RELAXED,
+                                                    __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        sample_list(s, n, counts, want, sc, set);
     }
     if (threadIdx.x == 0) a.put_found(m, s.found, sc);
 }
@@ -1126,7 +1137,6 @@ hipError_t launch_pieces(const SampleArgs& a, const Spaces& ws, hipStream_t stre
     hipLaunchKernelGGL(piece_most_kernel<E>, grid, dim3(kT), 0, stream, a, ws);
     hipLaunchKernelGGL(piece_histogram_kernel<E>, grid, dim3(kT), 0, stream, a, ws);
     hipLaunchKernelGGL(piece_gather_kernel<E>, grid, dim3(kT), 0, stream, a, ws);
-    hipLaunchKernelGGL(finish_row_kernel<E>, dim3((unsigned)a.M), dim3(kT), 0, stream, a, ws);
     return hipGetLastError();
 }
 
