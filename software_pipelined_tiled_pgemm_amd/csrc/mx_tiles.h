@@ -77,12 +77,12 @@ struct Copy {
         const int c = (lane & 3) ^ dm::aswz16(lane >> 2);
 #pragma unroll
         for (int t = 0; t < PER; ++t) off[t] = (uint32_t)((r + 16 * t) * (int)ld + c * 16);
-        rsrc = rsrc_words(base, (int64_t)(min(rows, ROWS) - 1) * ld + row_bytes);
+        rsrc = lp::scalar4(rsrc_words(base, (int64_t)(min(rows, ROWS) - 1) * ld + row_bytes));
     }
     // Copy c of a step: its elements start at byte k of a row.
     __device__ __forceinline__ void go(int c, uint32_t k, uint32_t stage, int wave) const {
         const int t = c / PIECES, p = c % PIECES;
-        dma16s(lp::scalar4(rsrc), off[t], k + p * 64,
+        dma16s(rsrc, off[t], k + p * 64,
                stage + p * (ROWS * 64) + (wave * PER + t) * 1024);
     }
     __device__ static __forceinline__ int lane_offset(int row0, int lane) {
@@ -177,14 +177,14 @@ void product_kernel(const Args g, const Epi epi) {
         const uint8_t* const base_s = of_x ? g.xs + (int64_t)(m0 + row_o) * g.ldxs
                                            : g.ws + (int64_t)(n0 + row_o) * g.ldws;
         // no rows inside: a descriptor of size 0
-        const u32x4 rsrc_s =
-            rsrc_words(base_s, has_s && rows_s > 0 ? (int64_t)(min(rows_s, 64) - 1) * ld_s + bytes_s : 0);
+        const u32x4 rsrc_s = lp::scalar4(rsrc_words(
+            base_s, has_s && rows_s > 0 ? (int64_t)(min(rows_s, 64) - 1) * ld_s + bytes_s : 0));
         const uint32_t off_s = (uint32_t)(lane * (int)ld_s);
         const int groups = (g.steps + 3) / 4, group0 = first / 4;
         // Scales of group u; past the last group the last one's again.
         auto copy_scales = [&](int u) __attribute__((always_inline)) {
             if (has_s)
-                dma16s(lp::scalar4(rsrc_s), off_s, (uint32_t)(min(group0 + u, groups - 1) * 16),
+                dma16s(rsrc_s, off_s, (uint32_t)(min(group0 + u, groups - 1) * 16),
                        ring + TL::RING + row_s * 16);
         };
         auto turn_scales = [&]() __attribute__((always_inline)) {
@@ -239,6 +239,7 @@ void product_kernel(const Args g, const Epi epi) {
         auto step = [&](int t, auto quarter) __attribute__((always_inline)) {
             constexpr int Q = decltype(quarter)::value;  // t % 4
             constexpr int B = Q & 1;                     // the buffer of w's fragments
+            if constexpr (S == 4) slot = Q;  // the loop over t starts at slot 0
             const int next = slot + 1 == S ? 0 : slot + 1;
             const char* const cur = smem + slot * TL::STAGE;
             const char* const nxt = smem + next * TL::STAGE;
