@@ -26,11 +26,18 @@ struct MxArgs {
     const uint8_t *x, *xs, *w, *ws;
     int64_t ldx, ldxs, ldw, ldws;
     int M, N, steps;  // steps of 128 columns
+    // where not NULL, x in 16 bits, `cols` columns, which the kernel quantises
+    const uint16_t* x16;
+    int64_t ldx16;
+    int cols;
     int tiles_m, tiles_n;
     int chunk;    // split: steps per split, a multiple of 4
     float* part;  // split: partials [split][M][part_ld]
     int part_ld;
 };
+
+// Values of x (padded) that the kernel for few rows quantises itself.
+constexpr int64_t kMxFewValues = 16384;
 
 // How a product is cut: the kernel for few rows, or tiles (256 or 128 rows) with the
 // contraction in `splits` parts of `chunk` steps.

@@ -10,11 +10,48 @@ namespace pgemm {
 namespace layer {
 namespace {
 
+// Estimated microseconds of tiles, with constants measured on MI355X: a step of 128
+// columns takes `step` in the 256 x 256 tiles (256 x 128 for 8-bit elements on both
+// sides), `pair` in two 128 x 128 tiles on a CU and `alone` in a single one; a round of
+// workgroups adds its first copies and its epilogue, and a split a second launch and
+// the partials' traffic.
+struct Rates {
+    int columns;
+    double step, pair, alone;
+};
+double cut_time(const Rates& q, int64_t M, int64_t N, int steps, int cus, bool big, int splits) {
+    const int64_t bm = big ? 256 : 128, bn = big ? q.columns : 128;
+    const int64_t wgs = ((M + bm - 1) / bm) * ((N + bn - 1) / bn) * splits;
+    const int64_t slots = big ? cus : 2 * cus;
+    const double step = big ? q.step : wgs <= cus ? q.alone : q.pair;
+    const double rounds = (double)((wgs + slots - 1) / slots);
+    double t = rounds * ((double)((steps + splits - 1) / splits) * step + (big ? 8.0 : 3.0));
+    if (splits > 1) t += 8.0 + (double)splits * M * N * 8.0 / 4.0e6;
+    return t;
+}
+
 MxCut choose_mx_cut(int xformat, int wformat, int64_t M, int64_t N, int steps, int cus) {
     if (M <= 64) return {true, false, 1, steps};
-    const int64_t bn = xformat == PMX_E4M3 && wformat == PMX_E4M3 ? 128 : 256;
-    const int64_t big = ((M + 255) / 256) * ((N + bn - 1) / bn);
-    return {false, big >= cus, 1, steps};
+    const int eights = (xformat == PMX_E4M3) + (wformat == PMX_E4M3);
+    const Rates q = eights == 0   ? Rates{256, 0.85, 0.75, 0.33}
+                    : eights == 1 ? Rates{256, 1.35, 0.97, 0.45}
+                                  : Rates{128, 0.95, 1.05, 0.70};
+    MxCut best = {false, false, 1, steps};
+    double best_t = 1e300;
+    for (int s : {1, 2, 3, 4, 6, 8}) {
+        // at least 8 steps a split, whole groups of 4
+        const int chunk = s == 1 ? steps : ((steps + s - 1) / s + 3) / 4 * 4;
+        if (s > 1 && chunk < 8) break;
+        const int parts = s == 1 ? 1 : (steps + chunk - 1) / chunk;
+        for (bool big : {false, true}) {
+            const double t = cut_time(q, M, N, steps, cus, big, parts);
+            if (t < best_t) {
+                best_t = t;
+                best = {false, big, parts, parts > 1 ? chunk : steps};
+            }
+        }
+    }
+    return best;
 }
 
 }  // namespace
@@ -22,7 +59,17 @@ MxCut choose_mx_cut(int xformat, int wformat, int64_t M, int64_t N, int steps, i
 hipError_t mx_linear(const MxLinearCall& c, Arena& ar, hipStream_t stream) {
     if (c.M == 0 || c.N == 0) return hipSuccess;
     MxRows x = c.x;
-    if (c.x16) {
+    MxArgs a = {};
+    a.M = (int)c.M, a.N = (int)c.N, a.steps = (int)(mx_padded(c.K) / kMxGroup);
+    const MxCut cut = choose_mx_cut(x.format, c.w.format, c.M, c.N, a.steps, compute_units());
+    a.chunk = cut.chunk;
+    if (c.x16 && cut.few && c.M <= 4 && c.M * mx_padded(c.K) <= kMxFewValues) {
+        // quantised by the kernel: 1 x 4096 x 8192 16.9 -> 12.8 us a call, since a launch
+        // of its own costs more than every workgroup's doing it
+        a.x16 = static_cast<const uint16_t*>(c.x16);
+        a.ldx16 = c.ldx16;
+        a.cols = (int)c.K;
+    } else if (c.x16) {
         x.ld = mx_row_bytes(x.format, c.K);
         x.lds = round_up(mx_scale_bytes(c.K), 16);
         x.codes = static_cast<uint8_t*>(ar.take(c.M * x.ld));
@@ -32,12 +79,8 @@ hipError_t mx_linear(const MxLinearCall& c, Arena& ar, hipStream_t stream) {
             if (rc != hipSuccess) return rc;
         }
     }
-    MxArgs a = {};
     a.x = x.codes, a.xs = x.scales, a.w = c.w.codes, a.ws = c.w.scales;
     a.ldx = x.ld, a.ldxs = x.lds, a.ldw = c.w.ld, a.ldws = c.w.lds;
-    a.M = (int)c.M, a.N = (int)c.N, a.steps = (int)(mx_padded(c.K) / kMxGroup);
-    const MxCut cut = choose_mx_cut(x.format, c.w.format, c.M, c.N, a.steps, compute_units());
-    a.chunk = cut.chunk;
     if (cut.splits > 1) {
         a.part_ld = (int)round_up(a.N, 8);
         a.part = static_cast<float*>(ar.take((int64_t)cut.splits * a.M * a.part_ld * 4));

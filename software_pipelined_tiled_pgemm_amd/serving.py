@@ -21,6 +21,22 @@ def _torch():
     return _l._torch or _l._base()
 
 
+def _rows(t, name, like, M, D):
+    """_mat for a matrix like the call's first one, which most are: contiguous, of
+    its type, shape and device."""
+    if (isinstance(t, _l._TENSOR) and t.dtype is like.dtype and t.shape == like.shape
+            and t.is_contiguous() and t.get_device() == like.get_device()):
+        return D or 1
+    return _mat(t, name, like, M, D)
+
+
+def _empty_like(x, M, D, stream):
+    """A new matrix of x's type and shape."""
+    if stream is None and x.is_contiguous():
+        return _l._torch.empty_like(x)
+    return _new((M, D), x.dtype, x.device, stream)
+
+
 def _format(f):
     c = FORMATS.get(f) if isinstance(f, str) else None
     if c is None:
@@ -33,11 +49,11 @@ class MxMatrix:
     uint8 tensors laid out as include/pgemm.h says (codes of "e4m3" may be a
     float8_e4m3fn tensor, scales a float8_e8m0fnu one), for `cols` columns in the
     format "e2m1" or "e4m3".  shape is (rows, cols)."""
-    __slots__ = ("codes", "scales", "cols", "format", "_code")
+    __slots__ = ("cols", "format", "_code", "_codes", "_scales", "_rows", "_pitch", "_whole")
 
     def __init__(self, codes, scales, cols, format):
         self._code = _format(format)
-        self.codes, self.scales, self.cols, self.format = codes, scales, int(cols), format
+        self.cols, self.format = int(cols), format
         for t, name in ((codes, "codes"), (scales, "scales")):
             if not isinstance(t, _torch().Tensor):
                 raise TypeError("%s must be a torch.Tensor" % name)
@@ -52,17 +68,64 @@ class MxMatrix:
                 scales.shape[1] < (groups + 3) // 4 * 16:
             raise ValueError("codes %s and scales %s are too short for %d columns"
                              % (tuple(codes.shape), tuple(scales.shape), self.cols))
+        self._codes, self._scales, self._rows, self._whole = codes, scales, codes.shape[0], None
+
+    @classmethod
+    def _new(cls, rows, cols, code, like, stream):
+        """Codes and scales in one allocation (a small matrix's costs more than its
+        kernel); the tensors are made when they are asked for."""
+        pitch = _pitches.get((code, cols))
+        if pitch is None:
+            L = lib()
+            pitch = (L.pmx_codes_pitch(code, cols), L.pmx_scales_pitch(cols))
+            if min(pitch) < 0:
+                raise ValueError("%d columns are too many for a microscaled matrix" % cols)
+            if len(_pitches) >= 4096:
+                _pitches.clear()
+            _pitches[code, cols] = pitch
+        m = cls.__new__(cls)
+        m.cols, m.format, m._code, m._rows, m._pitch = cols, _NAMES[code], code, rows, pitch
+        # (codes' rows are multiples of 64 bytes: the scales are aligned too)
+        m._whole = _new(rows * (pitch[0] + pitch[1]), _torch().uint8, like.device, stream)
+        m._codes = m._scales = None
+        return m
+
+    def _split(self):
+        n, (pc, ps) = self._rows, self._pitch
+        self._codes = self._whole[:n * pc].view(n, pc)
+        self._scales = self._whole[n * pc:].view(n, ps)
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            self._split()
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            self._split()
+        return self._scales
+
+    @property
+    def _any(self):
+        """A tensor of the matrix's, for its device."""
+        return self._codes if self._whole is None else self._whole
 
     @property
     def shape(self):
-        return (self.codes.shape[0], self.cols)
+        return (self._rows, self.cols)
 
     @property
     def device(self):
-        return self.codes.device
+        return self._any.device
 
     def __repr__(self):
         return "MxMatrix(%s, %s, %s)" % (self.shape, self.format, self.device)
+
+
+_NAMES = ("e2m1", "e4m3")
+_pitches = {}
 
 
 def _pitched(t, name, like):
@@ -80,28 +143,25 @@ def _pitched(t, name, like):
 
 
 def _mx(m, name, like, rows=None, cols=None, format=None):
-    """(codes' pitch, scales' pitch) of a microscaled argument."""
+    """(address and pitch of the codes, and of the scales) of a microscaled
+    argument."""
     if not isinstance(m, MxMatrix):
         raise TypeError("%s must be an MxMatrix" % name)
-    if (rows is not None and m.shape[0] != rows) or (cols is not None and m.cols != cols):
+    if (rows is not None and m._rows != rows) or (cols is not None and m.cols != cols):
         raise ValueError("%s must have shape (%s, %s), got %s"
                          % (name, "any" if rows is None else rows, "any" if cols is None else cols,
                             m.shape))
     if format is not None and m._code != format:
         raise ValueError("%s is %s" % (name, m.format))
-    return _pitched(m.codes, name + ".codes", like), _pitched(m.scales, name + ".scales", like)
-
-
-def _new_mx(rows, cols, code, like, stream):
-    torch, L = _torch(), lib()
-    pc, ps = L.pmx_codes_pitch(code, cols), L.pmx_scales_pitch(cols)
-    if pc < 0 or ps < 0:
-        raise ValueError("%d columns are too many for a microscaled matrix" % cols)
-    m = MxMatrix.__new__(MxMatrix)
-    m.codes = _new((rows, pc), torch.uint8, like.device, stream)
-    m.scales = _new((rows, ps), torch.uint8, like.device, stream)
-    m.cols, m._code, m.format = cols, code, "e4m3" if code else "e2m1"
-    return m
+    whole = m._whole
+    if whole is not None:
+        if whole.get_device() != like.get_device():
+            raise ValueError("%s must be on the other tensors' device" % name)
+        p, (pc, ps) = whole.data_ptr(), m._pitch
+        return p, pc, p + m._rows * pc, ps
+    c, s = m._codes, m._scales
+    return (c.data_ptr(), _pitched(c, name + ".codes", like), s.data_ptr(),
+            _pitched(s, name + ".scales", like))
 
 
 def prmsnorm(x, weight=None, residual=None, eps=1e-6, h=None, format=None, out=None, stream=None):
@@ -115,23 +175,25 @@ def prmsnorm(x, weight=None, residual=None, eps=1e-6, h=None, format=None, out=N
     dt = _dtype(x, "x")
     ldx = _mat(x, "x", x)
     M, D = x.shape
-    ldr = _mat(residual, "residual", x, M, D) if residual is not None else 0
+    ldr = _rows(residual, "residual", x, M, D) if residual is not None else 0
     if weight is not None:
         _vec(weight, "weight", x, D)
-    ldh = _mat(h, "h", x, M, D) if h is not None else 0
+    ldh = _rows(h, "h", x, M, D) if h is not None else 0
     eps = float(eps)
     if not 0.0 <= eps < float("inf"):
         raise ValueError("eps must be finite and at least 0, got %r" % eps)
     if format is None:
         code, scales, lds = -1, None, 0
-        out, ldy = _out(out, "out", x, (M, D), stream)
+        if out is None:
+            out, ldy = _empty_like(x, M, D, stream), D or 1
+        else:
+            ldy = _rows(out, "out", x, M, D)
         y = out.data_ptr()
     else:
         code = _format(format)
         if out is None:
-            out = _new_mx(M, D, code, x, stream)
-        ldy, lds = _mx(out, "out", x, M, D, code)
-        y, scales = out.codes.data_ptr(), out.scales.data_ptr()
+            out = MxMatrix._new(M, D, code, x, stream)
+        y, ldy, scales, lds = _mx(out, "out", x, M, D, code)
     L = lib()
 
     def run(s):
@@ -150,17 +212,20 @@ def prmsnorm_bwd(dy, h, weight=None, eps=1e-6, dh=None, needs=(True, True), dx=N
     dt = _dtype(dy, "dy")
     lddy = _mat(dy, "dy", dy)
     M, D = dy.shape
-    ldh = _mat(h, "h", dy, M, D)
+    ldh = _rows(h, "h", dy, M, D)
     if weight is not None:
         _vec(weight, "weight", dy, D)
-    lddh = _mat(dh, "dh", dy, M, D) if dh is not None else 0
+    lddh = _rows(dh, "dh", dy, M, D) if dh is not None else 0
     eps = float(eps)
     if not 0.0 <= eps < float("inf"):
         raise ValueError("eps must be finite and at least 0, got %r" % eps)
     needs = (bool(needs[0]), bool(needs[1]) and weight is not None)
     lddx = 0
     if needs[0]:
-        dx, lddx = _out(dx, "dx", dy, (M, D), stream)
+        if dx is None:
+            dx, lddx = _empty_like(dy, M, D, stream), D or 1
+        else:
+            lddx = _rows(dx, "dx", dy, M, D)
     if needs[1]:
         if dweight is None:
             dweight = _new((D,), dy.dtype, dy.device, stream)
@@ -185,13 +250,12 @@ def pmx_quantize(x, format="e2m1", out=None, stream=None):
     ldx = _mat(x, "x", x)
     M, K = x.shape
     if out is None:
-        out = _new_mx(M, K, code, x, stream)
-    ldc, lds = _mx(out, "out", x, M, K, code)
+        out = MxMatrix._new(M, K, code, x, stream)
+    codes, ldc, scales, lds = _mx(out, "out", x, M, K, code)
     L = lib()
 
     def run(s):
-        return L.pmx_quantize(dt, x.data_ptr(), ldx, code, out.codes.data_ptr(), ldc,
-                              out.scales.data_ptr(), lds, M, K, s)
+        return L.pmx_quantize(dt, x.data_ptr(), ldx, code, codes, ldc, scales, lds, M, K, s)
     _call(_invoke(x, stream, run), "pmx_quantize")
     return out
 
@@ -202,28 +266,28 @@ def pmx_dequantize(m, dtype=None, out=None, stream=None):
     torch = _torch()
     if not isinstance(m, MxMatrix):
         raise TypeError("m must be an MxMatrix")
-    if not m.codes.is_cuda:
-        raise ValueError("m must be on a device (HIP), got %s" % m.codes.device)
-    ldc, lds = _mx(m, "m", m.codes)
+    like = m._any
+    if not like.is_cuda:
+        raise ValueError("m must be on a device (HIP), got %s" % like.device)
+    codes, ldc, scales, lds = _mx(m, "m", like)
     M, K = m.shape
     if out is None:
         if dtype is None:
             dtype = torch.bfloat16
         if dtype not in (torch.float16, torch.bfloat16):
             raise TypeError("dtype must be float16 or bfloat16, got %s" % dtype)
-        out = _new((M, K), dtype, m.codes.device, stream)
+        out = _new((M, K), dtype, like.device, stream)
     elif dtype is not None and out.dtype is not dtype:
         raise TypeError("out must be %s, got %s" % (dtype, out.dtype))
     dt = _dtype(out, "out")
-    if out.get_device() != m.codes.get_device():
+    if out.get_device() != like.get_device():
         raise ValueError("out is on another device than m")
     ldy = _mat(out, "out", out, M, K)
     L = lib()
 
     def run(s):
-        return L.pmx_dequantize(m._code, m.codes.data_ptr(), ldc, m.scales.data_ptr(), lds, dt,
-                                out.data_ptr(), ldy, M, K, s)
-    _call(_invoke(m.codes, stream, run), "pmx_dequantize")
+        return L.pmx_dequantize(m._code, codes, ldc, scales, lds, dt, out.data_ptr(), ldy, M, K, s)
+    _call(_invoke(like, stream, run), "pmx_dequantize")
     return out
 
 
@@ -241,13 +305,12 @@ def pmx_linear(x, w, bias=None, residual=None, act="none", format="e4m3", dtype=
     if not isinstance(w, MxMatrix):
         raise TypeError("w must be an MxMatrix")
     if isinstance(x, MxMatrix):
-        if not x.codes.is_cuda:
-            raise ValueError("x must be on a device (HIP), got %s" % x.codes.device)
-        like, xcode, quantizes = x.codes, x._code, 0
-        ldx, ldxs = _mx(x, "x", like)
+        like, xcode, quantizes = x._any, x._code, 0
+        if not like.is_cuda:
+            raise ValueError("x must be on a device (HIP), got %s" % like.device)
+        px, ldx, pxs, ldxs = _mx(x, "x", like)
         if dtype is None:
             dtype = next((t.dtype for t in (out, residual, bias) if t is not None), torch.bfloat16)
-        px, pxs = x.codes.data_ptr(), x.scales.data_ptr()
     else:
         _dtype(x, "x")
         like, xcode, quantizes = x, _format(format), 1
@@ -259,27 +322,27 @@ def pmx_linear(x, w, bias=None, residual=None, act="none", format="e4m3", dtype=
     if dtype not in (torch.float16, torch.bfloat16):
         raise TypeError("dtype must be float16 or bfloat16, got %s" % dtype)
     M, K = x.shape
-    ldw, ldws = _mx(w, "w", like, cols=K)
-    N = w.shape[0]
+    pw, ldw, pws, ldws = _mx(w, "w", like, cols=K)
+    N = w._rows
     if out is None:
-        out = _new((M, N), dtype, like.device, stream)
-    if _dtype(out, "out") != (0 if dtype is torch.float16 else 1):
-        raise TypeError("out must be %s, got %s" % (dtype, out.dtype))
-    if out.get_device() != like.get_device():
-        raise ValueError("out is on another device than the other tensors")
-    ldy = _mat(out, "out", out, M, N)
+        out, ldy = _new((M, N), dtype, like.device, stream), N or 1
+    else:
+        if _dtype(out, "out") != (0 if dtype is torch.float16 else 1):
+            raise TypeError("out must be %s, got %s" % (dtype, out.dtype))
+        if out.get_device() != like.get_device():
+            raise ValueError("out is on another device than the other tensors")
+        ldy = _mat(out, "out", out, M, N)
     if bias is not None:
         _vec(bias, "bias", out, N)
-    ldr = _mat(residual, "residual", out, M, N) if residual is not None else 0
+    ldr = _rows(residual, "residual", out, M, N) if residual is not None else 0
     dt = 0 if dtype is torch.float16 else 1
     L = lib()
     need = _need(L.pmx_linear_workspace_bytes, like, dt, xcode, quantizes, w._code, M, N, K)
     ws, nws, keep = _workspace(need, workspace, like, stream)
 
     def run(s):
-        return L.pmx_linear(dt, xcode, px, ldx, pxs, ldxs, w._code, w.codes.data_ptr(), ldw,
-                            w.scales.data_ptr(), ldws, _ptr(bias), _ptr(residual), ldr,
-                            out.data_ptr(), ldy, M, N, K, a, ws, nws, s)
+        return L.pmx_linear(dt, xcode, px, ldx, pxs, ldxs, w._code, pw, ldw, pws, ldws, _ptr(bias),
+                            _ptr(residual), ldr, out.data_ptr(), ldy, M, N, K, a, ws, nws, s)
     _call(_invoke(like, stream, run), "pmx_linear")
     return out
 

@@ -115,7 +115,7 @@ def test_quantize_outputs_apart(L):
 
 
 def linear(L, dtype=F16, xf=E4M3, x=X, ldx=128, xs=S, ldxs=16, wf=E2M1, w=W, ldw=64, ws_=Z, ldws=16,
-           b=None, r=None, ldr=0, y=Y, ldy=32, M=4, N=32, K=128, act=0, ws=WS, nws=1 << 20):
+           b=None, r=None, ldr=0, y=Y, ldy=32, M=16, N=32, K=128, act=0, ws=WS, nws=1 << 20):
     return L.pmx_linear(dtype, xf, x, ldx, xs, ldxs, wf, w, ldw, ws_, ldws, b, r, ldr, y, ldy, M, N, K,
                         act, ws, nws, None)
 
@@ -141,8 +141,10 @@ def test_mx_linear_checks(L, change, expected):
 
 
 def test_mx_linear_workspace(L):
-    need = L.pmx_linear_workspace_bytes(F16, E4M3, 1, E2M1, 4, 32, 128)
+    need = L.pmx_linear_workspace_bytes(F16, E4M3, 1, E2M1, 16, 32, 128)
     assert need > 0 and linear(L, xs=None, nws=need - 1) == EINVAL
+    # a token's few values are quantised by the kernel itself
+    assert L.pmx_linear_workspace_bytes(F16, E4M3, 1, E2M1, 1, 32, 128) == 0
     assert L.pmx_linear_workspace_bytes(F16, E4M3, 0, E2M1, -4, 32, 128) == EINVAL
     assert L.pmx_linear_workspace_bytes(F16, 5, 0, E2M1, 4, 32, 128) == EUNSUP
 

@@ -424,7 +424,8 @@ def check_mx(y, x, w, bias, residual, act, dtype, what):
 MX_SHAPES = [(1, 1, 1), (1, 16, 128), (2, 17, 129), (5, 100, 200), (16, 64, 512), (17, 33, 640), (33, 50, 2050),
              (64, 256, 1024), (65, 255, 96), (130, 130, 1153), (128, 256, 4096), (257, 384, 768),
              (300, 520, 999), (512, 512, 2560), (3, 40, 0), (1, 1000, 8192), (31, 4100, 300),
-             (700, 72, 5000), (1100, 1032, 384)]
+             (700, 72, 5000), (1100, 1032, 384), (4, 200, 4096), (3, 70, 5000), (4, 30, 4097),
+             (20, 300, 5000), (50, 40, 9000), (64, 24, 6000), (90, 500, 16384)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
