@@ -561,6 +561,7 @@ int pmx_dequantize(int format, const void* codes, int64_t ldc, const void* scale
  * The products are added by the matrix cores in fp32; with 8-bit elements on
  * either side an addend below 2^-11 of the largest of its 128 columns may lose
  * bits (2^-16 of the result for normally distributed values).
+ * PGEMM_EUNSUPPORTED also for y of 2^23 and more tiles of 128 x 128.
  */
 int pmx_linear(int dtype, int xformat, const void* x, int64_t ldx, const void* xscales,
                int64_t ldxs, int wformat, const void* w, int64_t ldw, const void* wscales,
@@ -592,7 +593,7 @@ int64_t pmx_linear_workspace_bytes(int dtype, int xformat, int quantizes, int wf
  * exactly.  PGEMM_EINVAL: V < 1, a temperature, top_p or min_p that is negative or
  * NaN, a min_p beyond 1; of the arrays' numbers a temperature that is not above 0
  * counts as 0, a NaN in top_p or min_p as off, a min_p beyond 1 as 1, a u outside
- * [0, 1) as the nearest number in it.  PGEMM_EUNSUPPORTED: V of 2^22 and more.
+ * [0, 1) as the nearest number in it (NaN: 0).  PGEMM_EUNSUPPORTED: V of 2^22 and more.
  */
 int psample(int dtype, const void* logits, int64_t ld, const float* u, float temperature,
             const float* temperatures, int32_t top_k, const int32_t* top_ks, float top_p,

@@ -242,6 +242,6 @@ const char* pgemm_status_string(int status) {
 
 int pgemm_last_hip_error(void) { return g_last_hip_error; }
 
-int pgemm_version(void) { return 300; }
+int pgemm_version(void) { return 400; }
 
 }  // extern "C"

@@ -48,6 +48,7 @@ int check_sizes(int dtype, int64_t M, int64_t D) {
     if (!known(dtype, PGEMM_ACT_NONE) || M >= kMaxRows || D >= kMaxCols) return PGEMM_EUNSUPPORTED;
     return PGEMM_OK;
 }
+constexpr int64_t kMaxTiles = (int64_t)1 << 23;
 bool valid_eps(float eps) { return eps >= 0.0f && eps < INFINITY; }
 
 int check_mx_linear(int dtype, int xformat, int wformat, int64_t M, int64_t N, int64_t K, int act) {
@@ -57,6 +58,8 @@ int check_mx_linear(int dtype, int xformat, int wformat, int64_t M, int64_t N, i
     // rows of codes have pitches below 2^22 bytes
     if (M >= kMaxRows || N >= kMaxCols || mx_padded(K) >= kMaxCols) return PGEMM_EUNSUPPORTED;
     if (K > 0 && (M > kMaxElems / K || N > kMaxElems / K)) return PGEMM_EUNSUPPORTED;
+    // a launch has fewer than 2^32 lanes: tiles of 128 x 128 by 256 lanes
+    if (((M + 127) / 128) * ((N + 127) / 128) >= kMaxTiles) return PGEMM_EUNSUPPORTED;
     return PGEMM_OK;
 }
 

@@ -128,6 +128,7 @@ def linear(L, dtype=F16, xf=E4M3, x=X, ldx=128, xs=S, ldxs=16, wf=E2M1, w=W, ldw
     (dict(ldw=72), EUNSUP), (dict(ldx=136), EUNSUP), (dict(w=W + 8), EUNSUP), (dict(ws_=Z + 4), EUNSUP),
     (dict(xs=S + 4), EUNSUP), (dict(b=H + 1), EUNSUP), (dict(y=Y + 1), EUNSUP),
     (dict(N=1 << 22, ldy=1 << 22), EUNSUP), (dict(M=1 << 31), EUNSUP), (dict(K=1 << 22), EUNSUP),
+    (dict(M=1 << 30), EUNSUP),                        # too many tiles for a launch
     (dict(y=X), EINVAL), (dict(y=S), EINVAL), (dict(y=W), EINVAL), (dict(y=Z), EINVAL),
     (dict(b=Y), EINVAL), (dict(r=Y + 2, ldr=32), EINVAL), (dict(r=R, ldr=31), EINVAL),
     # x in 16 bits, which is quantised into the workspace
