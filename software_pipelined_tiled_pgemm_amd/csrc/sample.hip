@@ -27,9 +27,9 @@
 //    logits next to each other): one search after the other, each cutting its
 //    bin into bins of its own until the list takes what is left, down to equal
 //    logits, which are taken by index.
-// A row stays in the registers of a workgroup where it fits; few long rows are cut
-// into pieces, a workgroup each, with the histogram and the list in the
-// workspace.
+// A row is kept in LDS where it fits; few long rows are cut into pieces, a workgroup
+// each, with the histogram and the list in the workspace.  Long rows of 16 bits
+// go another way, by a counter for each of the 65536 patterns.
 #include "sample.h"
 
 #include <type_traits>
@@ -113,6 +113,7 @@ struct Logits<F32> {
 };
 
 constexpr int kT = 1024;       // lanes of a row's workgroup
+constexpr int kMaxRow = 1 << 22;  // a row's logits are fewer
 constexpr int kBins = 2048;    // bins of a histogram
 constexpr int kList = 1024;    // elements that are sorted at once
 constexpr int kSmallK = 512;   // most of top-k for the way of counts alone
@@ -616,10 +617,6 @@ __device__ __forceinline__ u64 least_weight(float min_p) {
     return min_p > 0.0f ? (u64)ceil(fmin((double)min_p, 1.0) * kOne) : 0;
 }
 
-template <class V>
-__device__ __forceinline__ V at(const Setting<V>& s, int64_t row) {
-    return s.each ? s.each[row] : s.value;
-}
 
 struct Settings {
     float u, temperature, top_p, min_p;
@@ -818,8 +815,16 @@ struct SampleArgs {
     float* logprobs;
     int64_t M;
     int V;
+    // (All loads on their way at once: what has no array reads u's.)
+    template <class V>
+    __device__ __forceinline__ V of_row(const Setting<V>& s, int64_t m) const {
+        static_assert(sizeof(V) == sizeof(float), "");
+        V v;
+        __builtin_memcpy(&v, (s.each ? (const char*)s.each : (const char*)u) + 4 * m, 4);
+        return s.each ? v : s.value;
+    }
     __device__ __forceinline__ Settings settings(int64_t m) const {
-        return {u[m], at(temperature, m), at(top_p, m), at(min_p, m), at(top_k, m)};
+        return {u[m], of_row(temperature, m), of_row(top_p, m), of_row(min_p, m), of_row(top_k, m)};
     }
     __device__ __forceinline__ void put(int64_t m, int64_t token, float logprob) const {
         tokens[m] = token;
@@ -947,6 +952,358 @@ __global__ __launch_bounds__(kT) void sample_kernel(const SampleArgs a) {
             const Row<E, false> all = {row.ptr, a.V, nullptr};
             sample_searching(s, h.searches, all, sc, set);
         }
+        if (threadIdx.x == 0) a.put_found(m, s.found, sc);
+    }
+}
+
+// 16-bit logits, a workgroup per row: a counter for each of the 65536 patterns.  Then
+// only the patterns that occur are weighed, once each, a search ends at a pattern, and
+// equal logits need no list: the r-th of them by index is found in a last pass.  The
+// time hardly depends on the settings or on how the logits lie (by_patterns()).
+//
+// Patterns in descending order of their logits: d = 32767 - key, the key being the
+// pattern as a whole number of the same order, +0 and -0 the same.  A wave looks at
+// 64 of them, a group; groups[g] holds a group's sums.
+//
+// 256 x 65536 bf16: 33 us for 33.5 MB (1.0 TB/s).  About 18 us of it do not depend on
+// the length (the searches, each a chain of LDS reads and scans of one wave, barriers
+// and 143 KB of counters cleared); a piece of a lane takes 250 instructions over the
+// three passes, which keep the row in registers up to 65536.
+struct Groups {
+    u64 sum[1024];
+    uint32_t count[1024];
+};
+struct Patterns {
+    uint32_t counts[32768];  // d even in the low half
+    Groups groups;
+};
+
+// Where a search ended: the pattern, what comes before it, its weight and count.
+struct Place {
+    int d;
+    uint32_t count, before_count;
+    u64 weight, before;
+};
+
+template <class E>
+struct PatternSearch {
+    typedef Logits<E> L;
+    Shared& s;
+    Patterns& h;
+    const Scale& sc;
+    u64 upto;  // of lane i (of the first 16): the sum of the first i + 1 waves' groups
+    uint32_t upto_n;
+
+    __device__ static __forceinline__ float value(int d) {
+        const int key = 32767 - d;
+        return L::Ends::value(key < 0 ? key - 1 : key);
+    }
+    // The pattern nearest to l.
+    __device__ static __forceinline__ int pattern(float l) {
+        const int b = (int16_t)E::put(l), sign = b >> 15;
+        return 32767 - ((b ^ (sign & 0x7FFF)) - sign);
+    }
+    __device__ __forceinline__ uint32_t count(int d) const {
+        return (h.counts[d >> 1] >> (16 * (d & 1))) & 0xFFFFu;
+    }
+    __device__ __forceinline__ u64 weight(int d, uint32_t n) const {
+        if (n == 0) return 0;
+        const float l = value(d);
+        return sc.place(l) < (float)kLightBin ? sc.whole_weight(l) : 0;
+    }
+    // The sums of the groups first .. last, in turns of the waves; returns this lane's
+    // part of what min-p keeps.
+    __device__ __forceinline__ u64 weigh(int first, int last, u64 bound) {
+        u64 kept = 0;
+        const int lane = threadIdx.x & 63;
+#pragma unroll 1
+        for (int g0 = first + (threadIdx.x >> 6); g0 <= last; g0 += 4 * kWaves) {
+            uint32_t n[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                n[i] = g0 + i * kWaves <= last ? count(64 * (g0 + i * kWaves) + lane) : 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (__ballot(n[i] != 0) == 0) continue;
+                const int g = g0 + i * kWaves;
+                const u64 w = weight(64 * g + lane, n[i]), m = w * n[i];
+                kept += w >= bound ? m : 0;
+                const u64 sum = wave_scan(m, (u64)0, Plus{});
+                const uint32_t all = wave_scan(n[i], 0u, Plus{});
+                if (lane == 63) {
+                    h.groups.sum[g] = sum;
+                    h.groups.count[g] = all;
+                }
+            }
+        }
+        return kept;
+    }
+    // The running sums of each wave's groups, in their place.
+    __device__ __forceinline__ void sum_up() {
+        static_assert(kT == 1024, "a group a lane");
+        const int wave = threadIdx.x >> 6;
+        const u64 sum = wave_scan(h.groups.sum[threadIdx.x], (u64)0, Plus{});
+        const uint32_t n = wave_scan(h.groups.count[threadIdx.x], 0u, Plus{});
+        h.groups.sum[threadIdx.x] = sum;
+        h.groups.count[threadIdx.x] = n;
+        if ((threadIdx.x & 63) == 63) {
+            s.slots[0][wave] = sum;
+            s.slots[1][wave] = n;
+        }
+        __syncthreads();
+    }
+    // From here on the first wave's alone.
+    __device__ __forceinline__ void begin(u64& total, uint32_t& n) {
+        const int lane = threadIdx.x;
+        upto = wave_scan(lane < kWaves ? s.slots[0][lane] : 0, (u64)0, Plus{});
+        upto_n = wave_scan(lane < kWaves ? (uint32_t)s.slots[1][lane] : 0, 0u, Plus{});
+        total = from_lane(upto, 63);
+        n = from_lane(upto_n, 63);
+    }
+    // The first pattern at which the running sum (COUNT: count) reaches `goal`, at most
+    // the total.
+    template <bool COUNT>
+    __device__ __forceinline__ Place find(u64 goal) const {
+        const int lane = threadIdx.x;
+        // the wave, its group, the pattern
+        int at = __builtin_ctzll(__ballot(COUNT ? upto_n >= goal : upto >= goal) | 1ull << 15);
+        const int wave = at;
+        u64 before = at > 0 ? from_lane(upto, at - 1) : 0;
+        uint32_t before_n = at > 0 ? from_lane(upto_n, at - 1) : 0;
+        const u64 sum = before + h.groups.sum[64 * wave + lane];
+        const uint32_t num = before_n + h.groups.count[64 * wave + lane];
+        at = __builtin_ctzll(__ballot(COUNT ? num >= goal : sum >= goal) | 1ull << 63);
+        const int g = 64 * wave + at;
+        before = at > 0 ? from_lane(sum, at - 1) : before;
+        before_n = at > 0 ? from_lane(num, at - 1) : before_n;
+        const uint32_t n = count(64 * g + lane);
+        const u64 w = weight(64 * g + lane, n), m = w * n;
+        const u64 sum1 = before + wave_scan(m, (u64)0, Plus{});
+        const uint32_t num1 = before_n + wave_scan(n, 0u, Plus{});
+        at = __builtin_ctzll(__ballot(COUNT ? num1 >= goal : sum1 >= goal) | 1ull << 63);
+        return {64 * g + at, from_lane(n, at), from_lane(num1 - n, at), from_lane(w, at),
+                from_lane(sum1 - m, at)};
+    }
+};
+
+// A row's pieces, the workgroup's i-th 1024 in turn; up to HELD of them stay in
+// registers.  (HELD 0: read for each pass, 4 on their way at once.)
+template <class E, int HELD>
+struct Pieces {
+    typedef Row<E, false> R;
+    R row;
+    int t;
+    u4_t held[HELD > 0 ? HELD : 1];
+    __device__ __forceinline__ explicit Pieces(const R& r) : row(r), t(threadIdx.x) {
+        // What depends on the lane is not worked out ahead of the loop over rows, where
+        // it would fill the registers.
+        asm volatile("" : "+v"(t));
+        if constexpr (HELD > 0) {
+#pragma unroll
+            for (int i = 0; i < HELD; ++i) held[i] = row.piece((t + i * kT) * 8);
+        }
+    }
+    // f(piece's bits, its first index): whole waves, with pieces of -infinity behind
+    // the row's end.
+    template <class Fn>
+    __device__ __forceinline__ void each(Fn&& f) const {
+        const int first = __builtin_amdgcn_readfirstlane(t) * 8, own = (t & 63) * 8;
+        if constexpr (HELD > 0) {
+#pragma unroll
+            for (int i = 0; i < HELD; ++i) {
+                const int c = first + i * kT * 8;
+                if (c < row.V) f(held[i], c + own);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {
+#pragma unroll 1
+            for (int c = first; c < row.V; c += 4 * kT * 8) {
+                u4_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = row.piece(c + i * kT * 8 + own);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (c + i * kT * 8 < row.V) f(w[i], c + i * kT * 8 + own);
+            }
+        }
+    }
+};
+
+template <class E, int HELD>
+__global__ __launch_bounds__(kT) void sample_patterns_kernel(const SampleArgs a) {
+    __shared__ Shared s;
+    __shared__ __attribute__((aligned(16))) union {
+        Patterns patterns;
+        Searches searches;
+        uint32_t matches[8192];  // of each wave's pieces
+    } h;
+    static_assert(sizeof(h.matches) / 4 * 64 * 8 >= (size_t)kMaxRow, "a place for each");
+    typedef Row<E, false> R;
+    typedef PatternSearch<E> P;
+    for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
+        const R row = {static_cast<const uint16_t*>(a.logits) + m * a.ld, a.V, nullptr};
+        const Pieces<E, HELD> pieces(row);
+        const int wave = pieces.t >> 6, lane = pieces.t & 63;
+        const Settings set = a.settings(m);
+        __syncthreads();  // the row before is done
+        if (m == blockIdx.x) fill_powers(s);
+        for (int i = threadIdx.x; i < (int)(sizeof(Patterns) / 16); i += kT)
+            reinterpret_cast<u4_t*>(&h.patterns)[i] = u4_t{};
+        typename Logits<E>::Ends ends;
+        pieces.each([&](u4_t w, int) __attribute__((always_inline)) { ends.add(w); });
+        const float most = logit_in_order(over_block_once(ends.order(), 0u, s.fewest, Larger{}));
+        if (!(most > -INFINITY)) {
+            if (threadIdx.x == 0) a.put(m, -1, __builtin_nanf(""));
+            continue;
+        }
+        // The elements whose logit is l, a bit for each.
+        auto matches = [](u4_t w, float l) __attribute__((always_inline)) {
+            const uint32_t pair = E::put(l) * 0x10001u, mask = l == 0.0f ? 0x7FFF7FFFu : 0xFFFFFFFFu;
+            uint32_t found = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t x = (w[q] ^ pair) & mask;
+                found |= (x & 0xFFFFu) == 0 ? 1u << (2 * q) : 0;
+                found |= x < 0x10000u ? 2u << (2 * q) : 0;
+            }
+            return found;
+        };
+        if (!(set.temperature > 0.0f)) {
+            // Greedy: the first of the largest.
+            uint32_t first = 0xFFFFFFFFu;
+            pieces.each([&](u4_t w, int c) __attribute__((always_inline)) {
+                const uint32_t f = matches(w, most);
+                if (f) first = min(first, (uint32_t)(c + __builtin_ctz(f)));
+            });
+            first = over_block_once(first, 0xFFFFFFFFu, s.wave_count, Smaller{});
+            if (threadIdx.x == 0) a.put(m, first, 0.0f);
+            continue;
+        }
+        const Scale sc = scale_for(s, most, set.temperature);
+        bool counted = false;
+        // The last pattern that may have weight; -infinity has none.
+        const int last = min(P::pattern(most - (float)kLightBin / sc.per) + 2, P::pattern(-INFINITY) - 1);
+        if (sc.ordinary()) {
+            uint32_t all = 0;
+            pieces.each([&](u4_t w, int) __attribute__((always_inline)) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t word = w[q];
+                    const s2_t b = __builtin_bit_cast(s2_t, word);
+                    const s2_t sign = b >> 15;
+                    const s2_t d = (s2_t)0x7FFF - ((b ^ (sign & (s2_t)0x7FFF)) - sign);
+                    const uint32_t two = __builtin_bit_cast(uint32_t, d);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t p = e ? two >> 16 : two & 0xFFFFu;
+                        if (p <= (uint32_t)last) {
+                            atomicAdd(&h.patterns.counts[p >> 1], p & 1 ? 0x10000u : 1u);
+                            ++all;
+                        }
+                    }
+                }
+            });
+            __syncthreads();
+            counted = true;
+            if (a.V >= 65536) {
+                // A pattern that occurs more often than its counter holds takes 65535 or
+                // 65536 off the counters' sum each time, which nothing makes up for.
+                for (int i = threadIdx.x; i < 32768; i += kT) {
+                    const uint32_t v = h.patterns.counts[i];
+                    all -= (v & 0xFFFFu) + (v >> 16);
+                }
+                counted = over_block_once(all, 0u, s.wave_count, Plus{}) == 0;
+            }
+        }
+        if (__builtin_expect(!counted, 0)) {
+            sample_searching(s, h.searches, row, sc, set);
+            if (threadIdx.x == 0) a.put_found(m, s.found, sc);
+            continue;
+        }
+        P ps = {s, h.patterns, sc};
+        u64 kept = ps.weigh(P::pattern(most) >> 6, last >> 6, least_weight(set.min_p));
+        if (set.min_p > 0.0f) {
+            kept = wave_scan(kept, (u64)0, Plus{});
+            if (lane == 63) s.slots[2][wave] = kept;
+        }
+        __syncthreads();
+        ps.sum_up();
+        if (wave == 0) {
+            u64 Z;
+            uint32_t n;
+            ps.begin(Z, n);
+            // the first to reach a sum is the r-th of a pattern's equal logits
+            auto rank = [](const Place& at, u64 goal) __attribute__((always_inline)) {
+                const u64 x = goal - at.before;
+                u64 r = (u64)((double)x / (double)at.weight);  // off by one at most
+                r += r * at.weight < x ? 1 : 0;
+                r += r * at.weight < x ? 1 : 0;
+                return r - ((r - 1) * at.weight >= x ? 1 : 0);
+            };
+            if (set.top_k > 0 && (uint32_t)set.top_k < n) {
+                const Place at = ps.template find<true>((u64)set.top_k);
+                Z = at.before + ((u64)set.top_k - at.before_count) * at.weight;
+            }
+            if (set.top_p < 1.0f) {
+                const u64 goal = least_sum((double)set.top_p * (double)Z, false, Z);
+                const Place at = ps.template find<false>(goal);
+                Z = at.before + rank(at, goal) * at.weight;
+            }
+            if (set.min_p > 0.0f)
+                Z = min(Z, from_lane(wave_scan(lane < kWaves ? s.slots[2][lane] : 0, (u64)0, Plus{}), 63));
+            const u64 goal = least_sum((double)set.u * (double)Z, true, Z);
+            const Place at = ps.template find<false>(goal);
+            if (lane == 0) {
+                s.found.sum = Z;
+                s.found.logit = P::value(at.d);
+                s.before_count = rank(at, goal);
+                s.flag = at.count == 1;
+            }
+        }
+        __syncthreads();
+        // The r-th one by index.
+        const float l = s.found.logit;
+        if (s.flag) {
+            pieces.each([&](u4_t w, int c) __attribute__((always_inline)) {
+                const uint32_t f = matches(w, l);
+                if (f) s.found.index = c + __builtin_ctz(f);
+            });
+        } else {
+            const uint32_t r = (uint32_t)s.before_count;
+            pieces.each([&](u4_t w, int c) __attribute__((always_inline)) {
+                const uint32_t n =
+                    wave_scan((uint32_t)__builtin_popcount(matches(w, l)), 0u, Plus{});
+                if (lane == 63) h.matches[c / (64 * 8)] = n;
+            });
+            __syncthreads();
+            // The 64 pieces that hold it: each lane sums a stretch of theirs.
+            const int entries = (a.V + 64 * 8 - 1) / (64 * 8), per = (entries + kT - 1) / kT;
+            const int e0 = min((int)threadIdx.x * per, entries), e1 = min(e0 + per, entries);
+            uint32_t mine = 0;
+            for (int e = e0; e < e1; ++e) mine += h.matches[e];
+            uint32_t upto = (uint32_t)running_sum(mine, s.slots[3]) - mine;
+            for (int e = e0; e < e1; ++e) {
+                const uint32_t n = h.matches[e];
+                if (upto < r && r <= upto + n) {
+                    s.bin = e;
+                    s.flag = (int)(r - upto);
+                }
+                upto += n;
+            }
+            __syncthreads();
+            if (wave == 0) {
+                const int c = (s.bin * 64 + lane) * 8;
+                uint32_t f = matches(row.piece(c), l);
+                const uint32_t own = __builtin_popcount(f);
+                const uint32_t sum = wave_scan(own, 0u, Plus{});
+                uint32_t left = (uint32_t)s.flag;
+                if (sum >= left && sum - own < left) {
+                    for (left -= sum - own; left > 1; --left) f &= f - 1;
+                    s.found.index = c + __builtin_ctz(f);
+                }
+            }
+        }
+        __syncthreads();
         if (threadIdx.x == 0) a.put_found(m, s.found, sc);
     }
 }
@@ -1131,6 +1488,23 @@ bool cuts(int dtype, int64_t M, int64_t V) {
     return bytes > 32768 && M <= 64;
 }
 
+// Whether top-k keeps more than the histogram's counts find.
+bool keeps_many(const SampleCall& c) {
+    return !c.top_k.each && c.top_k.value > kSmallK && c.top_k.value < c.V && c.V >= 8192;
+}
+// Whether rows of 16 bits, a workgroup each, go by patterns: long ones, and shorter ones
+// of which top-k keeps many.  Not where all of them keep up to kSmallK.  256 rows of
+// bf16, us, by histogram / by patterns:
+//     V         top-k 50    top-p 0.9   top-k 1000   crowded (temperature 8)
+//     8192      12 / 19     12 / 18     26 / 18      20 / 18
+//     32768     20 / 26     26 / 25     51 / 26      73 / 25
+//     65536     27 / 34     38 / 33     78 / 33      136 / 33
+//     131072    40 / 50     63 / 50     132 / 50     298 / 50
+bool by_patterns(const SampleCall& c) {
+    const int64_t k = c.top_k.each ? 0 : c.top_k.value;
+    return keeps_many(c) || (c.V >= 32768 && !(k > 0 && k <= kSmallK));
+}
+
 template <class E>
 hipError_t launch_pieces(const SampleArgs& a, const Spaces& ws, hipStream_t stream) {
     const dim3 grid((unsigned)ws.pieces, (unsigned)a.M);
@@ -1153,7 +1527,23 @@ hipError_t launch(const SampleCall& c, Arena& ar, hipStream_t stream) {
     const unsigned blocks = (unsigned)(c.M < (1 << 20) ? c.M : 1 << 20);
     const SampleArgs a = {c.logits, c.ld, c.u, c.temperature, c.top_p, c.min_p, c.top_k,
                           c.tokens, c.logprobs, c.M, (int)c.V};
-    if (cut) return launch_pieces<E>(a, ws, stream);
+    // (16-bit rows of which top-k keeps many would be left to one workgroup in the end.)
+    if (cut && !(!std::is_same<E, F32>::value && keeps_many(c)))
+        return launch_pieces<E>(a, ws, stream);
+    if constexpr (!std::is_same<E, F32>::value) {
+        auto go = [&](auto held) {
+            hipLaunchKernelGGL((sample_patterns_kernel<E, decltype(held)::value>), dim3(blocks),
+                               dim3(kT), 0, stream, a);
+            return hipGetLastError();
+        };
+        if (by_patterns(c)) {
+            const int64_t rounds = (c.V + kT * 8 - 1) / (kT * 8);
+            if (rounds <= 2) return go(std::integral_constant<int, 2>{});
+            if (rounds <= 4) return go(std::integral_constant<int, 4>{});
+            if (rounds <= 8) return go(std::integral_constant<int, 8>{});
+            return go(std::integral_constant<int, 0>{});
+        }
+    }
     const int64_t bytes = (c.V + Logits<E>::kWidth - 1) / Logits<E>::kWidth * 16;
     auto go = [&](auto held) {
         hipLaunchKernelGGL((sample_kernel<E, decltype(held)::value>), dim3(blocks), dim3(kT), 0,

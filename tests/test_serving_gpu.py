@@ -12,9 +12,9 @@ Tolerances, derived before the first run.  u is the output type's rounding
  - Quantisation and back: no tolerance.
  - The product: exact operands; fp32 sums of K products in any order, (K + 16)
    2^-23 of the sum of magnitudes; with 8-bit elements on either side the matrix
-   instruction may drop what lies below 2^-11 of the largest of 128 products,
-   from each of them: 128 2^-11 2^-... is far too coarse to be reached, so the
-   bound is taken per instruction as 2^-10 of its largest product.  The epilogue
+   instruction may drop what lies below 2^-11 of the largest of 128 products: the
+   bound per instruction is 2^-10 of its largest product (128 such losses of one
+   sign would be more, and do not occur together).  The epilogue
    adds a few fp32 roundings, the activation's of up to 2^-19 relative.
  - Sampling: tokens are equal; logprobs within 2^-22 (1 + |logprob|)."""
 import sys
@@ -634,6 +634,46 @@ def test_sample_ties(V):
     l[:, ::2] = -1.0
     l[:, 5] = -0.0
     check_sample(l, u, pg.psample(l, u, top_k=V // 2 + 7), "two values", k=V // 2 + 7)
+
+
+@pytest.mark.parametrize("V", [8200, 32768, 65537, 100001])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_sample_long_rows_of_16_bits(V, dtype):
+    """Rows that share few values: both zeros, masked logits, infinities, more equal
+    ones than 16 bits count, one alone among them; top-k of many and by row."""
+    M, rng = 66, np.random.default_rng(V)
+    l = torch.from_numpy((rng.integers(-40, 41, (M, V)) / 8.0).astype(np.float32))
+    l[0] = 0.0
+    l[1] = 0.0
+    l[1, ::2] = -0.0
+    l[2] = -3.0
+    l[2, V - 1] = -2.5
+    l[3] = float("-inf")
+    l[3, [5, V - 2]] = -60000.0
+    l[4, : V - 3] = float("-inf")
+    l[5, 7] = float("inf")
+    l[6, V // 2] = float("nan")
+    l[7] = float("-inf")
+    l[8] = -1.0
+    l[8, 1000:1003] = 20.0
+    l[9, :] = torch.from_numpy(rng.standard_normal(V).astype(np.float32)) * 1e-7
+    l[10, 70:] = 1.0
+    l[10, :70] = 1.5
+    l[11:40] = torch.from_numpy(rng.standard_normal((29, V)).astype(np.float32)) * 4
+    l[20:60, ::7] = float("-inf")
+    l = l.to(dtype).cuda()
+    u = uniform(M, V)
+    u[2:11] = 0.7
+    for s in (dict(), dict(k=600), dict(k=V // 2, p=0.9), dict(t=8.0, p=0.7, m=0.3), dict(t=0.0),
+              dict(k=V - 1, m=0.02), dict(t=1e-3, k=5000)):
+        say("long rows", V, dtype, s)
+        got = pg.psample(l, u, temperature=s.get("t", 1.0), top_k=s.get("k", 0), top_p=s.get("p", 1.0),
+                         min_p=s.get("m", 0.0))
+        check_sample(l, u, got, s, **s)
+    k = torch.from_numpy(rng.integers(-1, V, M).astype(np.int32)).cuda()
+    k[::3] = torch.from_numpy(rng.integers(1, 90, 22).astype(np.int32)).cuda()
+    p = torch.from_numpy(rng.uniform(0.2, 1.1, M).astype(np.float32)).cuda()
+    check_sample(l, u, pg.psample(l, u, top_k=k, top_p=p), "by row", k=k, p=p)
 
 
 def test_sample_crowded():
