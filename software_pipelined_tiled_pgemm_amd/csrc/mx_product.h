@@ -8,7 +8,8 @@ namespace layer {
 
 namespace {
 // Tiles: 256 x 256 where both operands' slots fit three times into LDS, 256 x 128 for 8-bit
-// elements on both sides.
+// elements on both sides (256 x 256 with two slots spilled 38 registers: 1800 TFLOP/s
+// instead of 2240 at 4096 x 4096 x 32768).
 template <int FX, int FW>
 struct MxTiles {
     static constexpr int kBytes = mxp::Frag<FX>::kChunks + mxp::Frag<FW>::kChunks;

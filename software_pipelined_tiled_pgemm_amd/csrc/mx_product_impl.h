@@ -33,7 +33,7 @@ using mxp::Frag;
 // way.
 //
 // Bound by the weights' way from memory, a token's also by the launch: 1 x 4096 x
-// 8192 e4m3 x e2m1 6.9 us (17.8 MB at 2.6 TB/s).  (16 waves for long rows and few strips
+// 8192 e4m3 x e2m1 6.3 us (17.8 MB at 2.8 TB/s).  (16 waves for long rows and few strips
 // were no faster, and half as fast with 4 blocks of rows, which need the registers.)
 constexpr int kFewWaves = 8;
 

@@ -625,8 +625,8 @@ struct Settings {
 
 // The row by one search after the other.
 template <class R>
-__device__ __forceinline__ void sample_searching(Shared& s, Searches& h, const R& row, const Scale& sc,
-                                                 const Settings& set) {
+__device__ __forceinline__ void sample_searching(Shared& s, Searches& h, const R& row,
+                                                 const Scale& sc, const Settings& set) {
     __syncthreads();
     clear(h.all);
     __syncthreads();
@@ -893,7 +893,8 @@ __device__ __forceinline__ void gather_wanted(Shared& s, const R& row, const Sca
         });
 }
 
-// A workgroup per row.  HELD: bytes of LDS that keep the row (0: none).
+// A workgroup per row.  HELD: bytes of LDS that keep the row (0: none).  Bound by
+// instructions, 45 an element where each is weighed.  256 rows of bf16: 12 us of 8192 (top-k 50), 20 of 32768, 27 of 65536.
 template <class E, int HELD>
 __global__ __launch_bounds__(kT) void sample_kernel(const SampleArgs a) {
     __shared__ Shared s;
@@ -965,10 +966,11 @@ __global__ __launch_bounds__(kT) void sample_kernel(const SampleArgs a) {
 // pattern as a whole number of the same order, +0 and -0 the same.  A wave looks at
 // 64 of them, a group; groups[g] holds a group's sums.
 //
-// 256 x 65536 bf16: 33 us for 33.5 MB (1.0 TB/s).  About 18 us of it do not depend on
-// the length (the searches, each a chain of LDS reads and scans of one wave, barriers
-// and 143 KB of counters cleared); a piece of a lane takes 250 instructions over the
-// three passes, which keep the row in registers up to 65536.
+// 256 x 65536 bf16: 33 us for 33.5 MB (1.0 TB/s).  A wave's 2300 vector instructions, most
+// of them in three passes over the row, which stays in registers up to 65536, are 15
+// us of it with four waves a SIMD; the rest is the first read, 143 KB of counters
+// cleared, and the searches, chains of LDS reads and scans of one wave.  (With all waves
+// searching, and barriers between, 38 us.)
 struct Groups {
     u64 sum[1024];
     uint32_t count[1024];
@@ -1182,7 +1184,8 @@ __global__ __launch_bounds__(kT) void sample_patterns_kernel(const SampleArgs a)
         const Scale sc = scale_for(s, most, set.temperature);
         bool counted = false;
         // The last pattern that may have weight; -infinity has none.
-        const int last = min(P::pattern(most - (float)kLightBin / sc.per) + 2, P::pattern(-INFINITY) - 1);
+        const int last =
+            min(P::pattern(most - (float)kLightBin / sc.per) + 2, P::pattern(-INFINITY) - 1);
         if (sc.ordinary()) {
             uint32_t all = 0;
             pieces.each([&](u4_t w, int) __attribute__((always_inline)) {
@@ -1250,7 +1253,8 @@ __global__ __launch_bounds__(kT) void sample_patterns_kernel(const SampleArgs a)
                 Z = at.before + rank(at, goal) * at.weight;
             }
             if (set.min_p > 0.0f)
-                Z = min(Z, from_lane(wave_scan(lane < kWaves ? s.slots[2][lane] : 0, (u64)0, Plus{}), 63));
+                Z = min(Z, from_lane(wave_scan(lane < kWaves ? s.slots[2][lane] : 0, (u64)0, Plus{}),
+                                     63));
             const u64 goal = least_sum((double)set.u * (double)Z, true, Z);
             const Place at = ps.template find<false>(goal);
             if (lane == 0) {
@@ -1343,7 +1347,9 @@ struct Piece {
     }
 };
 
-// The largest logit of each piece; the spaces cleared.
+// The largest logit of each piece; the spaces cleared.  (1 x 131072 fp32, top-k 50: 2.4,
+// 3.5 and 8.5 us in the three launches: latency, the last one with one workgroup at its
+// end that sorts and sums.)
 template <class E>
 __global__ __launch_bounds__(kT) void piece_most_kernel(const SampleArgs a, const Spaces ws) {
     __shared__ uint32_t slots[kT / 64];
