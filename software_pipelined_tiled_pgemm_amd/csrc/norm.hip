@@ -505,7 +505,8 @@ hipError_t forward_as(const NormCall& c, hipStream_t stream) {
     });
     if (!held)
         hipLaunchKernelGGL((norm_long_kernel<E, FORMAT>),
-                           dim3((unsigned)std::min(c.M, kMostBlocks)), dim3(kLongT), 0, stream, x, c.ldx, r, c.ldr, w, h, c.ldh, y, c.ldy, c.mx, c.M, D, c.eps);
+                           dim3((unsigned)std::min(c.M, kMostBlocks)), dim3(kLongT), 0, stream, x,
+                           c.ldx, r, c.ldr, w, h, c.ldh, y, c.ldy, c.mx, c.M, D, c.eps);
     return hipGetLastError();
 }
 
@@ -542,8 +543,8 @@ hipError_t backward_as(const NormGradCall& c, Arena& ar, hipStream_t stream) {
         }
         if (!ar.dry() && c.M > 0) {
             hipLaunchKernelGGL((norm_grad_long_kernel<E>),
-                               dim3((unsigned)std::min(c.M, kMostBlocks)), dim3(kLongT), 0, stream, dy, c.lddy, h, c.ldh, w, dh, c.lddh, dx, c.lddx, factors, c.M,
-                               D, c.eps);
+                               dim3((unsigned)std::min(c.M, kMostBlocks)), dim3(kLongT), 0, stream, dy,
+                               c.lddy, h, c.ldh, w, dh, c.lddh, dx, c.lddx, factors, c.M, D, c.eps);
             if (c.dw)
                 hipLaunchKernelGGL((norm_columns_kernel<E>),
                                    dim3((unsigned)((c.D + 2047) / 2048), (unsigned)parts), dim3(256),
