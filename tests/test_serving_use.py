@@ -254,6 +254,69 @@ def test_rows_stay():
         assert (t[5:] == 7).all() and (t[:, :3] == 7).all() and (t[:, 303:] == 7).all()
 
 
+@pytest.mark.parametrize("M,D", [((1 << 22) + 37, 8), ((1 << 20) + 3, 2056), ((1 << 22) + 70000, 128)])
+def test_more_rows_than_workgroups(M, D):
+    """Launches whose workgroups walk the rows: the ends' rows are what they are by
+    themselves."""
+    print(M, D, flush=True)
+    x = torch.randn(M, D, device="cuda", dtype=torch.bfloat16)
+    w = torch.randn(D, device="cuda").bfloat16()
+    ends = [slice(0, 40), slice(M - 40, M)]
+    y = pg.prmsnorm(x, w)
+    for e in ends:
+        assert torch.equal(y[e], pg.prmsnorm(x[e], w))
+    y = pg.pmx_dequantize(pg.prmsnorm(x, w, format="e2m1"))
+    for e in ends:
+        assert torch.equal(y[e], pg.pmx_dequantize(pg.prmsnorm(x[e], w, format="e2m1")))
+    m = pg.pmx_quantize(x, "e4m3")
+    y = pg.pmx_dequantize(m)
+    for e in ends:
+        q = pg.pmx_quantize(x[e], "e4m3")
+        assert torch.equal(m.codes[e], q.codes)
+        assert torch.equal(y[e], pg.pmx_dequantize(q))
+    y, _ = pg.prmsnorm_bwd(x, x, w, needs=(True, False))
+    for e in ends:
+        assert torch.equal(y[e], pg.prmsnorm_bwd(x[e], x[e], w, needs=(True, False))[0])
+
+
+@pytest.mark.parametrize("V,dtype,k", [(16, torch.float32, 0), (70, torch.float16, 5),
+                                       (8192, torch.bfloat16, 600)])
+def test_more_sampled_rows_than_workgroups(V, dtype, k):
+    M = (1 << 20) + 90
+    print(M, V, flush=True)
+    l = torch.randn(M, V, device="cuda", dtype=dtype) * 3
+    u = torch.rand(M, device="cuda")
+    tokens, logprobs = pg.psample(l, u, top_k=k, top_p=0.9)
+    for e in (slice(0, 80), slice(M - 80, M)):
+        t, p = pg.psample(l[e], u[e], top_k=k, top_p=0.9)
+        assert torch.equal(tokens[e], t) and torch.equal(logprobs[e], p)
+
+
+@pytest.mark.parametrize("by_row", [False, True])
+def test_long_rows_of_16_bits_in_a_graph(by_row):
+    """Many long rows: replays with other logits in the same places, and another call
+    on a second stream meanwhile."""
+    M, V = 90, 50000
+    l, u = torch.empty(M, V, dtype=torch.bfloat16, device="cuda"), torch.rand(M, device="cuda")
+    k = torch.arange(M, dtype=torch.int32, device="cuda") * 9 if by_row else 0
+    ls = [(torch.randn(M, V, device="cuda") * s).bfloat16() for s in (3, 0.1, 40)]
+    ref = [pg.psample(x, u, top_k=k, top_p=0.9) for x in ls]
+    l.copy_(ls[0])
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = pg.psample(l, u, top_k=k, top_p=0.9)
+    for _ in range(2):
+        for x, r in zip(ls, ref):
+            l.copy_(x)
+            other = pg.psample(ls[1], u, top_k=k, top_p=0.9, stream=s)
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out[0], r[0]) and torch.equal(out[1], r[1])
+            assert torch.equal(other[0], ref[1][0])
+
+
 def test_offsets_past_32_bits():
     """Row pitches and row counts whose products pass 2^32 bytes."""
     M, K, pitch = 2100, 200, (1 << 20) + 8
