@@ -30,12 +30,18 @@ namespace pgemm {
 namespace layer {
 namespace {
 
-// 8 columns of a row from any 2-byte boundary, zeros from `cols` on.
+// 8 columns of a row from any 2-byte boundary, zeros from `cols` on.  PAST: past the
+// caches.
+template <bool PAST = false>
 __device__ __forceinline__ u4_t chunk_bits(const uint16_t* row, int col, int cols) {
     const int nv = min(8, cols - col);
     u4_t w = {};
     if (nv == 8) {
-        __builtin_memcpy(&w, row + col, 16);
+        typedef u4_t u4_any __attribute__((aligned(2)));
+        if constexpr (PAST)
+            w = __builtin_nontemporal_load(reinterpret_cast<const u4_any*>(row + col));
+        else
+            __builtin_memcpy(&w, row + col, 16);
     } else if (nv > 0) {
 #pragma unroll
         for (int q = 0; q < 8; ++q)
@@ -43,9 +49,15 @@ __device__ __forceinline__ u4_t chunk_bits(const uint16_t* row, int col, int col
     }
     return w;
 }
+// past: whether what is stored will not be found in a cache anyway (kPast).
 template <class E>
-__device__ __forceinline__ void put_chunk(uint16_t* row, int col, int cols, const float (&v)[8]) {
-    if (col < cols) store8<E, false>(Rows{row, 0, 0}, 0, col, min(8, cols - col), v);
+__device__ __forceinline__ void put_chunk(uint16_t* row, int col, int cols, const float (&v)[8],
+                                          bool past) {
+    if (col >= cols) return;
+    if (past)
+        store8<E, true>(Rows{row, 0, 0}, 0, col, min(8, cols - col), v);
+    else
+        store8<E, false>(Rows{row, 0, 0}, 0, col, min(8, cols - col), v);
 }
 
 struct Add {
@@ -103,7 +115,7 @@ template <class E, int T, int NC, int FORMAT>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_kernel(
     const uint16_t* x, int64_t ldx, const uint16_t* r, int64_t ldr, const uint16_t* __restrict__ w,
     uint16_t* h, int64_t ldh, uint16_t* y, int64_t ldy, const MxRows mx, int64_t M, int D,
-    float eps) {
+    float eps, bool past) {
     constexpr int RPB = T < 256 ? 256 / T : 1;
     __shared__ RowSums<T> sums;
     int turn = 0;
@@ -153,7 +165,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_kernel(
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int col = (t + T * i) * 8;
-            if (h) put_chunk<E>(h + row * ldh, col, D, s[i]);
+            if (h) put_chunk<E>(h + row * ldh, col, D, s[i], past);
             float v[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] = s[i][q] * k * inv;
@@ -164,7 +176,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_kernel(
                 for (int q = 0; q < 8; ++q) v[q] *= f[q];
             }
             if constexpr (FORMAT < 0) {
-                put_chunk<E>(y + row * ldy, col, D, v);
+                put_chunk<E>(y + row * ldy, col, D, v, past);
             } else {
                 typedef Mx<FORMAT> F;
                 // An infinite inv (0 / 0) leaves NaN in the padding too: none there.
@@ -193,7 +205,7 @@ template <class E, int FORMAT>
 __global__ __launch_bounds__(kLongT) void norm_long_kernel(
     const uint16_t* x, int64_t ldx, const uint16_t* r, int64_t ldr, const uint16_t* __restrict__ w,
     uint16_t* h, int64_t ldh, uint16_t* y, int64_t ldy, const MxRows mx, int64_t M, int D,
-    float eps) {
+    float eps, bool past) {
     __shared__ RowSums<kLongT> sums;
     int turn = 0;
     const int padded = (D + kMxGroup - 1) / kMxGroup * kMxGroup;
@@ -240,9 +252,9 @@ __global__ __launch_bounds__(kLongT) void norm_long_kernel(
 #pragma unroll
                 for (int q = 0; q < 8; ++q) v[q] *= f[q];
             }
-            if (h) put_chunk<E>(h + row * ldh, col, D, s);
+            if (h) put_chunk<E>(h + row * ldh, col, D, s, past);
             if constexpr (FORMAT < 0) {
-                put_chunk<E>(y + row * ldy, col, D, v);
+                put_chunk<E>(y + row * ldy, col, D, v, past);
             } else {
                 typedef Mx<FORMAT> F;
 #pragma unroll
@@ -259,13 +271,14 @@ __global__ __launch_bounds__(kLongT) void norm_long_kernel(
 }
 
 // Backward: a workgroup takes rows blockIdx.x * RPB + .., gridDim.x * RPB apart,
-// and leaves its part of dw in part[blockIdx.x][D].  With the next row's loads issued
+// and leaves its part of dw in part[blockIdx.x][D].  READS_PAST: dy, h and dh too are read
+// past the caches (kReadPast).  With the next row's loads issued
 // ahead 16384 x 4096 took 116 us instead of 113, and 2039 x 1025 15 instead of 10.
-template <class E, int T, int NC>
+template <class E, int T, int NC, bool READS_PAST>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_grad_kernel(
     const uint16_t* dy, int64_t lddy, const uint16_t* __restrict__ h, int64_t ldh,
     const uint16_t* __restrict__ w, const uint16_t* dh, int64_t lddh, uint16_t* dx, int64_t lddx,
-    float* __restrict__ part, int64_t M, int D, float eps) {
+    float* __restrict__ part, int64_t M, int D, float eps, bool past) {
     constexpr int RPB = T < 256 ? 256 / T : 1;
     __shared__ RowSums<T> sums;
     __shared__ float joined[RPB > 1 ? RPB : 1][RPB > 1 ? T * 8 : 1];
@@ -282,12 +295,12 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_grad_kernel(
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int col = (t + T * i) * 8;
-            yb[i] = chunk_bits(dy + row * lddy, col, D);
-            hb[i] = chunk_bits(h + row * ldh, col, D);
+            yb[i] = chunk_bits<READS_PAST>(dy + row * lddy, col, D);
+            hb[i] = chunk_bits<READS_PAST>(h + row * ldh, col, D);
         }
         if (dh) {
 #pragma unroll
-            for (int i = 0; i < NC; ++i) ab[i] = chunk_bits(dh + row * lddh, (t + T * i) * 8, D);
+            for (int i = 0; i < NC; ++i) ab[i] = chunk_bits<READS_PAST>(dh + row * lddh, (t + T * i) * 8, D);
         }
         // g of a chunk (times 1 without a weight), and h times k.
         auto chunk = [&](int i, float k, float(&g)[8], float(&n)[8]) __attribute__((always_inline)) {
@@ -349,7 +362,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_grad_kernel(
                 if (dh) unpack8<E>(ab[i], a);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) a[q] += (g[q] - n[q] * mean) * factor;
-                put_chunk<E>(dx + row * lddx, (t + T * i) * 8, D, a);
+                put_chunk<E>(dx + row * lddx, (t + T * i) * 8, D, a, past);
             }
         }
     }
@@ -383,7 +396,7 @@ template <class E>
 __global__ __launch_bounds__(kLongT) void norm_grad_long_kernel(
     const uint16_t* __restrict__ dy, int64_t lddy, const uint16_t* __restrict__ h, int64_t ldh,
     const uint16_t* __restrict__ w, const uint16_t* dh, int64_t lddh, uint16_t* dx, int64_t lddx,
-    float* __restrict__ factors, int64_t M, int D, float eps) {
+    float* __restrict__ factors, int64_t M, int D, float eps, bool past) {
     __shared__ RowSums<kLongT> sums;
     int turn = 0;
     for (int64_t row = blockIdx.x; row < M; row += gridDim.x) {
@@ -437,7 +450,7 @@ __global__ __launch_bounds__(kLongT) void norm_grad_long_kernel(
             if (dh) unpack8<E>(chunk_bits(dh + row * lddh, col, D), a);
 #pragma unroll
             for (int q = 0; q < 8; ++q) a[q] += (g[q] - n[q] * inv * mean) * (inv * k);
-            put_chunk<E>(dx + row * lddx, col, D, a);
+            put_chunk<E>(dx + row * lddx, col, D, a, past);
         });
     }
 }
@@ -488,6 +501,16 @@ bool with_shape(int64_t cols, Run&& run) {
     return true;
 }
 
+// Results of this many bytes and more are stored past the caches: what they would hold of
+// them is gone before the next kernel reads it, and other data with it.  (16384 x 4096
+// bf16 92 -> 75 us forward, 65536 x 1024 98 -> 76, 4096 x 4096 the same, among
+// repetitions; smaller ones stay in the L2 for their reader.)
+constexpr int64_t kPast = 32 << 20;
+// The backward pass reads past the caches as well where its matrices are this large
+// together: 16384 x 4096 100 -> 91 us and 16384 x 8192 205 -> 185; where the memory-side
+// cache (256 MB) still has them it costs 3-10% (4096 x 4096, 16384 x 2048).
+constexpr int64_t kReadPast = 512 << 20;
+
 template <class E, int FORMAT>
 hipError_t forward_as(const NormCall& c, hipStream_t stream) {
     const uint16_t* x = static_cast<const uint16_t*>(c.x);
@@ -496,17 +519,18 @@ hipError_t forward_as(const NormCall& c, hipStream_t stream) {
     uint16_t* h = static_cast<uint16_t*>(c.h);
     uint16_t* y = static_cast<uint16_t*>(c.y);
     const int D = (int)c.D;
+    const bool past = c.M * c.D * 2 >= kPast;
     const bool held = with_shape(FORMAT < 0 ? c.D : mx_padded(c.D), [&](auto s) {
         constexpr int T = decltype(s)::T, NC = decltype(s)::NC;
         constexpr int RPB = T < 256 ? 256 / T : 1;
         const unsigned blocks = (unsigned)std::min((c.M + RPB - 1) / RPB, kMostBlocks);
         hipLaunchKernelGGL((norm_kernel<E, T, NC, FORMAT>), dim3(blocks), dim3(RPB * T), 0, stream, x,
-                           c.ldx, r, c.ldr, w, h, c.ldh, y, c.ldy, c.mx, c.M, D, c.eps);
+                           c.ldx, r, c.ldr, w, h, c.ldh, y, c.ldy, c.mx, c.M, D, c.eps, past);
     });
     if (!held)
         hipLaunchKernelGGL((norm_long_kernel<E, FORMAT>),
                            dim3((unsigned)std::min(c.M, kMostBlocks)), dim3(kLongT), 0, stream, x,
-                           c.ldx, r, c.ldr, w, h, c.ldh, y, c.ldy, c.mx, c.M, D, c.eps);
+                           c.ldx, r, c.ldr, w, h, c.ldh, y, c.ldy, c.mx, c.M, D, c.eps, past);
     return hipGetLastError();
 }
 
@@ -522,6 +546,9 @@ hipError_t backward_as(const NormGradCall& c, Arena& ar, hipStream_t stream) {
     uint16_t* dx = static_cast<uint16_t*>(c.dx);
     const int D = (int)c.D;
     const int dtype = std::is_same<E, BF16>::value ? kBF16 : kF16;
+    const int64_t bytes = c.M * c.D * 2;
+    const bool past = bytes >= kPast,
+               reads_past = bytes * (2 + (dh ? 1 : 0) + (dx ? 1 : 0)) >= kReadPast;
     int64_t parts = 0;
     float* part = nullptr;
     const bool held = with_shape(c.D, [&](auto s) {
@@ -530,9 +557,13 @@ hipError_t backward_as(const NormGradCall& c, Arena& ar, hipStream_t stream) {
         parts = std::min<int64_t>((c.M + RPB - 1) / RPB, kGradBlocks);
         if (c.dw) part = static_cast<float*>(ar.take(std::max<int64_t>(parts, 1) * c.D * 4));
         if (ar.dry() || parts == 0) return;
-        hipLaunchKernelGGL((norm_grad_kernel<E, T, NC>), dim3((unsigned)parts), dim3(RPB * T), 0,
-                           stream, dy, c.lddy, h, c.ldh, w, dh, c.lddh, dx, c.lddx, part, c.M, D,
-                           c.eps);
+        auto go = [&](auto reads_past) {
+            hipLaunchKernelGGL((norm_grad_kernel<E, T, NC, decltype(reads_past)::value>),
+                               dim3((unsigned)parts), dim3(RPB * T), 0, stream, dy, c.lddy, h, c.ldh,
+                               w, dh, c.lddh, dx, c.lddx, part, c.M, D, c.eps, past);
+        };
+        if (reads_past) go(std::true_type{});
+        else go(std::false_type{});
     });
     if (!held) {
         parts = std::min<int64_t>((c.M + kLongRows - 1) / kLongRows, 64);
@@ -544,7 +575,8 @@ hipError_t backward_as(const NormGradCall& c, Arena& ar, hipStream_t stream) {
         if (!ar.dry() && c.M > 0) {
             hipLaunchKernelGGL((norm_grad_long_kernel<E>),
                                dim3((unsigned)std::min(c.M, kMostBlocks)), dim3(kLongT), 0, stream, dy,
-                               c.lddy, h, c.ldh, w, dh, c.lddh, dx, c.lddx, factors, c.M, D, c.eps);
+                               c.lddy, h, c.ldh, w, dh, c.lddh, dx, c.lddx, factors, c.M, D, c.eps,
+                               past);
             if (c.dw)
                 hipLaunchKernelGGL((norm_columns_kernel<E>),
                                    dim3((unsigned)((c.D + 2047) / 2048), (unsigned)parts), dim3(256),

@@ -254,7 +254,8 @@ def test_rows_stay():
         assert (t[5:] == 7).all() and (t[:, :3] == 7).all() and (t[:, 303:] == 7).all()
 
 
-@pytest.mark.parametrize("M,D", [((1 << 22) + 37, 8), ((1 << 20) + 3, 2056), ((1 << 22) + 70000, 128)])
+@pytest.mark.parametrize("M,D", [((1 << 22) + 37, 8), ((1 << 20) + 3, 2056), ((1 << 22) + 70000, 128),
+                                 ((1 << 18) + 5, 1001)])
 def test_more_rows_than_workgroups(M, D):
     """Launches whose workgroups walk the rows: the ends' rows are what they are by
     themselves."""
@@ -274,9 +275,18 @@ def test_more_rows_than_workgroups(M, D):
         q = pg.pmx_quantize(x[e], "e4m3")
         assert torch.equal(m.codes[e], q.codes)
         assert torch.equal(y[e], pg.pmx_dequantize(q))
-    y, _ = pg.prmsnorm_bwd(x, x, w, needs=(True, False))
+    y, dw = pg.prmsnorm_bwd(x, x, w)
     for e in ends:
         assert torch.equal(y[e], pg.prmsnorm_bwd(x[e], x[e], w, needs=(True, False))[0])
+    # dw: n 2^-17 off; up to M / 512 + 512 additions; its rounding
+    exact, size = torch.zeros(D, device="cuda").double(), torch.zeros(D, device="cuda").double()
+    for r in range(0, M, 1 << 18):
+        c = x[r:r + (1 << 18)].double()
+        c = c * c / (c.square().mean(dim=1, keepdim=True) + 1e-6).sqrt()
+        exact += c.sum(dim=0)
+        size += c.abs().sum(dim=0)
+    bound = 2.0 ** -8 * exact.abs() + ((M / 512 + 512) * 2.0 ** -24 + 2.0 ** -17) * size
+    assert ((dw.double() - exact).abs() <= bound).all()
 
 
 @pytest.mark.parametrize("V,dtype,k", [(16, torch.float32, 0), (70, torch.float16, 5),
