@@ -2,7 +2,7 @@
 //
 // A lane takes 8 columns (16 bytes of 16-bit values), 4 neighbouring lanes a
 // block of 32: the block's largest magnitude is two lane exchanges.  Bound by
-// memory: 16384 x 4096 bf16 to e2m1 32-34 us (5.2 TB/s), back 26-27 (6.4).
+// memory: 16384 x 4096 bf16 to e2m1 32-34 us (5.2 TB/s), back 26 (6.5).
 #include <algorithm>
 
 #include "layer_math.h"
@@ -79,7 +79,8 @@ __global__ __launch_bounds__(256) void quantize_kernel(const uint16_t* __restric
 
 template <class E, int FORMAT, int AHEAD>
 __global__ __launch_bounds__(256) void dequantize_kernel(const MxRows x, uint16_t* __restrict__ y,
-                                                         int64_t ldy, const Walk<AHEAD> walk, int cols) {
+                                                         int64_t ldy, const Walk<AHEAD> walk, int cols,
+                                                         bool past) {
     typedef Mx<FORMAT> F;
     const int c = walk.chunk();
     if (c >= walk.chunks) return;
@@ -92,7 +93,11 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const MxRows x, uint16_
               [&](int u, int64_t r) __attribute__((always_inline)) {
                   float v[8];
                   F::decode8(w[u], mx_scale(s[u]), v);
-                  store8<E, false>(Rows{y + r * ldy, 0, 0}, 0, c * 8, min(8, cols - c * 8), v);
+                  const Rows to = {y + r * ldy, 0, 0};
+                  if (past)
+                      store8<E, true>(to, 0, c * 8, min(8, cols - c * 8), v);
+                  else
+                      store8<E, false>(to, 0, c * 8, min(8, cols - c * 8), v);
               });
 }
 
@@ -134,6 +139,11 @@ hipError_t mx_quantize(int dtype, const void* x, int64_t ldx, const MxRows& out,
     });
 }
 
+// Values of this many bytes and more are stored past the caches (16384 x 4096 bf16, one
+// of four matrices in turn, 31.7 -> 26.2 us); smaller ones stay in the L2 for their
+// reader.
+constexpr int64_t kPast = 32 << 20;
+
 hipError_t mx_dequantize(const MxRows& x, int dtype, void* y, int64_t ldy, int64_t rows,
                          int64_t cols, hipStream_t stream) {
     if (rows == 0 || cols == 0) return hipSuccess;
@@ -141,7 +151,8 @@ hipError_t mx_dequantize(const MxRows& x, int dtype, void* y, int64_t ldy, int64
         with_walk(rows, (int)((cols + 7) / 8), [&](auto walk, dim3 grid) {
             hipLaunchKernelGGL(
                 (dequantize_kernel<decltype(e), decltype(f)::value, decltype(walk)::kAhead>), grid,
-                dim3(256), 0, stream, x, static_cast<uint16_t*>(y), ldy, walk, (int)cols);
+                dim3(256), 0, stream, x, static_cast<uint16_t*>(y), ldy, walk, (int)cols,
+                rows * cols * 2 >= kPast);
         });
     });
 }
