@@ -2,7 +2,7 @@
 //
 // A lane takes 8 columns (16 bytes of 16-bit values), 4 neighbouring lanes a
 // block of 32: the block's largest magnitude is two lane exchanges.  Bound by
-// memory: 16384 x 4096 bf16 to e2m1 32-34 us (5.2 TB/s), back 26 (6.5).
+// memory: 16384 x 4096 bf16 to e2m1 28-33 us (5.2-6.0 TB/s), back 26 (6.5).
 #include <algorithm>
 
 #include "layer_math.h"

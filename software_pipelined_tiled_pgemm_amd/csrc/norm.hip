@@ -11,9 +11,9 @@
 //
 // A row is held in registers by 64 lanes (no barrier) or by a workgroup; all
 // passes over it after the first are free of memory, which bounds both:
-//   16384 x 4096 bf16 (134 MB a matrix)   forward 84-85 us (6.4 TB/s), backward
-//   106-113 (4.9) and 5 for the sum of dw's parts;
-//   4096 x 4096 bf16 to e4m3   22-24 us (5.1 TB/s).
+//   16384 x 4096 bf16 (134 MB a matrix)   forward 79-82 us (6.6 TB/s), backward
+//   91-102 (5.3-5.9) and 5 for the sum of dw's parts;
+//   4096 x 4096 bf16 to e4m3   19-20 us (5.9 TB/s).
 // Small ones are bound by latency: 1 x 4096 2.8 us, 2039 x 1025 fp16 7 and 10.
 //
 // Squares leave fp32's range for |h| around 2^64 (bf16) and lose bits below
@@ -165,7 +165,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_kernel(
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int col = (t + T * i) * 8;
-            if (h) put_chunk<E>(h + row * ldh, col, D, s[i], past);
+            if (h) put_chunk<E>(h + row * ldh, col, D, s[i], past && FORMAT >= 0);
             float v[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] = s[i][q] * k * inv;
@@ -252,7 +252,7 @@ __global__ __launch_bounds__(kLongT) void norm_long_kernel(
 #pragma unroll
                 for (int q = 0; q < 8; ++q) v[q] *= f[q];
             }
-            if (h) put_chunk<E>(h + row * ldh, col, D, s, past);
+            if (h) put_chunk<E>(h + row * ldh, col, D, s, past && FORMAT >= 0);
             if constexpr (FORMAT < 0) {
                 put_chunk<E>(y + row * ldy, col, D, v, past);
             } else {
@@ -502,9 +502,10 @@ bool with_shape(int64_t cols, Run&& run) {
 }
 
 // Results of this many bytes and more are stored past the caches: what they would hold of
-// them is gone before the next kernel reads it, and other data with it.  (16384 x 4096
-// bf16 92 -> 75 us forward, 65536 x 1024 98 -> 76, 4096 x 4096 the same, among
-// repetitions; smaller ones stay in the L2 for their reader.)
+// them is gone before the next kernel reads it, and other data with it; smaller ones
+// stay in the L2 for their reader.  h only beside a microscaled y: the backward pass
+// reads it (a step of 16384 x 4096 bf16 took 200 us with neither, 186 with both, 177 with
+// y alone; 4096 x 4096 to e4m3 and back 31 without h, 28 with it).
 constexpr int64_t kPast = 32 << 20;
 // The backward pass reads past the caches as well where its matrices are this large
 // together: 16384 x 4096 100 -> 91 us and 16384 x 8192 205 -> 185; where the memory-side
