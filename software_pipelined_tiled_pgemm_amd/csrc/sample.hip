@@ -1463,8 +1463,11 @@ __global__ __launch_bounds__(kT) void piece_gather_kernel(const SampleArgs a, co
         }
     }
     // This workgroup's entries are written before it counts itself, and the last
-    // one's reads come after its count.  (One lane's fence for all: a fence of every
+    // one's reads come after its count: every wave waits until its own stores, which go
+    // past its CU's cache, are done; then one lane counts for all.  (The barrier alone
+    // waits for LDS, and the lane's release for its own wave's stores.  A release of every
     // wave took 10 us.)
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (threadIdx.x == 0)
         s.bin = __hip_atomic_fetch_add(&space.done, 1u, __ATOMIC_ACQ_REL,
