@@ -534,6 +534,17 @@ int prmsnorm_bwd(int dtype, const void* dy, int64_t lddy, const void* h, int64_t
                  const void* weight, const void* dh, int64_t lddh, void* dx, int64_t lddx,
                  void* dweight, int64_t M, int64_t D, float eps, void* workspace,
                  int64_t workspace_bytes, pgemm_stream_t stream);
+/*
+ * The same at h = x + residual in fp32, which the forward pass normed, instead of
+ * that sum rounded to dtype: for one matrix more to read, dweight has one
+ * rounding less (16384 rows of bf16: 1.6e-3 of its norm off, which its own rounding
+ * is, instead of 2.4e-3).  residual [M,D] is not NULL; the workspace is
+ * prmsnorm_bwd's.
+ */
+int prmsnorm_bwd_sum(int dtype, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                     const void* residual, int64_t ldr, const void* weight, const void* dh,
+                     int64_t lddh, void* dx, int64_t lddx, void* dweight, int64_t M, int64_t D,
+                     float eps, void* workspace, int64_t workspace_bytes, pgemm_stream_t stream);
 int64_t prmsnorm_bwd_workspace_bytes(int dtype, int64_t M, int64_t D, int need_dx,
                                      int need_dweight);
 

@@ -74,6 +74,8 @@ def _declare(lib):
                            ctypes.c_float, p]),
         "prmsnorm_bwd": (i32, [i32, p, i64, p, i64, p, p, i64, p, i64, p, i64, i64,
                                ctypes.c_float, p, i64, p]),
+        "prmsnorm_bwd_sum": (i32, [i32, p, i64, p, i64, p, i64, p, p, i64, p, i64, p, i64, i64,
+                                   ctypes.c_float, p, i64, p]),
         "prmsnorm_bwd_workspace_bytes": (i64, [i32, i64, i64, i32, i32]),
         "pmx_quantize": (i32, [i32, p, i64, i32, p, i64, p, i64, i64, i64, p]),
         "pmx_dequantize": (i32, [i32, p, i64, p, i64, i32, p, i64, i64, i64, p]),

@@ -32,6 +32,8 @@ struct NormGradCall {
     int64_t lddy;
     const void* h;
     int64_t ldh;
+    const void* residual;  // where not NULL, added to h in fp32
+    int64_t ldr;
     const void* weight;
     const void* dh;
     int64_t lddh;

@@ -6,8 +6,10 @@
 //
 // h is summed in fp32 and normed as it is; what is stored of it is rounded once.
 // The backward pass takes the stored h and computes the mean square again (the
-// row is in registers anyway), so the forward pass keeps nothing else.  dw adds
-// fp32 products in a fixed order.
+// row is in registers anyway), so the forward pass keeps nothing else.  That h is
+// rounded costs dw a rounding (16384 rows of bf16: 2.4e-3 of its norm off instead of
+// 1.6e-3) and saves a matrix; a caller who wants it exact gives x and r, whose sum is
+// taken again (SUM: 16384 x 4096 bf16 115 us with dw's sum instead of 93).  dw adds fp32 products in a fixed order.
 //
 // A row is held in registers by 64 lanes (no barrier) or by a workgroup; all
 // passes over it after the first are free of memory, which bounds both:
@@ -271,13 +273,13 @@ __global__ __launch_bounds__(kLongT) void norm_long_kernel(
 }
 
 // Backward: a workgroup takes rows blockIdx.x * RPB + .., gridDim.x * RPB apart,
-// and leaves its part of dw in part[blockIdx.x][D].  READS_PAST: dy, h and dh too are read
-// past the caches (kReadPast).  With the next row's loads issued
+// and leaves its part of dw in part[blockIdx.x][D].  SUM: h is h + r in fp32.
+// READS_PAST: dy, h, r and dh too are read past the caches (kReadPast).  With the next row's loads issued
 // ahead 16384 x 4096 took 116 us instead of 113, and 2039 x 1025 15 instead of 10.
-template <class E, int T, int NC, bool READS_PAST>
+template <class E, int T, int NC, bool SUM, bool READS_PAST>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_grad_kernel(
     const uint16_t* dy, int64_t lddy, const uint16_t* __restrict__ h, int64_t ldh,
-    const uint16_t* __restrict__ w, const uint16_t* dh, int64_t lddh, uint16_t* dx, int64_t lddx,
+    const uint16_t* __restrict__ r, int64_t ldr, const uint16_t* __restrict__ w, const uint16_t* dh, int64_t lddh, uint16_t* dx, int64_t lddx,
     float* __restrict__ part, int64_t M, int D, float eps, bool past) {
     constexpr int RPB = T < 256 ? 256 / T : 1;
     __shared__ RowSums<T> sums;
@@ -291,21 +293,31 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_grad_kernel(
         if (w) wb[i] = chunk_bits(w, (t + T * i) * 8, D);
     for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / T; row < M;
          row += (int64_t)gridDim.x * RPB) {
-        u4_t yb[NC], hb[NC], ab[NC];
+        u4_t yb[NC], hb[NC], rb[NC], ab[NC];
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int col = (t + T * i) * 8;
             yb[i] = chunk_bits<READS_PAST>(dy + row * lddy, col, D);
             hb[i] = chunk_bits<READS_PAST>(h + row * ldh, col, D);
+            if constexpr (SUM) rb[i] = chunk_bits<READS_PAST>(r + row * ldr, col, D);
         }
         if (dh) {
 #pragma unroll
             for (int i = 0; i < NC; ++i) ab[i] = chunk_bits<READS_PAST>(dh + row * lddh, (t + T * i) * 8, D);
         }
+        auto normed = [&](int i, float(&n)[8]) __attribute__((always_inline)) {
+            unpack8<E>(hb[i], n);
+            if constexpr (SUM) {
+                float v[8];
+                unpack8<E>(rb[i], v);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) n[q] += v[q];
+            }
+        };
         // g of a chunk (times 1 without a weight), and h times k.
         auto chunk = [&](int i, float k, float(&g)[8], float(&n)[8]) __attribute__((always_inline)) {
             unpack8<E>(yb[i], g);
-            unpack8<E>(hb[i], n);
+            normed(i, n);
             if (w) {
                 float f[8];
                 unpack8<E>(wb[i], f);
@@ -337,7 +349,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_grad_kernel(
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 float v[8];
-                unpack8<E>(hb[i], v);
+                normed(i, v);
                 most = max(most, most8(v));
             }
             k = scale_of(over_row<T>(most, sums.slots, turn, Most{}));
@@ -390,12 +402,25 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_grad_kernel(
     }
 }
 
+// h of a chunk, with r (where not NULL) added.
+template <class E>
+__device__ __forceinline__ void sum_chunk(const uint16_t* h, const uint16_t* r, int col, int cols,
+                                          float (&n)[8]) {
+    unpack8<E>(chunk_bits(h, col, cols), n);
+    if (r) {
+        float v[8];
+        unpack8<E>(chunk_bits(r, col, cols), v);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) n[q] += v[q];
+    }
+}
+
 // Rows longer than what registers hold: dx, and the factors k and inv of each row,
 // from which the columns' sums are made.
 template <class E>
 __global__ __launch_bounds__(kLongT) void norm_grad_long_kernel(
     const uint16_t* __restrict__ dy, int64_t lddy, const uint16_t* __restrict__ h, int64_t ldh,
-    const uint16_t* __restrict__ w, const uint16_t* dh, int64_t lddh, uint16_t* dx, int64_t lddx,
+    const uint16_t* __restrict__ r, int64_t ldr, const uint16_t* __restrict__ w, const uint16_t* dh, int64_t lddh, uint16_t* dx, int64_t lddx,
     float* __restrict__ factors, int64_t M, int D, float eps, bool past) {
     __shared__ RowSums<kLongT> sums;
     int turn = 0;
@@ -404,7 +429,7 @@ __global__ __launch_bounds__(kLongT) void norm_grad_long_kernel(
             for (int col = threadIdx.x * 8; col < D; col += kLongT * 8) {
                 float g[8], n[8];
                 unpack8<E>(chunk_bits(dy + row * lddy, col, D), g);
-                unpack8<E>(chunk_bits(h + row * ldh, col, D), n);
+                sum_chunk<E>(h + row * ldh, r ? r + row * ldr : nullptr, col, D, n);
                 if (w) {
                     float v[8];
                     unpack8<E>(chunk_bits(w, col, D), v);
@@ -460,7 +485,8 @@ constexpr int kLongRows = 64;
 template <class E>
 __global__ __launch_bounds__(256) void norm_columns_kernel(
     const uint16_t* __restrict__ dy, int64_t lddy, const uint16_t* __restrict__ h, int64_t ldh,
-    const float* __restrict__ factors, float* __restrict__ part, int64_t M, int D) {
+    const uint16_t* __restrict__ res, int64_t ldr, const float* __restrict__ factors,
+    float* __restrict__ part, int64_t M, int D) {
     const int col = (blockIdx.x * 256 + threadIdx.x) * 8;
     if (col >= D) return;
     float s[8] = {};
@@ -470,7 +496,7 @@ __global__ __launch_bounds__(256) void norm_columns_kernel(
         for (int64_t r = b * kLongRows; r < r1; ++r) {
             float d[8], n[8];
             unpack8<E>(chunk_bits(dy + r * lddy, col, D), d);
-            unpack8<E>(chunk_bits(h + r * ldh, col, D), n);
+            sum_chunk<E>(h + r * ldh, res ? res + r * ldr : nullptr, col, D, n);
             const float k = factors[2 * r], inv = factors[2 * r + 1];
 #pragma unroll
             for (int q = 0; q < 8; ++q) s[q] = fmaf(d[q], n[q] * k * inv, s[q]);
@@ -542,6 +568,7 @@ template <class E>
 hipError_t backward_as(const NormGradCall& c, Arena& ar, hipStream_t stream) {
     const uint16_t* dy = static_cast<const uint16_t*>(c.dy);
     const uint16_t* h = static_cast<const uint16_t*>(c.h);
+    const uint16_t* r = static_cast<const uint16_t*>(c.residual);
     const uint16_t* w = static_cast<const uint16_t*>(c.weight);
     const uint16_t* dh = static_cast<const uint16_t*>(c.dh);
     uint16_t* dx = static_cast<uint16_t*>(c.dx);
@@ -549,7 +576,7 @@ hipError_t backward_as(const NormGradCall& c, Arena& ar, hipStream_t stream) {
     const int dtype = std::is_same<E, BF16>::value ? kBF16 : kF16;
     const int64_t bytes = c.M * c.D * 2;
     const bool past = bytes >= kPast,
-               reads_past = bytes * (2 + (dh ? 1 : 0) + (dx ? 1 : 0)) >= kReadPast;
+               reads_past = bytes * (2 + (r ? 1 : 0) + (dh ? 1 : 0) + (dx ? 1 : 0)) >= kReadPast;
     int64_t parts = 0;
     float* part = nullptr;
     const bool held = with_shape(c.D, [&](auto s) {
@@ -558,13 +585,18 @@ hipError_t backward_as(const NormGradCall& c, Arena& ar, hipStream_t stream) {
         parts = std::min<int64_t>((c.M + RPB - 1) / RPB, kGradBlocks);
         if (c.dw) part = static_cast<float*>(ar.take(std::max<int64_t>(parts, 1) * c.D * 4));
         if (ar.dry() || parts == 0) return;
-        auto go = [&](auto reads_past) {
-            hipLaunchKernelGGL((norm_grad_kernel<E, T, NC, decltype(reads_past)::value>),
-                               dim3((unsigned)parts), dim3(RPB * T), 0, stream, dy, c.lddy, h, c.ldh,
-                               w, dh, c.lddh, dx, c.lddx, part, c.M, D, c.eps, past);
+        auto go = [&](auto sum, auto reads_past) {
+            hipLaunchKernelGGL(
+                (norm_grad_kernel<E, T, NC, decltype(sum)::value, decltype(reads_past)::value>),
+                dim3((unsigned)parts), dim3(RPB * T), 0, stream, dy, c.lddy, h, c.ldh, r, c.ldr, w,
+                dh, c.lddh, dx, c.lddx, part, c.M, D, c.eps, past);
         };
-        if (reads_past) go(std::true_type{});
-        else go(std::false_type{});
+        auto with_sum = [&](auto reads_past) {
+            if (r) go(std::true_type{}, reads_past);
+            else go(std::false_type{}, reads_past);
+        };
+        if (reads_past) with_sum(std::true_type{});
+        else with_sum(std::false_type{});
     });
     if (!held) {
         parts = std::min<int64_t>((c.M + kLongRows - 1) / kLongRows, 64);
@@ -576,12 +608,12 @@ hipError_t backward_as(const NormGradCall& c, Arena& ar, hipStream_t stream) {
         if (!ar.dry() && c.M > 0) {
             hipLaunchKernelGGL((norm_grad_long_kernel<E>),
                                dim3((unsigned)std::min(c.M, kMostBlocks)), dim3(kLongT), 0, stream, dy,
-                               c.lddy, h, c.ldh, w, dh, c.lddh, dx, c.lddx, factors, c.M, D, c.eps,
-                               past);
+                               c.lddy, h, c.ldh, r, c.ldr, w, dh, c.lddh, dx, c.lddx, factors, c.M, D,
+                               c.eps, past);
             if (c.dw)
                 hipLaunchKernelGGL((norm_columns_kernel<E>),
                                    dim3((unsigned)((c.D + 2047) / 2048), (unsigned)parts), dim3(256),
-                                   0, stream, dy, c.lddy, h, c.ldh, factors, part, c.M, D);
+                                   0, stream, dy, c.lddy, h, c.ldh, r, c.ldr, factors, part, c.M, D);
         }
     }
     if (ar.dry()) return hipSuccess;

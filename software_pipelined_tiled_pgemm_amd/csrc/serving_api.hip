@@ -63,6 +63,36 @@ int check_mx_linear(int dtype, int xformat, int wformat, int64_t M, int64_t N, i
     return PGEMM_OK;
 }
 
+// The norm's backward pass; `sum`: at h + residual.
+int norm_bwd(NormGradCall c, bool sum, void* workspace, int64_t workspace_bytes,
+             pgemm_stream_t stream) {
+    const int rc = check_sizes(c.dtype, c.M, c.D);
+    if (rc != PGEMM_OK) return rc;
+    if (!valid_eps(c.eps)) return PGEMM_EINVAL;
+    if (c.D == 0 || (!c.dx && !c.dw)) return PGEMM_OK;
+    const int64_t M = c.M, D = c.D;
+    const Mat mdy = mat(c.dy, M, D, c.lddy), mh = mat(c.h, M, D, c.ldh),
+              mr = mat(c.residual, M, D, c.ldr), mw = flat(c.weight, D, 2),
+              mdh = mat(c.dh, M, D, c.lddh), mdx = mat(c.dx, M, D, c.lddx), mdw = flat(c.dw, D, 2);
+    Outputs o;
+    o.add(check(mdy, true));
+    o.add(check(mh, true));
+    o.add(check(mr, sum));
+    for (const Mat* m : {&mw, &mdh, &mdx, &mdw}) o.add(check(*m, false));
+    if (o.rc != PGEMM_OK) return o.rc;
+    for (const Mat* out : {&mdx, &mdw}) {
+        for (const Mat* in : {&mdy, &mh, &mr, &mw}) o.apart(*out, *in);
+        o.apart(*out, mdh, out == &mdx);
+    }
+    o.apart(mdx, mdw);
+    if (o.rc != PGEMM_OK) return o.rc;
+    c.lddy = mdy.ld, c.ldh = mh.ld, c.ldr = mr.ld, c.lddh = mdh.ld, c.lddx = mdx.ld;
+    const Mat all[] = {mdy, mh, mr, mw, mdh, mdx, mdw};
+    return with_workspace(
+        [&](Arena& ar) { return norm_backward(c, ar, static_cast<hipStream_t>(stream)); },
+        workspace, workspace_bytes, all, 7);
+}
+
 }  // namespace
 
 extern "C" {
@@ -130,29 +160,18 @@ int prmsnorm_bwd(int dtype, const void* dy, int64_t lddy, const void* h, int64_t
                  const void* weight, const void* dh, int64_t lddh, void* dx, int64_t lddx,
                  void* dweight, int64_t M, int64_t D, float eps, void* workspace,
                  int64_t workspace_bytes, pgemm_stream_t stream) {
-    const int rc = check_sizes(dtype, M, D);
-    if (rc != PGEMM_OK) return rc;
-    if (!valid_eps(eps)) return PGEMM_EINVAL;
-    if (D == 0 || (!dx && !dweight)) return PGEMM_OK;
-    const Mat mdy = mat(dy, M, D, lddy), mh = mat(h, M, D, ldh), mw = flat(weight, D, 2),
-              mdh = mat(dh, M, D, lddh), mdx = mat(dx, M, D, lddx), mdw = flat(dweight, D, 2);
-    Outputs o;
-    o.add(check(mdy, true));
-    o.add(check(mh, true));
-    for (const Mat* m : {&mw, &mdh, &mdx, &mdw}) o.add(check(*m, false));
-    if (o.rc != PGEMM_OK) return o.rc;
-    for (const Mat* out : {&mdx, &mdw}) {
-        for (const Mat* in : {&mdy, &mh, &mw}) o.apart(*out, *in);
-        o.apart(*out, mdh, out == &mdx);
-    }
-    o.apart(mdx, mdw);
-    if (o.rc != PGEMM_OK) return o.rc;
-    const NormGradCall c = {dtype, dy, mdy.ld, h, mh.ld, weight, dh, mdh.ld, dx, mdx.ld, dweight,
-                            M, D, eps};
-    const Mat all[] = {mdy, mh, mw, mdh, mdx, mdw};
-    return with_workspace(
-        [&](Arena& ar) { return norm_backward(c, ar, static_cast<hipStream_t>(stream)); },
-        workspace, workspace_bytes, all, 6);
+    return norm_bwd({dtype, dy, lddy, h, ldh, nullptr, 0, weight, dh, lddh, dx, lddx, dweight, M, D,
+                     eps},
+                    false, workspace, workspace_bytes, stream);
+}
+
+int prmsnorm_bwd_sum(int dtype, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                     const void* residual, int64_t ldr, const void* weight, const void* dh,
+                     int64_t lddh, void* dx, int64_t lddx, void* dweight, int64_t M, int64_t D,
+                     float eps, void* workspace, int64_t workspace_bytes, pgemm_stream_t stream) {
+    return norm_bwd({dtype, dy, lddy, x, ldx, residual, ldr, weight, dh, lddh, dx, lddx, dweight, M,
+                     D, eps},
+                    true, workspace, workspace_bytes, stream);
 }
 
 int64_t prmsnorm_bwd_workspace_bytes(int dtype, int64_t M, int64_t D, int need_dx,

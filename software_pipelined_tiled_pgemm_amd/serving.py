@@ -204,15 +204,19 @@ def prmsnorm(x, weight=None, residual=None, eps=1e-6, h=None, format=None, out=N
 
 
 def prmsnorm_bwd(dy, h, weight=None, eps=1e-6, dh=None, needs=(True, True), dx=None, dweight=None,
-                 workspace=None, stream=None):
+                 workspace=None, stream=None, residual=None):
     """(dx, dweight) of prmsnorm for the gradient dy [M,D] of its result.  h: as
-    prmsnorm wrote it (x, where there was no residual).  dx is the gradient of x
-    and of residual; dh [M,D], the gradient that reaches h by other ways, is added
-    to it.  `needs` says which are computed (without a weight dweight is not)."""
+    prmsnorm wrote it (x, where there was no residual), rounded to its type; or, with
+    prmsnorm's residual given, its x: the sum is taken in fp32 then, as prmsnorm normed
+    it, and dweight has one rounding less, for one matrix more to read.  dx is the
+    gradient of x and of residual; dh [M,D], the gradient that reaches h by other
+    ways, is added to it.  `needs` says which are computed (without a weight dweight is
+    not)."""
     dt = _dtype(dy, "dy")
     lddy = _mat(dy, "dy", dy)
     M, D = dy.shape
     ldh = _rows(h, "h", dy, M, D)
+    ldr = _rows(residual, "residual", dy, M, D) if residual is not None else 0
     if weight is not None:
         _vec(weight, "weight", dy, D)
     lddh = _rows(dh, "dh", dy, M, D) if dh is not None else 0
@@ -236,6 +240,10 @@ def prmsnorm_bwd(dy, h, weight=None, eps=1e-6, dh=None, needs=(True, True), dx=N
     ws, nws, keep = _workspace(need, workspace, dy, stream)
 
     def run(s):
+        if residual is not None:
+            return L.prmsnorm_bwd_sum(dt, dy.data_ptr(), lddy, h.data_ptr(), ldh, residual.data_ptr(),
+                                      ldr, _ptr(weight), _ptr(dh), lddh, _ptr(dx), lddx,
+                                      _ptr(dweight), M, D, eps, ws, nws, s)
         return L.prmsnorm_bwd(dt, dy.data_ptr(), lddy, h.data_ptr(), ldh, _ptr(weight), _ptr(dh), lddh,
                               _ptr(dx), lddx, _ptr(dweight), M, D, eps, ws, nws, s)
     _call(_invoke(dy, stream, run), "prmsnorm_bwd")

@@ -1,0 +1,96 @@
+"""Calls of the norm, the microscaled operators and sampling that their other GPU
+tests do not make, against plain formulas in binary64 on the CPU.  Tolerances as
+derived in test_serving_gpu.py."""
+import numpy as np
+import pytest
+
+import software_pipelined_tiled_pgemm_amd as pg
+from .test_serving_gpu import (DTYPES, NORM_SHAPES, TINY, UNIT, check_sample, f64, near,
+                              norm_grad_exact, rand, say, uniform)
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", NORM_SHAPES + [(5000, 64), (2100, 520), (700, 4100), (300, 17000),
+                                                 (130, 33000)])
+def test_norm_backward_at_the_sum(shape, dtype):
+    """The gradient at x + residual as the forward pass normed it, in fp32: no rounding
+    but the results' own."""
+    M, D = shape
+    odd = (M + D) % 2
+    say("norm backward at the sum", shape, dtype)
+    dy = rand(shape, dtype, 11, pitch=D + 3 if odd else None)
+    x = rand(shape, dtype, 12, std=3.0, pitch=None if odd else D + 8)
+    r = rand(shape, dtype, 15, std=2.0, pitch=D + 5 if odd else None, offset=odd)
+    w, dh = rand((D,), dtype, 13), rand(shape, dtype, 14, pitch=D + 1)
+    kept = r.clone()
+    dx, dw = pg.prmsnorm_bwd(dy, x, w, eps=1e-5, dh=dh, residual=r)
+    DX, size, DW, wsize = norm_grad_exact(f64(dy), f64(x) + f64(r), f64(w), f64(dh), 1e-5)
+    u = UNIT[dtype]
+    near(dx, DX, u * np.abs(DX) + 2.0 ** -16 * size + TINY[dtype], "dx")
+    near(dw, DW, u * np.abs(DW) + (2.0 ** -17 + M * 2.0 ** -24) * wsize + TINY[dtype], "dw")
+    # each alone, in place of dh; without weight
+    only, none = pg.prmsnorm_bwd(dy, x, w, eps=1e-5, dh=dh, needs=(True, False), dx=dh, residual=r)
+    assert none is None and only is dh
+    none, only = pg.prmsnorm_bwd(dy, x, w, eps=1e-5, needs=(False, True), residual=r)
+    torch.cuda.synchronize()
+    assert none is None and torch.equal(only, dw) and torch.equal(dh, dx) and torch.equal(kept, r)
+    plain, none = pg.prmsnorm_bwd(dy, x, eps=1e-5, residual=r)
+    DX, size, _, _ = norm_grad_exact(f64(dy), f64(x) + f64(r), None, None, 1e-5)
+    assert none is None
+    near(plain, DX, u * np.abs(DX) + 2.0 ** -16 * size + TINY[dtype], "plain dx")
+    # a zero residual: the other form's bits
+    a = pg.prmsnorm_bwd(dy, x, w, eps=1e-5, residual=torch.zeros_like(r))
+    for p, q in zip(a, pg.prmsnorm_bwd(dy, x, w, eps=1e-5)):
+        assert torch.equal(p, q)
+
+
+def test_norm_backward_at_a_sum_beyond_the_type():
+    """x + residual past float16's largest, and squares outside fp32's range."""
+    D = 300
+    x, r = rand((3, D), torch.float16, 1).cpu(), rand((3, D), torch.float16, 2).cpu()
+    x[1], r[1] = 60000.0, x[1].sign() * 50000.0
+    r[2] = -x[2]
+    dy = rand((3, D), torch.float16, 3)
+    dx, dw = pg.prmsnorm_bwd(dy, x.cuda(), torch.ones(D, device="cuda").half(), eps=1e-5,
+                             residual=r.cuda())
+    S = x.double().numpy() + r.double().numpy()
+    DX, size, DW, wsize = norm_grad_exact(f64(dy), S, None, None, 1e-5)
+    near(dx, DX, 2.0 ** -11 * np.abs(DX) + 2.0 ** -16 * size + TINY[torch.float16], "dx")
+    near(dw, DW, 2.0 ** -11 * np.abs(DW) + 2.0 ** -16 * wsize + TINY[torch.float16], "dw")
+    bf = torch.bfloat16
+    scale = torch.tensor([1e30, 1e37, 1e-30, 1.0])[:, None]
+    x, r = ((rand((4, D), bf, s).float().cpu() * scale).to(bf) for s in (4, 5))
+    dy = rand((4, D), bf, 6)
+    dx, dw = pg.prmsnorm_bwd(dy, x.cuda(), torch.ones(D, device="cuda").to(bf), eps=1e-38,
+                             residual=r.cuda())
+    S = x.double().numpy() + r.double().numpy()
+    DX, size, DW, wsize = norm_grad_exact(f64(dy), S, None, None, 1e-38)
+    near(dx, DX, 2.0 ** -8 * np.abs(DX) + 2.0 ** -15 * size + 2.0 ** -133, "dx")
+    near(dw, DW, 2.0 ** -8 * np.abs(DW) + 2.0 ** -16 * wsize, "dw")
+
+
+def test_norm_backward_at_the_sum_refusals_and_graph():
+    x = torch.randn(9, 64, device="cuda").half()
+    w = torch.ones(64, device="cuda").half()
+    for bad in (x[:3], x.bfloat16(), x.cpu(), x.t()):
+        with pytest.raises((TypeError, ValueError)):
+            pg.prmsnorm_bwd(x, x, w, residual=bad)
+    with pytest.raises(pg.PgemmError):
+        pg.prmsnorm_bwd(x, x, w, residual=x.clone(), dx=x)
+    r, dy = torch.randn_like(x), torch.randn_like(x)
+    with pytest.raises(pg.PgemmError):
+        pg.prmsnorm_bwd(dy, x, w, residual=r, dx=r)
+    pg.prmsnorm_bwd(dy, x, w, residual=r)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = pg.prmsnorm_bwd(dy, x, w, residual=r)
+    for _ in range(3):
+        r.copy_(torch.randn_like(r))
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, pg.prmsnorm_bwd(dy, x, w, residual=r)):
+            assert torch.equal(a, b)
