@@ -194,11 +194,13 @@ struct Scale {
     __device__ __forceinline__ int bin(float l) const {
         return l == most ? 0 : (int)fminf((most - l) * per, (float)(kBins - 1));
     }
-    // Where the largest logit and the bins' width are finite numbers above 0 the
+    // Where the largest logit is finite, and the bins' width too and not so large that a
+    // difference beyond fp32's largest has weight (kLightBin / per is 2^127 then), the
     // difference needs no second look: a logit's place in bins is the quotient
-    // (-infinity: infinity), and what lies past kLightBin has no weight.
+    // (-infinity, and a difference that overflows: infinity), and what lies past kLightBin
+    // has no weight.
     __device__ __forceinline__ bool ordinary() const {
-        return fabsf(most) < INFINITY && per < INFINITY && per > 0.0f;
+        return fabsf(most) < INFINITY && per < INFINITY && per >= kLightBin * 0x1p-127f;
     }
     __device__ __forceinline__ float place(float l) const { return (most - l) * per; }
     // Of a logit whose place is below kLightBin: no clamp.

@@ -94,3 +94,25 @@ def test_norm_backward_at_the_sum_refusals_and_graph():
         torch.cuda.synchronize()
         for a, b in zip(out, pg.prmsnorm_bwd(dy, x, w, residual=r)):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("M,V,dtype", [(3, 500, torch.float32), (3, 40000, torch.float32),
+                                       (66, 500, torch.bfloat16), (66, 40000, torch.bfloat16),
+                                       (70, 40000, torch.float32), (2, 40000, torch.bfloat16)])
+def test_sample_differences_beyond_fp32(M, V, dtype):
+    """Finite logits further apart than fp32's largest, at temperatures that leave them
+    weight: for each way that rows go."""
+    l = torch.empty(M, V)
+    l[0] = torch.linspace(-3e38, 3e38, V)
+    l[1:] = torch.from_numpy(np.random.default_rng(V).uniform(-3.3e38, 3.3e38, (M - 1, V))).float()
+    l[1, ::2] = -3e38
+    l[1, 1::2] = 3e38
+    l = l.to(dtype).cuda()
+    u = uniform(M, V + 1)
+    u[:M] = torch.tensor(([0.9, 0.999, 1 - 2.0 ** -24] + u[3:].tolist())[:M])
+    for s in (dict(t=1e36), dict(t=1e37), dict(t=1.3e37), dict(t=1e38), dict(t=3e38, k=V // 2 + 3),
+              dict(t=1e38, k=100), dict(t=2e38, p=0.9), dict(t=1e38, p=0.999, m=0.01)):
+        say("differences beyond fp32", M, V, dtype, s)
+        got = pg.psample(l, u, temperature=s["t"], top_k=s.get("k", 0), top_p=s.get("p", 1.0),
+                         min_p=s.get("m", 0.0))
+        check_sample(l, u, got, s, **s)
