@@ -604,7 +604,7 @@ int64_t pmx_linear_workspace_bytes(int dtype, int xformat, int quantizes, int wf
  * exactly.  PGEMM_EINVAL: V < 1, a temperature, top_p or min_p that is negative or
  * NaN, a min_p beyond 1; of the arrays' numbers a temperature that is not above 0
  * counts as 0, a NaN in top_p or min_p as off, a min_p beyond 1 as 1, a u outside
- * [0, 1) as the nearest number in it (NaN: 0).  PGEMM_EUNSUPPORTED: V of 2^22 and more.
+ * [0, 1) as the nearest float in it (NaN: 0).  PGEMM_EUNSUPPORTED: V of 2^22 and more.
  */
 int psample(int dtype, const void* logits, int64_t ld, const float* u, float temperature,
             const float* temperatures, int32_t top_k, const int32_t* top_ks, float top_p,

@@ -826,7 +826,9 @@ struct SampleArgs {
         return s.each ? v : s.value;
     }
     __device__ __forceinline__ Settings settings(int64_t m) const {
-        return {u[m], of_row(temperature, m), of_row(top_p, m), of_row(min_p, m), of_row(top_k, m)};
+        // a number of 1 and more is the largest fp32 below 1 (below 0, and NaN: least_sum)
+        const float n = u[m];
+        return {n >= 1.0f ? 0x1.fffffep-1f : n, of_row(temperature, m), of_row(top_p, m), of_row(min_p, m), of_row(top_k, m)};
     }
     __device__ __forceinline__ void put(int64_t m, int64_t token, float logprob) const {
         tokens[m] = token;

@@ -116,3 +116,22 @@ def test_sample_differences_beyond_fp32(M, V, dtype):
         got = pg.psample(l, u, temperature=s["t"], top_k=s.get("k", 0), top_p=s.get("p", 1.0),
                          min_p=s.get("m", 0.0))
         check_sample(l, u, got, s, **s)
+
+
+@pytest.mark.parametrize("M,V,dtype", [(6, 2, torch.float32), (6, 300, torch.float16),
+                                       (6, 40000, torch.float32), (66, 40000, torch.bfloat16)])
+def test_sample_numbers_outside_the_interval(M, V, dtype):
+    """A random number of 1 and more draws as the largest float32 below 1 does, not
+    the least likely token; one below 0, and NaN, as 0 does."""
+    l = torch.full((M, V), -25.0, dtype=dtype)  # 1.4e-11 of the largest each
+    l[:, V // 2] = 0.0
+    l = l.cuda()
+    below = 1 - 2.0 ** -24
+    u = torch.tensor([1.0, 2.0, float("inf"), -1.0, float("nan"), float("-inf")] * (M // 6), device="cuda")
+    near_u = torch.tensor([below, below, below, 0.0, 0.0, 0.0] * (M // 6), device="cuda")
+    for s in (dict(), dict(top_k=V), dict(top_k=min(V, 40)), dict(top_p=0.9999999)):
+        say("numbers outside", M, V, dtype, s)
+        got, want = pg.psample(l, u, **s), pg.psample(l, near_u, **s)
+        if V <= 300:  # all of the others together are less than 2^-24 of the row
+            assert (want[0] == V // 2).all()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), s
