@@ -737,8 +737,9 @@ __device__ __forceinline__ Wanted wanted_bins(Shared& s, const Single& h, bool c
     __syncthreads();
     w.first = s.at[1].bin;
     w.before = s.at[1].before;
-    w.last = max(high != low ? s.at[2].bin : w.first, 0);
-    if (w.end <= w.last) w.last = max(w.last, w.end);
+    // high is at most the sum up to the end of top-p's bin, and the token's goal at most
+    // high: first <= last, and last <= end where top-p is on.
+    w.last = high != low ? s.at[2].bin : w.first;
     return w;
 }
 
@@ -898,7 +899,9 @@ __device__ __forceinline__ void gather_wanted(Shared& s, const R& row, const Sca
 }
 
 // A workgroup per row.  HELD: bytes of LDS that keep the row (0: none).  Bound by
-// instructions, 45 an element where each is weighed.  256 rows of bf16: 12 us of 8192 (top-k 50), 20 of 32768, 27 of 65536.
+// instructions, 45 an element where each is weighed.  256 rows of bf16: 12 us of 8192
+// (top-k 50), 20 of 32768, 27 of 65536.  (Up to 15 registers spill: constants that the
+// compiler works out before the loop over rows and reads once a row.)
 template <class E, int HELD>
 __global__ __launch_bounds__(kT) void sample_kernel(const SampleArgs a) {
     __shared__ Shared s;
@@ -974,7 +977,9 @@ __global__ __launch_bounds__(kT) void sample_kernel(const SampleArgs a) {
 // of them in three passes over the row, which stays in registers up to 65536, are 15
 // us of it with four waves a SIMD; the rest is the first read, 143 KB of counters
 // cleared, and the searches, chains of LDS reads and scans of one wave.  (With all waves
-// searching, and barriers between, 38 us.)
+// searching, and barriers between, 38 us.)  Of the 128 registers that 1024 lanes leave each
+// other 21-30 spill: constants from before the loop over rows, read once or twice a row,
+// and with HELD 8 one of its pieces.
 struct Groups {
     u64 sum[1024];
     uint32_t count[1024];
