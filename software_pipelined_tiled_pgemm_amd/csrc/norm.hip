@@ -11,8 +11,9 @@
 // 1.6e-3) and saves a matrix; a caller who wants it exact gives x and r, whose sum is
 // taken again (SUM: 16384 x 4096 bf16 115 us with dw's sum instead of 93).  dw adds fp32 products in a fixed order.
 //
-// A row is held in registers by 64 lanes (no barrier) or by a workgroup; all
-// passes over it after the first are free of memory, which bounds both:
+// A row of up to 32768 columns (backward: 16384) is held in registers by 64 lanes (no
+// barrier) or by a workgroup; all passes over it after the first are free of memory, which
+// bounds both (longer rows are read again for each pass):
 //   16384 x 4096 bf16 (134 MB a matrix)   forward 79-82 us (6.6 TB/s), backward
 //   91-102 (5.3-5.9) and 5 for the sum of dw's parts;
 //   4096 x 4096 bf16 to e4m3   19-20 us (5.9 TB/s).
@@ -512,8 +513,11 @@ struct Shape {
     static constexpr int T = T_, NC = NC_;
 };
 // run(Shape) for the lanes and chunks that hold `cols` columns; false where none
-// does.
-template <class Run>
+// does.  WIDE: up to 32768 columns, else 16384.  (The backward pass holds three times as
+// much of a row and dw's part besides, which the 128 registers that 1024 lanes leave each
+// other do not take: with 162-197 of them spilled 2016 x 16640 bf16 took 411 us, 1024 x
+// 32768 281 and 8 x 32768 46; read again for each pass 136, 124 and 21.)
+template <bool WIDE, class Run>
 bool with_shape(int64_t cols, Run&& run) {
     const int64_t chunks = (cols + 7) / 8;
     if (chunks <= 64) run(Shape<64, 1>{});
@@ -522,8 +526,8 @@ bool with_shape(int64_t cols, Run&& run) {
     else if (chunks <= 512) run(Shape<256, 2>{});
     else if (chunks <= 1024) run(Shape<256, 4>{});
     else if (chunks <= 2048) run(Shape<512, 4>{});
-    else if (chunks <= 4096) run(Shape<1024, 4>{});
-    else return false;
+    else if (!WIDE || chunks > 4096) return false;
+    else if constexpr (WIDE) run(Shape<1024, 4>{});
     return true;
 }
 
@@ -547,7 +551,7 @@ hipError_t forward_as(const NormCall& c, hipStream_t stream) {
     uint16_t* y = static_cast<uint16_t*>(c.y);
     const int D = (int)c.D;
     const bool past = c.M * c.D * 2 >= kPast;
-    const bool held = with_shape(FORMAT < 0 ? c.D : mx_padded(c.D), [&](auto s) {
+    const bool held = with_shape<true>(FORMAT < 0 ? c.D : mx_padded(c.D), [&](auto s) {
         constexpr int T = decltype(s)::T, NC = decltype(s)::NC;
         constexpr int RPB = T < 256 ? 256 / T : 1;
         const unsigned blocks = (unsigned)std::min((c.M + RPB - 1) / RPB, kMostBlocks);
@@ -579,7 +583,7 @@ hipError_t backward_as(const NormGradCall& c, Arena& ar, hipStream_t stream) {
                reads_past = bytes * (2 + (r ? 1 : 0) + (dh ? 1 : 0) + (dx ? 1 : 0)) >= kReadPast;
     int64_t parts = 0;
     float* part = nullptr;
-    const bool held = with_shape(c.D, [&](auto s) {
+    const bool held = with_shape<false>(c.D, [&](auto s) {
         constexpr int T = decltype(s)::T, NC = decltype(s)::NC;
         constexpr int RPB = T < 256 ? 256 / T : 1;
         parts = std::min<int64_t>((c.M + RPB - 1) / RPB, kGradBlocks);

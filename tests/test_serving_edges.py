@@ -135,3 +135,22 @@ def test_sample_numbers_outside_the_interval(M, V, dtype):
         if V <= 300:  # all of the others together are less than 2^-24 of the row
             assert (want[0] == V // 2).all()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), s
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [(1, 16384), (5, 16385), (130, 16392), (70, 20481), (65, 24576),
+                                   (64, 32768), (3, 32775)])
+def test_norm_backward_wide(shape, dtype):
+    """Rows on both sides of what the backward pass holds in registers."""
+    M, D = shape
+    say("norm backward, wide", shape, dtype)
+    dy, h = rand(shape, dtype, 1, pitch=D + D % 2), rand(shape, dtype, 2, std=3.0, pitch=D + 3)
+    w, dh = rand((D,), dtype, 3), rand(shape, dtype, 4)
+    dx, dw = pg.prmsnorm_bwd(dy, h, w, eps=1e-5, dh=dh)
+    DX, size, DW, wsize = norm_grad_exact(f64(dy), f64(h), f64(w), f64(dh), 1e-5)
+    u = UNIT[dtype]
+    near(dx, DX, u * np.abs(DX) + 2.0 ** -16 * size + TINY[dtype], "dx")
+    near(dw, DW, u * np.abs(DW) + (2.0 ** -17 + M * 2.0 ** -24) * wsize + TINY[dtype], "dw")
+    assert pg.prmsnorm_bwd(dy, h, w, eps=1e-5, dh=dh, needs=(True, False), dx=dh)[0] is dh
+    torch.cuda.synchronize()
+    assert torch.equal(dh, dx)
