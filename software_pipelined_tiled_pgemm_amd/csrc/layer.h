@@ -35,6 +35,8 @@ struct Args {
 enum Layout { kNN, kNT, kTN };
 enum Dtype { kF16 = 0, kBF16 = 1 };
 
+constexpr int64_t kMemorySide = 256 << 20;  // bytes of the memory-side cache
+
 inline int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -139,10 +139,15 @@ hipError_t mx_quantize(int dtype, const void* x, int64_t ldx, const MxRows& out,
     });
 }
 
-// Values of this many bytes and more are stored past the caches (16384 x 4096 bf16, one
-// of four matrices in turn, 31.7 -> 26.2 us); smaller ones stay in the L2 for their
-// reader.
-constexpr int64_t kPast = 32 << 20;
+// Values that take half of the memory-side cache and more are stored past the caches: what
+// their reader makes of them, as large again, would push them out.  us with the product that
+// reads them (4096 outputs; 256 outputs), kept / past, rows of 4096 bf16 from e2m1:
+//      8192 rows (64 MB)   194.7 / 196.9   44.1 / 50.5
+//     12288 (96)           287.2 / 294.1   54.4 / 69.6
+//     14336 (112)          366.9 / 376.2   68.0 / 75.2
+//     16384 (128)          395.5 / 393.2   89.8 / 80.9
+//     20480 (160)          484.5 / 488.4  106.9 / 103.6
+constexpr int64_t kPast = kMemorySide / 2;
 
 hipError_t mx_dequantize(const MxRows& x, int dtype, void* y, int64_t ldy, int64_t rows,
                          int64_t cols, hipStream_t stream) {

@@ -52,10 +52,10 @@ __device__ __forceinline__ u4_t chunk_bits(const uint16_t* row, int col, int col
     }
     return w;
 }
-// past: whether what is stored will not be found in a cache anyway (kPast).
+// past: past the caches.
 template <class E>
 __device__ __forceinline__ void put_chunk(uint16_t* row, int col, int cols, const float (&v)[8],
-                                          bool past) {
+                                          bool past = false) {
     if (col >= cols) return;
     if (past)
         store8<E, true>(Rows{row, 0, 0}, 0, col, min(8, cols - col), v);
@@ -113,7 +113,9 @@ __device__ __forceinline__ float inverse_root(float squares, float k, float eps,
     return __builtin_amdgcn_rsqf(squares * (1.0f / (float)D) + eps * k * k);
 }
 
-// T lanes a row, NC chunks of 8 columns a lane.  FORMAT below 0: y in 16 bits.
+// T lanes a row, NC chunks of 8 columns a lane.  FORMAT below 0: y in 16 bits.  past: the
+// larger result that is not read first, y in 16 bits or h beside a microscaled y, is stored
+// past the caches (stores_past()).
 template <class E, int T, int NC, int FORMAT>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_kernel(
     const uint16_t* x, int64_t ldx, const uint16_t* r, int64_t ldr, const uint16_t* __restrict__ w,
@@ -275,13 +277,13 @@ __global__ __launch_bounds__(kLongT) void norm_long_kernel(
 
 // Backward: a workgroup takes rows blockIdx.x * RPB + .., gridDim.x * RPB apart,
 // and leaves its part of dw in part[blockIdx.x][D].  SUM: h is h + r in fp32.
-// READS_PAST: dy, h, r and dh too are read past the caches (kReadPast).  With the next row's loads issued
+// READS_PAST: dy, h, r and dh too are read past the caches.  With the next row's loads issued
 // ahead 16384 x 4096 took 116 us instead of 113, and 2039 x 1025 15 instead of 10.
 template <class E, int T, int NC, bool SUM, bool READS_PAST>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_grad_kernel(
     const uint16_t* dy, int64_t lddy, const uint16_t* __restrict__ h, int64_t ldh,
     const uint16_t* __restrict__ r, int64_t ldr, const uint16_t* __restrict__ w, const uint16_t* dh, int64_t lddh, uint16_t* dx, int64_t lddx,
-    float* __restrict__ part, int64_t M, int D, float eps, bool past) {
+    float* __restrict__ part, int64_t M, int D, float eps) {
     constexpr int RPB = T < 256 ? 256 / T : 1;
     __shared__ RowSums<T> sums;
     __shared__ float joined[RPB > 1 ? RPB : 1][RPB > 1 ? T * 8 : 1];
@@ -375,7 +377,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_grad_kernel(
                 if (dh) unpack8<E>(ab[i], a);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) a[q] += (g[q] - n[q] * mean) * factor;
-                put_chunk<E>(dx + row * lddx, (t + T * i) * 8, D, a, past);
+                put_chunk<E>(dx + row * lddx, (t + T * i) * 8, D, a);
             }
         }
     }
@@ -422,7 +424,7 @@ template <class E>
 __global__ __launch_bounds__(kLongT) void norm_grad_long_kernel(
     const uint16_t* __restrict__ dy, int64_t lddy, const uint16_t* __restrict__ h, int64_t ldh,
     const uint16_t* __restrict__ r, int64_t ldr, const uint16_t* __restrict__ w, const uint16_t* dh, int64_t lddh, uint16_t* dx, int64_t lddx,
-    float* __restrict__ factors, int64_t M, int D, float eps, bool past) {
+    float* __restrict__ factors, int64_t M, int D, float eps) {
     __shared__ RowSums<kLongT> sums;
     int turn = 0;
     for (int64_t row = blockIdx.x; row < M; row += gridDim.x) {
@@ -476,7 +478,7 @@ __global__ __launch_bounds__(kLongT) void norm_grad_long_kernel(
             if (dh) unpack8<E>(chunk_bits(dh + row * lddh, col, D), a);
 #pragma unroll
             for (int q = 0; q < 8; ++q) a[q] += (g[q] - n[q] * inv * mean) * (inv * k);
-            put_chunk<E>(dx + row * lddx, col, D, a, past);
+            put_chunk<E>(dx + row * lddx, col, D, a);
         });
     }
 }
@@ -531,16 +533,32 @@ bool with_shape(int64_t cols, Run&& run) {
     return true;
 }
 
-// Results of this many bytes and more are stored past the caches: what they would hold of
-// them is gone before the next kernel reads it, and other data with it; smaller ones
-// stay in the L2 for their reader.  h only beside a microscaled y: the backward pass
-// reads it (a step of 16384 x 4096 bf16 took 200 us with neither, 186 with both, 177 with
-// y alone; 4096 x 4096 to e4m3 and back 31 without h, 28 with it).
-constexpr int64_t kPast = 32 << 20;
-// The backward pass reads past the caches as well where its matrices are this large
-// together: 16384 x 4096 100 -> 91 us and 16384 x 8192 205 -> 185; where the memory-side
-// cache (256 MB) still has them it costs 3-10% (4096 x 4096, 16384 x 2048).
-constexpr int64_t kReadPast = 512 << 20;
+// What goes past the caches, chosen with the readers of the results in the measurement (a
+// chain of norms, each with the projection that reads its y, the next norm taking h as its
+// residual); us a norm and its readers, rows of 4096 bf16.
+//
+// y in 16 bits, from the size on at which the call's matrices together fill the memory-side
+// cache and push each other out (kept / y past / h past too; 4096 outputs, 256 outputs):
+//      4096 rows (128 MB)   122.5 / 122.9 / 123.9    47.7 /  48.3 /  48.9
+//      8192 (256)           240.0 / 236.8 / 238.8    86.9 /  80.1 /  80.7
+//     12288 (384)           349.2 / 352.2 / 352.6   124.0 / 116.9 / 116.3
+//     16384 (512)           471.4 / 470.5 / 473.5   147.0 / 143.1 / 143.0
+// and the backward pass reads past them from that size on (the norm's backward pass and the
+// product on dx; kept / read past / dx past too): 4096 rows 112.1 / 110.7 / 113.2, 8192
+// 210.1 / 202.4 / 207.1, 16384 413.1 / 388.6 / 409.7; 16384 x 1024 (128 MB) 54.8 / 55.1 /
+// 56.0.  dx stays for its reader.  Norm, projection and both backward passes, 16384 rows: all
+// kept 1301, y and the reads past 1265, h too 1269, dx too 1308; alone, without the
+// products, dx past is the faster (176 instead of 184).
+//
+// h beside a microscaled y, where it is larger than the L2s together (32 MB): what is read
+// first is y, and h would push it out.  Kept / past: 2048 rows (16 MB) 47.7 / 48.0, 3584
+// (28 MB) 70.1 / 70.1, 4096 75.3 / 74.9, 8192 146.6 / 147.1, 12288 223.4 / 207.2, 16384 296.7 /
+// 293.9; with two products of 16384 between h and its reader 4096 445.7 / 443.5, 6144 704.0 /
+// 695.8, 12288 1332 / 1324.  Nothing reading it, 4096 rows to e4m3 and back: 32.4 / 31.2.
+constexpr int64_t kL2 = 32 << 20;
+inline bool stores_past(int format, int64_t bytes, int matrices) {
+    return format < 0 ? bytes * matrices >= kMemorySide : bytes >= kL2;
+}
 
 template <class E, int FORMAT>
 hipError_t forward_as(const NormCall& c, hipStream_t stream) {
@@ -550,7 +568,7 @@ hipError_t forward_as(const NormCall& c, hipStream_t stream) {
     uint16_t* h = static_cast<uint16_t*>(c.h);
     uint16_t* y = static_cast<uint16_t*>(c.y);
     const int D = (int)c.D;
-    const bool past = c.M * c.D * 2 >= kPast;
+    const bool past = stores_past(FORMAT, c.M * c.D * 2, 2 + (r ? 1 : 0) + (h ? 1 : 0));
     const bool held = with_shape<true>(FORMAT < 0 ? c.D : mx_padded(c.D), [&](auto s) {
         constexpr int T = decltype(s)::T, NC = decltype(s)::NC;
         constexpr int RPB = T < 256 ? 256 / T : 1;
@@ -578,9 +596,8 @@ hipError_t backward_as(const NormGradCall& c, Arena& ar, hipStream_t stream) {
     uint16_t* dx = static_cast<uint16_t*>(c.dx);
     const int D = (int)c.D;
     const int dtype = std::is_same<E, BF16>::value ? kBF16 : kF16;
-    const int64_t bytes = c.M * c.D * 2;
-    const bool past = bytes >= kPast,
-               reads_past = bytes * (2 + (r ? 1 : 0) + (dh ? 1 : 0) + (dx ? 1 : 0)) >= kReadPast;
+    const bool reads_past =
+        c.M * c.D * 2 * (2 + (r ? 1 : 0) + (dh ? 1 : 0) + (dx ? 1 : 0)) >= kMemorySide;
     int64_t parts = 0;
     float* part = nullptr;
     const bool held = with_shape<false>(c.D, [&](auto s) {
@@ -593,7 +610,7 @@ hipError_t backward_as(const NormGradCall& c, Arena& ar, hipStream_t stream) {
             hipLaunchKernelGGL(
                 (norm_grad_kernel<E, T, NC, decltype(sum)::value, decltype(reads_past)::value>),
                 dim3((unsigned)parts), dim3(RPB * T), 0, stream, dy, c.lddy, h, c.ldh, r, c.ldr, w,
-                dh, c.lddh, dx, c.lddx, part, c.M, D, c.eps, past);
+                dh, c.lddh, dx, c.lddx, part, c.M, D, c.eps);
         };
         auto with_sum = [&](auto reads_past) {
             if (r) go(std::true_type{}, reads_past);
@@ -613,7 +630,7 @@ hipError_t backward_as(const NormGradCall& c, Arena& ar, hipStream_t stream) {
             hipLaunchKernelGGL((norm_grad_long_kernel<E>),
                                dim3((unsigned)std::min(c.M, kMostBlocks)), dim3(kLongT), 0, stream, dy,
                                c.lddy, h, c.ldh, r, c.ldr, w, dh, c.lddh, dx, c.lddx, factors, c.M, D,
-                               c.eps, past);
+                               c.eps);
             if (c.dw)
                 hipLaunchKernelGGL((norm_columns_kernel<E>),
                                    dim3((unsigned)((c.D + 2047) / 2048), (unsigned)parts), dim3(256),

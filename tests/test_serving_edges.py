@@ -154,3 +154,29 @@ def test_norm_backward_wide(shape, dtype):
     assert pg.prmsnorm_bwd(dy, h, w, eps=1e-5, dh=dh, needs=(True, False), dx=dh)[0] is dh
     torch.cuda.synchronize()
     assert torch.equal(dh, dx)
+
+
+@pytest.mark.parametrize("D", [2056, 2051])
+def test_norm_past_the_caches(D):
+    """Calls larger than the memory-side cache, which store and read past it, give the
+    bits of calls on parts of their rows."""
+    M, dtype = 33000, torch.float16
+    say("norm past the caches", M, D)
+    x, r, dy, dh = (torch.randn(M, D, device="cuda", dtype=dtype) for _ in range(4))
+    w = torch.randn(D, device="cuda").to(dtype)
+    parts = [slice(a, a + 5000) for a in range(0, M, 5000)]
+    h = torch.empty_like(x)
+    y = pg.prmsnorm(x, w, residual=r, h=h)
+    h8 = torch.empty_like(x)
+    m = pg.prmsnorm(x, w, residual=r, h=h8, format="e4m3")
+    v = pg.pmx_dequantize(m, dtype=dtype)
+    dx, dw = pg.prmsnorm_bwd(dy, h, w, dh=dh)
+    sx, sw = pg.prmsnorm_bwd(dy, x, w, dh=dh, residual=r)
+    for p in parts:
+        hp = torch.empty_like(x[p])
+        assert torch.equal(y[p], pg.prmsnorm(x[p], w, residual=r[p], h=hp)) and torch.equal(h[p], hp)
+        q = pg.prmsnorm(x[p], w, residual=r[p], format="e4m3")
+        assert torch.equal(m.codes[p], q.codes) and torch.equal(h8[p], hp)
+        assert torch.equal(v[p], pg.pmx_dequantize(q, dtype=dtype))
+        assert torch.equal(dx[p], pg.prmsnorm_bwd(dy[p], h[p], w, dh=dh[p])[0])
+        assert torch.equal(sx[p], pg.prmsnorm_bwd(dy[p], x[p], w, dh=dh[p], residual=r[p])[0])
