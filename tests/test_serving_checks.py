@@ -28,3 +28,12 @@ def bwd(L, dtype=F16, dy=X, lddy=64, x=H, ldx=64, r=R, ldr=64, w=W, dh=DH, lddh=
 ])
 def test_norm_bwd_sum_checks(L, change, expected):  # noqa: F811
     assert bwd(L, **change) == expected
+
+
+def test_mx_linear_few_rows_of_many_columns(L):  # noqa: F811
+    """A few rows by a vocabulary's columns go by tiles, whose operand is quantised in the
+    workspace; by few columns they are quantised by the kernel itself."""
+    need = L.pmx_linear_workspace_bytes
+    for M in (1, 4):
+        assert need(F16, 1, 1, 0, M, 131072, 4096) > 0
+        assert need(F16, 1, 1, 0, M, 4096, 4096) == 0

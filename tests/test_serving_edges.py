@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 import software_pipelined_tiled_pgemm_amd as pg
-from .test_serving_gpu import (DTYPES, NORM_SHAPES, TINY, UNIT, check_sample, f64, near,
+from .test_serving_gpu import (DTYPES, NORM_SHAPES, TINY, UNIT, check_mx, check_sample, f64, near,
                               norm_grad_exact, rand, say, uniform)
 
 torch = pytest.importorskip("torch")
@@ -180,3 +180,26 @@ def test_norm_past_the_caches(D):
         assert torch.equal(v[p], pg.pmx_dequantize(q, dtype=dtype))
         assert torch.equal(dx[p], pg.prmsnorm_bwd(dy[p], h[p], w, dh=dh[p])[0])
         assert torch.equal(sx[p], pg.prmsnorm_bwd(dy[p], x[p], w, dh=dh[p], residual=r[p])[0])
+
+
+@pytest.mark.parametrize("xf,wf", [("e2m1", "e2m1"), ("e4m3", "e2m1"), ("e4m3", "e4m3"), ("e2m1", "e4m3")])
+@pytest.mark.parametrize("shape", [(1, 65500, 1100), (3, 32700, 2050), (16, 32700, 1153), (17, 16400, 4096),
+                                   (33, 9001, 8192), (64, 16300, 640), (64, 20000, 0), (2, 131000, 129)])
+def test_mx_linear_few_rows_of_many_columns(shape, xf, wf):
+    """Fewer rows than a tile has, by so many columns that they go by tiles."""
+    M, N, K = shape
+    dtype = torch.bfloat16 if M % 2 else torch.float16
+    say("mx linear, few rows of many columns", shape, xf, wf)
+    x = rand((M, K), dtype, 1)
+    w = pg.pmx_quantize(rand((N, K), dtype, 2, std=max(K, 1) ** -0.5), wf)
+    b, r = rand((N,), dtype, 3, std=0.3), rand((M, N), dtype, 4, pitch=N + 3)
+    q = pg.pmx_quantize(x, xf)
+    out = torch.full((M + 2, N + 1), 7.0, dtype=dtype, device="cuda")
+    y = pg.pmx_linear(q, w, bias=b, residual=r, act="silu", out=out[:M, :N])
+    check_mx(y, q, w, b, r, "silu", dtype, "y")
+    assert (out[M:] == 7).all() and (out[:, N] == 7).all()
+    # quantised within the call; in place of the residual
+    assert torch.equal(pg.pmx_linear(x, w, bias=b, residual=r, act="silu", format=xf), y)
+    assert pg.pmx_linear(q, w, bias=b, residual=r, act="silu", out=r) is r
+    torch.cuda.synchronize()
+    assert torch.equal(r, y)
