@@ -323,8 +323,7 @@ def _own(s):
         if h is not None:
             out["h"] = h
         if case["train"]:
-            out["dx"], out["dw"] = pg.prmsnorm_bwd(s["dy"], x if h is None else h, w, eps=EPS,
-                                                   dh=s["dh"])
+            out["dx"], out["dw"] = pg.prmsnorm_bwd(s["dy"], x, w, eps=EPS, dh=s["dh"], residual=r)
         return out
     if case["op"] == "quant":
         return pg.pmx_dequantize(pg.pmx_quantize(s["x"], case["to"]), dtype=dt)
