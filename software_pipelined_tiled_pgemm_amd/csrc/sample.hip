@@ -1500,10 +1500,19 @@ __global__ __launch_bounds__(kT) void piece_gather_kernel(const SampleArgs a, co
     if (threadIdx.x == 0) a.put_found(m, s.found, sc);
 }
 
-// Whether rows are cut into pieces.
+// Whether rows are cut into pieces: up to 16 of them.  In pieces / a workgroup each, us:
+//                        top-k 50                    top-p 0.9
+//     rows           8      16      32      64      16      32      64
+//     65536 fp32   18/22   21/23   32/24   53/24   23/34   36/37   60/38
+//     131072       21/35   31/35   50/35   92/36   40/60   63/61  114/61
+//     65536 bf16   17/22   18/22   22/23   32/23   24/29   28/30   44/30
+//     131072       18/29   21/30   32/31   54/31   32/38   45/39   74/39
+// Rows that the list does not take are left to the last workgroup, which searches them
+// alone: 1 x 131072 fp32 98 us with top-k 1000 and 222 crowded (temperature 8), bf16 crowded
+// 225 where patterns take 37.
 bool cuts(int dtype, int64_t M, int64_t V) {
     const int64_t bytes = V * (dtype == PGEMM_F32 ? 4 : 2);
-    return bytes > 32768 && M <= 64;
+    return bytes > 32768 && M <= 16;
 }
 
 // Whether top-k keeps more than the histogram's counts find.
@@ -1518,6 +1527,8 @@ bool keeps_many(const SampleCall& c) {
 //     32768     20 / 26     26 / 25     51 / 26      73 / 25
 //     65536     27 / 34     38 / 33     78 / 33      136 / 33
 //     131072    40 / 50     63 / 50     132 / 50     298 / 50
+// (By patterns also where each row has a top-k of its own, which the host does not know:
+// 65536 with 50 in every row 36 instead of 29.)
 bool by_patterns(const SampleCall& c) {
     const int64_t k = c.top_k.each ? 0 : c.top_k.value;
     return keeps_many(c) || (c.V >= 32768 && !(k > 0 && k <= kSmallK));

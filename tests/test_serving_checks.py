@@ -37,3 +37,11 @@ def test_mx_linear_few_rows_of_many_columns(L):  # noqa: F811
     for M in (1, 4):
         assert need(F16, 1, 1, 0, M, 131072, 4096) > 0
         assert need(F16, 1, 1, 0, M, 4096, 4096) == 0
+
+
+def test_sample_workspace(L):  # noqa: F811
+    """Up to 16 long rows are cut into pieces, which meet in the workspace."""
+    need = L.psample_workspace_bytes
+    for dtype, V in ((F16, 20000), (BF16, 131072), (F32, 9000)):
+        assert need(dtype, 1, V) > 0 and need(dtype, 16, V) > 0 and need(dtype, 17, V) == 0
+    assert need(F32, 1, 8192) == 0 and need(BF16, 1, 16384) == 0

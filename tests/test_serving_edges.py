@@ -203,3 +203,20 @@ def test_mx_linear_few_rows_of_many_columns(shape, xf, wf):
     assert pg.pmx_linear(q, w, bias=b, residual=r, act="silu", out=r) is r
     torch.cuda.synchronize()
     assert torch.equal(r, y)
+
+
+@pytest.mark.parametrize("M", [15, 16, 17, 40])
+@pytest.mark.parametrize("V,dtype", [(9001, torch.float32), (50000, torch.float32), (40001, torch.bfloat16),
+                                     (33000, torch.float16)])
+def test_sample_on_both_sides_of_pieces(M, V, dtype):
+    """As many long rows as are cut into pieces, and more."""
+    l = rand((M, V), dtype, V, std=3.0, pitch=V + 1)
+    l[M - 1, ::2] = 3.0
+    l[M - 2] = float("-inf")
+    u = uniform(M, M)
+    for s in (dict(), dict(k=50, p=0.95), dict(p=0.9, m=0.01), dict(k=1000), dict(t=8.0, p=0.9),
+              dict(t=0.0)):
+        say("both sides of pieces", M, V, dtype, s)
+        got = pg.psample(l, u, temperature=s.get("t", 1.0), top_k=s.get("k", 0), top_p=s.get("p", 1.0),
+                         min_p=s.get("m", 0.0))
+        check_sample(l, u, got, s, **s)
