@@ -9,15 +9,16 @@
 // row is in registers anyway), so the forward pass keeps nothing else.  That h is
 // rounded costs dw a rounding (16384 rows of bf16: 2.4e-3 of its norm off instead of
 // 1.6e-3) and saves a matrix; a caller who wants it exact gives x and r, whose sum is
-// taken again (SUM: 16384 x 4096 bf16 115 us with dw's sum instead of 93).  dw adds fp32 products in a fixed order.
+// taken again (SUM: 16384 x 4096 bf16 115 us with dw's sum instead of 93).  dw adds fp32
+// products in a fixed order.
 //
 // A row of up to 32768 columns (backward: 16384) is held in registers by 64 lanes (no
 // barrier) or by a workgroup; all passes over it after the first are free of memory, which
 // bounds both (longer rows are read again for each pass):
-//   16384 x 4096 bf16 (134 MB a matrix)   forward 79-82 us (6.6 TB/s), backward
-//   91-102 (5.3-5.9) and 5 for the sum of dw's parts;
-//   4096 x 4096 bf16 to e4m3   19-20 us (5.9 TB/s).
-// Small ones are bound by latency: 1 x 4096 2.8 us, 2039 x 1025 fp16 7 and 10.
+//   16384 x 4096 bf16 (134 MB a matrix)   forward 93-106 us (5.1-5.8 TB/s), backward at
+//   x + r 102-113 (5.9-6.6) and 5 for the sum of dw's parts, each after the other;
+//   4096 x 4096 bf16 to e4m3   21-23 us (5.1-5.6 TB/s).
+// Small ones are bound by latency: 1 x 4096 2.5 us, 2039 x 1025 fp16 8 and 11 (at x + r).
 //
 // Squares leave fp32's range for |h| around 2^64 (bf16) and lose bits below
 // 2^-60: a row whose sum of squares says so is summed again, scaled by a power of
@@ -277,13 +278,14 @@ __global__ __launch_bounds__(kLongT) void norm_long_kernel(
 
 // Backward: a workgroup takes rows blockIdx.x * RPB + .., gridDim.x * RPB apart,
 // and leaves its part of dw in part[blockIdx.x][D].  SUM: h is h + r in fp32.
-// READS_PAST: dy, h, r and dh too are read past the caches.  With the next row's loads issued
-// ahead 16384 x 4096 took 116 us instead of 113, and 2039 x 1025 15 instead of 10.
+// READS_PAST: dy, h, r and dh too are read past the caches.  (The next row's loads issued
+// ahead made 16384 x 4096 3% slower, and 2039 x 1025 15 us instead of 10.)
 template <class E, int T, int NC, bool SUM, bool READS_PAST>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_grad_kernel(
     const uint16_t* dy, int64_t lddy, const uint16_t* __restrict__ h, int64_t ldh,
-    const uint16_t* __restrict__ r, int64_t ldr, const uint16_t* __restrict__ w, const uint16_t* dh, int64_t lddh, uint16_t* dx, int64_t lddx,
-    float* __restrict__ part, int64_t M, int D, float eps) {
+    const uint16_t* __restrict__ r, int64_t ldr, const uint16_t* __restrict__ w, const uint16_t* dh,
+    int64_t lddh, uint16_t* dx, int64_t lddx, float* __restrict__ part, int64_t M, int D,
+    float eps) {
     constexpr int RPB = T < 256 ? 256 / T : 1;
     __shared__ RowSums<T> sums;
     __shared__ float joined[RPB > 1 ? RPB : 1][RPB > 1 ? T * 8 : 1];
@@ -306,7 +308,8 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_grad_kernel(
         }
         if (dh) {
 #pragma unroll
-            for (int i = 0; i < NC; ++i) ab[i] = chunk_bits<READS_PAST>(dh + row * lddh, (t + T * i) * 8, D);
+            for (int i = 0; i < NC; ++i)
+                ab[i] = chunk_bits<READS_PAST>(dh + row * lddh, (t + T * i) * 8, D);
         }
         auto normed = [&](int i, float(&n)[8]) __attribute__((always_inline)) {
             unpack8<E>(hb[i], n);
@@ -423,8 +426,9 @@ __device__ __forceinline__ void sum_chunk(const uint16_t* h, const uint16_t* r, 
 template <class E>
 __global__ __launch_bounds__(kLongT) void norm_grad_long_kernel(
     const uint16_t* __restrict__ dy, int64_t lddy, const uint16_t* __restrict__ h, int64_t ldh,
-    const uint16_t* __restrict__ r, int64_t ldr, const uint16_t* __restrict__ w, const uint16_t* dh, int64_t lddh, uint16_t* dx, int64_t lddx,
-    float* __restrict__ factors, int64_t M, int D, float eps) {
+    const uint16_t* __restrict__ r, int64_t ldr, const uint16_t* __restrict__ w, const uint16_t* dh,
+    int64_t lddh, uint16_t* dx, int64_t lddx, float* __restrict__ factors, int64_t M, int D,
+    float eps) {
     __shared__ RowSums<kLongT> sums;
     int turn = 0;
     for (int64_t row = blockIdx.x; row < M; row += gridDim.x) {
